@@ -1,5 +1,6 @@
 /*
- * topmoe.h — C ABI of the MI355X (gfx950) MiniMind FFN / top-k MoE forward.
+ * topmoe.h — C ABI of the MI355X (gfx950) MiniMind FFN / top-k MoE forward,
+ * its backward, and the operators of the block around it.
  *
  * Operations (definitions from the MiniMind course, lesson 13 "FFN and MoE",
  * sections 0, 1.2, 1.5, 1.6 and source walkthrough steps 3-6; minimind3
@@ -77,9 +78,10 @@ extern "C" {
 #define TOPMOE_ERR_WORKSPACE_TOO_SMALL  -4  /* workspace_bytes < *_workspace_bytes()  */
 #define TOPMOE_ERR_HIP                  -5  /* a HIP runtime call or launch failed    */
 #define TOPMOE_ERR_BAD_ARG              -6  /* aux_coef, z_coef or capacity_factor negative or not
-                                               finite; aux_grad or z_grad not finite; unknown
-                                               flag bits; misaligned pointer; a launch-shape
-                                               override that is not instantiated */
+                                               finite; aux_grad, z_grad or residual_scale not
+                                               finite; eps not positive and finite; unknown
+                                               flag bits or gate mode; misaligned pointer; a
+                                               launch-shape override that is not instantiated */
 #define TOPMOE_ERR_SCRATCH_TOO_SMALL    -7  /* moe_ffn_fwd_noalloc: the problem's workspace
                                                exceeds the fixed scratch */
 
@@ -334,6 +336,160 @@ int moe_ffn_bwd(const void* x, const float* Wr, const void* Wg, const void* Wu,
                 void* dx, float* dWr, void* dWg, void* dWu, void* dWd,
                 void* workspace, size_t workspace_bytes,
                 void* stream, void* const* stage_events);
+
+/* ---- rows by expert and back -------------------------------------------
+ * The dispatch and combine of a top-k MoE whose experts are the caller's own
+ * (the token loop of lesson 13, walkthrough step 5, without the SwiGLU
+ * experts): tokens' rows sorted by expert, and the experts' rows back to
+ * tokens with their weights; with their gradients.
+ *
+ * Entry i = t * k + j is slot j of token t.  Its rank is the number of earlier
+ * entries of the same expert (a token may name an expert twice: two entries).
+ * An expert keeps its first C = ceil(capacity_factor * N * k / E) entries (all
+ * of them for capacity_factor 0); an entry whose topk_idx is outside [0, E)
+ * -- a padding token's -1 -- is kept by none.  Kept entries take the rows
+ * [0, expert_offsets[E]), grouped by ascending expert and in rank order; the
+ * others take the rows behind them, by (expert, rank), those without an expert
+ * last, and their rows hold zeros.  Every row of the [N * k, H] outputs is
+ * written.
+ *
+ * H is a positive multiple of 8 up to 2^20, 1 <= k <= E <= 256, N * k < 2^31;
+ * tensor pointers 16-byte aligned, int32 / float32 arrays 4-byte aligned.
+ * Outputs must not alias inputs or each other, except where said.  With
+ * N == 0 only expert_offsets is written, and every other tensor may be NULL. */
+#define TOPMOE_DISPATCH_STAGES 2  /* 0 rows of the entries (empty for small calls),
+                                     1 copy                                        */
+#define TOPMOE_DISPATCH_MAX_EXPERTS 256
+
+/* Workspace needed by moe_dispatch_fwd: counts per chunk of entries.  Returns
+ * 0 for invalid sizes (a valid call needs at least 256 bytes). */
+size_t moe_dispatch_workspace_bytes(int64_t N, int E, int k);
+
+/* xs[row(i)] = x[t].
+ *   x        [N, H]     tokens (dtype)
+ *   topk_idx [N, k]     int32 experts
+ *   xs       [N*k, H]   output (dtype): the rows by expert, zeros behind them
+ *   expert_offsets [E+1] int32 output: first row of each expert; [E]: kept rows
+ *   row_entry [N*k]     int32 output: the entry of each kept row, then -1
+ *   entry_row [N, k]    int32 output: the entry's row, or -1 - row if not kept
+ *   workspace           at least moe_dispatch_workspace_bytes(N, E, k) bytes,
+ *                       256-byte aligned; contents on entry ignored. */
+int moe_dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t H, int E, int k,
+                     float capacity_factor, int dtype, void* xs, int32_t* expert_offsets,
+                     int32_t* row_entry, int32_t* entry_row, void* workspace,
+                     size_t workspace_bytes, void* stream, void* const* stage_events);
+/* dx[t] = the sum over t's kept entries, in slot order, of dxs[entry_row]
+ * (fp32, rounded once).  dxs [N*k, H], entry_row [N, k] as the dispatch wrote
+ * it, dx [N, H].  One stage. */
+int moe_dispatch_bwd(const void* dxs, const int32_t* entry_row, int64_t N, int64_t H, int k,
+                     int dtype, void* dx, void* stream, void* const* stage_events);
+/* y[t] = residual[t] (or 0) + the sum over t's kept entries, in slot order, of
+ * alpha * ys[entry_row] (fp32, rounded once).  A row that no kept entry names
+ * is not read, nor is the alpha of an entry that is not kept.
+ *   ys [N*k, H] (dtype), alpha [N, k] float32, residual [N, H] optional (may
+ *   alias y), y [N, H] (dtype).  One stage. */
+int moe_combine_fwd(const void* ys, const int32_t* entry_row, const float* alpha,
+                    const void* residual, int64_t N, int64_t H, int k, int dtype, void* y,
+                    void* stream, void* const* stage_events);
+/* dys[entry_row] = alpha * dy[t] for kept entries, zeros in the others' rows;
+ * dalpha = dy[t] . ys[entry_row] (fp32), 0 for entries that are not kept.
+ * entry_row must name each row once, as the dispatch's does.  The gradient of
+ * the residual is dy itself.  One stage. */
+int moe_combine_bwd(const void* dy, const void* ys, const int32_t* entry_row, const float* alpha,
+                    int64_t N, int64_t H, int k, int dtype, void* dys, float* dalpha,
+                    void* stream, void* const* stage_events);
+
+/* ---- norms around a block -----------------------------------------------
+ * The RMS norm before a block (the block's post_attention_layernorm of lesson
+ * 13, sections 1.3-1.4) and, after it, an optional RMS norm of its output, a
+ * gate, the residual stream with its scale, and the next block's norm, in one
+ * pass.  Per token, in fp32:
+ *   yh = y / sqrt(mean(y^2) + eps) with a post norm, y without (w NULL)
+ *   r  = residual_scale * residual + gate * w * yh,    out = r rounded once
+ *   n  = next_w * r / sqrt(mean(r^2) + eps), of the unrounded r, rounded once
+ * H is a multiple of 8 with 8 <= H <= 16384; N < 2^31; eps positive and finite;
+ * weights and gates have x's dtype; tensor pointers are 16-byte aligned (a
+ * token gate, its gradient and the float32 arrays: 4-byte).  Outputs must not
+ * alias inputs or each other, except where said.  With N == 0 tensors of that
+ * size may be NULL; weight gradients are then zero. */
+#define TOPMOE_NORM_BWD_STAGES 2  /* 0 rows, 1 sums over the tokens (forwards: one stage) */
+/* gate_mode: none (1); a value per channel, in gate_rows rows [gate_rows, H]
+ * of which row t / (N / gate_rows) belongs to token t (gate_rows divides N: 1
+ * shares one row, the batch size gives each sequence its own); a value per
+ * token [N]. */
+#define TOPMOE_GATE_NONE 0
+#define TOPMOE_GATE_CHANNEL 1
+#define TOPMOE_GATE_TOKEN 2
+
+/* n = w * x * rstd, rstd = 1 / sqrt(mean(x^2) + eps).  x, n [N, H], w [H],
+ * rstd [N] float32 output (for the backward). */
+int block_prenorm_fwd(const void* x, const void* w, int64_t N, int64_t H, float eps, int dtype,
+                      void* n, float* rstd, void* stream, void* const* stage_events);
+/* Workspace of either backward: float32 partial sums.  Returns 0 for invalid
+ * sizes.  gate_rows: of a channel gate, otherwise 1. */
+size_t block_norm_bwd_workspace_bytes(int64_t N, int64_t H, int64_t gate_rows);
+/* dx = dresidual (or 0) + rstd * (a - xh * mean(a * xh)), a = dn * w,
+ * xh = x * rstd; dw = sum over tokens of dn * xh.
+ *   dresidual [N, H] optional: the gradient that reaches x beside the norm,
+ *   along the residual stream (may alias dx).  dx [N, H], dw [H] outputs. */
+int block_prenorm_bwd(const void* dn, const void* x, const void* w, const float* rstd,
+                      const void* dresidual, int64_t N, int64_t H, int dtype, void* dx, void* dw,
+                      void* workspace, size_t workspace_bytes, void* stream,
+                      void* const* stage_events);
+/*   y, residual [N, H]; w [H] or NULL (no post norm); gate by gate_mode (NULL
+ *   for none); next_w [H] or NULL (no next norm)
+ *   out [N, H] (may alias residual); rstd [N] float32, needed with w; n [N, H]
+ *   and next_rstd [N] float32, needed with next_w */
+int block_postnorm_fwd(const void* y, const void* residual, const void* w, const void* gate,
+                       const void* next_w, int64_t N, int64_t H, int gate_mode,
+                       int64_t gate_rows, float residual_scale, float eps, int dtype, void* out,
+                       float* rstd, void* n, float* next_rstd, void* stream,
+                       void* const* stage_events);
+/* With dr = dout plus the next norm's gradient of out (as block_prenorm_bwd's)
+ * and b = dr * gate * w:
+ *   dresidual = residual_scale * dr;  dy = rstd * (b - yh * mean(b * yh)), or b
+ *   without a post norm;  dw = sum over tokens of gate * dr * yh;  dgate = the
+ *   sum of w * dr * yh over what shares the gate value;  dnext_w.
+ *   dout [N, H], may be NULL (0) with next_w; dn, out, next_rstd needed with
+ *   next_w; rstd, dw with w; dgate with a gate, in the gate's shape and dtype.
+ *   dresidual may alias dout. */
+int block_postnorm_bwd(const void* dout, const void* dn, const void* y, const void* out,
+                       const void* w, const void* gate, const void* next_w, const float* rstd,
+                       const float* next_rstd, int64_t N, int64_t H, int gate_mode,
+                       int64_t gate_rows, float residual_scale, int dtype, void* dy,
+                       void* dresidual, void* dw, void* dgate, void* dnext_w, void* workspace,
+                       size_t workspace_bytes, void* stream, void* const* stage_events);
+
+/* ---- activations in 8 bits ----------------------------------------------
+ * A [R, C] activation kept for the backward pass as OCP e4m3 values q [R, C]
+ * and one scale byte per 32 consecutive channels of a row, scale [R,
+ * ceil(C / 32)] (a row's last group may be shorter): value = q * 2^(byte -
+ * 127).  The exponent is the smallest of at least -127 for which the group's
+ * largest finite magnitude is at most 448 * 2^e (no element saturates; zeros
+ * have byte 0), and q is rounded to nearest even.  An element that is not
+ * finite is kept as NaN and takes no part in the scale.  (A value next to the
+ * dtype's largest may round up past it, and then unpacks to infinity.)
+ * C is a positive multiple of 8 below 2^31, R < 2^31; row pitches (ld*, in
+ * elements) are multiples of 8, at least C; q and scale are dense.  Tensor
+ * pointers 16-byte aligned, q 8-byte.  Outputs must not alias inputs or each
+ * other.  R == 0 is a no-op (pointers may be NULL).  One stage each. */
+#define TOPMOE_ACT8_GROUP 32
+int act8_pack(const void* x, int64_t ldx, int64_t R, int64_t C, int dtype, uint8_t* q,
+              uint8_t* scale, void* stream, void* const* stage_events);
+int act8_unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C, int dtype, void* x,
+                int64_t ldx, void* stream, void* const* stage_events);
+/* h = SiLU(g) * u [R, C] (dense, rounded once), and g, u kept.  g and u may be
+ * the halves of one [R, 2C] projection (pitch 2C). */
+int swiglu_act8_fwd(const void* g, int64_t ldg, const void* u, int64_t ldu, int64_t R, int64_t C,
+                    int dtype, void* h, uint8_t* gq, uint8_t* gscale, uint8_t* uq,
+                    uint8_t* uscale, void* stream, void* const* stage_events);
+/* From the kept g, u and dh [R, C] (dense): dg = dh * u * SiLU'(g),
+ * du = dh * SiLU(g) (pitches lddg, lddu) and, when h is not NULL, h = SiLU(g) * u
+ * again (dense). */
+int swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gscale, const uint8_t* uq,
+                    const uint8_t* uscale, const void* dh, int64_t R, int64_t C, int dtype,
+                    void* dg, int64_t lddg, void* du, int64_t lddu, void* h, void* stream,
+                    void* const* stage_events);
 
 /* Human-readable text for a status code (static storage). */
 const char* topmoe_strerror(int status);

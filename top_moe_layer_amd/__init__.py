@@ -8,6 +8,8 @@ fails loudly if the library has not been built.
 from ._binding import (  # noqa: F401
     DTYPE_BF16,
     DTYPE_FP32,
+    DISPATCH_STAGES,
+    DISPATCH_STAGE_NAMES,
     FFN_BWD_STAGES,
     FFN_BWD_STAGE_NAMES,
     FFN_STAGES,
@@ -16,6 +18,8 @@ from ._binding import (  # noqa: F401
     MOE_BWD_STAGE_NAMES,
     MOE_STAGES,
     MOE_STAGE_NAMES,
+    NORM_BWD_STAGES,
+    NORM_BWD_STAGE_NAMES,
     LIB_PATH,
     StageEvents,
     TopmoeError,
@@ -35,7 +39,16 @@ def __getattr__(name):
                 "moe_bwd_workspace_bytes", "FfnGrads", "MoeGrads"):
         from . import ops
         return getattr(ops, name)
-    if name in ("swiglu_ffn", "moe_ffn"):
+    if name in ("moe_dispatch_fwd", "moe_dispatch_bwd", "moe_combine_fwd", "moe_combine_bwd",
+                "moe_dispatch_workspace_bytes", "block_prenorm_fwd", "block_prenorm_bwd",
+                "block_postnorm_fwd", "block_postnorm_bwd", "block_norm_bwd_workspace_bytes",
+                "act8_pack", "act8_unpack", "swiglu_act8_fwd", "swiglu_act8_bwd", "Act8",
+                "MoeRows", "CombineGrads", "PrenormOutput", "PrenormGrads", "PostnormOutput",
+                "PostnormGrads", "SwigluAct8", "SwigluAct8Grads"):
+        from . import block
+        return getattr(block, name)
+    if name in ("swiglu_ffn", "moe_ffn", "moe_dispatch", "moe_combine", "block_prenorm",
+                "block_postnorm", "swiglu_act8"):
         from . import autograd
         return getattr(autograd, name)
     raise AttributeError(name)

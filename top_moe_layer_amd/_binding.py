@@ -32,6 +32,11 @@ FFN_STAGES = 2
 MOE_STAGES = 5
 FFN_BWD_STAGES = 7
 MOE_BWD_STAGES = 12
+DISPATCH_STAGES = 2
+NORM_BWD_STAGES = 2
+DISPATCH_MAX_EXPERTS = 256
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
+ACT8_GROUP = 32
 
 FFN_STAGE_NAMES = ["gateup_gemm", "down_gemm"]
 MOE_STAGE_NAMES = ["router", "permute", "gateup_gemm", "down_gemm", "combine"]
@@ -39,6 +44,8 @@ FFN_BWD_STAGE_NAMES = ["transpose_w", "transpose_act", "gu_gemm", "dh_gemm", "dx
                        "dwgu_gemm", "dwd_gemm"]
 MOE_BWD_STAGE_NAMES = ["router", "permute", "transpose_w", "transpose_act", "gu_gemm", "dh_gemm",
                        "dx_gemm", "router_bwd", "dx_combine", "dwr", "dwgu_gemm", "dwd_gemm"]
+DISPATCH_STAGE_NAMES = ["rows", "copy"]
+NORM_BWD_STAGE_NAMES = ["rows", "sums"]
 
 # Every function include/topmoe.h declares, with its ctypes signature.
 _vp, _i64, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -67,6 +74,26 @@ SIGNATURES = {
     "moe_ffn_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _vp, _vp, _i64, _i64, _i64,
                            _i32, _i32, _f32, _f32, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                            _sz, _vp, _vp]),
+    "moe_dispatch_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "moe_dispatch_fwd": (_i32, [_vp, _vp, _i64, _i64, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp,
+                                _vp, _sz, _vp, _vp]),
+    "moe_dispatch_bwd": (_i32, [_vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "moe_combine_fwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "moe_combine_bwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "block_prenorm_fwd": (_i32, [_vp, _vp, _i64, _i64, _f32, _i32, _vp, _vp, _vp, _vp]),
+    "block_norm_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "block_prenorm_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _sz,
+                                 _vp, _vp]),
+    "block_postnorm_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i64, _f32, _f32,
+                                  _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "block_postnorm_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32,
+                                  _i64, _f32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "act8_pack": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "act8_unpack": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp]),
+    "swiglu_act8_fwd": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
+                               _vp, _vp]),
+    "swiglu_act8_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _i64,
+                               _vp, _vp, _vp]),
     "topmoe_strerror": (ctypes.c_char_p, [_i32]),
     "topmoe_version": (_i32, []),
     "topmoe_set_tile_override": (_i32, [_i32, _vp]),

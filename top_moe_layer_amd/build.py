@@ -23,7 +23,7 @@ ARCH = os.environ.get("TOPMOE_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["plan.cpp", "api.hip", "router.hip", "permute.hip", "backward.hip", "gemm_bf16.hip",
-           "gemm_f32.hip"]
+           "gemm_f32.hip", "block_api.hip", "rows.hip", "norm.hip", "act8.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function"]
 # Device code: no packed fp32 instructions (they are generated from plain float

@@ -1,0 +1,279 @@
+// Activations kept in 8 bits between the forward and the backward pass.
+//
+// Each group of 32 consecutive channels of a row (the row's last group may be
+// shorter) shares one power-of-two scale 2^e and stores its elements as OCP
+// e4m3 values q = x * 2^-e, rounded to nearest even: e is the smallest integer
+// (at least -127) for which the group's largest finite magnitude is at most
+// 448 * 2^e, 448 being e4m3's largest value, so nothing saturates and the
+// scaling itself is exact.  The scale is stored as the byte e + 127.  An
+// element that is not finite is stored as NaN and takes no part in the scale:
+// a diverged activation stays visible in the gradients.
+//
+// One thread moves 8 channels; the four threads of a group find its largest
+// magnitude with two lane exchanges.  SwiGLU with its two operands kept:
+//   h  = SiLU(g) u          (from g, u as they came)
+//   dg = dh u s (1 + g (1 - s)),  du = dh g s,  h = g s u,  s = sigmoid(g)
+//                           (from the kept g, u; h for the down projection's
+//                            weight gradient)
+// Bound by memory.
+#include "kernels.h"
+#include "vec8.h"
+
+#include "../../include/topmoe.h"
+
+namespace topmoe {
+
+namespace {
+
+// Largest magnitude over the four lanes of a quad, as its fp32 bits (ordered
+// like the magnitudes).
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  uint32_t w = uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xF, 0xF, false));  // lane ^ 1
+  v = v > w ? v : w;
+  w = uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, false));  // lane ^ 2
+  return v > w ? v : w;
+}
+
+// Eight channels of a group to 8 bytes and the group's scale byte.  Every lane
+// of the quad must take part (lanes past the row's end with zeros).
+__device__ __forceinline__ uint32_t pack8(const float (&x)[8], uint32_t (&q)[2]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
+    m = b < 0x7f800000u && b > m ? b : m;
+  }
+  m = quad_max(m);
+  // 448 = 1.75 * 2^8: the exponent less 8, one more for a fraction above 1.75
+  int e = int(m >> 23) - 135 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = e < -127 ? -127 : e;
+  const float inv = __uint_as_float(uint32_t(127 - e) << 23);  // 2^-e, e in [-127, 120]
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool fine = (__float_as_uint(x[i]) & 0x7fffffffu) < 0x7f800000u;
+    v[i] = fine ? x[i] * inv : __uint_as_float(0x7fc00000u);
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    int d = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * w], v[4 * w + 1], 0, false);
+    q[w] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * w + 2], v[4 * w + 3], d, true));
+  }
+  return uint32_t(e + 127);
+}
+
+// 2^(byte - 127) (a byte of 0 is the subnormal 2^-127; 255 is NaN).
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return byte == 0 ? __uint_as_float(0x00400000u)
+                   : byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
+}
+
+__device__ __forceinline__ void unpack_q8(const uint32_t (&q)[2], float s, float (&v)[8]) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    v[4 * w + 0] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 0) * s;
+    v[4 * w + 1] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 1) * s;
+    v[4 * w + 2] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 2) * s;
+    v[4 * w + 3] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 3) * s;
+  }
+}
+
+__device__ __forceinline__ void load_q8(const uint8_t* p, uint32_t (&q)[2]) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+  q[0] = v.x;
+  q[1] = v.y;
+}
+__device__ __forceinline__ void store_q8(uint8_t* p, const uint32_t (&q)[2]) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  *reinterpret_cast<u32x2*>(p) = u32x2{q[0], q[1]};
+}
+
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
+}
+
+// The thread's row and piece: pieces of 8 channels, a row's pieces padded to
+// whole groups (pp = 4 ceil(C / 32)), so that a quad of lanes is one group.
+struct Place {
+  int64_t r;
+  int p;
+  bool any, in;  // any: within the launch's rows; in: and within the row
+};
+__device__ __forceinline__ Place place(int64_t r0, uint32_t pieces, uint32_t pp, int cv) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t dr = i / pp;
+  Place a;
+  a.r = r0 + dr;
+  a.p = int(i - dr * pp);
+  a.any = i < pieces;
+  a.in = a.any && a.p < cv;
+  return a;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_or_zero(const T* p, bool in, float (&v)[8]) {
+  const Raw8<T> raw = in ? load_raw8<T>(p) : zero_raw8<T>();
+  unpack8(raw, v);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void act8_pack_kernel(const T* __restrict__ x, int64_t ldx,
+                                                        int64_t r0, uint32_t pieces, uint32_t pp,
+                                                        int C, uint8_t* __restrict__ q,
+                                                        uint8_t* __restrict__ scale) {
+  const Place a = place(r0, pieces, pp, C / 8);
+  float v[8];
+  load_or_zero<T>(x + a.r * ldx + a.p * 8, a.in, v);
+  uint32_t b[2];
+  const uint32_t s = pack8(v, b);
+  if (a.in) store_q8(q + a.r * C + a.p * 8, b);
+  if (a.any && (a.p & 3) == 0) scale[a.r * (pp / 4) + a.p / 4] = uint8_t(s);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* __restrict__ q,
+                                                          const uint8_t* __restrict__ scale,
+                                                          int64_t r0, uint32_t pieces,
+                                                          uint32_t pp, int C, T* __restrict__ x,
+                                                          int64_t ldx) {
+  const Place a = place(r0, pieces, pp, C / 8);
+  if (!a.in) return;
+  uint32_t b[2];
+  load_q8(q + a.r * C + a.p * 8, b);
+  float v[8];
+  unpack_q8(b, scale_of(scale[a.r * (pp / 4) + a.p / 4]), v);
+  store8<T>(x + a.r * ldx + a.p * 8, v);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void swiglu_act8_fwd_kernel(
+    const T* __restrict__ g, const T* __restrict__ u, int64_t ldg, int64_t ldu, int64_t r0,
+    uint32_t pieces, uint32_t pp, int C, T* __restrict__ h, uint8_t* __restrict__ gq, uint8_t* __restrict__ gs,
+    uint8_t* __restrict__ uq, uint8_t* __restrict__ us) {
+  const Place a = place(r0, pieces, pp, C / 8);
+  float vg[8], vu[8], vh[8];
+  load_or_zero<T>(g + a.r * ldg + a.p * 8, a.in, vg);
+  load_or_zero<T>(u + a.r * ldu + a.p * 8, a.in, vu);
+  uint32_t bg[2], bu[2];
+  const uint32_t sg = pack8(vg, bg), su = pack8(vu, bu);
+  const int64_t o = a.r * C + a.p * 8;
+  if (a.in) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) vh[i] = silu_mul(vg[i], vu[i]);
+    store8<T>(h + o, vh);
+    store_q8(gq + o, bg);
+    store_q8(uq + o, bu);
+  }
+  if (a.any && (a.p & 3) == 0) {
+    const int64_t i = a.r * (pp / 4) + a.p / 4;
+    gs[i] = uint8_t(sg);
+    us[i] = uint8_t(su);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void swiglu_act8_bwd_kernel(
+    const uint8_t* __restrict__ gq, const uint8_t* __restrict__ gs,
+    const uint8_t* __restrict__ uq, const uint8_t* __restrict__ us, const T* __restrict__ dh,
+    int64_t r0, uint32_t pieces, uint32_t pp, int C, T* __restrict__ dg,
+    int64_t ldg, T* __restrict__ du, int64_t ldu, T* __restrict__ h) {
+  const Place a = place(r0, pieces, pp, C / 8);
+  if (!a.in) return;
+  const int64_t o = a.r * C + a.p * 8, si = a.r * (pp / 4) + a.p / 4;
+  uint32_t bg[2], bu[2];
+  load_q8(gq + o, bg);
+  load_q8(uq + o, bu);
+  float vg[8], vu[8], vd[8];
+  const Raw8<T> raw = load_raw8<T>(dh + o);
+  unpack_q8(bg, scale_of(gs[si]), vg);
+  unpack_q8(bu, scale_of(us[si]), vu);
+  unpack8(raw, vd);
+  float og[8], ou[8], oh[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = sigmoid(vg[i]), gsig = vg[i] * s;
+    ou[i] = vd[i] * gsig;
+    oh[i] = gsig * vu[i];
+    og[i] = vd[i] * vu[i] * (s * (1.0f + vg[i] * (1.0f - s)));
+  }
+  store8<T>(dg + a.r * ldg + a.p * 8, og);
+  store8<T>(du + a.r * ldu + a.p * 8, ou);
+  if (h != nullptr) store8<T>(h + o, oh);
+}
+
+// Launches over slabs of rows of at most 2^30 pieces, so that piece numbers
+// stay in 32 bits and a grid within its limit of threads.
+template <typename F>
+hipError_t for_slabs(int64_t R, int64_t C, const Launch& s, F launch) {
+  const uint32_t pp = uint32_t((C + kAct8Group - 1) / kAct8Group * 4);
+  int64_t slab = (int64_t(1) << 30) / pp;
+  if (slab < 1) slab = 1;
+  for (int64_t r0 = 0; r0 < R; r0 += slab) {
+    Launch L = s;
+    if (r0 > 0) L.start = nullptr;
+    if (r0 + slab < R) L.stop = nullptr;
+    const int64_t rows = r0 + slab < R ? slab : R - r0;
+    const uint32_t pieces = uint32_t(rows * pp);
+    const hipError_t e = launch(dim3((pieces + 255) / 256), r0, pieces, pp, L);
+    if (e != hipSuccess) return e;
+    s.launched = true;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+#define TOPMOE_ACT8(T, KERNEL, ...)                                                          \
+  for_slabs(R, C, s, [&](dim3 grid, int64_t r0, uint32_t pieces, uint32_t pp, const Launch& L) { \
+    return launch_kernel(KERNEL<T>, grid, dim3(256), 0, L, __VA_ARGS__);                        \
+  })
+
+hipError_t launch_act8_pack(const void* x, int64_t ldx, int64_t R, int64_t C, int dtype,
+                            uint8_t* q, uint8_t* scale, const Launch& s) {
+  if (dtype == TOPMOE_DTYPE_FP32)
+    return TOPMOE_ACT8(float, act8_pack_kernel, static_cast<const float*>(x), ldx, r0, pieces, pp,
+                       int(C), q, scale);
+  return TOPMOE_ACT8(bf16_t, act8_pack_kernel, static_cast<const bf16_t*>(x), ldx, r0, pieces, pp,
+                     int(C), q, scale);
+}
+
+hipError_t launch_act8_unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C,
+                              int dtype, void* x, int64_t ldx, const Launch& s) {
+  if (dtype == TOPMOE_DTYPE_FP32)
+    return TOPMOE_ACT8(float, act8_unpack_kernel, q, scale, r0, pieces, pp, int(C),
+                       static_cast<float*>(x), ldx);
+  return TOPMOE_ACT8(bf16_t, act8_unpack_kernel, q, scale, r0, pieces, pp, int(C),
+                     static_cast<bf16_t*>(x), ldx);
+}
+
+hipError_t launch_swiglu_act8_fwd(const void* g, int64_t ldg, const void* u, int64_t ldu,
+                                  int64_t R, int64_t C, int dtype, void* h, uint8_t* gq, uint8_t* gs, uint8_t* uq,
+                                  uint8_t* us, const Launch& s) {
+  if (dtype == TOPMOE_DTYPE_FP32)
+    return TOPMOE_ACT8(float, swiglu_act8_fwd_kernel, static_cast<const float*>(g),
+                       static_cast<const float*>(u), ldg, ldu, r0, pieces, pp, int(C),
+                       static_cast<float*>(h), gq, gs, uq, us);
+  return TOPMOE_ACT8(bf16_t, swiglu_act8_fwd_kernel, static_cast<const bf16_t*>(g),
+                     static_cast<const bf16_t*>(u), ldg, ldu, r0, pieces, pp, int(C),
+                     static_cast<bf16_t*>(h), gq, gs, uq, us);
+}
+
+hipError_t launch_swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gs, const uint8_t* uq,
+                                  const uint8_t* us, const void* dh, int64_t R, int64_t C,
+                                  int dtype, void* dg, int64_t ldg, void* du, int64_t ldu, void* h,
+                                  const Launch& s) {
+  if (dtype == TOPMOE_DTYPE_FP32)
+    return TOPMOE_ACT8(float, swiglu_act8_bwd_kernel, gq, gs, uq, us,
+                       static_cast<const float*>(dh), r0, pieces, pp, int(C),
+                       static_cast<float*>(dg), ldg, static_cast<float*>(du), ldu,
+                       static_cast<float*>(h));
+  return TOPMOE_ACT8(bf16_t, swiglu_act8_bwd_kernel, gq, gs, uq, us,
+                     static_cast<const bf16_t*>(dh), r0, pieces, pp, int(C),
+                     static_cast<bf16_t*>(dg), ldg, static_cast<bf16_t*>(du), ldu,
+                     static_cast<bf16_t*>(h));
+}
+
+#undef TOPMOE_ACT8
+
+}  // namespace topmoe

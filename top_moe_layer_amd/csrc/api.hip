@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "api_util.h"
 #include "kernels.h"
 #include "plan.h"
 
@@ -35,30 +36,6 @@ using namespace topmoe;
 
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Stage i's launch: the stream plus, when timing is requested, events
-// 2i / 2i+1 stamped by the stage's kernel dispatch.
-struct Stages {
-  void* const* ev;
-  hipStream_t s;
-  Launch at(int i) const {
-    Launch L;
-    L.s = s;
-    if (ev) {
-      L.start = static_cast<hipEvent_t>(ev[2 * i]);
-      L.stop = static_cast<hipEvent_t>(ev[2 * i + 1]);
-    }
-    return L;
-  }
-  // A stage that enqueued no kernel still gets both events (zero length).
-  hipError_t close(const Launch& L) const {
-    if (!ev || L.launched) return hipSuccess;
-    const hipError_t e = hipEventRecord(L.start, s);
-    return e != hipSuccess ? e : hipEventRecord(L.stop, s);
-  }
-};
-
 // Expert capacity ceil(capacity_factor * N * k / E); 0 = no capacity (also
 // when it could not be reached).
 int capacity_of(double capacity_factor, int64_t N, int k, int E) {
@@ -66,13 +43,6 @@ int capacity_of(double capacity_factor, int64_t N, int k, int E) {
   const double c = ceil(capacity_factor * double(N) * double(k) / double(E));
   return c >= double(N) ? 0 : int(c);
 }
-
-bool nonneg_finite(float v) { return v >= 0.0f && !isinf(v); }
-
-#define TOPMOE_TRY(expr)                              \
-  do {                                                \
-    if ((expr) != hipSuccess) return TOPMOE_ERR_HIP;  \
-  } while (0)
 
 }  // namespace
 
@@ -85,7 +55,8 @@ const char* topmoe_strerror(int status) {
     case TOPMOE_OK: return "ok";
     case TOPMOE_ERR_NULL_ARG: return "a required pointer argument is NULL";
     case TOPMOE_ERR_BAD_SHAPE:
-      return "shape outside the supported limits (H, I multiples of 64; 1 <= E <= 64; "
+      return "shape outside the supported limits (FFN: H, I multiples of 64, E <= 64; block "
+             "operators: H, C multiples of 8, E <= 256, gate rows dividing N, row pitches >= C; "
              "1 <= k <= E; N >= 0; sizes within 32-bit row ids)";
     case TOPMOE_ERR_UNSUPPORTED_DTYPE: return "dtype must be TOPMOE_DTYPE_FP32 or TOPMOE_DTYPE_BF16";
     case TOPMOE_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than the *_workspace_bytes() size";
@@ -95,8 +66,9 @@ const char* topmoe_strerror(int status) {
              "of moe_ffn_fwd_noalloc (TOPMOE_NOALLOC_SCRATCH_BYTES, 64 MiB)";
     case TOPMOE_ERR_BAD_ARG:
       return "invalid argument (aux_coef, z_coef or capacity_factor negative or not finite, "
-             "aux_grad or z_grad not finite, unknown flag bits, a misaligned pointer, or a "
-             "launch-shape override that is not instantiated)";
+             "aux_grad, z_grad or residual_scale not finite, eps not positive and finite, an "
+             "unknown gate mode, unknown flag bits, a misaligned pointer, or a launch-shape "
+             "override that is not instantiated)";
   }
   return "unknown status";
 }

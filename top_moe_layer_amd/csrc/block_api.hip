@@ -1,0 +1,348 @@
+// C ABI entry points of the operators around an FFN / MoE block: rows by
+// expert and back, norms with gate and residual, activations in 8 bits.  See
+// include/topmoe.h for the contract of every function.
+#include <stdint.h>
+
+#include "api_util.h"
+#include "kernels.h"
+#include "plan.h"
+
+#include "../../include/topmoe.h"
+
+using namespace topmoe;
+
+static_assert(kDispatchMaxExperts == TOPMOE_DISPATCH_MAX_EXPERTS, "expert limit");
+static_assert(kAct8Group == TOPMOE_ACT8_GROUP, "scale group");
+static_assert(kGateNone == TOPMOE_GATE_NONE && kGateChannel == TOPMOE_GATE_CHANNEL &&
+                  kGateToken == TOPMOE_GATE_TOKEN,
+              "gate modes");
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+
+bool known_dtype(int dtype) {
+  return dtype == TOPMOE_DTYPE_FP32 || dtype == TOPMOE_DTYPE_BF16;
+}
+
+// ---- rows by expert
+int rows_shape(int64_t N, int64_t H, int k) {
+  if (N < 0 || k < 1 || k > kDispatchMaxExperts || N > kMaxRows / k) return TOPMOE_ERR_BAD_SHAPE;
+  if (H <= 0 || H % 8 != 0 || H > (int64_t(1) << 20)) return TOPMOE_ERR_BAD_SHAPE;
+  return TOPMOE_OK;
+}
+
+// Entries an expert keeps: ceil(capacity_factor * N * k / E); INT32_MAX = all.
+int kept_entries(double capacity_factor, int64_t N, int k, int E) {
+  if (capacity_factor <= 0.0) return INT32_MAX;
+  const double c = ceil(capacity_factor * double(N) * double(k) / double(E));
+  return c >= double(N) * double(k) ? INT32_MAX : int(c);
+}
+
+// ---- norms
+int norm_shape(int64_t N, int64_t H, int64_t gate_rows) {
+  if (N < 0 || N > kMaxRows) return TOPMOE_ERR_BAD_SHAPE;
+  if (H <= 0 || H % 8 != 0 || H > kNormMaxH) return TOPMOE_ERR_BAD_SHAPE;
+  if (gate_rows < 0 || gate_rows > kMaxRows || (gate_rows == 0 && N > 0) ||
+      (gate_rows > 0 && N % gate_rows != 0))
+    return TOPMOE_ERR_BAD_SHAPE;
+  return TOPMOE_OK;
+}
+
+// Tokens that share a row of the gate (the whole batch for the other modes).
+int64_t span_of(int64_t N, int64_t gate_rows) {
+  const int64_t s = gate_rows > 0 ? N / gate_rows : N;
+  return s > 0 ? s : 1;
+}
+
+size_t norm_bwd_bytes(const NormUnits& u, int64_t H) {
+  return align_up(size_t(2) * size_t(u.count) * size_t(H) * sizeof(float) + 1);
+}
+
+// ---- 8-bit activations
+int act8_shape(int64_t R, int64_t C) {
+  if (R < 0 || R > kMaxRows || C <= 0 || C % 8 != 0 || C > kMaxRows) return TOPMOE_ERR_BAD_SHAPE;
+  return TOPMOE_OK;
+}
+bool pitch_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_dispatch_workspace_bytes(int64_t N, int E, int k) {
+  if (E < 1 || E > kDispatchMaxExperts || k > E || rows_shape(N, 8, k) != TOPMOE_OK) return 0;
+  return align_up(plan_dispatch(N * k, E).bytes + 1);
+}
+
+int moe_dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t H, int E, int k,
+                     float capacity_factor, int dtype, void* xs, int32_t* expert_offsets,
+                     int32_t* row_entry, int32_t* entry_row, void* workspace,
+                     size_t workspace_bytes, void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  if (E < 1 || E > kDispatchMaxExperts || k > E) return TOPMOE_ERR_BAD_SHAPE;
+  const int status = rows_shape(N, H, k);
+  if (status != TOPMOE_OK) return status;
+  if (!expert_offsets || !workspace ||
+      (N > 0 && (!x || !topk_idx || !xs || !row_entry || !entry_row)))
+    return TOPMOE_ERR_NULL_ARG;
+  if (!nonneg_finite(capacity_factor)) return TOPMOE_ERR_BAD_ARG;
+  if (workspace_bytes < moe_dispatch_workspace_bytes(N, E, k))
+    return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(topk_idx, 4) || !aligned(expert_offsets, 4) ||
+      !aligned(row_entry, 4) || !aligned(entry_row, 4) || !aligned(workspace, 256))
+    return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch rows = st.at(0), copy = st.at(1);
+  TOPMOE_TRY(launch_dispatch_rows(x, topk_idx, N, int(H), E, k,
+                                  kept_entries(capacity_factor, N, k, E), dtype, xs,
+                                  expert_offsets, row_entry, entry_row,
+                                  static_cast<int32_t*>(workspace), rows, copy));
+  TOPMOE_TRY(st.close(rows));
+  TOPMOE_TRY(st.close(copy));
+  return TOPMOE_OK;
+}
+
+int moe_dispatch_bwd(const void* dxs, const int32_t* entry_row, int64_t N, int64_t H, int k,
+                     int dtype, void* dx, void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = rows_shape(N, H, k);
+  if (status != TOPMOE_OK) return status;
+  if (N > 0 && (!dxs || !entry_row || !dx)) return TOPMOE_ERR_NULL_ARG;
+  if (!aligned(dxs, 16) || !aligned(dx, 16) || !aligned(entry_row, 4)) return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_gather_sum(dxs, entry_row, nullptr, nullptr, N, int(H), k, dtype, dx, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+int moe_combine_fwd(const void* ys, const int32_t* entry_row, const float* alpha,
+                    const void* residual, int64_t N, int64_t H, int k, int dtype, void* y,
+                    void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = rows_shape(N, H, k);
+  if (status != TOPMOE_OK) return status;
+  if (N > 0 && (!ys || !entry_row || !alpha || !y)) return TOPMOE_ERR_NULL_ARG;
+  if (!aligned(ys, 16) || !aligned(residual, 16) || !aligned(y, 16) || !aligned(entry_row, 4) ||
+      !aligned(alpha, 4))
+    return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_gather_sum(ys, entry_row, alpha, residual, N, int(H), k, dtype, y, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+int moe_combine_bwd(const void* dy, const void* ys, const int32_t* entry_row, const float* alpha,
+                    int64_t N, int64_t H, int k, int dtype, void* dys, float* dalpha,
+                    void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = rows_shape(N, H, k);
+  if (status != TOPMOE_OK) return status;
+  if (N > 0 && (!dy || !ys || !entry_row || !alpha || !dys || !dalpha)) return TOPMOE_ERR_NULL_ARG;
+  if (!aligned(dy, 16) || !aligned(ys, 16) || !aligned(dys, 16) || !aligned(entry_row, 4) ||
+      !aligned(alpha, 4) || !aligned(dalpha, 4))
+    return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_moe_combine_bwd(dy, ys, entry_row, alpha, N, int(H), k, dtype, dys, dalpha, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+int block_prenorm_fwd(const void* x, const void* w, int64_t N, int64_t H, float eps, int dtype,
+                      void* n, float* rstd, void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = norm_shape(N, H, N > 0 ? 1 : 0);
+  if (status != TOPMOE_OK) return status;
+  if (!w || (N > 0 && (!x || !n || !rstd))) return TOPMOE_ERR_NULL_ARG;
+  if (!(eps > 0.f) || isinf(eps)) return TOPMOE_ERR_BAD_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(n, 16) || !aligned(rstd, 4))
+    return TOPMOE_ERR_BAD_ARG;
+  NormFwd a{};
+  a.y = x; a.next_w = w; a.n = n; a.next_rstd = rstd;
+  a.N = N; a.H = int(H); a.hv = int(H / 8); a.eps = eps; a.gate_span = 1;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_norm_fwd(a, false, true, dtype, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+size_t block_norm_bwd_workspace_bytes(int64_t N, int64_t H, int64_t gate_rows) {
+  if (norm_shape(N, H, gate_rows) != TOPMOE_OK) return 0;
+  return norm_bwd_bytes(plan_norm_units(N, gate_rows, span_of(N, gate_rows)), H);
+}
+
+int block_prenorm_bwd(const void* dn, const void* x, const void* w, const float* rstd,
+                      const void* dresidual, int64_t N, int64_t H, int dtype, void* dx, void* dw,
+                      void* workspace, size_t workspace_bytes, void* stream,
+                      void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = norm_shape(N, H, 1);
+  if (status != TOPMOE_OK) return status;
+  if (!w || !dw || !workspace || (N > 0 && (!dn || !x || !rstd || !dx))) return TOPMOE_ERR_NULL_ARG;
+  NormBwd a{};
+  a.gate_span = span_of(N, 1);
+  a.units = plan_norm_units(N, 1, a.gate_span);
+  if (workspace_bytes < norm_bwd_bytes(a.units, H)) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(dn, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(rstd, 4) ||
+      !aligned(dresidual, 16) || !aligned(dx, 16) || !aligned(dw, 16) || !aligned(workspace, 256))
+    return TOPMOE_ERR_BAD_ARG;
+  a.dout = dresidual; a.dn = dn; a.out = x; a.next_w = w; a.next_rstd = rstd;
+  a.dy = dx; a.dnext_w = dw; a.part_next = static_cast<float*>(workspace);
+  a.N = N; a.gate_rows = 1; a.H = int(H); a.hv = int(H / 8);
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch rows = st.at(0), sums = st.at(1);
+  TOPMOE_TRY(launch_norm_bwd(a, false, true, dtype, rows, sums));
+  TOPMOE_TRY(st.close(rows));
+  TOPMOE_TRY(st.close(sums));
+  return TOPMOE_OK;
+}
+
+int block_postnorm_fwd(const void* y, const void* residual, const void* w, const void* gate,
+                       const void* next_w, int64_t N, int64_t H, int gate_mode,
+                       int64_t gate_rows, float residual_scale, float eps, int dtype, void* out,
+                       float* rstd, void* n, float* next_rstd, void* stream,
+                       void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  if (gate_mode != kGateNone && gate_mode != kGateChannel && gate_mode != kGateToken)
+    return TOPMOE_ERR_BAD_ARG;
+  const int status = norm_shape(N, H, gate_mode == kGateChannel ? gate_rows : 1);
+  if (status != TOPMOE_OK) return status;
+  if (N > 0 && (!y || !residual || !out || (gate_mode != kGateNone && !gate) || (w && !rstd) ||
+                (next_w && (!n || !next_rstd))))
+    return TOPMOE_ERR_NULL_ARG;
+  if (!(eps > 0.f) || isinf(eps) || !isfinite(residual_scale)) return TOPMOE_ERR_BAD_ARG;
+  if (!aligned(y, 16) || !aligned(residual, 16) || !aligned(w, 16) ||
+      !aligned(gate, gate_mode == kGateChannel ? 16 : 4) || !aligned(next_w, 16) ||
+      !aligned(out, 16) || !aligned(rstd, 4) || !aligned(n, 16) || !aligned(next_rstd, 4))
+    return TOPMOE_ERR_BAD_ARG;
+  NormFwd a{};
+  a.y = y; a.residual = residual; a.w = w; a.gate = gate; a.next_w = next_w;
+  a.out = out; a.n = n; a.rstd = rstd; a.next_rstd = next_rstd;
+  a.N = N; a.H = int(H); a.hv = int(H / 8); a.gate_mode = gate_mode;
+  a.gate_span = span_of(N, gate_mode == kGateChannel ? gate_rows : 1);
+  a.scale = residual_scale; a.eps = eps;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_norm_fwd(a, true, next_w != nullptr, dtype, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+int block_postnorm_bwd(const void* dout, const void* dn, const void* y, const void* out,
+                       const void* w, const void* gate, const void* next_w, const float* rstd,
+                       const float* next_rstd, int64_t N, int64_t H, int gate_mode,
+                       int64_t gate_rows, float residual_scale, int dtype, void* dy,
+                       void* dresidual, void* dw, void* dgate, void* dnext_w, void* workspace,
+                       size_t workspace_bytes, void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  if (gate_mode != kGateNone && gate_mode != kGateChannel && gate_mode != kGateToken)
+    return TOPMOE_ERR_BAD_ARG;
+  const bool channel = gate_mode == kGateChannel;
+  const int status = norm_shape(N, H, channel ? gate_rows : 1);
+  if (status != TOPMOE_OK) return status;
+  if (!workspace || (w && !dw) || (next_w && !dnext_w) ||
+      (channel && gate_rows > 0 && (!gate || !dgate)))
+    return TOPMOE_ERR_NULL_ARG;
+  if (N > 0 && (!y || !dy || !dresidual || (!dout && !next_w) || (w && !rstd) ||
+                (next_w && (!dn || !out || !next_rstd)) ||
+                (gate_mode == kGateToken && (!gate || !dgate))))
+    return TOPMOE_ERR_NULL_ARG;
+  if (!isfinite(residual_scale)) return TOPMOE_ERR_BAD_ARG;
+  NormBwd a{};
+  a.gate_rows = channel ? gate_rows : 1;
+  a.gate_span = span_of(N, a.gate_rows);
+  a.units = plan_norm_units(N, a.gate_rows, a.gate_span);
+  if (workspace_bytes < norm_bwd_bytes(a.units, H)) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(dout, 16) || !aligned(dn, 16) || !aligned(y, 16) || !aligned(out, 16) ||
+      !aligned(w, 16) || !aligned(gate, channel ? 16 : 4) || !aligned(next_w, 16) ||
+      !aligned(rstd, 4) || !aligned(next_rstd, 4) || !aligned(dy, 16) || !aligned(dresidual, 16) ||
+      !aligned(dw, 16) || !aligned(dgate, channel ? 16 : 4) || !aligned(dnext_w, 16) ||
+      !aligned(workspace, 256))
+    return TOPMOE_ERR_BAD_ARG;
+  a.dout = dout; a.dn = dn; a.y = y; a.out = out; a.w = w; a.gate = gate; a.next_w = next_w;
+  a.rstd = w ? rstd : nullptr; a.next_rstd = next_rstd;
+  a.dy = dy; a.dresidual = dresidual; a.dw = w ? dw : nullptr; a.dgate = dgate; a.dnext_w = dnext_w;
+  float* part = static_cast<float*>(workspace);
+  a.part = w || channel ? part : nullptr;
+  a.part_next = part + size_t(a.units.count) * size_t(H);
+  a.N = N; a.H = int(H); a.hv = int(H / 8); a.gate_mode = gate_mode; a.scale = residual_scale;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch rows = st.at(0), sums = st.at(1);
+  TOPMOE_TRY(launch_norm_bwd(a, true, next_w != nullptr, dtype, rows, sums));
+  TOPMOE_TRY(st.close(rows));
+  TOPMOE_TRY(st.close(sums));
+  return TOPMOE_OK;
+}
+
+int act8_pack(const void* x, int64_t ldx, int64_t R, int64_t C, int dtype, uint8_t* q,
+              uint8_t* scale, void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = act8_shape(R, C);
+  if (status != TOPMOE_OK) return status;
+  if (!pitch_ok(ldx, C)) return TOPMOE_ERR_BAD_SHAPE;
+  if (R > 0 && (!x || !q || !scale)) return TOPMOE_ERR_NULL_ARG;
+  if (!aligned(x, 16) || !aligned(q, 8)) return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_act8_pack(x, ldx, R, C, dtype, q, scale, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+int act8_unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C, int dtype, void* x,
+                int64_t ldx, void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = act8_shape(R, C);
+  if (status != TOPMOE_OK) return status;
+  if (!pitch_ok(ldx, C)) return TOPMOE_ERR_BAD_SHAPE;
+  if (R > 0 && (!x || !q || !scale)) return TOPMOE_ERR_NULL_ARG;
+  if (!aligned(x, 16) || !aligned(q, 8)) return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_act8_unpack(q, scale, R, C, dtype, x, ldx, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+int swiglu_act8_fwd(const void* g, int64_t ldg, const void* u, int64_t ldu, int64_t R, int64_t C,
+                    int dtype, void* h, uint8_t* gq, uint8_t* gscale, uint8_t* uq,
+                    uint8_t* uscale, void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = act8_shape(R, C);
+  if (status != TOPMOE_OK) return status;
+  if (!pitch_ok(ldg, C) || !pitch_ok(ldu, C)) return TOPMOE_ERR_BAD_SHAPE;
+  if (R > 0 && (!g || !u || !h || !gq || !gscale || !uq || !uscale)) return TOPMOE_ERR_NULL_ARG;
+  if (!aligned(g, 16) || !aligned(u, 16) || !aligned(h, 16) || !aligned(gq, 8) || !aligned(uq, 8))
+    return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_swiglu_act8_fwd(g, ldg, u, ldu, R, C, dtype, h, gq, gscale, uq, uscale, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+int swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gscale, const uint8_t* uq,
+                    const uint8_t* uscale, const void* dh, int64_t R, int64_t C, int dtype,
+                    void* dg, int64_t lddg, void* du, int64_t lddu, void* h, void* stream,
+                    void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  const int status = act8_shape(R, C);
+  if (status != TOPMOE_OK) return status;
+  if (!pitch_ok(lddg, C) || !pitch_ok(lddu, C)) return TOPMOE_ERR_BAD_SHAPE;
+  if (R > 0 && (!gq || !gscale || !uq || !uscale || !dh || !dg || !du)) return TOPMOE_ERR_NULL_ARG;
+  if (!aligned(gq, 8) || !aligned(uq, 8) || !aligned(dh, 16) || !aligned(dg, 16) ||
+      !aligned(du, 16) || !aligned(h, 16))
+    return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  TOPMOE_TRY(launch_swiglu_act8_bwd(gq, gscale, uq, uscale, dh, R, C, dtype, dg, lddg, du, lddu,
+                                    h, L));
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+}  // extern "C"

@@ -209,4 +209,97 @@ int dwr_chunks(int64_t N);
 hipError_t launch_dwr(const void* x, const float* dr, int64_t N, int H, int E, int dtype,
                       float* part, float* dWr, const Launch& s);
 
+// ---- rows by expert and back (rows.hip)
+constexpr int kDispatchMaxExperts = 256;
+// Most entries (N * k) of the one-launch dispatch.
+constexpr int kDispatchSmall = 1024;
+// Chunks of entries counted by one block each (none for small calls) and the
+// bytes of their counts [nchunk, E + 1].
+struct DispatchPlan {
+  int chunk = 0, nchunk = 0;
+  size_t bytes = 0;
+};
+DispatchPlan plan_dispatch(int64_t n, int E);
+// cap: entries an expert keeps (INT32_MAX: all).  `rows` is the stage that
+// finds the rows (empty for small calls), `copy` the one that moves them.
+hipError_t launch_dispatch_rows(const void* x, const int32_t* idx, int64_t N, int H, int E, int k,
+                                int cap, int dtype, void* xs, int32_t* offsets,
+                                int32_t* row_entry, int32_t* entry_row, int32_t* part,
+                                const Launch& rows, const Launch& copy);
+// alpha NULL: weights 1.
+hipError_t launch_gather_sum(const void* rows, const int32_t* entry_row, const float* alpha,
+                             const void* residual, int64_t N, int H, int k, int dtype, void* out,
+                             const Launch& s);
+hipError_t launch_moe_combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
+                                  const float* alpha, int64_t N, int H, int k, int dtype,
+                                  void* dys, float* dalpha, const Launch& s);
+
+// ---- norms around a block (norm.hip)
+constexpr int kNormMaxH = 16384;
+enum GateMode { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };
+struct NormFwd {
+  const void* y;         // [N, H] block output (pre-norm alone: x)
+  const void* residual;  // [N, H]
+  const void* w;         // [H] post norm's weight, or NULL: no post norm
+  const void* gate;      // channel: [gate_rows, H]; token: [N]
+  const void* next_w;    // [H]
+  void* out;             // [N, H]
+  void* n;               // [N, H]
+  float* rstd;           // [N]
+  float* next_rstd;      // [N]
+  int64_t N, t0;         // t0: first row of this launch
+  int64_t gate_span;     // tokens that share a gate row
+  int H, hv, gate_mode;  // hv = H / 8
+  float scale, eps;
+};
+hipError_t launch_norm_fwd(const NormFwd& a, bool post, bool next, int dtype, const Launch& s);
+
+// Units of consecutive rows for the backward's column sums: pieces of one gate
+// group (per_group of them in each), or whole groups (per_group == 0).
+constexpr int kNormUnits = 1024;
+struct NormUnits {
+  int64_t rows = 0;   // rows of a unit (the last of a group may have fewer)
+  int64_t per_group = 0, count = 0;
+};
+NormUnits plan_norm_units(int64_t N, int64_t gate_rows, int64_t gate_span);
+struct NormBwd {
+  const void* dout;         // [N, H] or NULL: 0
+  const void* dn;           // [N, H]
+  const void* y;            // [N, H]
+  const void* out;          // [N, H] (pre-norm alone: x)
+  const void* w;
+  const void* gate;
+  const void* next_w;
+  const float* rstd;        // [N] or NULL: no post norm
+  const float* next_rstd;   // [N]
+  void* dy;                 // [N, H] (pre-norm alone: dx)
+  void* dresidual;          // [N, H]
+  void* dw;                 // [H] or NULL
+  void* dgate;              // channel: [gate_rows, H]; token: [N]
+  void* dnext_w;            // [H]
+  float* part;              // [units, H], or NULL where neither dw nor dgate needs it
+  float* part_next;         // [units, H]
+  int64_t N, gate_rows, gate_span;
+  NormUnits units;
+  int H, hv, gate_mode, first_role;
+  float scale;
+};
+hipError_t launch_norm_bwd(const NormBwd& a, bool post, bool next, int dtype, const Launch& rows,
+                           const Launch& sums);
+
+// ---- activations in 8 bits (act8.hip)
+constexpr int kAct8Group = 32;  // channels that share a scale
+// Row pitches in elements; q [R, C] and scale [R, ceil(C / 32)] are dense.
+hipError_t launch_act8_pack(const void* x, int64_t ldx, int64_t R, int64_t C, int dtype,
+                            uint8_t* q, uint8_t* scale, const Launch& s);
+hipError_t launch_act8_unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C,
+                              int dtype, void* x, int64_t ldx, const Launch& s);
+hipError_t launch_swiglu_act8_fwd(const void* g, int64_t ldg, const void* u, int64_t ldu,
+                                  int64_t R, int64_t C, int dtype, void* h, uint8_t* gq, uint8_t* gs, uint8_t* uq,
+                                  uint8_t* us, const Launch& s);
+hipError_t launch_swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gs, const uint8_t* uq,
+                                  const uint8_t* us, const void* dh, int64_t R, int64_t C,
+                                  int dtype, void* dg, int64_t ldg, void* du, int64_t ldu, void* h,
+                                  const Launch& s);
+
 }  // namespace topmoe

@@ -1,0 +1,484 @@
+// The RMS norms before and after a block, fused with the block's gate, its
+// residual stream and the residual's scale; forward and backward.
+//
+// Per token (row of H channels), all in fp32:
+//   after   yh = y * rstd_y,  rstd_y = 1 / sqrt(mean(y^2) + eps)   (no norm: yh = y, w = 1)
+//           r  = s * residual + gate * w * yh,   out = round(r)
+//   before  n  = round(r * rstd_r * w_next),  rstd_r = 1 / sqrt(mean(r^2) + eps)
+// A pre-norm alone is the second line with r = x.  Gradients, with
+// rh = out * rstd_r and a = dn * w_next:
+//   dr   = dout + rstd_r * (a - rh * mean(a * rh)),      dw_next = sum_t dn * rh
+//   dres = s * dr,   b = dr * gate * w
+//   dy   = rstd_y * (b - yh * mean(b * yh))  (no norm: b)
+//   dw   = sum_t gate * dr * yh,   dgate = the sum of w * dr * yh over what shares the gate
+//
+// One block of W wavefronts per row (W = 1: one wavefront per row, four rows a
+// block): the row stays in registers between its statistics and its use, so
+// every tensor is read once and written once.  Bound by memory.
+//
+// Column sums of the backward pass (dw, dgate, dw_next) are taken in two fixed
+// steps without atomics: each unit of consecutive rows sums its own rows in
+// registers and writes one fp32 row of partial sums; a second launch adds the
+// units' rows in order.  A channel gate may have G rows, each shared by
+// N / G consecutive tokens: units either lie within one such group (their
+// partial sums are of dr * yh, weighted by the gate and by w afterwards), or
+// hold whole groups, whose dgate they then write themselves (the partial sums
+// are of gate * dr * yh).
+#include "kernels.h"
+#include "vec8.h"
+
+#include "../../include/topmoe.h"
+
+namespace topmoe {
+
+namespace {
+
+// Sum over the W wavefronts of a row, in wavefront order.  `slot` (2 x W
+// floats of LDS) alternates between calls: a wavefront writing a slot again
+// has passed the barrier of the call in between, which every reader of the
+// slot's last use reached after reading it.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float (&slot)[2][W], int& turn, int wave) {
+  v = wave_sum(v);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) slot[turn][wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += slot[turn][i];
+    turn ^= 1;
+  }
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_f(const T* p, float (&v)[8]) {
+  unpack8(load_raw8<T>(p), v);
+}
+
+// POST: the norm after the block with gate and residual (else r = y = x).
+// NEXT: the norm before the next block.
+template <typename T, int W, int V, bool POST, bool NEXT>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_fwd_kernel(NormFwd a) {
+  __shared__ float slot[2][W];
+  const int lane = W == 1 ? int(threadIdx.x & 63) : int(threadIdx.x);
+  const int wave = int(threadIdx.x >> 6);
+  const int64_t t = a.t0 + (W == 1 ? int64_t(blockIdx.x) * 4 + wave : int64_t(blockIdx.x));
+  if (W == 1 && t >= a.N) return;
+  int turn = 0;
+  const T* y = static_cast<const T*>(a.y) + t * a.H;
+  Raw8<T> yr[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = lane + v * 64 * W;
+    yr[v] = p < a.hv ? load_raw8<T>(y + p * 8) : zero_raw8<T>();
+  }
+  const float inv_h = 1.0f / float(a.H);
+  float rs[V][8];  // r
+  if constexpr (POST) {
+    Raw8<T> res[V];
+    const T* rp = static_cast<const T*>(a.residual) + t * a.H;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = lane + v * 64 * W;
+      res[v] = p < a.hv ? load_raw8<T>(rp + p * 8) : zero_raw8<T>();
+    }
+    float rstd = 1.f;
+    if (a.w != nullptr) {
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float f[8];
+        unpack8(yr[v], f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s = fmaf(f[c], f[c], s);
+      }
+      rstd = 1.0f / sqrtf(row_sum<W>(s, slot, turn, wave) * inv_h + a.eps);
+      if (lane == 0) a.rstd[t] = rstd;
+    }
+    float gt = 1.f;
+    const T* gp = nullptr;
+    if (a.gate_mode == kGateToken) gt = to_f32<T>(static_cast<const T*>(a.gate)[t]);
+    if (a.gate_mode == kGateChannel) gp = static_cast<const T*>(a.gate) + (t / a.gate_span) * a.H;
+    T* out = static_cast<T*>(a.out) + t * a.H;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = lane + v * 64 * W;
+      float f[8], q[8];
+      unpack8(yr[v], f);
+      unpack8(res[v], q);
+      if (p < a.hv) {
+        float m[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m[c] = rstd * gt;
+        if (a.w != nullptr) {
+          float w[8];
+          load_f<T>(static_cast<const T*>(a.w) + p * 8, w);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) m[c] *= w[c];
+        }
+        if (gp != nullptr) {
+          float g[8];
+          load_f<T>(gp + p * 8, g);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) m[c] *= g[c];
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) rs[v][c] = fmaf(f[c], m[c], a.scale * q[c]);
+        store8<T>(out + p * 8, rs[v]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) rs[v][c] = 0.f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) unpack8(yr[v], rs[v]);
+  }
+  if constexpr (NEXT) {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s = fmaf(rs[v][c], rs[v][c], s);
+    const float rstd = 1.0f / sqrtf(row_sum<W>(s, slot, turn, wave) * inv_h + a.eps);
+    if (lane == 0) a.next_rstd[t] = rstd;
+    T* n = static_cast<T*>(a.n) + t * a.H;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = lane + v * 64 * W;
+      if (p >= a.hv) continue;
+      float w[8];
+      load_f<T>(static_cast<const T*>(a.next_w) + p * 8, w);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[c] = rs[v][c] * rstd * w[c];
+      store8<T>(n + p * 8, w);
+    }
+  }
+}
+
+// One unit of rows per block (see NormUnits): row gradients, and the unit's
+// column sums in registers.
+template <typename T, int W, int V, bool POST, bool NEXT>
+__global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
+  __shared__ float slot[2][W];
+  const int lane = int(threadIdx.x), wave = int(threadIdx.x >> 6);
+  int turn = 0;
+  const float inv_h = 1.0f / float(a.H);
+  const int64_t unit = blockIdx.x;
+  int64_t r0, r1;
+  if (a.units.per_group > 0) {  // a piece of one gate group
+    const int64_t g = unit / a.units.per_group, c = unit - g * a.units.per_group;
+    r0 = g * a.gate_span + c * a.units.rows;
+    r1 = r0 + a.units.rows;
+    const int64_t end = (g + 1) * a.gate_span;
+    r1 = r1 < end ? r1 : end;
+  } else {  // whole gate groups
+    r0 = unit * a.units.rows;
+    r1 = r0 + a.units.rows;
+    r1 = r1 < a.N ? r1 : a.N;
+  }
+  float sw[V][8], sg[V][8], sn[V][8];  // sums for dw, dgate (of the current group), dw_next
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sw[v][c] = sg[v][c] = sn[v][c] = 0.f;
+
+  for (int64_t t = r0; t < r1; ++t) {
+    float dr[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = lane + v * 64 * W;
+      if (a.dout != nullptr && p < a.hv) {
+        load_f<T>(static_cast<const T*>(a.dout) + t * a.H + p * 8, dr[v]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dr[v][c] = 0.f;
+      }
+    }
+    Raw8<T> yr[V];
+    if constexpr (POST) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int p = lane + v * 64 * W;
+        yr[v] = p < a.hv ? load_raw8<T>(static_cast<const T*>(a.y) + t * a.H + p * 8)
+                         : zero_raw8<T>();
+      }
+    }
+    if constexpr (NEXT) {
+      const float rstd = a.next_rstd[t];
+      float rh[V][8], av[V][8];
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int p = lane + v * 64 * W;
+        if (p < a.hv) {
+          float w[8];
+          load_f<T>(static_cast<const T*>(a.out) + t * a.H + p * 8, rh[v]);
+          load_f<T>(static_cast<const T*>(a.dn) + t * a.H + p * 8, av[v]);
+          load_f<T>(static_cast<const T*>(a.next_w) + p * 8, w);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            rh[v][c] *= rstd;
+            sn[v][c] = fmaf(av[v][c], rh[v][c], sn[v][c]);
+            av[v][c] *= w[c];
+            s = fmaf(av[v][c], rh[v][c], s);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) rh[v][c] = av[v][c] = 0.f;
+        }
+      }
+      const float m = row_sum<W>(s, slot, turn, wave) * inv_h;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dr[v][c] += rstd * (av[v][c] - rh[v][c] * m);
+    }
+    if constexpr (!POST) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int p = lane + v * 64 * W;
+        if (p < a.hv) store8<T>(static_cast<T*>(a.dy) + t * a.H + p * 8, dr[v]);
+      }
+    } else {
+      const float rstd = a.rstd != nullptr ? a.rstd[t] : 1.f;
+      const float gt = a.gate_mode == kGateToken ? to_f32<T>(static_cast<const T*>(a.gate)[t]) : 1.f;
+      const T* gp = a.gate_mode == kGateChannel
+                        ? static_cast<const T*>(a.gate) + (t / a.gate_span) * a.H : nullptr;
+      float b[V][8];  // dr * channel gate * w
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int p = lane + v * 64 * W;
+        float yh[8];
+        unpack8(yr[v], yh);
+        if (p < a.hv) {
+          float q[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            q[c] = a.scale * dr[v][c];
+            yh[c] *= rstd;
+            sg[v][c] = fmaf(dr[v][c] * gt, yh[c], sg[v][c]);
+            b[v][c] = dr[v][c];
+          }
+          store8<T>(static_cast<T*>(a.dresidual) + t * a.H + p * 8, q);
+          if (a.w != nullptr) {
+            float w[8];
+            load_f<T>(static_cast<const T*>(a.w) + p * 8, w);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) b[v][c] *= w[c];
+          }
+          if (gp != nullptr) {
+            float g[8];
+            load_f<T>(gp + p * 8, g);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) b[v][c] *= g[c];
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) s = fmaf(b[v][c], yh[c], s);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) b[v][c] = 0.f;
+        }
+      }
+      float m = 0.f;
+      if (a.w != nullptr || a.gate_mode == kGateToken) {
+        s = row_sum<W>(s, slot, turn, wave);
+        if (a.gate_mode == kGateToken && lane == 0)
+          static_cast<T*>(a.dgate)[t] = from_f32<T>(s);
+        m = a.w != nullptr ? s * inv_h : 0.f;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int p = lane + v * 64 * W;
+        if (p >= a.hv) continue;
+        float yh[8];
+        unpack8(yr[v], yh);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) yh[c] = gt * rstd * (b[v][c] - yh[c] * rstd * m);
+        store8<T>(static_cast<T*>(a.dy) + t * a.H + p * 8, yh);
+      }
+      if (a.units.per_group == 0 && (t + 1) % a.gate_span == 0) {  // a gate group ends
+        const int64_t g = t / a.gate_span;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int p = lane + v * 64 * W;
+          if (p >= a.hv) continue;
+          float w[8], q[8];
+          load_f<T>(static_cast<const T*>(a.gate) + g * a.H + p * 8, q);
+          if (a.w != nullptr) load_f<T>(static_cast<const T*>(a.w) + p * 8, w);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            sw[v][c] = fmaf(q[c], sg[v][c], sw[v][c]);
+            q[c] = a.w != nullptr ? w[c] * sg[v][c] : sg[v][c];
+            sg[v][c] = 0.f;
+          }
+          store8<T>(static_cast<T*>(a.dgate) + g * a.H + p * 8, q);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = lane + v * 64 * W;
+    if (p >= a.hv) continue;
+    if constexpr (POST) {
+      if (a.part != nullptr)
+        store8<float>(a.part + unit * a.H + p * 8, a.units.per_group > 0 ? sg[v] : sw[v]);
+    }
+    if constexpr (NEXT) store8<float>(a.part_next + unit * a.H + p * 8, sn[v]);
+  }
+}
+
+// Column sums of the units' partial rows: blockIdx.y = 0 dw, 1 dw_next,
+// 2 + g gate row g.  64 channels a block; wavefront s adds units s, s + 16,
+// ... and the 16 sums are added in order.
+template <typename T>
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
+  __shared__ float sm[16][64];
+  const int lane = threadIdx.x & 63, s = threadIdx.x >> 6;
+  const int h = blockIdx.x * 64 + lane;
+  const bool in = h < a.H;
+  const int role = a.first_role + int(blockIdx.y);
+  const float* part = role == 1 ? a.part_next : a.part;
+  int64_t u0 = 0, u1 = a.units.count;
+  if (role >= 2) {
+    u0 = int64_t(role - 2) * a.units.per_group;
+    u1 = u0 + a.units.per_group < u1 ? u0 + a.units.per_group : u1;  // no units: sums of nothing
+  }
+  const bool gated = role == 0 && a.units.per_group > 0 && a.gate_mode == kGateChannel;
+  float acc = 0.f;
+  if (in) {
+    for (int64_t u = u0 + s; u < u1; u += 16) {
+      float v = part[u * a.H + h];
+      if (gated) v *= to_f32<T>(static_cast<const T*>(a.gate)[(u / a.units.per_group) * a.H + h]);
+      acc += v;
+    }
+  }
+  sm[s][lane] = acc;
+  __syncthreads();
+  if (s != 0 || !in) return;
+  acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc += sm[i][lane];
+  if (role == 0) static_cast<T*>(a.dw)[h] = from_f32<T>(acc);
+  if (role == 1) static_cast<T*>(a.dnext_w)[h] = from_f32<T>(acc);
+  if (role >= 2) {
+    if (a.w != nullptr) acc *= to_f32<T>(static_cast<const T*>(a.w)[h]);
+    static_cast<T*>(a.dgate)[int64_t(role - 2) * a.H + h] = from_f32<T>(acc);
+  }
+}
+
+template <typename T, int W, int V>
+hipError_t fwd_flags(const NormFwd& a, bool post, bool next, int64_t blocks, const Launch& L) {
+  const dim3 grid(static_cast<unsigned>(blocks)), block(W == 1 ? 256 : 64 * W);
+  if (post && next) return launch_kernel(norm_fwd_kernel<T, W, V, true, true>, grid, block, 0, L, a);
+  if (post) return launch_kernel(norm_fwd_kernel<T, W, V, true, false>, grid, block, 0, L, a);
+  return launch_kernel(norm_fwd_kernel<T, W, V, false, true>, grid, block, 0, L, a);
+}
+
+template <typename T>
+hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
+  // rows of one launch: at most 2^22, so that a grid keeps below 2^32 threads
+  const int64_t slab = int64_t(1) << 22, N = a.N;
+  for (int64_t t0 = 0; t0 < N; t0 += slab) {
+    Launch L = s;
+    if (t0 > 0) L.start = nullptr;
+    if (t0 + slab < N) L.stop = nullptr;
+    a.t0 = t0;
+    const int64_t rows = t0 + slab < N ? slab : N - t0;
+    hipError_t e;
+    if (a.hv <= 64) e = fwd_flags<T, 1, 1>(a, post, next, (rows + 3) / 4, L);
+    else if (a.hv <= 256) e = fwd_flags<T, 4, 1>(a, post, next, rows, L);
+    else if (a.hv <= 512) e = fwd_flags<T, 4, 2>(a, post, next, rows, L);
+    else if (a.hv <= 1024) e = fwd_flags<T, 4, 4>(a, post, next, rows, L);
+    else e = fwd_flags<T, 8, 4>(a, post, next, rows, L);
+    if (e != hipSuccess) return e;
+    s.launched = true;
+  }
+  return hipSuccess;
+}
+
+template <typename T, int W, int V>
+hipError_t bwd_flags(const NormBwd& a, bool post, bool next, const Launch& L) {
+  const dim3 grid(static_cast<unsigned>(a.units.count)), block(64 * W);
+  if (post && next) return launch_kernel(norm_bwd_kernel<T, W, V, true, true>, grid, block, 0, L, a);
+  if (post) return launch_kernel(norm_bwd_kernel<T, W, V, true, false>, grid, block, 0, L, a);
+  return launch_kernel(norm_bwd_kernel<T, W, V, false, true>, grid, block, 0, L, a);
+}
+
+template <typename T>
+hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
+                     const Launch& sums) {
+  if (a.units.count > 0) {
+    hipError_t e;
+    if (a.hv <= 64) e = bwd_flags<T, 1, 1>(a, post, next, rows);
+    else if (a.hv <= 256) e = bwd_flags<T, 4, 1>(a, post, next, rows);
+    else if (a.hv <= 512) e = bwd_flags<T, 4, 2>(a, post, next, rows);
+    else if (a.hv <= 1024) e = bwd_flags<T, 8, 2>(a, post, next, rows);
+    else e = bwd_flags<T, 16, 2>(a, post, next, rows);
+    if (e != hipSuccess) return e;
+  }
+  // roles: 0 dw, 1 dw_next, 2.. the gate's rows (where the units did not write
+  // them); neighbouring roles share a launch (a grid has at most 65535 rows)
+  const bool dw = post && a.dw != nullptr;
+  const int64_t gates =
+      post && a.gate_mode == kGateChannel && a.units.per_group > 0 ? a.gate_rows : 0;
+  const int64_t first = dw ? 0 : next ? 1 : 2, end = gates > 0 ? 2 + gates : next ? 2 : dw ? 1 : 0;
+  Launch L = sums;
+  for (int64_t r = first; r < end;) {
+    if (r == 1 && !next) {
+      r = 2;
+      continue;
+    }
+    int64_t stop = r == 0 && !next ? 1 : end;
+    if (stop - r > 65535) stop = r + 65535;
+    L.stop = stop == end ? sums.stop : nullptr;
+    NormBwd b = a;
+    b.first_role = int(r);
+    const hipError_t e =
+        launch_kernel(norm_reduce_kernel<T>, dim3(unsigned((a.H + 63) / 64), unsigned(stop - r)),
+                      dim3(1024), 0, L, b);
+    if (e != hipSuccess) return e;
+    sums.launched = true;
+    L.start = nullptr;
+    r = stop;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+NormUnits plan_norm_units(int64_t N, int64_t gate_rows, int64_t gate_span) {
+  NormUnits u;
+  if (N <= 0) {  // no units: the sums are of nothing
+    u.per_group = 1;
+    return u;
+  }
+  // about kNormUnits units, of at least one row
+  int64_t rows = (N + kNormUnits - 1) / kNormUnits;
+  if (gate_span >= rows) {
+    u.per_group = (gate_span + rows - 1) / rows;
+    u.rows = rows;
+    u.count = gate_rows * u.per_group;
+  } else {
+    u.per_group = 0;
+    u.rows = rows / gate_span * gate_span;
+    u.count = (N + u.rows - 1) / u.rows;
+  }
+  return u;
+}
+
+hipError_t launch_norm_fwd(const NormFwd& a, bool post, bool next, int dtype, const Launch& s) {
+  return dtype == TOPMOE_DTYPE_FP32 ? fwd_typed<float>(a, post, next, s)
+                                    : fwd_typed<bf16_t>(a, post, next, s);
+}
+
+hipError_t launch_norm_bwd(const NormBwd& a, bool post, bool next, int dtype, const Launch& rows,
+                           const Launch& sums) {
+  return dtype == TOPMOE_DTYPE_FP32 ? bwd_typed<float>(a, post, next, rows, sums)
+                                    : bwd_typed<bf16_t>(a, post, next, rows, sums);
+}
+
+}  // namespace topmoe

@@ -1,0 +1,431 @@
+// Tokens sorted by expert and back, with their weights, and the gradients:
+// the dispatch and combine of a top-k MoE whose experts are the caller's own.
+//
+// Entry i = t * k + j is token t's slot j with expert idx[i].  Its rank within
+// the expert counts the earlier entries of the same expert, so the sort is
+// stable; an expert keeps its first `cap` entries (all without a capacity).
+// The kept entries' rows come first, grouped by ascending expert; entries not
+// kept -- over the capacity, or with idx outside [0, E), as a padding token's
+// -- get the rows behind them, by (expert, rank), those without an expert last
+// ("bucket" E).  entry -> row is thus a bijection on [0, N k): row, or
+// -1 - row for an entry that is not kept, whose row holds zeros.
+//
+//   dispatch      xs[row(i)] = x[t]            dx[t] = sum_j dxs[row(t, j)]
+//   combine       y[t] = residual[t] + sum_j alpha[t, j] ys[row(t, j)]
+//   its gradient  dys[row(i)] = alpha[i] dy[t],  dalpha[i] = dy[t] . ys[row(i)]
+//
+// Sums run over the slots in order, in fp32, and are rounded once.  Everything
+// here only moves rows: bound by memory, and at decode sizes by the launches.
+#include "kernels.h"
+#include "vec8.h"
+
+#include "../../include/topmoe.h"
+
+namespace topmoe {
+
+namespace {
+
+__device__ __forceinline__ int bucket_of(int e, int E) { return e >= 0 && e < E ? e : E; }
+
+// Offsets of the kept rows and of the rows behind them, from the buckets'
+// totals in LDS: off[b] = sum of min(tot, cap) before b, tail[b] = all kept
+// rows + sum of the entries not kept before b.  One wavefront.
+__device__ __forceinline__ void scan_buckets(const int* tot, int E, int cap, int* off, int* tail,
+                                             int lane) {
+  int kept0 = 0, left0 = 0;
+  for (int b0 = 0; b0 <= E; b0 += 64) {
+    const int b = b0 + lane;
+    const int c = b <= E ? tot[b] : 0;
+    const int keep = b >= E ? 0 : (cap < c ? cap : c);
+    const int ks = wave_inclusive_scan(keep, lane), ls = wave_inclusive_scan(c - keep, lane);
+    if (b <= E) {
+      off[b] = kept0 + ks - keep;
+      tail[b] = left0 + ls - (c - keep);
+    }
+    kept0 += __shfl(ks, 63, 64);
+    left0 += __shfl(ls, 63, 64);
+  }
+  for (int b = lane; b <= E; b += 64) tail[b] += kept0;
+}
+
+// Row of an entry of bucket b with rank r: the row, or -1 - row if not kept.
+__device__ __forceinline__ int row_of(int b, int r, int E, int cap, const int* tot,
+                                      const int* off, const int* tail) {
+  const int lim = b >= E ? 0 : (cap < tot[b] ? cap : tot[b]);
+  return r < lim ? off[b] + r : -1 - (tail[b] + r - lim);
+}
+
+// ---- large calls: counts per chunk of entries, rows, then the copy ---------
+__global__ __launch_bounds__(256) void dispatch_count_kernel(const int32_t* __restrict__ idx,
+                                                             int64_t n, int chunk, int E,
+                                                             int32_t* __restrict__ part) {
+  __shared__ int hist[kDispatchMaxExperts + 1];
+  for (int b = threadIdx.x; b <= E; b += 256) hist[b] = 0;
+  __syncthreads();
+  const int64_t i0 = int64_t(blockIdx.x) * chunk;
+  const int64_t i1 = i0 + chunk < n ? i0 + chunk : n;
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) atomicAdd(&hist[bucket_of(idx[i], E)], 1);
+  __syncthreads();
+  for (int b = threadIdx.x; b <= E; b += 256) part[int64_t(blockIdx.x) * (E + 1) + b] = hist[b];
+}
+
+// One block per chunk: every bucket's total and the count in earlier chunks
+// from the counts of all chunks, then the rank of each of its entries.  The
+// four wavefronts take a quarter of the chunk each, 64 entries at a time;
+// lanes of the same bucket find each other with one ballot per bit of it.
+__global__ __launch_bounds__(256) void dispatch_place_kernel(
+    const int32_t* __restrict__ idx, int64_t n, int chunk, int nchunk, int E, int bits, int cap,
+    const int32_t* __restrict__ part, int32_t* __restrict__ offsets,
+    int32_t* __restrict__ row_entry, int32_t* __restrict__ entry_row) {
+  __shared__ int tot[kDispatchMaxExperts + 1], off[kDispatchMaxExperts + 1];
+  __shared__ int tail[kDispatchMaxExperts + 1];
+  __shared__ int run[4][kDispatchMaxExperts + 1];  // next rank of each wavefront's entries
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int B = E + 1;
+  for (int b = tid; b < B; b += 256) {
+    tot[b] = 0;
+    for (int w = 0; w < 4; ++w) run[w][b] = 0;
+  }
+  __syncthreads();
+  const int64_t quarter = chunk / 4;  // chunk is a multiple of 256
+  const int64_t w0 = int64_t(blockIdx.x) * chunk + wave * quarter;
+  const int64_t w1 = w0 + quarter < n ? w0 + quarter : n;
+  for (int64_t i = w0 + lane; i < w1; i += 64) atomicAdd(&run[wave][bucket_of(idx[i], E)], 1);
+  __syncthreads();
+  int shift = 0;
+  while ((1 << shift) < B && shift < 8) ++shift;  // lanes per chunk of counts
+  const int span = 1 << shift, slices = 256 >> shift;
+  // counts before this chunk go to tail[] first (free until the scan)
+  for (int b = tid; b < B; b += 256) tail[b] = 0;
+  __syncthreads();
+  for (int b = tid & (span - 1); b < B; b += span) {
+    int all = 0, before = 0;
+    for (int c = tid >> shift; c < nchunk; c += slices) {
+      const int v = part[int64_t(c) * B + b];
+      all += v;
+      before += c < int(blockIdx.x) ? v : 0;
+    }
+    atomicAdd(&tot[b], all);
+    atomicAdd(&tail[b], before);
+  }
+  __syncthreads();
+  for (int b = tid; b < B; b += 256) {  // first rank of each wavefront's entries
+    int r = tail[b];
+    for (int w = 0; w < 4; ++w) {
+      const int c = run[w][b];
+      run[w][b] = r;
+      r += c;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    scan_buckets(tot, E, cap, off, tail, lane);
+    if (blockIdx.x == 0)
+      for (int b = lane; b <= E; b += 64) offsets[b] = off[b];
+  }
+  __syncthreads();
+  const uint64_t lt_mask = lane == 0 ? 0ull : (~0ull >> (64 - lane));
+  for (int64_t base = w0; base < w1; base += 64) {
+    const int64_t i = base + lane;
+    const bool valid = i < w1;
+    const int b = valid ? bucket_of(idx[i], E) : 0;
+    uint64_t peers = __ballot(valid);
+    for (int s = 0; s < bits; ++s) {
+      const uint64_t m = __ballot((b >> s) & 1);
+      peers &= ((b >> s) & 1) ? m : ~m;
+    }
+    if (valid) {
+      const int r = row_of(b, run[wave][b] + __popcll(peers & lt_mask), E, cap, tot, off, tail);
+      entry_row[i] = r;
+      row_entry[r < 0 ? -1 - r : r] = r < 0 ? -1 : int32_t(i);
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (valid && (peers & lt_mask) == 0ull) run[wave][b] += __popcll(peers);
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Token-major copy: each thread reads one piece of a token's row once and
+// writes it to the token's k rows (zeros to the rows of entries not kept).
+template <typename T>
+__global__ __launch_bounds__(256) void dispatch_copy_kernel(const T* __restrict__ x,
+                                                            const int32_t* __restrict__ entry_row,
+                                                            int64_t t0, uint32_t pieces, int hv,
+                                                            int H, int k, T* __restrict__ xs) {
+  const uint32_t g = blockIdx.x * 256u + threadIdx.x;
+  if (g >= pieces) return;
+  const uint32_t dt = g / uint32_t(hv);
+  const int64_t t = t0 + dt;
+  const int64_t h = int64_t(g - dt * uint32_t(hv)) * 8;
+  const Raw8<T> v = load_raw8<T>(x + t * H + h);
+  for (int j = 0; j < k; ++j) {
+    const int r = entry_row[t * k + j];
+    if (r >= 0) store_raw8<T>(xs + int64_t(r) * H + h, v);
+    else store_raw8<T>(xs + int64_t(-1 - r) * H + h, zero_raw8<T>());
+  }
+}
+
+// ---- small calls: one launch, one block per token --------------------------
+// Every block counts all n entries itself (n * 4 bytes, from L2) and finds its
+// own entries' ranks by comparing, so no block waits for another.
+template <typename T>
+__global__ __launch_bounds__(256) void dispatch_small_kernel(
+    const T* __restrict__ x, const int32_t* __restrict__ idx, int n, int hv, int H, int E, int k,
+    int cap, T* __restrict__ xs, int32_t* __restrict__ offsets, int32_t* __restrict__ row_entry,
+    int32_t* __restrict__ entry_row) {
+  __shared__ int tot[kDispatchMaxExperts + 1], off[kDispatchMaxExperts + 1];
+  __shared__ int tail[kDispatchMaxExperts + 1];
+  __shared__ int rank[kDispatchMaxExperts];  // k <= E
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int t = blockIdx.x, e0 = t * k;
+  for (int b = tid; b <= E; b += 256) tot[b] = 0;
+  for (int j = tid; j < k; j += 256) rank[j] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += 256) {
+    const int b = bucket_of(idx[i], E);
+    atomicAdd(&tot[b], 1);
+    for (int j = 0; j < k; ++j)
+      if (i < e0 + j && b == bucket_of(idx[e0 + j], E)) atomicAdd(&rank[j], 1);
+  }
+  __syncthreads();
+  if (tid < 64) {
+    scan_buckets(tot, E, cap, off, tail, lane);
+    if (t == 0)
+      for (int b = lane; b <= E; b += 64) offsets[b] = off[b];
+  }
+  __syncthreads();
+  for (int j = tid; j < k; j += 256) {
+    const int r = row_of(bucket_of(idx[e0 + j], E), rank[j], E, cap, tot, off, tail);
+    rank[j] = r;
+    entry_row[e0 + j] = r;
+    row_entry[r < 0 ? -1 - r : r] = r < 0 ? -1 : e0 + j;
+  }
+  __syncthreads();
+  for (int p = tid; p < hv; p += 256) {
+    const int64_t h = int64_t(p) * 8;
+    const Raw8<T> v = load_raw8<T>(x + int64_t(t) * H + h);
+    for (int j = 0; j < k; ++j) {
+      const int r = rank[j];
+      if (r >= 0) store_raw8<T>(xs + int64_t(r) * H + h, v);
+      else store_raw8<T>(xs + int64_t(-1 - r) * H + h, zero_raw8<T>());
+    }
+  }
+}
+
+__global__ void dispatch_empty_kernel(int E, int32_t* offsets) {
+  for (int b = threadIdx.x; b <= E; b += 256) offsets[b] = 0;
+}
+
+// ---- back to tokens ---------------------------------------------------------
+// out[t] = residual[t] (or 0) + sum_j w[t, j] rows[entry_row[t, j]], the
+// combine (w = alpha) and the dispatch's gradient (w = 1).  A row id outside
+// [0, nrows) adds nothing.  Four slots' pieces are in flight at a time.
+template <typename T, bool WEIGHTED>
+__global__ __launch_bounds__(256) void gather_sum_kernel(
+    const T* __restrict__ rows, const int32_t* __restrict__ entry_row,
+    const float* __restrict__ alpha, const T* residual, int64_t nrows, int64_t t0,
+    uint32_t pieces, int hv, int H, int k, T* out) {
+  const uint32_t g = blockIdx.x * 256u + threadIdx.x;
+  if (g >= pieces) return;
+  const uint32_t dt = g / uint32_t(hv);
+  const int64_t t = t0 + dt;
+  const int64_t h = int64_t(g - dt * uint32_t(hv)) * 8;
+  float acc[8];
+  if (residual != nullptr) {
+    unpack8(load_raw8<T>(residual + t * H + h), acc);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  }
+  const int32_t* er = entry_row + t * k;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    Raw8<T> v[4];
+    float w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t r = j0 + u < k ? int64_t(er[j0 + u]) : -1;
+      const bool use = r >= 0 && r < nrows;
+      w[u] = !use ? 0.f : WEIGHTED ? alpha[t * k + j0 + u] : 1.f;
+      v[u] = use ? load_raw8<T>(rows + r * H + h) : zero_raw8<T>();
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float f[8];
+      unpack8(v[u], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = WEIGHTED ? fmaf(w[u], f[i], acc[i]) : acc[i] + f[i];
+    }
+  }
+  store8<T>(out + t * H + h, acc);
+}
+
+// dys[row(i)] = alpha[i] dy[t] and dalpha[i] = dy[t] . ys[row(i)]: one
+// wavefront per entry, consecutive entries in a block, so that a token's k
+// wavefronts share its dy row in the caches.
+template <typename T>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(
+    const T* __restrict__ dy, const T* __restrict__ ys, const int32_t* __restrict__ entry_row,
+    const float* __restrict__ alpha, int64_t n, int64_t i0, int hv, int H, int k,
+    T* __restrict__ dys, float* __restrict__ dalpha) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = i0 + int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (i >= n) return;
+  const int64_t r = entry_row[i];
+  const int64_t row = r < 0 ? -1 - r : r;
+  if (row >= n) {  // not a row of this call
+    if (lane == 0) dalpha[i] = 0.f;
+    return;
+  }
+  T* o = dys + row * H;
+  if (r < 0) {
+    for (int p = lane; p < hv; p += 64) store_raw8<T>(o + p * 8, zero_raw8<T>());
+    if (lane == 0) dalpha[i] = 0.f;
+    return;
+  }
+  const T* d = dy + (i / k) * H;
+  const T* s = ys + row * H;
+  const float a = alpha[i];
+  float dot = 0.f;
+  for (int p = lane; p < hv; p += 64) {
+    float fd[8], fs[8];
+    unpack8(load_raw8<T>(d + p * 8), fd);
+    unpack8(load_raw8<T>(s + p * 8), fs);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      dot = fmaf(fd[c], fs[c], dot);
+      fd[c] *= a;
+    }
+    store8<T>(o + p * 8, fd);
+  }
+  dot = wave_sum(dot);
+  if (lane == 0) dalpha[i] = dot;
+}
+
+// Tokens of one launch: at most 2^30 pieces, so that piece numbers stay in 32
+// bits and a grid within its limit of threads.
+int64_t slab_rows(int hv) {
+  const int64_t m = (int64_t(1) << 30) / hv;
+  return m > 0 ? m : 1;
+}
+
+template <typename F>
+hipError_t for_slabs(int64_t N, int64_t slab, const Launch& L, F launch) {
+  for (int64_t t0 = 0; t0 < N; t0 += slab) {
+    Launch one = L;
+    if (t0 > 0) one.start = nullptr;
+    if (t0 + slab < N) one.stop = nullptr;
+    const hipError_t e = launch(t0, t0 + slab < N ? slab : N - t0, one);
+    if (e != hipSuccess) return e;
+    L.launched = true;
+  }
+  return hipSuccess;
+}
+
+template <typename T>
+hipError_t dispatch_small(const void* x, const int32_t* idx, int64_t N, int H, int E, int k,
+                          int cap, void* xs, int32_t* offsets, int32_t* row_entry,
+                          int32_t* entry_row, const Launch& s) {
+  return launch_kernel(dispatch_small_kernel<T>, dim3(unsigned(N)), dim3(256), 0, s,
+                       static_cast<const T*>(x), idx, int(N * k), H / 8, H, E, k, cap,
+                       static_cast<T*>(xs), offsets, row_entry, entry_row);
+}
+
+template <typename T>
+hipError_t dispatch_copy(const void* x, const int32_t* entry_row, int64_t N, int H, int k,
+                         void* xs, const Launch& s) {
+  const int hv = H / 8;
+  return for_slabs(N, slab_rows(hv), s, [&](int64_t t0, int64_t rows, const Launch& L) {
+    const uint32_t pieces = uint32_t(rows * hv);
+    return launch_kernel(dispatch_copy_kernel<T>, dim3((pieces + 255) / 256), dim3(256), 0, L,
+                         static_cast<const T*>(x), entry_row, t0, pieces, hv, H, k,
+                         static_cast<T*>(xs));
+  });
+}
+
+template <typename T, bool WEIGHTED>
+hipError_t gather_sum(const void* rows, const int32_t* entry_row, const float* alpha,
+                      const void* residual, int64_t N, int H, int k, void* out,
+                      const Launch& s) {
+  const int hv = H / 8;
+  return for_slabs(N, slab_rows(hv), s, [&](int64_t t0, int64_t m, const Launch& L) {
+    const uint32_t pieces = uint32_t(m * hv);
+    return launch_kernel(gather_sum_kernel<T, WEIGHTED>, dim3((pieces + 255) / 256), dim3(256), 0,
+                         L, static_cast<const T*>(rows), entry_row, alpha,
+                         static_cast<const T*>(residual), N * k, t0, pieces, hv, H, k,
+                         static_cast<T*>(out));
+  });
+}
+
+template <typename T>
+hipError_t combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
+                       const float* alpha, int64_t N, int H, int k, void* dys, float* dalpha,
+                       const Launch& s) {
+  const int64_t n = N * k;
+  return for_slabs(n, int64_t(1) << 24, s, [&](int64_t i0, int64_t m, const Launch& L) {
+    return launch_kernel(combine_bwd_kernel<T>, dim3(unsigned((m + 3) / 4)), dim3(256), 0, L,
+                         static_cast<const T*>(dy), static_cast<const T*>(ys), entry_row, alpha,
+                         n, i0, H / 8, H, k, static_cast<T*>(dys), dalpha);
+  });
+}
+
+}  // namespace
+
+DispatchPlan plan_dispatch(int64_t n, int E) {
+  DispatchPlan p;
+  if (n <= kDispatchSmall) return p;
+  int64_t c = (n + 255) / 256;           // at most 256 chunks
+  c = (c + 255) / 256 * 256;
+  p.chunk = c < 1024 ? 1024 : int(c);
+  p.nchunk = int((n + p.chunk - 1) / p.chunk);
+  p.bytes = size_t(p.nchunk) * (E + 1) * sizeof(int32_t);
+  return p;
+}
+
+hipError_t launch_dispatch_rows(const void* x, const int32_t* idx, int64_t N, int H, int E, int k,
+                                int cap, int dtype, void* xs, int32_t* offsets,
+                                int32_t* row_entry, int32_t* entry_row, int32_t* part,
+                                const Launch& rows, const Launch& copy) {
+  const int64_t n = N * k;
+  const DispatchPlan p = plan_dispatch(n, E);
+  const bool f32 = dtype == TOPMOE_DTYPE_FP32;
+  if (n == 0) return launch_kernel(dispatch_empty_kernel, dim3(1), dim3(256), 0, rows, E, offsets);
+  if (p.nchunk == 0)
+    return f32 ? dispatch_small<float>(x, idx, N, H, E, k, cap, xs, offsets, row_entry, entry_row,
+                                       copy)
+               : dispatch_small<bf16_t>(x, idx, N, H, E, k, cap, xs, offsets, row_entry,
+                                        entry_row, copy);
+  int bits = 0;
+  while ((E >> bits) != 0) ++bits;
+  Launch first = rows, second = rows;
+  first.stop = nullptr;
+  second.start = nullptr;
+  hipError_t e = launch_kernel(dispatch_count_kernel, dim3(p.nchunk), dim3(256), 0, first, idx, n,
+                               p.chunk, E, part);
+  if (e != hipSuccess) return e;
+  e = launch_kernel(dispatch_place_kernel, dim3(p.nchunk), dim3(256), 0, second, idx, n, p.chunk,
+                    p.nchunk, E, bits, cap, part, offsets, row_entry, entry_row);
+  if (e != hipSuccess) return e;
+  rows.launched = true;
+  return f32 ? dispatch_copy<float>(x, entry_row, N, H, k, xs, copy)
+             : dispatch_copy<bf16_t>(x, entry_row, N, H, k, xs, copy);
+}
+
+hipError_t launch_gather_sum(const void* rows, const int32_t* entry_row, const float* alpha,
+                             const void* residual, int64_t N, int H, int k, int dtype, void* out,
+                             const Launch& s) {
+  if (dtype == TOPMOE_DTYPE_FP32)
+    return alpha ? gather_sum<float, true>(rows, entry_row, alpha, residual, N, H, k, out, s)
+                 : gather_sum<float, false>(rows, entry_row, alpha, residual, N, H, k, out, s);
+  return alpha ? gather_sum<bf16_t, true>(rows, entry_row, alpha, residual, N, H, k, out, s)
+               : gather_sum<bf16_t, false>(rows, entry_row, alpha, residual, N, H, k, out, s);
+}
+
+hipError_t launch_moe_combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
+                                  const float* alpha, int64_t N, int H, int k, int dtype,
+                                  void* dys, float* dalpha, const Launch& s) {
+  return dtype == TOPMOE_DTYPE_FP32
+             ? combine_bwd<float>(dy, ys, entry_row, alpha, N, H, k, dys, dalpha, s)
+             : combine_bwd<bf16_t>(dy, ys, entry_row, alpha, N, H, k, dys, dalpha, s);
+}
+
+}  // namespace topmoe
