@@ -13,13 +13,20 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _binding as B
-from .ops import _buffer, _dtype_code, _need, _ptr, _torch_stream, _workspace
+from .ops import _buffer, _dtype_code, _need, _ptr, _torch_stream
+
+
+# The current stream's handle without a Stream object (0.1 us a call instead of 2.8).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_empty = torch.empty
+_CODES = {torch.float32: B.DTYPE_FP32, torch.bfloat16: B.DTYPE_BF16}
 
 
 def _on_kernel_stream(fn):
-    """Call ``fn(..., stream=handle)`` with the stream its kernels run on as
-    torch's current stream.  By default that is the current stream of the first
-    argument's device, which is already so unless another device is current."""
+    """Call ``fn`` with the stream its kernels run on as torch's current
+    stream: ``stream`` (an object or a raw handle; ``fn`` itself never sees
+    it) or, by default, the current stream of the first argument's device,
+    where ``fn`` is called as it is."""
     name = next(iter(inspect.signature(fn).parameters))
 
     @functools.wraps(fn)
@@ -27,32 +34,64 @@ def _on_kernel_stream(fn):
         t = args[0] if args else kw.get(name)
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{fn.__name__}: {name} must be a torch.Tensor")
-        dev = t.device
-        if dev.type != "cuda":
-            raise ValueError(f"{name} must be a GPU tensor (got {dev}); the library has no CPU path")
-        if stream is None and dev.index == torch.cuda.current_device():
-            return fn(*args, stream=torch.cuda.current_stream().cuda_stream, **kw)
-        ts = _torch_stream(dev, stream)
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor (got {t.device}); the library has no "
+                             f"CPU path")
+        if stream is None and t.get_device() == torch.cuda.current_device():
+            return fn(*args, **kw)
+        ts = _torch_stream(t.device, stream)
+        if ts.device != t.device:
+            raise ValueError(f"stream is on {ts.device}, {name} on {t.device}")
         with torch.cuda.stream(ts):
-            return fn(*args, stream=ts.cuda_stream, **kw)
+            return fn(*args, **kw)
     return wrapped
 
 
-def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
-    """[..., H] as [N, H] without a copy."""
-    if t.dim() < 1:
-        raise ValueError(f"{name} needs at least one dimension")
+def _code(dt: torch.dtype) -> int:
+    code = _CODES.get(dt)
+    return _dtype_code(dt) if code is None else code
+
+
+def _is(t, name: str, shape, dt, dev) -> None:
+    """ops._need, which words the refusal, behind the checks in their quickest order."""
+    try:
+        if t.shape == shape and t.dtype is dt and t.is_contiguous() and t.device == dev:
+            return
+    except AttributeError:
+        pass
+    _need(t, name, shape, dt, dev)
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(N, H) of a contiguous [..., H] tensor."""
+    shape = t.shape
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t if t.dim() == 2 else t.view(t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1])
+    if len(shape) == 2:
+        return shape
+    if not shape:
+        raise ValueError(f"{name} needs at least one dimension")
+    return (t.numel() // shape[-1] if shape[-1] else 0), shape[-1]
+
+
+def _scratch(nbytes: int, what: str, dev, ws: Optional[torch.Tensor]):
+    """(pointer, bytes, tensor) of a workspace; nbytes 0 is a size the library refuses."""
+    if nbytes == 0:
+        B.check(B.ERR_BAD_SHAPE, what)
+    if ws is None:
+        ws = _empty(nbytes, dtype=torch.uint8, device=dev)
+        return ws.data_ptr(), nbytes, ws
+    _buffer(ws, "workspace", nbytes, dev)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def _events(e: Optional[B.StageEvents]):
-    return e.ptr if e is not None else None
+    return None if e is None else e.ptr
 
 
-def _call(name: str, *args) -> None:
-    st = getattr(B.lib(), name)(*args)
+def _call(name: str, dev, events, *args) -> None:
+    """The C entry point, on torch's current stream of ``dev``."""
+    st = getattr(B.lib(), name)(*args, _raw_stream(dev.index), _events(events))
     if st != B.OK:
         raise B.TopmoeError(st, name)
 
@@ -80,35 +119,32 @@ def moe_dispatch_workspace_bytes(N: int, E: int, k: int) -> int:
 @_on_kernel_stream
 def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
                      capacity_factor: float = 0.0, xs: Optional[torch.Tensor] = None,
-                     workspace: Optional[torch.Tensor] = None, stream=None,
-                     stage_events: Optional[B.StageEvents] = None) -> MoeRows:
+                     workspace: Optional[torch.Tensor] = None,
+                     stream=None, stage_events: Optional[B.StageEvents] = None) -> MoeRows:
     """The tokens' rows sorted by expert (stable: ascending token within an
     expert).  x [..., H]; topk_idx [N, k] int32, entries outside [0, E) (a
     padding token's -1) belong to no expert.  ``capacity_factor`` > 0 keeps
     the first ceil(factor * N * k / E) entries of each expert.  Entries not
     kept have zero rows behind the experts' (from expert_offsets[E])."""
     dev, dt = x.device, x.dtype
-    code = _dtype_code(dt)
-    xf = _rows(x, "x")
-    N, H = xf.shape
+    code = _code(dt)
+    N, H = _rows(x, "x")
     if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
         raise ValueError("topk_idx must be a [N, k] tensor")
     k = topk_idx.shape[1]
-    _need(topk_idx, "topk_idx", (N, k), torch.int32, dev)
+    _is(topk_idx, "topk_idx", (N, k), torch.int32, dev)
     nbytes = moe_dispatch_workspace_bytes(N, E, k)
-    if nbytes == 0:
-        B.check(B.ERR_BAD_SHAPE, "moe_dispatch_fwd")
-    ws = _workspace(nbytes, dev, workspace)
+    wp, wn, ws = _scratch(nbytes, "moe_dispatch_fwd", dev, workspace)
     if xs is None:
-        xs = torch.empty((N * k, H), dtype=dt, device=dev)
-    _need(xs, "xs", (N * k, H), dt, dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    row_entry = torch.empty(N * k, dtype=torch.int32, device=dev)
-    entry_row = torch.empty((N, k), dtype=torch.int32, device=dev)
-    _call("moe_dispatch_fwd", xf.data_ptr(), topk_idx.data_ptr(), N, H, E, k,
+        xs = _empty((N * k, H), dtype=dt, device=dev)
+    else:
+        _is(xs, "xs", (N * k, H), dt, dev)
+    offsets = _empty(E + 1, dtype=torch.int32, device=dev)
+    row_entry = _empty(N * k, dtype=torch.int32, device=dev)
+    entry_row = _empty((N, k), dtype=torch.int32, device=dev)
+    _call("moe_dispatch_fwd", dev, stage_events, x.data_ptr(), topk_idx.data_ptr(), N, H, E, k,
           float(capacity_factor), code, xs.data_ptr(), offsets.data_ptr(), row_entry.data_ptr(),
-          entry_row.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), stream,
-          _events(stage_events))
+          entry_row.data_ptr(), wp, wn)
     return MoeRows(xs, offsets, row_entry, entry_row)
 
 
@@ -117,27 +153,29 @@ def _entry_rows(rows: torch.Tensor, name: str, entry_row: torch.Tensor):
     if not isinstance(entry_row, torch.Tensor) or entry_row.dim() != 2:
         raise ValueError("entry_row must be a [N, k] tensor")
     N, k = entry_row.shape
-    _need(entry_row, "entry_row", (N, k), torch.int32, rows.device)
+    _is(entry_row, "entry_row", (N, k), torch.int32, rows.device)
     if rows.dim() != 2:
         raise ValueError(f"{name} must be a [N*k, H] tensor")
     H = rows.shape[1]
-    _need(rows, name, (N * k, H), rows.dtype, rows.device)
+    _is(rows, name, (N * k, H), rows.dtype, rows.device)
     return N, H, k
 
 
 @_on_kernel_stream
 def moe_dispatch_bwd(dxs: torch.Tensor, entry_row: torch.Tensor, *,
-                     dx: Optional[torch.Tensor] = None, stream=None,
-                     stage_events: Optional[B.StageEvents] = None) -> torch.Tensor:
+                     dx: Optional[torch.Tensor] = None,
+                     stream=None, stage_events: Optional[B.StageEvents] = None) -> torch.Tensor:
     """Gradient of the dispatch: dx [N, H], each token's kept rows of dxs
     [N*k, H] added in slot order (fp32, rounded once)."""
     N, H, k = _entry_rows(dxs, "dxs", entry_row)
-    code = _dtype_code(dxs.dtype)
+    dev, dt = dxs.device, dxs.dtype
+    code = _code(dt)
     if dx is None:
-        dx = torch.empty((N, H), dtype=dxs.dtype, device=dxs.device)
-    _need(dx, "dx", (N, H), dxs.dtype, dxs.device)
-    _call("moe_dispatch_bwd", dxs.data_ptr(), entry_row.data_ptr(), N, H, k, code, dx.data_ptr(),
-          stream, _events(stage_events))
+        dx = _empty((N, H), dtype=dt, device=dev)
+    else:
+        _is(dx, "dx", (N, H), dt, dev)
+    _call("moe_dispatch_bwd", dev, stage_events, dxs.data_ptr(), entry_row.data_ptr(), N, H, k,
+          code, dx.data_ptr())
     return dx
 
 
@@ -150,34 +188,35 @@ def moe_combine_fwd(ys: torch.Tensor, entry_row: torch.Tensor, alpha: torch.Tens
     (float32) times their rows of ys [N*k, H]."""
     dev, dt = ys.device, ys.dtype
     N, H, k = _entry_rows(ys, "ys", entry_row)
-    code = _dtype_code(dt)
-    _need(alpha, "alpha", (N, k), torch.float32, dev)
+    code = _code(dt)
+    _is(alpha, "alpha", (N, k), torch.float32, dev)
     if residual is not None:
-        _need(residual, "residual", (N, H), dt, dev)
+        _is(residual, "residual", (N, H), dt, dev)
     if y is None:
-        y = torch.empty((N, H), dtype=dt, device=dev)
-    _need(y, "y", (N, H), dt, dev)
-    _call("moe_combine_fwd", ys.data_ptr(), entry_row.data_ptr(), alpha.data_ptr(), _ptr(residual),
-          N, H, k, code, y.data_ptr(), stream, _events(stage_events))
+        y = _empty((N, H), dtype=dt, device=dev)
+    else:
+        _is(y, "y", (N, H), dt, dev)
+    _call("moe_combine_fwd", dev, stage_events, ys.data_ptr(), entry_row.data_ptr(),
+          alpha.data_ptr(), _ptr(residual), N, H, k, code, y.data_ptr())
     return y
 
 
 @_on_kernel_stream
 def moe_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, entry_row: torch.Tensor,
-                    alpha: torch.Tensor, *, stream=None,
-                    stage_events: Optional[B.StageEvents] = None) -> CombineGrads:
+                    alpha: torch.Tensor, *,
+                    stream=None, stage_events: Optional[B.StageEvents] = None) -> CombineGrads:
     """Gradients of the combine for dy [N, H]: dys [N*k, H] (zero rows for
     entries that are not kept) and dalpha [N, k] float32.  entry_row must name
     each row once, as moe_dispatch_fwd's does."""
     dev, dt = ys.device, ys.dtype
     N, H, k = _entry_rows(ys, "ys", entry_row)
-    code = _dtype_code(dt)
-    _need(dy, "dy", (N, H), dt, dev)
-    _need(alpha, "alpha", (N, k), torch.float32, dev)
-    dys = torch.empty((N * k, H), dtype=dt, device=dev)
-    dalpha = torch.empty((N, k), dtype=torch.float32, device=dev)
-    _call("moe_combine_bwd", dy.data_ptr(), ys.data_ptr(), entry_row.data_ptr(), alpha.data_ptr(),
-          N, H, k, code, dys.data_ptr(), dalpha.data_ptr(), stream, _events(stage_events))
+    code = _code(dt)
+    _is(dy, "dy", (N, H), dt, dev)
+    _is(alpha, "alpha", (N, k), torch.float32, dev)
+    dys = _empty((N * k, H), dtype=dt, device=dev)
+    dalpha = _empty((N, k), dtype=torch.float32, device=dev)
+    _call("moe_combine_bwd", dev, stage_events, dy.data_ptr(), ys.data_ptr(), entry_row.data_ptr(),
+          alpha.data_ptr(), N, H, k, code, dys.data_ptr(), dalpha.data_ptr())
     return CombineGrads(dys, dalpha)
 
 
@@ -213,51 +252,47 @@ def block_norm_bwd_workspace_bytes(N: int, H: int, gate_rows: int = 1) -> int:
 
 @_on_kernel_stream
 def block_prenorm_fwd(x: torch.Tensor, w: torch.Tensor, *, eps: float = 1e-5,
-                      n: Optional[torch.Tensor] = None, stream=None,
-                      stage_events: Optional[B.StageEvents] = None) -> PrenormOutput:
+                      n: Optional[torch.Tensor] = None,
+                      stream=None, stage_events: Optional[B.StageEvents] = None) -> PrenormOutput:
     """RMS norm before a block: n = w * x * rstd, rstd = 1 / sqrt(mean(x^2) +
     eps) over the last dimension.  x [..., H], w [H]; n has x's shape, rstd
     [N] is float32 (for the backward)."""
     dev, dt = x.device, x.dtype
-    code = _dtype_code(dt)
-    xf = _rows(x, "x")
-    N, H = xf.shape
-    _need(w, "w", (H,), dt, dev)
+    code = _code(dt)
+    N, H = _rows(x, "x")
+    _is(w, "w", (H,), dt, dev)
     if n is None:
-        n = torch.empty(x.shape, dtype=dt, device=dev)
-    _need(n, "n", x.shape, dt, dev)
-    rstd = torch.empty(N, dtype=torch.float32, device=dev)
-    _call("block_prenorm_fwd", xf.data_ptr(), w.data_ptr(), N, H, float(eps), code, n.data_ptr(),
-          rstd.data_ptr(), stream, _events(stage_events))
+        n = _empty(x.shape, dtype=dt, device=dev)
+    else:
+        _is(n, "n", x.shape, dt, dev)
+    rstd = _empty(N, dtype=torch.float32, device=dev)
+    _call("block_prenorm_fwd", dev, stage_events, x.data_ptr(), w.data_ptr(), N, H, float(eps),
+          code, n.data_ptr(), rstd.data_ptr())
     return PrenormOutput(n, rstd)
 
 
 @_on_kernel_stream
 def block_prenorm_bwd(dn: torch.Tensor, x: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, *,
                       dresidual: Optional[torch.Tensor] = None,
-                      workspace: Optional[torch.Tensor] = None, stream=None,
-                      stage_events: Optional[B.StageEvents] = None) -> PrenormGrads:
+                      workspace: Optional[torch.Tensor] = None,
+                      stream=None, stage_events: Optional[B.StageEvents] = None) -> PrenormGrads:
     """Gradients of block_prenorm_fwd for dn (x's shape).  ``dresidual``: the
     gradient that reaches x along the residual stream, added to dx in the
     same pass."""
     dev, dt = x.device, x.dtype
-    code = _dtype_code(dt)
-    xf = _rows(x, "x")
-    N, H = xf.shape
-    _need(dn, "dn", x.shape, dt, dev)
-    _need(w, "w", (H,), dt, dev)
-    _need(rstd, "rstd", (N,), torch.float32, dev)
+    code = _code(dt)
+    N, H = _rows(x, "x")
+    _is(dn, "dn", x.shape, dt, dev)
+    _is(w, "w", (H,), dt, dev)
+    _is(rstd, "rstd", (N,), torch.float32, dev)
     if dresidual is not None:
-        _need(dresidual, "dresidual", x.shape, dt, dev)
+        _is(dresidual, "dresidual", x.shape, dt, dev)
     nbytes = block_norm_bwd_workspace_bytes(N, H)
-    if nbytes == 0:
-        B.check(B.ERR_BAD_SHAPE, "block_prenorm_bwd")
-    ws = _workspace(nbytes, dev, workspace)
-    dx = torch.empty(x.shape, dtype=dt, device=dev)
-    dw = torch.empty(H, dtype=dt, device=dev)
-    _call("block_prenorm_bwd", dn.data_ptr(), xf.data_ptr(), w.data_ptr(), rstd.data_ptr(),
-          _ptr(dresidual), N, H, code, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(),
-          ws.numel() * ws.element_size(), stream, _events(stage_events))
+    wp, wn, ws = _scratch(nbytes, "block_prenorm_bwd", dev, workspace)
+    dx = _empty(x.shape, dtype=dt, device=dev)
+    dw = _empty(H, dtype=dt, device=dev)
+    _call("block_prenorm_bwd", dev, stage_events, dn.data_ptr(), x.data_ptr(), w.data_ptr(),
+          rstd.data_ptr(), _ptr(dresidual), N, H, code, dx.data_ptr(), dw.data_ptr(), wp, wn)
     return PrenormGrads(dx, dw)
 
 
@@ -269,7 +304,7 @@ def _gate(gate: Optional[torch.Tensor], N: int, H: int, dt, dev):
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
     shape = tuple(gate.shape)
-    _need(gate, "gate", shape, dt, dev)
+    _is(gate, "gate", shape, dt, dev)
     if len(shape) > 1 and shape[-1] == 1 and gate.numel() == N:
         return B.GATE_TOKEN, 1
     if shape and shape[-1] == H:
@@ -284,35 +319,35 @@ def _gate(gate: Optional[torch.Tensor], N: int, H: int, dt, dev):
 def block_postnorm_fwd(y: torch.Tensor, residual: torch.Tensor, w: Optional[torch.Tensor] = None, *,
                        gate: Optional[torch.Tensor] = None, next_w: Optional[torch.Tensor] = None,
                        residual_scale: float = 1.0, eps: float = 1e-5,
-                       out: Optional[torch.Tensor] = None, stream=None,
-                       stage_events: Optional[B.StageEvents] = None) -> PostnormOutput:
+                       out: Optional[torch.Tensor] = None,
+                       stream=None, stage_events: Optional[B.StageEvents] = None) -> PostnormOutput:
     """After a block with output y [..., H]: out = residual_scale * residual +
     gate * w * y / rms(y), without the norm where ``w`` is None, and with
     ``next_w`` the next block's norm n = next_w * out / rms(out) in the same
     pass.  ``gate``: [H], [G, H] (each row for N / G consecutive tokens) or
     one value per token [..., 1].  ``out`` may be the residual itself."""
     dev, dt = y.device, y.dtype
-    code = _dtype_code(dt)
-    yf = _rows(y, "y")
-    N, H = yf.shape
-    _need(residual, "residual", y.shape, dt, dev)
+    code = _code(dt)
+    N, H = _rows(y, "y")
+    _is(residual, "residual", y.shape, dt, dev)
     if w is not None:
-        _need(w, "w", (H,), dt, dev)
+        _is(w, "w", (H,), dt, dev)
     if next_w is not None:
-        _need(next_w, "next_w", (H,), dt, dev)
+        _is(next_w, "next_w", (H,), dt, dev)
     mode, gate_rows = _gate(gate, N, H, dt, dev)
     if out is None:
-        out = torch.empty(y.shape, dtype=dt, device=dev)
-    _need(out, "out", y.shape, dt, dev)
+        out = _empty(y.shape, dtype=dt, device=dev)
+    else:
+        _is(out, "out", y.shape, dt, dev)
     rstd = n = next_rstd = None
     if w is not None:
-        rstd = torch.empty(N, dtype=torch.float32, device=dev)
+        rstd = _empty(N, dtype=torch.float32, device=dev)
     if next_w is not None:
-        n = torch.empty(y.shape, dtype=dt, device=dev)
-        next_rstd = torch.empty(N, dtype=torch.float32, device=dev)
-    _call("block_postnorm_fwd", yf.data_ptr(), residual.data_ptr(), _ptr(w), _ptr(gate),
-          _ptr(next_w), N, H, mode, gate_rows, float(residual_scale), float(eps), code,
-          out.data_ptr(), _ptr(rstd), _ptr(n), _ptr(next_rstd), stream, _events(stage_events))
+        n = _empty(y.shape, dtype=dt, device=dev)
+        next_rstd = _empty(N, dtype=torch.float32, device=dev)
+    _call("block_postnorm_fwd", dev, stage_events, y.data_ptr(), residual.data_ptr(), _ptr(w),
+          _ptr(gate), _ptr(next_w), N, H, mode, gate_rows, float(residual_scale), float(eps), code,
+          out.data_ptr(), _ptr(rstd), _ptr(n), _ptr(next_rstd))
     return PostnormOutput(out, rstd, n, next_rstd)
 
 
@@ -322,41 +357,37 @@ def block_postnorm_bwd(dout: torch.Tensor, y: torch.Tensor,
                        gate: Optional[torch.Tensor] = None, dn: Optional[torch.Tensor] = None,
                        out: Optional[torch.Tensor] = None, next_w: Optional[torch.Tensor] = None,
                        next_rstd: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
-                       workspace: Optional[torch.Tensor] = None, stream=None,
-                       stage_events: Optional[B.StageEvents] = None) -> PostnormGrads:
+                       workspace: Optional[torch.Tensor] = None,
+                       stream=None, stage_events: Optional[B.StageEvents] = None) -> PostnormGrads:
     """Gradients of block_postnorm_fwd for dout (and, with ``next_w``, dn):
     dy, dresidual (y's shape), dw, dnext_w [H] and dgate (the gate's shape).
     ``rstd``, ``out`` and ``next_rstd`` as the forward returned them."""
     dev, dt = y.device, y.dtype
-    code = _dtype_code(dt)
-    yf = _rows(y, "y")
-    N, H = yf.shape
-    _need(dout, "dout", y.shape, dt, dev)
+    code = _code(dt)
+    N, H = _rows(y, "y")
+    _is(dout, "dout", y.shape, dt, dev)
     if w is not None:
-        _need(w, "w", (H,), dt, dev)
-        _need(rstd, "rstd", (N,), torch.float32, dev)
+        _is(w, "w", (H,), dt, dev)
+        _is(rstd, "rstd", (N,), torch.float32, dev)
     if next_w is not None:
-        _need(next_w, "next_w", (H,), dt, dev)
-        _need(dn, "dn", y.shape, dt, dev)
-        _need(out, "out", y.shape, dt, dev)
-        _need(next_rstd, "next_rstd", (N,), torch.float32, dev)
+        _is(next_w, "next_w", (H,), dt, dev)
+        _is(dn, "dn", y.shape, dt, dev)
+        _is(out, "out", y.shape, dt, dev)
+        _is(next_rstd, "next_rstd", (N,), torch.float32, dev)
     elif dn is not None:
         raise ValueError("dn needs next_w")
     mode, gate_rows = _gate(gate, N, H, dt, dev)
     nbytes = block_norm_bwd_workspace_bytes(N, H, gate_rows)
-    if nbytes == 0:
-        B.check(B.ERR_BAD_SHAPE, "block_postnorm_bwd")
-    ws = _workspace(nbytes, dev, workspace)
-    dy = torch.empty(y.shape, dtype=dt, device=dev)
-    dresidual = torch.empty(y.shape, dtype=dt, device=dev)
-    dw = torch.empty(H, dtype=dt, device=dev) if w is not None else None
-    dnext_w = torch.empty(H, dtype=dt, device=dev) if next_w is not None else None
-    dgate = torch.empty(gate.shape, dtype=dt, device=dev) if gate is not None else None
-    _call("block_postnorm_bwd", dout.data_ptr(), _ptr(dn), yf.data_ptr(), _ptr(out), _ptr(w),
-          _ptr(gate), _ptr(next_w), _ptr(rstd), _ptr(next_rstd), N, H, mode, gate_rows,
-          float(residual_scale), code, dy.data_ptr(), dresidual.data_ptr(), _ptr(dw), _ptr(dgate),
-          _ptr(dnext_w), ws.data_ptr(), ws.numel() * ws.element_size(), stream,
-          _events(stage_events))
+    wp, wn, ws = _scratch(nbytes, "block_postnorm_bwd", dev, workspace)
+    dy = _empty(y.shape, dtype=dt, device=dev)
+    dresidual = _empty(y.shape, dtype=dt, device=dev)
+    dw = _empty(H, dtype=dt, device=dev) if w is not None else None
+    dnext_w = _empty(H, dtype=dt, device=dev) if next_w is not None else None
+    dgate = _empty(gate.shape, dtype=dt, device=dev) if gate is not None else None
+    _call("block_postnorm_bwd", dev, stage_events, dout.data_ptr(), _ptr(dn), y.data_ptr(),
+          _ptr(out), _ptr(w), _ptr(gate), _ptr(next_w), _ptr(rstd), _ptr(next_rstd), N, H, mode,
+          gate_rows, float(residual_scale), code, dy.data_ptr(), dresidual.data_ptr(), _ptr(dw),
+          _ptr(dgate), _ptr(dnext_w), wp, wn)
     return PostnormGrads(dy, dresidual, dw, dgate, dnext_w)
 
 
@@ -386,9 +417,9 @@ def _pitched(t: torch.Tensor, name: str, shape, dt, dev) -> int:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev} (the library has no CPU path)")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dt:
+    if t.dtype is not dt:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dt}")
     R, C = shape
     if t.numel() == 0 or (R == 1 and t.stride(1) == 1):
@@ -399,13 +430,13 @@ def _pitched(t: torch.Tensor, name: str, shape, dt, dev) -> int:
 
 
 def _need_act8(a: Act8, name: str, R: int, C: int, dev) -> None:
-    _need(a.q, f"{name}.q", (R, C), torch.float8_e4m3fn, dev)
-    _need(a.scale, f"{name}.scale", (R, -(-C // B.ACT8_GROUP)), torch.uint8, dev)
+    _is(a.q, f"{name}.q", (R, C), torch.float8_e4m3fn, dev)
+    _is(a.scale, f"{name}.scale", (R, -(-C // B.ACT8_GROUP)), torch.uint8, dev)
 
 
 def _new_act8(R: int, C: int, dev) -> Act8:
-    return Act8(torch.empty((R, C), dtype=torch.float8_e4m3fn, device=dev),
-                torch.empty((R, -(-C // B.ACT8_GROUP)), dtype=torch.uint8, device=dev))
+    return Act8(_empty((R, C), dtype=torch.float8_e4m3fn, device=dev),
+                _empty((R, -(-C // B.ACT8_GROUP)), dtype=torch.uint8, device=dev))
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -419,29 +450,30 @@ def act8_pack(x: torch.Tensor, *, stream=None,
               stage_events: Optional[B.StageEvents] = None) -> Act8:
     """x [R, C] (contiguous rows; a row pitch is fine) in 8 bits."""
     R, C = _matrix(x, "x")
-    code = _dtype_code(x.dtype)
-    ld = _pitched(x, "x", (R, C), x.dtype, x.device)
-    a = _new_act8(R, C, x.device)
-    _call("act8_pack", x.data_ptr(), ld, R, C, code, a.q.data_ptr(), a.scale.data_ptr(), stream,
-          _events(stage_events))
+    dev, dt = x.device, x.dtype
+    code = _code(dt)
+    ld = _pitched(x, "x", (R, C), dt, dev)
+    a = _new_act8(R, C, dev)
+    _call("act8_pack", dev, stage_events, x.data_ptr(), ld, R, C, code, a.q.data_ptr(),
+          a.scale.data_ptr())
     return a
 
 
 @_on_kernel_stream
 def act8_unpack(q: torch.Tensor, scale: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
-                x: Optional[torch.Tensor] = None, stream=None,
-                stage_events: Optional[B.StageEvents] = None) -> torch.Tensor:
+                x: Optional[torch.Tensor] = None,
+                stream=None, stage_events: Optional[B.StageEvents] = None) -> torch.Tensor:
     """The activation that act8_pack kept, [R, C] in ``dtype`` (or into ``x``,
     whose rows may be pitched)."""
     R, C = _matrix(q, "q")
     dev = q.device
     _need_act8(Act8(q, scale), "act8", R, C, dev)
     if x is None:
-        x = torch.empty((R, C), dtype=dtype, device=dev)
-    code = _dtype_code(x.dtype)
+        x = _empty((R, C), dtype=dtype, device=dev)
+    code = _code(x.dtype)
     ld = _pitched(x, "x", (R, C), x.dtype, dev)
-    _call("act8_unpack", q.data_ptr(), scale.data_ptr(), R, C, code, x.data_ptr(), ld, stream,
-          _events(stage_events))
+    _call("act8_unpack", dev, stage_events, q.data_ptr(), scale.data_ptr(), R, C, code,
+          x.data_ptr(), ld)
     return x
 
 
@@ -452,16 +484,16 @@ def swiglu_act8_fwd(g: torch.Tensor, u: torch.Tensor, *, h: Optional[torch.Tenso
     swiglu_act8_bwd.  g and u may be the halves of one [R, 2C] projection."""
     R, C = _matrix(g, "g")
     dev, dt = g.device, g.dtype
-    code = _dtype_code(dt)
+    code = _code(dt)
     ldg = _pitched(g, "g", (R, C), dt, dev)
     ldu = _pitched(u, "u", (R, C), dt, dev)
     if h is None:
-        h = torch.empty((R, C), dtype=dt, device=dev)
-    _need(h, "h", (R, C), dt, dev)
+        h = _empty((R, C), dtype=dt, device=dev)
+    else:
+        _is(h, "h", (R, C), dt, dev)
     g8, u8 = _new_act8(R, C, dev), _new_act8(R, C, dev)
-    _call("swiglu_act8_fwd", g.data_ptr(), ldg, u.data_ptr(), ldu, R, C, code, h.data_ptr(),
-          g8.q.data_ptr(), g8.scale.data_ptr(), u8.q.data_ptr(), u8.scale.data_ptr(), stream,
-          _events(stage_events))
+    _call("swiglu_act8_fwd", dev, stage_events, g.data_ptr(), ldg, u.data_ptr(), ldu, R, C, code,
+          h.data_ptr(), g8.q.data_ptr(), g8.scale.data_ptr(), u8.q.data_ptr(), u8.scale.data_ptr())
     return SwigluAct8(h, g8, u8)
 
 
@@ -474,19 +506,19 @@ def swiglu_act8_bwd(dh: torch.Tensor, g8: Act8, u8: Act8, *, with_h: bool = True
     default dg and du are the halves of one new [R, 2C] tensor."""
     R, C = _matrix(dh, "dh")
     dev, dt = dh.device, dh.dtype
-    code = _dtype_code(dt)
-    _need(dh, "dh", (R, C), dt, dev)
+    code = _code(dt)
+    _is(dh, "dh", (R, C), dt, dev)
     _need_act8(g8, "g8", R, C, dev)
     _need_act8(u8, "u8", R, C, dev)
     if (dg is None) != (du is None):
         raise ValueError("dg and du go together")
     if dg is None:
-        dgu = torch.empty((R, 2 * C), dtype=dt, device=dev)
+        dgu = _empty((R, 2 * C), dtype=dt, device=dev)
         dg, du = dgu[:, :C], dgu[:, C:]
     lddg = _pitched(dg, "dg", (R, C), dt, dev)
     lddu = _pitched(du, "du", (R, C), dt, dev)
-    h = torch.empty((R, C), dtype=dt, device=dev) if with_h else None
-    _call("swiglu_act8_bwd", g8.q.data_ptr(), g8.scale.data_ptr(), u8.q.data_ptr(),
-          u8.scale.data_ptr(), dh.data_ptr(), R, C, code, dg.data_ptr(), lddg, du.data_ptr(), lddu,
-          _ptr(h), stream, _events(stage_events))
+    h = _empty((R, C), dtype=dt, device=dev) if with_h else None
+    _call("swiglu_act8_bwd", dev, stage_events, g8.q.data_ptr(), g8.scale.data_ptr(),
+          u8.q.data_ptr(), u8.scale.data_ptr(), dh.data_ptr(), R, C, code, dg.data_ptr(), lddg,
+          du.data_ptr(), lddu, _ptr(h))
     return SwigluAct8Grads(dg, du, h)

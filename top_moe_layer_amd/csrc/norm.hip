@@ -157,83 +157,129 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_fwd_kernel(NormFwd
   }
 }
 
-// One unit of rows per block (see NormUnits): row gradients, and the unit's
-// column sums in registers.
+// What one row of the backward pass reads, as loaded.
+template <typename T, int V, bool POST, bool NEXT>
+struct BwdRow {
+  Raw8<T> dout[V], y[V], out[V], dn[V];
+  float rstd, next_rstd, gate;  // gate: of a token gate
+};
+
 template <typename T, int W, int V, bool POST, bool NEXT>
+__device__ __forceinline__ void load_row(const NormBwd& a, int64_t t, int lane,
+                                         BwdRow<T, V, POST, NEXT>& r) {
+  const int64_t row = t * a.H;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int p = lane + v * 64 * W;
+    const bool in = p < a.hv;
+    const int64_t at = row + p * 8;
+    if constexpr (NEXT) {
+      r.out[v] = in ? load_raw8<T>(static_cast<const T*>(a.out) + at) : zero_raw8<T>();
+      r.dn[v] = in ? load_raw8<T>(static_cast<const T*>(a.dn) + at) : zero_raw8<T>();
+    }
+    r.dout[v] = in && a.dout != nullptr ? load_raw8<T>(static_cast<const T*>(a.dout) + at)
+                                        : zero_raw8<T>();
+    if constexpr (POST)
+      r.y[v] = in ? load_raw8<T>(static_cast<const T*>(a.y) + at) : zero_raw8<T>();
+  }
+  if constexpr (NEXT) r.next_rstd = a.next_rstd[t];
+  if constexpr (POST) {
+    r.rstd = a.rstd != nullptr ? a.rstd[t] : 1.f;
+    r.gate = a.gate_mode == kGateToken ? to_f32<T>(static_cast<const T*>(a.gate)[t]) : 1.f;
+  }
+}
+
+// One unit of rows per block (see NormUnits): row gradients, and the unit's
+// column sums in registers.  FLUSH: units of whole gate groups.  PRE: the
+// weights stay in registers, and the next row's loads are issued before a
+// row's sums, so that they run under its barriers; the widest rows have no
+// registers left for that and load what they need when they need it.
+template <typename T, int W, int V, bool POST, bool NEXT, bool FLUSH, bool PRE>
 __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
   __shared__ float slot[2][W];
   const int lane = int(threadIdx.x), wave = int(threadIdx.x >> 6);
   int turn = 0;
   const float inv_h = 1.0f / float(a.H);
   const int64_t unit = blockIdx.x;
-  int64_t r0, r1;
-  if (a.units.per_group > 0) {  // a piece of one gate group
-    const int64_t g = unit / a.units.per_group, c = unit - g * a.units.per_group;
-    r0 = g * a.gate_span + c * a.units.rows;
-    r1 = r0 + a.units.rows;
-    const int64_t end = (g + 1) * a.gate_span;
-    r1 = r1 < end ? r1 : end;
-  } else {  // whole gate groups
+  int64_t r0, r1, group = 0;
+  if constexpr (!FLUSH) {  // a piece of one gate group
+    group = unit / a.units.per_group;
+    r0 = group * a.gate_span + (unit - group * a.units.per_group) * a.units.rows;
+    const int64_t end = (group + 1) * a.gate_span;
+    r1 = r0 + a.units.rows < end ? r0 + a.units.rows : end;
+  } else {
     r0 = unit * a.units.rows;
-    r1 = r0 + a.units.rows;
-    r1 = r1 < a.N ? r1 : a.N;
+    r1 = r0 + a.units.rows < a.N ? r0 + a.units.rows : a.N;
+    group = r0 / a.gate_span;
   }
-  float sw[V][8], sg[V][8], sn[V][8];  // sums for dw, dgate (of the current group), dw_next
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) sw[v][c] = sg[v][c] = sn[v][c] = 0.f;
-
-  for (int64_t t = r0; t < r1; ++t) {
-    float dr[V][8];
+  const T* cgate = POST && a.gate_mode == kGateChannel
+                       ? static_cast<const T*>(a.gate) + group * a.H : nullptr;
+  Raw8<T> w[V], nw[V], cg[V];  // PRE: post and next weight, the current group's gate
+  auto hold = [&](Raw8<T>(&r)[V], const void* from) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * 64 * W;
-      if (a.dout != nullptr && p < a.hv) {
-        load_f<T>(static_cast<const T*>(a.dout) + t * a.H + p * 8, dr[v]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) dr[v][c] = 0.f;
-      }
+      r[v] = from != nullptr && p < a.hv ? load_raw8<T>(static_cast<const T*>(from) + p * 8)
+                                         : zero_raw8<T>();
     }
-    Raw8<T> yr[V];
+  };
+  auto held = [&](const Raw8<T>& r, const void* from, int p, float(&f)[8]) {
+    if constexpr (PRE) unpack8(r, f);
+    else unpack8(p < a.hv ? load_raw8<T>(static_cast<const T*>(from) + p * 8) : zero_raw8<T>(), f);
+  };
+  if constexpr (PRE) {
+    if constexpr (NEXT) hold(nw, a.next_w);
     if constexpr (POST) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int p = lane + v * 64 * W;
-        yr[v] = p < a.hv ? load_raw8<T>(static_cast<const T*>(a.y) + t * a.H + p * 8)
-                         : zero_raw8<T>();
-      }
+      hold(w, a.w);
+      hold(cg, cgate);
     }
+  }
+  float sg[V][8], sn[V][8];   // sums for dgate and dw (of the current group), dw_next
+  float sw[FLUSH ? V : 1][8];  // for dw, of the finished groups
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      sg[v][c] = sn[v][c] = 0.f;
+      if constexpr (FLUSH) sw[v][c] = 0.f;
+    }
+
+  BwdRow<T, V, POST, NEXT> cur;
+  if constexpr (PRE) load_row<T, W>(a, r0, lane, cur);
+  int64_t left = FLUSH ? a.gate_span : 0;  // rows to the end of the group
+  for (int64_t t = r0; t < r1; ++t) {
+    BwdRow<T, V, POST, NEXT> nxt;
+    if constexpr (PRE) load_row<T, W>(a, t + 1 < r1 ? t + 1 : t, lane, nxt);
+    else load_row<T, W>(a, t, lane, cur);
+    float dr[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) unpack8(cur.dout[v], dr[v]);
     if constexpr (NEXT) {
-      const float rstd = a.next_rstd[t];
-      float rh[V][8], av[V][8];
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int p = lane + v * 64 * W;
-        if (p < a.hv) {
-          float w[8];
-          load_f<T>(static_cast<const T*>(a.out) + t * a.H + p * 8, rh[v]);
-          load_f<T>(static_cast<const T*>(a.dn) + t * a.H + p * 8, av[v]);
-          load_f<T>(static_cast<const T*>(a.next_w) + p * 8, w);
+        float rh[8], av[8], wv[8];
+        unpack8(cur.out[v], rh);
+        unpack8(cur.dn[v], av);
+        held(nw[v], a.next_w, lane + v * 64 * W, wv);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            rh[v][c] *= rstd;
-            sn[v][c] = fmaf(av[v][c], rh[v][c], sn[v][c]);
-            av[v][c] *= w[c];
-            s = fmaf(av[v][c], rh[v][c], s);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) rh[v][c] = av[v][c] = 0.f;
+        for (int c = 0; c < 8; ++c) {
+          rh[c] *= cur.next_rstd;
+          sn[v][c] = fmaf(av[c], rh[c], sn[v][c]);
+          s = fmaf(av[c] * wv[c], rh[c], s);
         }
       }
       const float m = row_sum<W>(s, slot, turn, wave) * inv_h;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        float rh[8], av[8], wv[8];
+        unpack8(cur.out[v], rh);
+        unpack8(cur.dn[v], av);
+        held(nw[v], a.next_w, lane + v * 64 * W, wv);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) dr[v][c] += rstd * (av[v][c] - rh[v][c] * m);
+        for (int c = 0; c < 8; ++c)
+          dr[v][c] += cur.next_rstd * (av[c] * wv[c] - rh[c] * cur.next_rstd * m);
+      }
     }
     if constexpr (!POST) {
 #pragma unroll
@@ -242,45 +288,31 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
         if (p < a.hv) store8<T>(static_cast<T*>(a.dy) + t * a.H + p * 8, dr[v]);
       }
     } else {
-      const float rstd = a.rstd != nullptr ? a.rstd[t] : 1.f;
-      const float gt = a.gate_mode == kGateToken ? to_f32<T>(static_cast<const T*>(a.gate)[t]) : 1.f;
-      const T* gp = a.gate_mode == kGateChannel
-                        ? static_cast<const T*>(a.gate) + (t / a.gate_span) * a.H : nullptr;
-      float b[V][8];  // dr * channel gate * w
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int p = lane + v * 64 * W;
-        float yh[8];
-        unpack8(yr[v], yh);
-        if (p < a.hv) {
-          float q[8];
+        float q[8], yh[8], g[8];
+        unpack8(cur.y[v], yh);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            q[c] = a.scale * dr[v][c];
-            yh[c] *= rstd;
-            sg[v][c] = fmaf(dr[v][c] * gt, yh[c], sg[v][c]);
-            b[v][c] = dr[v][c];
-          }
-          store8<T>(static_cast<T*>(a.dresidual) + t * a.H + p * 8, q);
-          if (a.w != nullptr) {
-            float w[8];
-            load_f<T>(static_cast<const T*>(a.w) + p * 8, w);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) b[v][c] *= w[c];
-          }
-          if (gp != nullptr) {
-            float g[8];
-            load_f<T>(gp + p * 8, g);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) b[v][c] *= g[c];
-          }
-#pragma unroll
-          for (int c = 0; c < 8; ++c) s = fmaf(b[v][c], yh[c], s);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) b[v][c] = 0.f;
+        for (int c = 0; c < 8; ++c) {
+          q[c] = a.scale * dr[v][c];
+          yh[c] *= cur.rstd;
+          sg[v][c] = fmaf(dr[v][c] * cur.gate, yh[c], sg[v][c]);
         }
+        if (p < a.hv) store8<T>(static_cast<T*>(a.dresidual) + t * a.H + p * 8, q);
+        if (a.w != nullptr) {  // from here dr is b without a token gate
+          held(w[v], a.w, p, g);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) dr[v][c] *= g[c];
+        }
+        if (cgate != nullptr) {
+          held(cg[v], cgate, p, g);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) dr[v][c] *= g[c];
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s = fmaf(dr[v][c], yh[c], s);
       }
       float m = 0.f;
       if (a.w != nullptr || a.gate_mode == kGateToken) {
@@ -289,85 +321,106 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
           static_cast<T*>(a.dgate)[t] = from_f32<T>(s);
         m = a.w != nullptr ? s * inv_h : 0.f;
       }
+      const float k = cur.gate * cur.rstd;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int p = lane + v * 64 * W;
-        if (p >= a.hv) continue;
         float yh[8];
-        unpack8(yr[v], yh);
+        unpack8(cur.y[v], yh);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) yh[c] = gt * rstd * (b[v][c] - yh[c] * rstd * m);
-        store8<T>(static_cast<T*>(a.dy) + t * a.H + p * 8, yh);
+        for (int c = 0; c < 8; ++c) yh[c] = k * (dr[v][c] - yh[c] * cur.rstd * m);
+        if (p < a.hv) store8<T>(static_cast<T*>(a.dy) + t * a.H + p * 8, yh);
       }
-      if (a.units.per_group == 0 && (t + 1) % a.gate_span == 0) {  // a gate group ends
-        const int64_t g = t / a.gate_span;
+      if constexpr (FLUSH) {
+        if (--left == 0) {  // the group ends
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int p = lane + v * 64 * W;
-          if (p >= a.hv) continue;
-          float w[8], q[8];
-          load_f<T>(static_cast<const T*>(a.gate) + g * a.H + p * 8, q);
-          if (a.w != nullptr) load_f<T>(static_cast<const T*>(a.w) + p * 8, w);
+          for (int v = 0; v < V; ++v) {
+            const int p = lane + v * 64 * W;
+            float g[8], q[8];
+            held(cg[v], cgate, p, g);
+            if (a.w != nullptr) held(w[v], a.w, p, q);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            sw[v][c] = fmaf(q[c], sg[v][c], sw[v][c]);
-            q[c] = a.w != nullptr ? w[c] * sg[v][c] : sg[v][c];
-            sg[v][c] = 0.f;
+            for (int c = 0; c < 8; ++c) {
+              sw[v][c] = fmaf(g[c], sg[v][c], sw[v][c]);
+              q[c] = a.w != nullptr ? q[c] * sg[v][c] : sg[v][c];
+              sg[v][c] = 0.f;
+            }
+            if (p < a.hv) store8<T>(static_cast<T*>(a.dgate) + group * a.H + p * 8, q);
           }
-          store8<T>(static_cast<T*>(a.dgate) + g * a.H + p * 8, q);
+          left = a.gate_span;
+          ++group;
+          cgate += a.H;
+          if (PRE && t + 1 < r1) hold(cg, cgate);
         }
       }
     }
+    if constexpr (PRE) cur = nxt;
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int p = lane + v * 64 * W;
     if (p >= a.hv) continue;
     if constexpr (POST) {
-      if (a.part != nullptr)
-        store8<float>(a.part + unit * a.H + p * 8, a.units.per_group > 0 ? sg[v] : sw[v]);
+      if (a.part != nullptr) {
+        if constexpr (FLUSH) store8<float>(a.part + unit * a.H + p * 8, sw[v]);
+        else store8<float>(a.part + unit * a.H + p * 8, sg[v]);
+      }
     }
     if constexpr (NEXT) store8<float>(a.part_next + unit * a.H + p * 8, sn[v]);
   }
 }
 
-// Column sums of the units' partial rows: blockIdx.y = 0 dw, 1 dw_next,
-// 2 + g gate row g.  64 channels a block; wavefront s adds units s, s + 16,
-// ... and the 16 sums are added in order.
+// Column sums of the units' partial rows.  Role 0: dw, and dgate of a gate with
+// one row, from the same sums; 1: dw_next; 2 + g: row g of a gate with several.
+// 32 channels a block; slice s of 32 adds units s, s + 32, ..., eight loads in
+// flight, and the 32 sums are added in order.
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
-  __shared__ float sm[16][64];
-  const int lane = threadIdx.x & 63, s = threadIdx.x >> 6;
-  const int h = blockIdx.x * 64 + lane;
+  __shared__ float sm[32][32];
+  const int col = threadIdx.x & 31, s = threadIdx.x >> 5;
+  const int h = blockIdx.x * 32 + col;
   const bool in = h < a.H;
   const int role = a.first_role + int(blockIdx.y);
-  const float* part = role == 1 ? a.part_next : a.part;
+  const float* part = (role == 1 ? a.part_next : a.part) + (in ? h : 0);
   int64_t u0 = 0, u1 = a.units.count;
   if (role >= 2) {
     u0 = int64_t(role - 2) * a.units.per_group;
     u1 = u0 + a.units.per_group < u1 ? u0 + a.units.per_group : u1;  // no units: sums of nothing
   }
-  const bool gated = role == 0 && a.units.per_group > 0 && a.gate_mode == kGateChannel;
+  // several gate rows: dw adds each unit's sums times its group's gate
+  const bool gated = role == 0 && a.gate_mode == kGateChannel && a.units.per_group > 0 &&
+                     a.gate_rows > 1;
+  const T* gate = static_cast<const T*>(a.gate) + (in ? h : 0);
   float acc = 0.f;
-  if (in) {
-    for (int64_t u = u0 + s; u < u1; u += 16) {
-      float v = part[u * a.H + h];
-      if (gated) v *= to_f32<T>(static_cast<const T*>(a.gate)[(u / a.units.per_group) * a.H + h]);
-      acc += v;
+  for (int64_t u = u0 + s; u < u1; u += 32 * 8) {
+    float v[8], g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t x = u + i * 32;
+      v[i] = x < u1 ? part[x * a.H] : 0.f;
+      g[i] = gated && x < u1 ? to_f32<T>(gate[(x / a.units.per_group) * a.H]) : 1.f;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc = fmaf(v[i], g[i], acc);
   }
-  sm[s][lane] = acc;
+  sm[s][col] = acc;
   __syncthreads();
   if (s != 0 || !in) return;
   acc = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc += sm[i][lane];
-  if (role == 0) static_cast<T*>(a.dw)[h] = from_f32<T>(acc);
-  if (role == 1) static_cast<T*>(a.dnext_w)[h] = from_f32<T>(acc);
-  if (role >= 2) {
-    if (a.w != nullptr) acc *= to_f32<T>(static_cast<const T*>(a.w)[h]);
-    static_cast<T*>(a.dgate)[int64_t(role - 2) * a.H + h] = from_f32<T>(acc);
+  for (int i = 0; i < 32; ++i) acc += sm[i][col];
+  if (role == 1) {
+    static_cast<T*>(a.dnext_w)[h] = from_f32<T>(acc);
+    return;
   }
+  const bool one = role == 0 && a.gate_mode == kGateChannel && a.units.per_group > 0 &&
+                   a.gate_rows == 1;  // an empty batch's gate may have no row at all
+  if (role >= 2 || one) {
+    const float w = a.w != nullptr ? to_f32<T>(static_cast<const T*>(a.w)[h]) : 1.f;
+    static_cast<T*>(a.dgate)[int64_t(role >= 2 ? role - 2 : 0) * a.H + h] = from_f32<T>(acc * w);
+  }
+  if (role == 0 && a.dw != nullptr)
+    static_cast<T*>(a.dw)[h] = from_f32<T>(one ? acc * to_f32<T>(gate[0]) : acc);
 }
 
 template <typename T, int W, int V>
@@ -400,12 +453,19 @@ hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
   return hipSuccess;
 }
 
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool PRE>
 hipError_t bwd_flags(const NormBwd& a, bool post, bool next, const Launch& L) {
   const dim3 grid(static_cast<unsigned>(a.units.count)), block(64 * W);
-  if (post && next) return launch_kernel(norm_bwd_kernel<T, W, V, true, true>, grid, block, 0, L, a);
-  if (post) return launch_kernel(norm_bwd_kernel<T, W, V, true, false>, grid, block, 0, L, a);
-  return launch_kernel(norm_bwd_kernel<T, W, V, false, true>, grid, block, 0, L, a);
+#define TOPMOE_NORM_BWD(POST, NEXT, FLUSH) \
+  return launch_kernel(norm_bwd_kernel<T, W, V, POST, NEXT, FLUSH, PRE>, grid, block, 0, L, a)
+  if (!post) TOPMOE_NORM_BWD(false, true, false);
+  if (a.units.per_group == 0) {
+    if (next) TOPMOE_NORM_BWD(true, true, true);
+    TOPMOE_NORM_BWD(true, false, true);
+  }
+  if (next) TOPMOE_NORM_BWD(true, true, false);
+  TOPMOE_NORM_BWD(true, false, false);
+#undef TOPMOE_NORM_BWD
 }
 
 template <typename T>
@@ -413,19 +473,20 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
                      const Launch& sums) {
   if (a.units.count > 0) {
     hipError_t e;
-    if (a.hv <= 64) e = bwd_flags<T, 1, 1>(a, post, next, rows);
-    else if (a.hv <= 256) e = bwd_flags<T, 4, 1>(a, post, next, rows);
-    else if (a.hv <= 512) e = bwd_flags<T, 4, 2>(a, post, next, rows);
-    else if (a.hv <= 1024) e = bwd_flags<T, 8, 2>(a, post, next, rows);
-    else e = bwd_flags<T, 16, 2>(a, post, next, rows);
+    if (a.hv <= 64) e = bwd_flags<T, 1, 1, true>(a, post, next, rows);
+    else if (a.hv <= 256) e = bwd_flags<T, 4, 1, true>(a, post, next, rows);
+    else if (a.hv <= 512) e = bwd_flags<T, 8, 1, true>(a, post, next, rows);
+    else if (a.hv <= 1024) e = bwd_flags<T, 16, 1, false>(a, post, next, rows);
+    else e = bwd_flags<T, 16, 2, false>(a, post, next, rows);
     if (e != hipSuccess) return e;
   }
-  // roles: 0 dw, 1 dw_next, 2.. the gate's rows (where the units did not write
-  // them); neighbouring roles share a launch (a grid has at most 65535 rows)
-  const bool dw = post && a.dw != nullptr;
-  const int64_t gates =
-      post && a.gate_mode == kGateChannel && a.units.per_group > 0 ? a.gate_rows : 0;
-  const int64_t first = dw ? 0 : next ? 1 : 2, end = gates > 0 ? 2 + gates : next ? 2 : dw ? 1 : 0;
+  // The roles of the sums; neighbouring ones share a launch (a grid has at
+  // most 65535 rows).
+  const bool channel = post && a.gate_mode == kGateChannel && a.units.per_group > 0;
+  const bool first_role = post && (a.dw != nullptr || (channel && a.gate_rows == 1));
+  const int64_t gates = channel && a.gate_rows > 1 ? a.gate_rows : 0;
+  const int64_t first = first_role ? 0 : next ? 1 : 2;
+  const int64_t end = gates > 0 ? 2 + gates : next ? 2 : first_role ? 1 : 0;
   Launch L = sums;
   for (int64_t r = first; r < end;) {
     if (r == 1 && !next) {
@@ -438,7 +499,7 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
     NormBwd b = a;
     b.first_role = int(r);
     const hipError_t e =
-        launch_kernel(norm_reduce_kernel<T>, dim3(unsigned((a.H + 63) / 64), unsigned(stop - r)),
+        launch_kernel(norm_reduce_kernel<T>, dim3(unsigned((a.H + 31) / 32), unsigned(stop - r)),
                       dim3(1024), 0, L, b);
     if (e != hipSuccess) return e;
     sums.launched = true;
