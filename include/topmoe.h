@@ -357,12 +357,14 @@ int moe_ffn_bwd(const void* x, const float* Wr, const void* Wg, const void* Wu,
  * tensor pointers 16-byte aligned, int32 / float32 arrays 4-byte aligned.
  * Outputs must not alias inputs or each other, except where said.  With
  * N == 0 only expert_offsets is written, and every other tensor may be NULL. */
-#define TOPMOE_DISPATCH_STAGES 2  /* 0 rows of the entries (empty for small calls),
-                                     1 copy                                        */
+#define TOPMOE_DISPATCH_STAGES 2  /* 0 rows of the entries (empty in the one-launch
+                                     dispatch), 1 copy                             */
 #define TOPMOE_DISPATCH_MAX_EXPERTS 256
+#define TOPMOE_DISPATCH_ONE 32768  /* most entries (N * k) of the one-launch dispatch,
+                                      which needs no workspace                     */
 
 /* Workspace needed by moe_dispatch_fwd: counts per chunk of entries.  Returns
- * 0 for invalid sizes (a valid call needs at least 256 bytes). */
+ * 0 for invalid sizes (and at least 256 for valid ones). */
 size_t moe_dispatch_workspace_bytes(int64_t N, int E, int k);
 
 /* xs[row(i)] = x[t].
@@ -373,7 +375,8 @@ size_t moe_dispatch_workspace_bytes(int64_t N, int E, int k);
  *   row_entry [N*k]     int32 output: the entry of each kept row, then -1
  *   entry_row [N, k]    int32 output: the entry's row, or -1 - row if not kept
  *   workspace           at least moe_dispatch_workspace_bytes(N, E, k) bytes,
- *                       256-byte aligned; contents on entry ignored. */
+ *                       256-byte aligned; contents on entry ignored.  Not used,
+ *                       and may be NULL, up to TOPMOE_DISPATCH_ONE entries. */
 int moe_dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t H, int E, int k,
                      float capacity_factor, int dtype, void* xs, int32_t* expert_offsets,
                      int32_t* row_entry, int32_t* entry_row, void* workspace,

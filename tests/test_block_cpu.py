@@ -18,7 +18,7 @@ def call(name, base, **over):
     return getattr(B.lib(), name)(*a.values(), None, None)
 
 
-DISPATCH = dict(x=FAKE, idx=FAKE, N=8, H=64, E=4, k=2, cf=0.0, dtype=BF16, xs=FAKE, off=FAKE,
+DISPATCH = dict(x=FAKE, idx=FAKE, N=32768, H=64, E=4, k=2, cf=0.0, dtype=BF16, xs=FAKE, off=FAKE,
                 row_entry=FAKE, entry_row=FAKE, ws=FAKE, ws_bytes=0)
 DISPATCH_BWD = dict(dxs=FAKE, entry_row=FAKE, N=8, H=64, k=2, dtype=BF16, dx=None)
 COMBINE = dict(ys=FAKE, entry_row=FAKE, alpha=FAKE, residual=None, N=8, H=64, k=2, dtype=BF16,
@@ -69,8 +69,9 @@ def test_rows_refusals(name):
             assert call(name, base, **over) == B.ERR_BAD_SHAPE, over
         for cf in (-1.0, NAN, INF):
             assert call(name, base, cf=cf) == B.ERR_BAD_ARG
-        need = tm.moe_dispatch_workspace_bytes(8, 4, 2)
-        assert call(name, base, ws_bytes=need - 1) == B.ERR_WORKSPACE_TOO_SMALL
+        need = tm.moe_dispatch_workspace_bytes(32768, 4, 2)
+        assert call(name, base, ws_bytes=64 * 4) == B.ERR_WORKSPACE_TOO_SMALL
+        assert call(name, base, ws=None) == B.ERR_NULL_ARG
         for p, off in (("x", 8), ("xs", 8), ("idx", 2), ("off", 1), ("entry_row", 2), ("ws", 64)):
             assert call(name, base, ws_bytes=need, **{p: FAKE + off}) == B.ERR_BAD_ARG, p
 

@@ -41,8 +41,11 @@ ROUTES = [  # N, H, E, k, capacity factor, share of padding tokens, one expert t
     (5, 24, 3, 3, 0.0, 0.4, False),
     (32, 768, 256, 8, 0.0, 0.0, False),
     (33, 40, 256, 256, 0.5, 0.1, False),
-    (128, 64, 8, 8, 1.0, 0.0, True),     # the last one-launch size
-    (129, 64, 8, 8, 1.0, 0.1, False),    # the first three-launch size
+    (128, 64, 8, 8, 1.0, 0.0, True),
+    (257, 4096, 8, 4, 1.0, 0.1, False),  # blocks of two tokens, the last of one
+    (16384, 8, 7, 2, 1.0, 0.1, False),   # the last one-launch size
+    (128, 16, 256, 256, 0.0, 0.0, False),
+    (16385, 8, 7, 2, 1.0, 0.1, False),   # the first with three launches
     (700, 104, 5, 2, 0.0, 0.0, False),
     (700, 104, 5, 2, 0.01, 0.3, True),
     (3001, 16, 64, 6, 1.25, 0.05, False),
@@ -478,7 +481,8 @@ def same(a, b):
                for x, y in zip(a, b))
 
 
-@pytest.mark.parametrize("N,H,E,k,dt", [(32, 256, 8, 2, "bf16"), (1500, 104, 16, 2, "fp32")])
+@pytest.mark.parametrize("N,H,E,k,dt", [(32, 256, 8, 2, "bf16"), (1500, 104, 16, 2, "fp32"),
+                                           (16500, 40, 16, 2, "bf16")])
 def test_deterministic_streams_and_graph(env, N, H, E, k, dt):
     dev, tm = env
     announce(f"block pass N={N} H={H} {dt}: again, another stream, captured")
@@ -517,7 +521,7 @@ def test_deterministic_streams_and_graph(env, N, H, E, k, dt):
 
 def test_stage_events(env):
     dev, tm = env
-    for N in (16, 4000):  # one launch, three launches
+    for N in (16, 40000):  # one launch, three launches
         x, idx = rnd(1, N, 64).to(dev), route(1, N, 4, 1, 0.0, False).to(dev)
         ev = tm.StageEvents(tm.DISPATCH_STAGES)
         o = tm.moe_dispatch_fwd(x, idx, 4, stage_events=ev)

@@ -46,7 +46,8 @@ def __getattr__(name):
                 "MoeRows", "CombineGrads", "PrenormOutput", "PrenormGrads", "PostnormOutput",
                 "PostnormGrads", "SwigluAct8", "SwigluAct8Grads"):
         from . import block
-        return getattr(block, name)
+        globals()[name] = v = getattr(block, name)  # found without this function from now on
+        return v
     if name in ("swiglu_ffn", "moe_ffn", "moe_dispatch", "moe_combine", "block_prenorm",
                 "block_postnorm", "swiglu_act8"):
         from . import autograd

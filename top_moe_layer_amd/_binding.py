@@ -35,6 +35,7 @@ MOE_BWD_STAGES = 12
 DISPATCH_STAGES = 2
 NORM_BWD_STAGES = 2
 DISPATCH_MAX_EXPERTS = 256
+DISPATCH_ONE = 32768
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 ACT8_GROUP = 32
 

@@ -133,18 +133,20 @@ def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
         raise ValueError("topk_idx must be a [N, k] tensor")
     k = topk_idx.shape[1]
     _is(topk_idx, "topk_idx", (N, k), torch.int32, dev)
-    nbytes = moe_dispatch_workspace_bytes(N, E, k)
-    wp, wn, ws = _scratch(nbytes, "moe_dispatch_fwd", dev, workspace)
+    wp = wn = ws = None
+    if workspace is not None or N * k > B.DISPATCH_ONE:
+        nbytes = moe_dispatch_workspace_bytes(N, E, k)
+        wp, wn, ws = _scratch(nbytes, "moe_dispatch_fwd", dev, workspace)
     if xs is None:
         xs = _empty((N * k, H), dtype=dt, device=dev)
     else:
         _is(xs, "xs", (N * k, H), dt, dev)
-    offsets = _empty(E + 1, dtype=torch.int32, device=dev)
+    offsets = _empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
     row_entry = _empty(N * k, dtype=torch.int32, device=dev)
-    entry_row = _empty((N, k), dtype=torch.int32, device=dev)
+    entry_row = torch.empty_like(topk_idx)
     _call("moe_dispatch_fwd", dev, stage_events, x.data_ptr(), topk_idx.data_ptr(), N, H, E, k,
           float(capacity_factor), code, xs.data_ptr(), offsets.data_ptr(), row_entry.data_ptr(),
-          entry_row.data_ptr(), wp, wn)
+          entry_row.data_ptr(), wp, wn or 0)
     return MoeRows(xs, offsets, row_entry, entry_row)
 
 
@@ -213,8 +215,7 @@ def moe_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, entry_row: torch.Tensor,
     code = _code(dt)
     _is(dy, "dy", (N, H), dt, dev)
     _is(alpha, "alpha", (N, k), torch.float32, dev)
-    dys = _empty((N * k, H), dtype=dt, device=dev)
-    dalpha = _empty((N, k), dtype=torch.float32, device=dev)
+    dys, dalpha = torch.empty_like(ys), torch.empty_like(alpha)
     _call("moe_combine_bwd", dev, stage_events, dy.data_ptr(), ys.data_ptr(), entry_row.data_ptr(),
           alpha.data_ptr(), N, H, k, code, dys.data_ptr(), dalpha.data_ptr())
     return CombineGrads(dys, dalpha)
@@ -262,7 +263,7 @@ def block_prenorm_fwd(x: torch.Tensor, w: torch.Tensor, *, eps: float = 1e-5,
     N, H = _rows(x, "x")
     _is(w, "w", (H,), dt, dev)
     if n is None:
-        n = _empty(x.shape, dtype=dt, device=dev)
+        n = torch.empty_like(x)
     else:
         _is(n, "n", x.shape, dt, dev)
     rstd = _empty(N, dtype=torch.float32, device=dev)
@@ -289,8 +290,7 @@ def block_prenorm_bwd(dn: torch.Tensor, x: torch.Tensor, w: torch.Tensor, rstd: 
         _is(dresidual, "dresidual", x.shape, dt, dev)
     nbytes = block_norm_bwd_workspace_bytes(N, H)
     wp, wn, ws = _scratch(nbytes, "block_prenorm_bwd", dev, workspace)
-    dx = _empty(x.shape, dtype=dt, device=dev)
-    dw = _empty(H, dtype=dt, device=dev)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
     _call("block_prenorm_bwd", dev, stage_events, dn.data_ptr(), x.data_ptr(), w.data_ptr(),
           rstd.data_ptr(), _ptr(dresidual), N, H, code, dx.data_ptr(), dw.data_ptr(), wp, wn)
     return PrenormGrads(dx, dw)
@@ -336,14 +336,14 @@ def block_postnorm_fwd(y: torch.Tensor, residual: torch.Tensor, w: Optional[torc
         _is(next_w, "next_w", (H,), dt, dev)
     mode, gate_rows = _gate(gate, N, H, dt, dev)
     if out is None:
-        out = _empty(y.shape, dtype=dt, device=dev)
+        out = torch.empty_like(y)
     else:
         _is(out, "out", y.shape, dt, dev)
     rstd = n = next_rstd = None
     if w is not None:
         rstd = _empty(N, dtype=torch.float32, device=dev)
     if next_w is not None:
-        n = _empty(y.shape, dtype=dt, device=dev)
+        n = torch.empty_like(y)
         next_rstd = _empty(N, dtype=torch.float32, device=dev)
     _call("block_postnorm_fwd", dev, stage_events, y.data_ptr(), residual.data_ptr(), _ptr(w),
           _ptr(gate), _ptr(next_w), N, H, mode, gate_rows, float(residual_scale), float(eps), code,
@@ -379,11 +379,11 @@ def block_postnorm_bwd(dout: torch.Tensor, y: torch.Tensor,
     mode, gate_rows = _gate(gate, N, H, dt, dev)
     nbytes = block_norm_bwd_workspace_bytes(N, H, gate_rows)
     wp, wn, ws = _scratch(nbytes, "block_postnorm_bwd", dev, workspace)
-    dy = _empty(y.shape, dtype=dt, device=dev)
-    dresidual = _empty(y.shape, dtype=dt, device=dev)
-    dw = _empty(H, dtype=dt, device=dev) if w is not None else None
-    dnext_w = _empty(H, dtype=dt, device=dev) if next_w is not None else None
-    dgate = _empty(gate.shape, dtype=dt, device=dev) if gate is not None else None
+    new = torch.empty_like
+    dy, dresidual = new(y), new(y)
+    dw = new(w) if w is not None else None
+    dnext_w = new(next_w) if next_w is not None else None
+    dgate = new(gate) if gate is not None else None
     _call("block_postnorm_bwd", dev, stage_events, dout.data_ptr(), _ptr(dn), y.data_ptr(),
           _ptr(out), _ptr(w), _ptr(gate), _ptr(next_w), _ptr(rstd), _ptr(next_rstd), N, H, mode,
           gate_rows, float(residual_scale), code, dy.data_ptr(), dresidual.data_ptr(), _ptr(dw),
@@ -517,7 +517,7 @@ def swiglu_act8_bwd(dh: torch.Tensor, g8: Act8, u8: Act8, *, with_h: bool = True
         dg, du = dgu[:, :C], dgu[:, C:]
     lddg = _pitched(dg, "dg", (R, C), dt, dev)
     lddu = _pitched(du, "du", (R, C), dt, dev)
-    h = _empty((R, C), dtype=dt, device=dev) if with_h else None
+    h = torch.empty_like(dh) if with_h else None
     _call("swiglu_act8_bwd", dev, stage_events, g8.q.data_ptr(), g8.scale.data_ptr(),
           u8.q.data_ptr(), u8.scale.data_ptr(), dh.data_ptr(), R, C, code, dg.data_ptr(), lddg,
           du.data_ptr(), lddu, _ptr(h))

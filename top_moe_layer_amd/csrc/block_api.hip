@@ -12,6 +12,7 @@
 using namespace topmoe;
 
 static_assert(kDispatchMaxExperts == TOPMOE_DISPATCH_MAX_EXPERTS, "expert limit");
+static_assert(kDispatchOne == TOPMOE_DISPATCH_ONE, "one-launch limit");
 static_assert(kAct8Group == TOPMOE_ACT8_GROUP, "scale group");
 static_assert(kGateNone == TOPMOE_GATE_NONE && kGateChannel == TOPMOE_GATE_CHANNEL &&
                   kGateToken == TOPMOE_GATE_TOKEN,
@@ -83,12 +84,12 @@ int moe_dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t 
   if (E < 1 || E > kDispatchMaxExperts || k > E) return TOPMOE_ERR_BAD_SHAPE;
   const int status = rows_shape(N, H, k);
   if (status != TOPMOE_OK) return status;
-  if (!expert_offsets || !workspace ||
+  const size_t need = plan_dispatch(N * k, E).bytes;
+  if (!expert_offsets || (need > 0 && !workspace) ||
       (N > 0 && (!x || !topk_idx || !xs || !row_entry || !entry_row)))
     return TOPMOE_ERR_NULL_ARG;
   if (!nonneg_finite(capacity_factor)) return TOPMOE_ERR_BAD_ARG;
-  if (workspace_bytes < moe_dispatch_workspace_bytes(N, E, k))
-    return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && workspace_bytes < need) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(topk_idx, 4) || !aligned(expert_offsets, 4) ||
       !aligned(row_entry, 4) || !aligned(entry_row, 4) || !aligned(workspace, 256))
     return TOPMOE_ERR_BAD_ARG;

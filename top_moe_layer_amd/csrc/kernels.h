@@ -212,16 +212,17 @@ hipError_t launch_dwr(const void* x, const float* dr, int64_t N, int H, int E, i
 // ---- rows by expert and back (rows.hip)
 constexpr int kDispatchMaxExperts = 256;
 // Most entries (N * k) of the one-launch dispatch.
-constexpr int kDispatchSmall = 1024;
-// Chunks of entries counted by one block each (none for small calls) and the
-// bytes of their counts [nchunk, E + 1].
+constexpr int kDispatchOne = 32768;
+// Chunks of entries counted by one block each (none in the one-launch
+// dispatch) and the bytes of their counts [nchunk, E + 1].
 struct DispatchPlan {
   int chunk = 0, nchunk = 0;
   size_t bytes = 0;
 };
 DispatchPlan plan_dispatch(int64_t n, int E);
 // cap: entries an expert keeps (INT32_MAX: all).  `rows` is the stage that
-// finds the rows (empty for small calls), `copy` the one that moves them.
+// finds the rows (empty in the one-launch dispatch), `copy` the one that moves
+// them.
 hipError_t launch_dispatch_rows(const void* x, const int32_t* idx, int64_t N, int H, int E, int k,
                                 int cap, int dtype, void* xs, int32_t* offsets,
                                 int32_t* row_entry, int32_t* entry_row, int32_t* part,

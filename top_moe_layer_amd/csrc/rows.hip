@@ -25,6 +25,9 @@ namespace topmoe {
 
 namespace {
 
+// Words of a histogram's copies: 32 of them up to 71 experts, 8 at 256.
+constexpr int kDispatchHist = 32 * 72;
+
 __device__ __forceinline__ int bucket_of(int e, int E) { return e >= 0 && e < E ? e : E; }
 
 // Offsets of the kept rows and of the rows behind them, from the buckets'
@@ -53,6 +56,16 @@ __device__ __forceinline__ int row_of(int b, int r, int E, int cap, const int* t
                                       const int* off, const int* tail) {
   const int lim = b >= E ? 0 : (cap < tot[b] ? cap : tot[b]);
   return r < lim ? off[b] + r : -1 - (tail[b] + r - lim);
+}
+
+// The lanes with the same bucket (of the valid ones), by one ballot per bit of it.
+__device__ __forceinline__ uint64_t same_bucket(int b, bool valid, int bits) {
+  uint64_t peers = __ballot(valid);
+  for (int s = 0; s < bits; ++s) {
+    const uint64_t m = __ballot((b >> s) & 1);
+    peers &= ((b >> s) & 1) ? m : ~m;
+  }
+  return peers;
 }
 
 // ---- large calls: counts per chunk of entries, rows, then the copy ---------
@@ -129,11 +142,7 @@ __global__ __launch_bounds__(256) void dispatch_place_kernel(
     const int64_t i = base + lane;
     const bool valid = i < w1;
     const int b = valid ? bucket_of(idx[i], E) : 0;
-    uint64_t peers = __ballot(valid);
-    for (int s = 0; s < bits; ++s) {
-      const uint64_t m = __ballot((b >> s) & 1);
-      peers &= ((b >> s) & 1) ? m : ~m;
-    }
+    const uint64_t peers = same_bucket(b, valid, bits);
     if (valid) {
       const int r = row_of(b, run[wave][b] + __popcll(peers & lt_mask), E, cap, tot, off, tail);
       entry_row[i] = r;
@@ -165,51 +174,96 @@ __global__ __launch_bounds__(256) void dispatch_copy_kernel(const T* __restrict_
   }
 }
 
-// ---- small calls: one launch, one block per token --------------------------
-// Every block counts all n entries itself (n * 4 bytes, from L2) and finds its
-// own entries' ranks by comparing, so no block waits for another.
-template <typename T>
-__global__ __launch_bounds__(256) void dispatch_small_kernel(
-    const T* __restrict__ x, const int32_t* __restrict__ idx, int n, int hv, int H, int E, int k,
-    int cap, T* __restrict__ xs, int32_t* __restrict__ offsets, int32_t* __restrict__ row_entry,
+// ---- up to kDispatchOne entries: one launch ----------------------------------
+// Every block counts all n entries itself (n * 4 bytes, from L2) and so knows
+// its own entries' rows without waiting for another block.  Counts go to one
+// of `copies` histograms by lane (up to 32, as many as the space holds), so
+// that the lanes of a wavefront that meet the same expert seldom add to the
+// same word.  The first pieces of the block's own tokens are loaded before the
+// counting.
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void dispatch_one_kernel(
+    const T* __restrict__ x, const int32_t* __restrict__ idx, int n, int N, int tb, int hv, int H,
+    int E, int k, int bits, int copies, int cap, T* __restrict__ xs,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ row_entry,
     int32_t* __restrict__ entry_row) {
-  __shared__ int tot[kDispatchMaxExperts + 1], off[kDispatchMaxExperts + 1];
-  __shared__ int tail[kDispatchMaxExperts + 1];
-  __shared__ int rank[kDispatchMaxExperts];  // k <= E
+  constexpr int kPre = 6, kIn = 16;  // pieces and entries in flight per thread
+  __shared__ int hist[2][kDispatchHist];  // [copies][B]: entries before the block's, from it on
+  __shared__ int tot[kDispatchMaxExperts + 1], run[kDispatchMaxExperts + 1];
+  __shared__ int off[kDispatchMaxExperts + 1], tail[kDispatchMaxExperts + 1];
+  __shared__ int rows[kDispatchOne / 256 + kDispatchMaxExperts];  // tb * k <= n / 256 + k
   const int tid = threadIdx.x, lane = tid & 63;
-  const int t = blockIdx.x, e0 = t * k;
-  for (int b = tid; b <= E; b += 256) tot[b] = 0;
-  for (int j = tid; j < k; j += 256) rank[j] = 0;
+  const int B = E + 1;
+  const int t0 = blockIdx.x * tb, t1 = t0 + tb < N ? t0 + tb : N;
+  const int e0 = t0 * k, e1 = t1 * k;
+  const int pieces = (t1 - t0) * hv;
+  const T* xb = x + int64_t(t0) * H;
+  Raw8<T> pre[kPre];
+#pragma unroll
+  for (int u = 0; u < kPre; ++u) {  // a block's rows are consecutive: piece p is at 8 p
+    const int p = tid + u * NT;
+    pre[u] = p < pieces ? load_raw8<T>(xb + int64_t(p) * 8) : zero_raw8<T>();
+  }
+  for (int i = tid; i < copies * B; i += NT) hist[0][i] = hist[1][i] = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += 256) {
-    const int b = bucket_of(idx[i], E);
-    atomicAdd(&tot[b], 1);
-    for (int j = 0; j < k; ++j)
-      if (i < e0 + j && b == bucket_of(idx[e0 + j], E)) atomicAdd(&rank[j], 1);
+  const int mine = (lane & (copies - 1)) * B;
+  for (int i0 = tid; i0 < n; i0 += NT * kIn) {
+    int e[kIn];
+#pragma unroll
+    for (int u = 0; u < kIn; ++u) e[u] = i0 + u * NT < n ? idx[i0 + u * NT] : 0;
+#pragma unroll
+    for (int u = 0; u < kIn; ++u) {
+      const int i = i0 + u * NT;
+      if (i < n) atomicAdd(&hist[i < e0 ? 0 : 1][mine + bucket_of(e[u], E)], 1);
+    }
+  }
+  __syncthreads();
+  for (int b = tid; b < B; b += NT) {
+    int before = 0, after = 0;
+    for (int c = 0; c < copies; ++c) {
+      before += hist[0][c * B + b];
+      after += hist[1][c * B + b];
+    }
+    run[b] = before;
+    tot[b] = before + after;
   }
   __syncthreads();
   if (tid < 64) {
     scan_buckets(tot, E, cap, off, tail, lane);
-    if (t == 0)
+    if (blockIdx.x == 0)
       for (int b = lane; b <= E; b += 64) offsets[b] = off[b];
+    __builtin_amdgcn_wave_barrier();
+    const uint64_t lt_mask = lane == 0 ? 0ull : (~0ull >> (64 - lane));
+    for (int base = e0; base < e1; base += 64) {
+      const int i = base + lane;
+      const bool valid = i < e1;
+      const int b = valid ? bucket_of(idx[i], E) : 0;
+      const uint64_t peers = same_bucket(b, valid, bits);
+      if (valid) {
+        const int r = row_of(b, run[b] + __popcll(peers & lt_mask), E, cap, tot, off, tail);
+        rows[i - e0] = r;
+        entry_row[i] = r;
+        row_entry[r < 0 ? -1 - r : r] = r < 0 ? -1 : i;
+      }
+      __builtin_amdgcn_wave_barrier();
+      if (valid && (peers & lt_mask) == 0ull) run[b] += __popcll(peers);
+      __builtin_amdgcn_wave_barrier();
+    }
   }
   __syncthreads();
-  for (int j = tid; j < k; j += 256) {
-    const int r = row_of(bucket_of(idx[e0 + j], E), rank[j], E, cap, tot, off, tail);
-    rank[j] = r;
-    entry_row[e0 + j] = r;
-    row_entry[r < 0 ? -1 - r : r] = r < 0 ? -1 : e0 + j;
-  }
-  __syncthreads();
-  for (int p = tid; p < hv; p += 256) {
-    const int64_t h = int64_t(p) * 8;
-    const Raw8<T> v = load_raw8<T>(x + int64_t(t) * H + h);
+  auto put = [&](int p, const Raw8<T>& v) {
+    const int t = p / hv;
+    const int64_t h = int64_t(p - t * hv) * 8;
     for (int j = 0; j < k; ++j) {
-      const int r = rank[j];
+      const int r = rows[t * k + j];
       if (r >= 0) store_raw8<T>(xs + int64_t(r) * H + h, v);
       else store_raw8<T>(xs + int64_t(-1 - r) * H + h, zero_raw8<T>());
     }
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kPre; ++u)
+    if (tid + u * NT < pieces) put(tid + u * NT, pre[u]);
+  for (int p = tid + kPre * NT; p < pieces; p += NT) put(p, load_raw8<T>(xb + int64_t(p) * 8));
 }
 
 __global__ void dispatch_empty_kernel(int E, int32_t* offsets) {
@@ -322,12 +376,20 @@ hipError_t for_slabs(int64_t N, int64_t slab, const Launch& L, F launch) {
 }
 
 template <typename T>
-hipError_t dispatch_small(const void* x, const int32_t* idx, int64_t N, int H, int E, int k,
-                          int cap, void* xs, int32_t* offsets, int32_t* row_entry,
-                          int32_t* entry_row, const Launch& s) {
-  return launch_kernel(dispatch_small_kernel<T>, dim3(unsigned(N)), dim3(256), 0, s,
-                       static_cast<const T*>(x), idx, int(N * k), H / 8, H, E, k, cap,
-                       static_cast<T*>(xs), offsets, row_entry, entry_row);
+hipError_t dispatch_one(const void* x, const int32_t* idx, int64_t N, int H, int E, int k,
+                        int bits, int cap, void* xs, int32_t* offsets, int32_t* row_entry,
+                        int32_t* entry_row, const Launch& s) {
+  const int tb = int((N + 255) / 256);
+  int copies = 32;
+  while (copies * (E + 1) > kDispatchHist) copies /= 2;
+  const dim3 grid(unsigned((N + tb - 1) / tb));
+#define TOPMOE_LAUNCH_ONE(NT)                                                               \
+  return launch_kernel(dispatch_one_kernel<T, NT>, grid, dim3(NT), 0, s,                      \
+                       static_cast<const T*>(x), idx, int(N * k), int(N), tb, H / 8, H, E, k, \
+                       bits, copies, cap, static_cast<T*>(xs), offsets, row_entry, entry_row)
+  if (N * k <= 1024) TOPMOE_LAUNCH_ONE(256);
+  TOPMOE_LAUNCH_ONE(1024);
+#undef TOPMOE_LAUNCH_ONE
 }
 
 template <typename T>
@@ -372,7 +434,7 @@ hipError_t combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
 
 DispatchPlan plan_dispatch(int64_t n, int E) {
   DispatchPlan p;
-  if (n <= kDispatchSmall) return p;
+  if (n <= kDispatchOne) return p;
   int64_t c = (n + 255) / 256;           // at most 256 chunks
   c = (c + 255) / 256 * 256;
   p.chunk = c < 1024 ? 1024 : int(c);
@@ -389,13 +451,13 @@ hipError_t launch_dispatch_rows(const void* x, const int32_t* idx, int64_t N, in
   const DispatchPlan p = plan_dispatch(n, E);
   const bool f32 = dtype == TOPMOE_DTYPE_FP32;
   if (n == 0) return launch_kernel(dispatch_empty_kernel, dim3(1), dim3(256), 0, rows, E, offsets);
-  if (p.nchunk == 0)
-    return f32 ? dispatch_small<float>(x, idx, N, H, E, k, cap, xs, offsets, row_entry, entry_row,
-                                       copy)
-               : dispatch_small<bf16_t>(x, idx, N, H, E, k, cap, xs, offsets, row_entry,
-                                        entry_row, copy);
   int bits = 0;
   while ((E >> bits) != 0) ++bits;
+  if (p.nchunk == 0)
+    return f32 ? dispatch_one<float>(x, idx, N, H, E, k, bits, cap, xs, offsets, row_entry,
+                                     entry_row, copy)
+               : dispatch_one<bf16_t>(x, idx, N, H, E, k, bits, cap, xs, offsets, row_entry,
+                                      entry_row, copy);
   Launch first = rows, second = rows;
   first.stop = nullptr;
   second.start = nullptr;
