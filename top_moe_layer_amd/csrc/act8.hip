@@ -25,6 +25,8 @@ namespace topmoe {
 
 namespace {
 
+constexpr bool kNtLoad = true, kNtKeep = true;
+
 // Largest magnitude over the four lanes of a quad, as its fp32 bits (ordered
 // like the magnitudes).
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
@@ -80,13 +82,13 @@ __device__ __forceinline__ void unpack_q8(const uint32_t (&q)[2], float s, float
 
 __device__ __forceinline__ void load_q8(const uint8_t* p, uint32_t (&q)[2]) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+  const u32x2 v = load_vec<kNtLoad, u32x2>(p);
   q[0] = v.x;
   q[1] = v.y;
 }
 __device__ __forceinline__ void store_q8(uint8_t* p, const uint32_t (&q)[2]) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  *reinterpret_cast<u32x2*>(p) = u32x2{q[0], q[1]};
+  store_vec<kNtKeep, u32x2>(p, u32x2{q[0], q[1]});
 }
 
 __device__ __forceinline__ float sigmoid(float g) {
@@ -113,7 +115,7 @@ __device__ __forceinline__ Place place(int64_t r0, uint32_t pieces, uint32_t pp,
 
 template <typename T>
 __device__ __forceinline__ void load_or_zero(const T* p, bool in, float (&v)[8]) {
-  const Raw8<T> raw = in ? load_raw8<T>(p) : zero_raw8<T>();
+  const Raw8<T> raw = in ? load_raw8<T, kNtLoad>(p) : zero_raw8<T>();
   unpack8(raw, v);
 }
 
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const T* __restrict__ x,
   if (a.any && (a.p & 3) == 0) scale[a.r * (pp / 4) + a.p / 4] = uint8_t(s);
 }
 
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* __restrict__ q,
                                                           const uint8_t* __restrict__ scale,
                                                           int64_t r0, uint32_t pieces,
@@ -143,10 +145,10 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* __restr
   load_q8(q + a.r * C + a.p * 8, b);
   float v[8];
   unpack_q8(b, scale_of(scale[a.r * (pp / 4) + a.p / 4]), v);
-  store8<T>(x + a.r * ldx + a.p * 8, v);
+  store8<T, NT>(x + a.r * ldx + a.p * 8, v);
 }
 
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void swiglu_act8_fwd_kernel(
     const T* __restrict__ g, const T* __restrict__ u, int64_t ldg, int64_t ldu, int64_t r0,
     uint32_t pieces, uint32_t pp, int C, T* __restrict__ h, uint8_t* __restrict__ gq, uint8_t* __restrict__ gs,
@@ -161,7 +163,7 @@ __global__ __launch_bounds__(256) void swiglu_act8_fwd_kernel(
   if (a.in) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) vh[i] = silu_mul(vg[i], vu[i]);
-    store8<T>(h + o, vh);
+    store8<T, NT>(h + o, vh);
     store_q8(gq + o, bg);
     store_q8(uq + o, bu);
   }
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(256) void swiglu_act8_fwd_kernel(
   }
 }
 
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void swiglu_act8_bwd_kernel(
     const uint8_t* __restrict__ gq, const uint8_t* __restrict__ gs,
     const uint8_t* __restrict__ uq, const uint8_t* __restrict__ us, const T* __restrict__ dh,
@@ -185,7 +187,7 @@ __global__ __launch_bounds__(256) void swiglu_act8_bwd_kernel(
   load_q8(gq + o, bg);
   load_q8(uq + o, bu);
   float vg[8], vu[8], vd[8];
-  const Raw8<T> raw = load_raw8<T>(dh + o);
+  const Raw8<T> raw = load_raw8<T, kNtLoad>(dh + o);
   unpack_q8(bg, scale_of(gs[si]), vg);
   unpack_q8(bu, scale_of(us[si]), vu);
   unpack8(raw, vd);
@@ -197,9 +199,9 @@ __global__ __launch_bounds__(256) void swiglu_act8_bwd_kernel(
     oh[i] = gsig * vu[i];
     og[i] = vd[i] * vu[i] * (s * (1.0f + vg[i] * (1.0f - s)));
   }
-  store8<T>(dg + a.r * ldg + a.p * 8, og);
-  store8<T>(du + a.r * ldu + a.p * 8, ou);
-  if (h != nullptr) store8<T>(h + o, oh);
+  store8<T, NT>(dg + a.r * ldg + a.p * 8, og);
+  store8<T, NT>(du + a.r * ldu + a.p * 8, ou);
+  if (h != nullptr) store8<T, NT>(h + o, oh);
 }
 
 // Launches over slabs of rows of at most 2^30 pieces, so that piece numbers
@@ -224,56 +226,77 @@ hipError_t for_slabs(int64_t R, int64_t C, const Launch& s, F launch) {
 
 }  // namespace
 
-#define TOPMOE_ACT8(T, KERNEL, ...)                                                          \
+#define TOPMOE_ACT8(KERNEL, ...)                                                                 \
   for_slabs(R, C, s, [&](dim3 grid, int64_t r0, uint32_t pieces, uint32_t pp, const Launch& L) { \
-    return launch_kernel(KERNEL<T>, grid, dim3(256), 0, L, __VA_ARGS__);                        \
+    return launch_kernel(KERNEL, grid, dim3(256), 0, L, __VA_ARGS__);                            \
   })
+// KERNEL<T, NT> by the outputs' bytes.
+#define TOPMOE_ACT8_NT(T, KERNEL, BYTES, ...)                     \
+  return (BYTES) > kNtBytes ? TOPMOE_ACT8((KERNEL<T, true>), __VA_ARGS__)  \
+                            : TOPMOE_ACT8((KERNEL<T, false>), __VA_ARGS__)
+
+namespace {
+
+template <typename T>
+hipError_t unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C, void* x,
+                  int64_t ldx, const Launch& s) {
+  TOPMOE_ACT8_NT(T, act8_unpack_kernel, R * C * int64_t(sizeof(T)), q, scale, r0, pieces, pp,
+                 int(C), static_cast<T*>(x), ldx);
+}
+
+template <typename T>
+hipError_t swiglu_fwd(const void* g, int64_t ldg, const void* u, int64_t ldu, int64_t R,
+                      int64_t C, void* h, uint8_t* gq, uint8_t* gs, uint8_t* uq, uint8_t* us,
+                      const Launch& s) {
+  TOPMOE_ACT8_NT(T, swiglu_act8_fwd_kernel, R * C * int64_t(sizeof(T)),
+                 static_cast<const T*>(g), static_cast<const T*>(u), ldg, ldu, r0, pieces, pp,
+                 int(C), static_cast<T*>(h), gq, gs, uq, us);
+}
+
+template <typename T>
+hipError_t swiglu_bwd(const uint8_t* gq, const uint8_t* gs, const uint8_t* uq, const uint8_t* us,
+                      const void* dh, int64_t R, int64_t C, void* dg, int64_t ldg, void* du,
+                      int64_t ldu, void* h, const Launch& s) {
+  TOPMOE_ACT8_NT(T, swiglu_act8_bwd_kernel, R * C * int64_t(sizeof(T)) * (h != nullptr ? 3 : 2),
+                 gq, gs, uq, us, static_cast<const T*>(dh), r0, pieces, pp, int(C),
+                 static_cast<T*>(dg), ldg, static_cast<T*>(du), ldu, static_cast<T*>(h));
+}
+
+}  // namespace
 
 hipError_t launch_act8_pack(const void* x, int64_t ldx, int64_t R, int64_t C, int dtype,
                             uint8_t* q, uint8_t* scale, const Launch& s) {
   if (dtype == TOPMOE_DTYPE_FP32)
-    return TOPMOE_ACT8(float, act8_pack_kernel, static_cast<const float*>(x), ldx, r0, pieces, pp,
+    return TOPMOE_ACT8(act8_pack_kernel<float>, static_cast<const float*>(x), ldx, r0, pieces, pp,
                        int(C), q, scale);
-  return TOPMOE_ACT8(bf16_t, act8_pack_kernel, static_cast<const bf16_t*>(x), ldx, r0, pieces, pp,
+  return TOPMOE_ACT8(act8_pack_kernel<bf16_t>, static_cast<const bf16_t*>(x), ldx, r0, pieces, pp,
                      int(C), q, scale);
 }
 
 hipError_t launch_act8_unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C,
                               int dtype, void* x, int64_t ldx, const Launch& s) {
-  if (dtype == TOPMOE_DTYPE_FP32)
-    return TOPMOE_ACT8(float, act8_unpack_kernel, q, scale, r0, pieces, pp, int(C),
-                       static_cast<float*>(x), ldx);
-  return TOPMOE_ACT8(bf16_t, act8_unpack_kernel, q, scale, r0, pieces, pp, int(C),
-                     static_cast<bf16_t*>(x), ldx);
+  return dtype == TOPMOE_DTYPE_FP32 ? unpack<float>(q, scale, R, C, x, ldx, s)
+                                    : unpack<bf16_t>(q, scale, R, C, x, ldx, s);
 }
 
 hipError_t launch_swiglu_act8_fwd(const void* g, int64_t ldg, const void* u, int64_t ldu,
-                                  int64_t R, int64_t C, int dtype, void* h, uint8_t* gq, uint8_t* gs, uint8_t* uq,
-                                  uint8_t* us, const Launch& s) {
-  if (dtype == TOPMOE_DTYPE_FP32)
-    return TOPMOE_ACT8(float, swiglu_act8_fwd_kernel, static_cast<const float*>(g),
-                       static_cast<const float*>(u), ldg, ldu, r0, pieces, pp, int(C),
-                       static_cast<float*>(h), gq, gs, uq, us);
-  return TOPMOE_ACT8(bf16_t, swiglu_act8_fwd_kernel, static_cast<const bf16_t*>(g),
-                     static_cast<const bf16_t*>(u), ldg, ldu, r0, pieces, pp, int(C),
-                     static_cast<bf16_t*>(h), gq, gs, uq, us);
+                                  int64_t R, int64_t C, int dtype, void* h, uint8_t* gq,
+                                  uint8_t* gs, uint8_t* uq, uint8_t* us, const Launch& s) {
+  return dtype == TOPMOE_DTYPE_FP32
+             ? swiglu_fwd<float>(g, ldg, u, ldu, R, C, h, gq, gs, uq, us, s)
+             : swiglu_fwd<bf16_t>(g, ldg, u, ldu, R, C, h, gq, gs, uq, us, s);
 }
 
 hipError_t launch_swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gs, const uint8_t* uq,
                                   const uint8_t* us, const void* dh, int64_t R, int64_t C,
                                   int dtype, void* dg, int64_t ldg, void* du, int64_t ldu, void* h,
                                   const Launch& s) {
-  if (dtype == TOPMOE_DTYPE_FP32)
-    return TOPMOE_ACT8(float, swiglu_act8_bwd_kernel, gq, gs, uq, us,
-                       static_cast<const float*>(dh), r0, pieces, pp, int(C),
-                       static_cast<float*>(dg), ldg, static_cast<float*>(du), ldu,
-                       static_cast<float*>(h));
-  return TOPMOE_ACT8(bf16_t, swiglu_act8_bwd_kernel, gq, gs, uq, us,
-                     static_cast<const bf16_t*>(dh), r0, pieces, pp, int(C),
-                     static_cast<bf16_t*>(dg), ldg, static_cast<bf16_t*>(du), ldu,
-                     static_cast<bf16_t*>(h));
+  return dtype == TOPMOE_DTYPE_FP32
+             ? swiglu_bwd<float>(gq, gs, uq, us, dh, R, C, dg, ldg, du, ldu, h, s)
+             : swiglu_bwd<bf16_t>(gq, gs, uq, us, dh, R, C, dg, ldg, du, ldu, h, s);
 }
 
 #undef TOPMOE_ACT8
+#undef TOPMOE_ACT8_NT
 
 }  // namespace topmoe

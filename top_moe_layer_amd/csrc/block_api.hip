@@ -57,7 +57,7 @@ int64_t span_of(int64_t N, int64_t gate_rows) {
 }
 
 size_t norm_bwd_bytes(const NormUnits& u, int64_t H) {
-  return align_up(size_t(2) * size_t(u.count) * size_t(H) * sizeof(float) + 1);
+  return align_up(size_t(2) * size_t(u.count / u.blocks_of) * size_t(H) * sizeof(float) + 1);
 }
 
 // ---- 8-bit activations
@@ -173,7 +173,7 @@ int block_prenorm_fwd(const void* x, const void* w, int64_t N, int64_t H, float 
 
 size_t block_norm_bwd_workspace_bytes(int64_t N, int64_t H, int64_t gate_rows) {
   if (norm_shape(N, H, gate_rows) != TOPMOE_OK) return 0;
-  return norm_bwd_bytes(plan_norm_units(N, gate_rows, span_of(N, gate_rows)), H);
+  return norm_bwd_bytes(plan_norm_units(N, H, gate_rows, span_of(N, gate_rows)), H);
 }
 
 int block_prenorm_bwd(const void* dn, const void* x, const void* w, const float* rstd,
@@ -186,7 +186,7 @@ int block_prenorm_bwd(const void* dn, const void* x, const void* w, const float*
   if (!w || !dw || !workspace || (N > 0 && (!dn || !x || !rstd || !dx))) return TOPMOE_ERR_NULL_ARG;
   NormBwd a{};
   a.gate_span = span_of(N, 1);
-  a.units = plan_norm_units(N, 1, a.gate_span);
+  a.units = plan_norm_units(N, H, 1, a.gate_span);
   if (workspace_bytes < norm_bwd_bytes(a.units, H)) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(dn, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(rstd, 4) ||
       !aligned(dresidual, 16) || !aligned(dx, 16) || !aligned(dw, 16) || !aligned(workspace, 256))
@@ -256,7 +256,7 @@ int block_postnorm_bwd(const void* dout, const void* dn, const void* y, const vo
   NormBwd a{};
   a.gate_rows = channel ? gate_rows : 1;
   a.gate_span = span_of(N, a.gate_rows);
-  a.units = plan_norm_units(N, a.gate_rows, a.gate_span);
+  a.units = plan_norm_units(N, H, a.gate_rows, a.gate_span);
   if (workspace_bytes < norm_bwd_bytes(a.units, H)) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(dout, 16) || !aligned(dn, 16) || !aligned(y, 16) || !aligned(out, 16) ||
       !aligned(w, 16) || !aligned(gate, channel ? 16 : 4) || !aligned(next_w, 16) ||
@@ -269,7 +269,7 @@ int block_postnorm_bwd(const void* dout, const void* dn, const void* y, const vo
   a.dy = dy; a.dresidual = dresidual; a.dw = w ? dw : nullptr; a.dgate = dgate; a.dnext_w = dnext_w;
   float* part = static_cast<float*>(workspace);
   a.part = w || channel ? part : nullptr;
-  a.part_next = part + size_t(a.units.count) * size_t(H);
+  a.part_next = part + size_t(a.units.count / a.units.blocks_of) * size_t(H);
   a.N = N; a.H = int(H); a.hv = int(H / 8); a.gate_mode = gate_mode; a.scale = residual_scale;
   const Stages st{stage_events, static_cast<hipStream_t>(stream)};
   const Launch rows = st.at(0), sums = st.at(1);

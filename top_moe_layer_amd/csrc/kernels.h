@@ -209,6 +209,10 @@ int dwr_chunks(int64_t N);
 hipError_t launch_dwr(const void* x, const float* dr, int64_t N, int H, int E, int dtype,
                       float* part, float* dWr, const Launch& s);
 
+// Outputs of more bytes than the Infinity Cache (256 MiB) holds are written
+// non-temporally: no reader would find them there.
+constexpr int64_t kNtBytes = int64_t(256) << 20;
+
 // ---- rows by expert and back (rows.hip)
 constexpr int kDispatchMaxExperts = 256;
 // Most entries (N * k) of the one-launch dispatch.
@@ -256,13 +260,14 @@ struct NormFwd {
 hipError_t launch_norm_fwd(const NormFwd& a, bool post, bool next, int dtype, const Launch& s);
 
 // Units of consecutive rows for the backward's column sums: pieces of one gate
-// group (per_group of them in each), or whole groups (per_group == 0).
-constexpr int kNormUnits = 1024;
+// group (per_group of them in each), or whole groups (per_group == 0); a block
+// takes blocks_of of them and writes one partial row.
 struct NormUnits {
-  int64_t rows = 0;   // rows of a unit (the last of a group may have fewer)
+  int64_t rows = 0;   // rows of a unit (a group's last may have fewer, or none)
   int64_t per_group = 0, count = 0;
+  int blocks_of = 1;
 };
-NormUnits plan_norm_units(int64_t N, int64_t gate_rows, int64_t gate_span);
+NormUnits plan_norm_units(int64_t N, int64_t H, int64_t gate_rows, int64_t gate_span);
 struct NormBwd {
   const void* dout;         // [N, H] or NULL: 0
   const void* dn;           // [N, H]
@@ -278,8 +283,8 @@ struct NormBwd {
   void* dw;                 // [H] or NULL
   void* dgate;              // channel: [gate_rows, H]; token: [N]
   void* dnext_w;            // [H]
-  float* part;              // [units, H], or NULL where neither dw nor dgate needs it
-  float* part_next;         // [units, H]
+  float* part;              // [blocks, H], or NULL where neither dw nor dgate needs it
+  float* part_next;         // [blocks, H]
   int64_t N, gate_rows, gate_span;
   NormUnits units;
   int H, hv, gate_mode, first_role;

@@ -12,9 +12,10 @@
 //   dy   = rstd_y * (b - yh * mean(b * yh))  (no norm: b)
 //   dw   = sum_t gate * dr * yh,   dgate = the sum of w * dr * yh over what shares the gate
 //
-// One block of W wavefronts per row (W = 1: one wavefront per row, four rows a
-// block): the row stays in registers between its statistics and its use, so
-// every tensor is read once and written once.  Bound by memory.
+// R threads per row, V pieces of 8 channels each: a block of R / 64 wavefronts,
+// or for narrow rows a wavefront or a part of one, 256 / R rows a block.  The
+// row stays in registers between its statistics and its use, so every tensor
+// is read once and written once.  Bound by memory.
 //
 // Column sums of the backward pass (dw, dgate, dw_next) are taken in two fixed
 // steps without atomics: each unit of consecutive rows sums its own rows in
@@ -33,13 +34,22 @@ namespace topmoe {
 
 namespace {
 
-// Sum over the W wavefronts of a row, in wavefront order.  `slot` (2 x W
-// floats of LDS) alternates between calls: a wavefront writing a slot again
-// has passed the barrier of the call in between, which every reader of the
-// slot's last use reached after reading it.
-template <int W>
+// Rows a block holds side by side, and wavefronts of a row.
+template <int R>
+constexpr int kSide = R <= 64 ? 256 / R : 1;
+template <int R>
+constexpr int kWaves = R <= 64 ? 1 : R / 64;
+template <int R>
+constexpr int kThreads = R <= 64 ? 256 : R;
+
+// Sum over a row's R threads, lanes as a butterfly and wavefronts in order.
+// `slot` (2 x W floats of LDS) alternates between calls: a wavefront writing a
+// slot again has passed the barrier of the call in between, which every reader
+// of the slot's last use reached after reading it.
+template <int R, int W = kWaves<R>>
 __device__ __forceinline__ float row_sum(float v, float (&slot)[2][W], int& turn, int wave) {
-  v = wave_sum(v);
+#pragma unroll
+  for (int o = R < 64 ? R / 2 : 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) slot[turn][wave] = v;
     __syncthreads();
@@ -58,19 +68,18 @@ __device__ __forceinline__ void load_f(const T* p, float (&v)[8]) {
 
 // POST: the norm after the block with gate and residual (else r = y = x).
 // NEXT: the norm before the next block.
-template <typename T, int W, int V, bool POST, bool NEXT>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_fwd_kernel(NormFwd a) {
-  __shared__ float slot[2][W];
-  const int lane = W == 1 ? int(threadIdx.x & 63) : int(threadIdx.x);
-  const int wave = int(threadIdx.x >> 6);
-  const int64_t t = a.t0 + (W == 1 ? int64_t(blockIdx.x) * 4 + wave : int64_t(blockIdx.x));
-  if (W == 1 && t >= a.N) return;
+template <typename T, int R, int V, bool POST, bool NEXT>
+__global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
+  __shared__ float slot[2][kWaves<R>];
+  const int lane = int(threadIdx.x) % R, wave = int(threadIdx.x >> 6);
+  const int64_t t = a.t0 + int64_t(blockIdx.x) * kSide<R> + int(threadIdx.x) / R;
+  if (kSide<R> > 1 && t >= a.N) return;
   int turn = 0;
   const T* y = static_cast<const T*>(a.y) + t * a.H;
   Raw8<T> yr[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int p = lane + v * 64 * W;
+    const int p = lane + v * R;
     yr[v] = p < a.hv ? load_raw8<T>(y + p * 8) : zero_raw8<T>();
   }
   const float inv_h = 1.0f / float(a.H);
@@ -80,7 +89,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_fwd_kernel(NormFwd
     const T* rp = static_cast<const T*>(a.residual) + t * a.H;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int p = lane + v * 64 * W;
+      const int p = lane + v * R;
       res[v] = p < a.hv ? load_raw8<T>(rp + p * 8) : zero_raw8<T>();
     }
     float rstd = 1.f;
@@ -93,7 +102,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_fwd_kernel(NormFwd
 #pragma unroll
         for (int c = 0; c < 8; ++c) s = fmaf(f[c], f[c], s);
       }
-      rstd = 1.0f / sqrtf(row_sum<W>(s, slot, turn, wave) * inv_h + a.eps);
+      rstd = 1.0f / sqrtf(row_sum<R>(s, slot, turn, wave) * inv_h + a.eps);
       if (lane == 0) a.rstd[t] = rstd;
     }
     float gt = 1.f;
@@ -103,7 +112,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_fwd_kernel(NormFwd
     T* out = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int p = lane + v * 64 * W;
+      const int p = lane + v * R;
       float f[8], q[8];
       unpack8(yr[v], f);
       unpack8(res[v], q);
@@ -141,12 +150,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_fwd_kernel(NormFwd
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int c = 0; c < 8; ++c) s = fmaf(rs[v][c], rs[v][c], s);
-    const float rstd = 1.0f / sqrtf(row_sum<W>(s, slot, turn, wave) * inv_h + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<R>(s, slot, turn, wave) * inv_h + a.eps);
     if (lane == 0) a.next_rstd[t] = rstd;
     T* n = static_cast<T*>(a.n) + t * a.H;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int p = lane + v * 64 * W;
+      const int p = lane + v * R;
       if (p >= a.hv) continue;
       float w[8];
       load_f<T>(static_cast<const T*>(a.next_w) + p * 8, w);
@@ -164,23 +173,23 @@ struct BwdRow {
   float rstd, next_rstd, gate;  // gate: of a token gate
 };
 
-template <typename T, int W, int V, bool POST, bool NEXT>
+template <typename T, int R, int V, bool POST, bool NEXT>
 __device__ __forceinline__ void load_row(const NormBwd& a, int64_t t, int lane,
                                          BwdRow<T, V, POST, NEXT>& r) {
   const int64_t row = t * a.H;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int p = lane + v * 64 * W;
+    const int p = lane + v * R;
     const bool in = p < a.hv;
     const int64_t at = row + p * 8;
     if constexpr (NEXT) {
-      r.out[v] = in ? load_raw8<T>(static_cast<const T*>(a.out) + at) : zero_raw8<T>();
-      r.dn[v] = in ? load_raw8<T>(static_cast<const T*>(a.dn) + at) : zero_raw8<T>();
+      r.out[v] = in ? load_raw8<T, true>(static_cast<const T*>(a.out) + at) : zero_raw8<T>();
+      r.dn[v] = in ? load_raw8<T, true>(static_cast<const T*>(a.dn) + at) : zero_raw8<T>();
     }
-    r.dout[v] = in && a.dout != nullptr ? load_raw8<T>(static_cast<const T*>(a.dout) + at)
+    r.dout[v] = in && a.dout != nullptr ? load_raw8<T, true>(static_cast<const T*>(a.dout) + at)
                                         : zero_raw8<T>();
     if constexpr (POST)
-      r.y[v] = in ? load_raw8<T>(static_cast<const T*>(a.y) + at) : zero_raw8<T>();
+      r.y[v] = in ? load_raw8<T, true>(static_cast<const T*>(a.y) + at) : zero_raw8<T>();
   }
   if constexpr (NEXT) r.next_rstd = a.next_rstd[t];
   if constexpr (POST) {
@@ -193,14 +202,17 @@ __device__ __forceinline__ void load_row(const NormBwd& a, int64_t t, int lane,
 // column sums in registers.  FLUSH: units of whole gate groups.  PRE: the
 // weights stay in registers, and the next row's loads are issued before a
 // row's sums, so that they run under its barriers; the widest rows have no
-// registers left for that and load what they need when they need it.
-template <typename T, int W, int V, bool POST, bool NEXT, bool FLUSH, bool PRE>
-__global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
-  __shared__ float slot[2][W];
-  const int lane = int(threadIdx.x), wave = int(threadIdx.x >> 6);
+// registers left for that and load what they need when they need it.  The units
+// side by side in a block of narrow rows add their sums to one partial row.
+template <typename T, int R, int V, bool POST, bool NEXT, bool FLUSH, bool PRE>
+__global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
+  constexpr int G = kSide<R>;
+  __shared__ float slot[2][kWaves<R>];
+  const int wave = int(threadIdx.x >> 6), side = int(threadIdx.x) / R;
+  const int lane = int(threadIdx.x) % R;
   int turn = 0;
   const float inv_h = 1.0f / float(a.H);
-  const int64_t unit = blockIdx.x;
+  const int64_t unit = int64_t(blockIdx.x) * G + side;
   int64_t r0, r1, group = 0;
   if constexpr (!FLUSH) {  // a piece of one gate group
     group = unit / a.units.per_group;
@@ -212,13 +224,14 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
     r1 = r0 + a.units.rows < a.N ? r0 + a.units.rows : a.N;
     group = r0 / a.gate_span;
   }
-  const T* cgate = POST && a.gate_mode == kGateChannel
+  const bool any = r0 < r1;  // a block's last units may have no rows
+  const T* cgate = POST && any && a.gate_mode == kGateChannel
                        ? static_cast<const T*>(a.gate) + group * a.H : nullptr;
   Raw8<T> w[V], nw[V], cg[V];  // PRE: post and next weight, the current group's gate
   auto hold = [&](Raw8<T>(&r)[V], const void* from) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int p = lane + v * 64 * W;
+      const int p = lane + v * R;
       r[v] = from != nullptr && p < a.hv ? load_raw8<T>(static_cast<const T*>(from) + p * 8)
                                          : zero_raw8<T>();
     }
@@ -245,12 +258,12 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
     }
 
   BwdRow<T, V, POST, NEXT> cur;
-  if constexpr (PRE) load_row<T, W>(a, r0, lane, cur);
+  if (PRE && any) load_row<T, R>(a, r0, lane, cur);
   int64_t left = FLUSH ? a.gate_span : 0;  // rows to the end of the group
   for (int64_t t = r0; t < r1; ++t) {
     BwdRow<T, V, POST, NEXT> nxt;
-    if constexpr (PRE) load_row<T, W>(a, t + 1 < r1 ? t + 1 : t, lane, nxt);
-    else load_row<T, W>(a, t, lane, cur);
+    if constexpr (PRE) load_row<T, R>(a, t + 1 < r1 ? t + 1 : t, lane, nxt);
+    else load_row<T, R>(a, t, lane, cur);
     float dr[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) unpack8(cur.dout[v], dr[v]);
@@ -261,7 +274,7 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
         float rh[8], av[8], wv[8];
         unpack8(cur.out[v], rh);
         unpack8(cur.dn[v], av);
-        held(nw[v], a.next_w, lane + v * 64 * W, wv);
+        held(nw[v], a.next_w, lane + v * R, wv);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           rh[c] *= cur.next_rstd;
@@ -269,13 +282,13 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
           s = fmaf(av[c] * wv[c], rh[c], s);
         }
       }
-      const float m = row_sum<W>(s, slot, turn, wave) * inv_h;
+      const float m = row_sum<R>(s, slot, turn, wave) * inv_h;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float rh[8], av[8], wv[8];
         unpack8(cur.out[v], rh);
         unpack8(cur.dn[v], av);
-        held(nw[v], a.next_w, lane + v * 64 * W, wv);
+        held(nw[v], a.next_w, lane + v * R, wv);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           dr[v][c] += cur.next_rstd * (av[c] * wv[c] - rh[c] * cur.next_rstd * m);
@@ -284,14 +297,14 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
     if constexpr (!POST) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int p = lane + v * 64 * W;
+        const int p = lane + v * R;
         if (p < a.hv) store8<T>(static_cast<T*>(a.dy) + t * a.H + p * 8, dr[v]);
       }
     } else {
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int p = lane + v * 64 * W;
+        const int p = lane + v * R;
         float q[8], yh[8], g[8];
         unpack8(cur.y[v], yh);
 #pragma unroll
@@ -316,7 +329,7 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
       }
       float m = 0.f;
       if (a.w != nullptr || a.gate_mode == kGateToken) {
-        s = row_sum<W>(s, slot, turn, wave);
+        s = row_sum<R>(s, slot, turn, wave);
         if (a.gate_mode == kGateToken && lane == 0)
           static_cast<T*>(a.dgate)[t] = from_f32<T>(s);
         m = a.w != nullptr ? s * inv_h : 0.f;
@@ -324,7 +337,7 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
       const float k = cur.gate * cur.rstd;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int p = lane + v * 64 * W;
+        const int p = lane + v * R;
         float yh[8];
         unpack8(cur.y[v], yh);
 #pragma unroll
@@ -335,7 +348,7 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
         if (--left == 0) {  // the group ends
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            const int p = lane + v * 64 * W;
+            const int p = lane + v * R;
             float g[8], q[8];
             held(cg[v], cgate, p, g);
             if (a.w != nullptr) held(w[v], a.w, p, q);
@@ -356,23 +369,43 @@ __global__ __launch_bounds__(64 * W) void norm_bwd_kernel(NormBwd a) {
     }
     if constexpr (PRE) cur = nxt;
   }
+  // One partial row per block: the units' sums added in order.
+  __shared__ float sums[G > 1 ? G - 1 : 1][G > 1 ? R * V * 8 : 1];
+  auto out = [&](float(&acc)[V][8], float* part) {
+    if constexpr (G > 1) {
+      __syncthreads();
+      if (side > 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int p = lane + v * 64 * W;
-    if (p >= a.hv) continue;
-    if constexpr (POST) {
-      if (a.part != nullptr) {
-        if constexpr (FLUSH) store8<float>(a.part + unit * a.H + p * 8, sw[v]);
-        else store8<float>(a.part + unit * a.H + p * 8, sg[v]);
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) sums[side - 1][(v * 8 + c) * R + lane] = acc[v][c];
       }
+      __syncthreads();
+      if (side > 0) return;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          for (int g = 0; g < G - 1; ++g) acc[v][c] += sums[g][(v * 8 + c) * R + lane];
     }
-    if constexpr (NEXT) store8<float>(a.part_next + unit * a.H + p * 8, sn[v]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = lane + v * R;
+      if (p < a.hv) store8<float>(part + int64_t(blockIdx.x) * a.H + p * 8, acc[v]);
+    }
+  };
+  if constexpr (POST) {
+    if (a.part != nullptr) {
+      if constexpr (FLUSH) out(sw, a.part);
+      else out(sg, a.part);
+    }
   }
+  if constexpr (NEXT) out(sn, a.part_next);
 }
 
-// Column sums of the units' partial rows.  Role 0: dw, and dgate of a gate with
+// Column sums of the blocks' partial rows.  Role 0: dw, and dgate of a gate with
 // one row, from the same sums; 1: dw_next; 2 + g: row g of a gate with several.
-// 32 channels a block; slice s of 32 adds units s, s + 32, ..., eight loads in
+// 32 channels a block; slice s of 32 adds rows s, s + 32, ..., eight loads in
 // flight, and the 32 sums are added in order.
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
@@ -382,10 +415,11 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
   const bool in = h < a.H;
   const int role = a.first_role + int(blockIdx.y);
   const float* part = (role == 1 ? a.part_next : a.part) + (in ? h : 0);
-  int64_t u0 = 0, u1 = a.units.count;
+  const int64_t per_group = a.units.per_group / a.units.blocks_of;
+  int64_t u0 = 0, u1 = a.units.count / a.units.blocks_of;
   if (role >= 2) {
-    u0 = int64_t(role - 2) * a.units.per_group;
-    u1 = u0 + a.units.per_group < u1 ? u0 + a.units.per_group : u1;  // no units: sums of nothing
+    u0 = int64_t(role - 2) * per_group;
+    u1 = u0 + per_group < u1 ? u0 + per_group : u1;  // no units: sums of nothing
   }
   // several gate rows: dw adds each unit's sums times its group's gate
   const bool gated = role == 0 && a.gate_mode == kGateChannel && a.units.per_group > 0 &&
@@ -398,7 +432,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
     for (int i = 0; i < 8; ++i) {
       const int64_t x = u + i * 32;
       v[i] = x < u1 ? part[x * a.H] : 0.f;
-      g[i] = gated && x < u1 ? to_f32<T>(gate[(x / a.units.per_group) * a.H]) : 1.f;
+      g[i] = gated && x < u1 ? to_f32<T>(gate[(x / per_group) * a.H]) : 1.f;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc = fmaf(v[i], g[i], acc);
@@ -423,12 +457,12 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
     static_cast<T*>(a.dw)[h] = from_f32<T>(one ? acc * to_f32<T>(gate[0]) : acc);
 }
 
-template <typename T, int W, int V>
-hipError_t fwd_flags(const NormFwd& a, bool post, bool next, int64_t blocks, const Launch& L) {
-  const dim3 grid(static_cast<unsigned>(blocks)), block(W == 1 ? 256 : 64 * W);
-  if (post && next) return launch_kernel(norm_fwd_kernel<T, W, V, true, true>, grid, block, 0, L, a);
-  if (post) return launch_kernel(norm_fwd_kernel<T, W, V, true, false>, grid, block, 0, L, a);
-  return launch_kernel(norm_fwd_kernel<T, W, V, false, true>, grid, block, 0, L, a);
+template <typename T, int R, int V>
+hipError_t fwd_flags(const NormFwd& a, bool post, bool next, int64_t rows, const Launch& L) {
+  const dim3 grid(unsigned((rows + kSide<R> - 1) / kSide<R>)), block(kThreads<R>);
+  if (post && next) return launch_kernel(norm_fwd_kernel<T, R, V, true, true>, grid, block, 0, L, a);
+  if (post) return launch_kernel(norm_fwd_kernel<T, R, V, true, false>, grid, block, 0, L, a);
+  return launch_kernel(norm_fwd_kernel<T, R, V, false, true>, grid, block, 0, L, a);
 }
 
 template <typename T>
@@ -442,22 +476,26 @@ hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
     a.t0 = t0;
     const int64_t rows = t0 + slab < N ? slab : N - t0;
     hipError_t e;
-    if (a.hv <= 64) e = fwd_flags<T, 1, 1>(a, post, next, (rows + 3) / 4, L);
-    else if (a.hv <= 256) e = fwd_flags<T, 4, 1>(a, post, next, rows, L);
-    else if (a.hv <= 512) e = fwd_flags<T, 4, 2>(a, post, next, rows, L);
-    else if (a.hv <= 1024) e = fwd_flags<T, 4, 4>(a, post, next, rows, L);
-    else e = fwd_flags<T, 8, 4>(a, post, next, rows, L);
+    if (a.hv <= 16) e = fwd_flags<T, 16, 1>(a, post, next, rows, L);
+    else if (a.hv <= 32) e = fwd_flags<T, 32, 1>(a, post, next, rows, L);
+    else if (a.hv <= 64) e = fwd_flags<T, 64, 1>(a, post, next, rows, L);
+    else if (a.hv <= 128) e = fwd_flags<T, 64, 2>(a, post, next, rows, L);
+    else if (a.hv <= 256) e = fwd_flags<T, 128, 2>(a, post, next, rows, L);
+    else if (a.hv <= 512) e = fwd_flags<T, 256, 2>(a, post, next, rows, L);
+    else if (a.hv <= 1024) e = fwd_flags<T, 256, 4>(a, post, next, rows, L);
+    else e = fwd_flags<T, 512, 4>(a, post, next, rows, L);
     if (e != hipSuccess) return e;
     s.launched = true;
   }
   return hipSuccess;
 }
 
-template <typename T, int W, int V, bool PRE>
+template <typename T, int R, int V, bool PRE>
 hipError_t bwd_flags(const NormBwd& a, bool post, bool next, const Launch& L) {
-  const dim3 grid(static_cast<unsigned>(a.units.count)), block(64 * W);
+  const dim3 grid(static_cast<unsigned>(a.units.count / a.units.blocks_of));
+  const dim3 block(kThreads<R>);
 #define TOPMOE_NORM_BWD(POST, NEXT, FLUSH) \
-  return launch_kernel(norm_bwd_kernel<T, W, V, POST, NEXT, FLUSH, PRE>, grid, block, 0, L, a)
+  return launch_kernel(norm_bwd_kernel<T, R, V, POST, NEXT, FLUSH, PRE>, grid, block, 0, L, a)
   if (!post) TOPMOE_NORM_BWD(false, true, false);
   if (a.units.per_group == 0) {
     if (next) TOPMOE_NORM_BWD(true, true, true);
@@ -473,11 +511,14 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
                      const Launch& sums) {
   if (a.units.count > 0) {
     hipError_t e;
-    if (a.hv <= 64) e = bwd_flags<T, 1, 1, true>(a, post, next, rows);
-    else if (a.hv <= 256) e = bwd_flags<T, 4, 1, true>(a, post, next, rows);
-    else if (a.hv <= 512) e = bwd_flags<T, 8, 1, true>(a, post, next, rows);
-    else if (a.hv <= 1024) e = bwd_flags<T, 16, 1, false>(a, post, next, rows);
-    else e = bwd_flags<T, 16, 2, false>(a, post, next, rows);
+    if (a.hv <= 16) e = bwd_flags<T, 16, 1, true>(a, post, next, rows);
+    else if (a.hv <= 32) e = bwd_flags<T, 32, 1, true>(a, post, next, rows);
+    else if (a.hv <= 64) e = bwd_flags<T, 64, 1, true>(a, post, next, rows);
+    else if (a.hv <= 128) e = bwd_flags<T, 128, 1, true>(a, post, next, rows);
+    else if (a.hv <= 256) e = bwd_flags<T, 256, 1, true>(a, post, next, rows);
+    else if (a.hv <= 512) e = bwd_flags<T, 512, 1, true>(a, post, next, rows);
+    else if (a.hv <= 1024) e = bwd_flags<T, 1024, 1, false>(a, post, next, rows);
+    else e = bwd_flags<T, 1024, 2, false>(a, post, next, rows);
     if (e != hipSuccess) return e;
   }
   // The roles of the sums; neighbouring ones share a launch (a grid has at
@@ -511,22 +552,29 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
 
 }  // namespace
 
-NormUnits plan_norm_units(int64_t N, int64_t gate_rows, int64_t gate_span) {
+// Units of one launch: as many as the chip holds at once (256 CUs x 16
+// wavefronts, of which a wider row's block takes more), each of at least one
+// row.
+NormUnits plan_norm_units(int64_t N, int64_t H, int64_t gate_rows, int64_t gate_span) {
   NormUnits u;
+  // units side by side in a block: kSide of the backward's threads per row
+  u.blocks_of = H <= 128 ? 16 : H <= 256 ? 8 : H <= 512 ? 4 : 1;
   if (N <= 0) {  // no units: the sums are of nothing
-    u.per_group = 1;
+    u.per_group = u.blocks_of;
     return u;
   }
-  // about kNormUnits units, of at least one row
-  int64_t rows = (N + kNormUnits - 1) / kNormUnits;
+  const int64_t most = H <= 512 ? 768 * u.blocks_of : H <= 1024 ? 2048 : H <= 2048 ? 1024
+                       : H <= 4096 ? 512 : 256;
+  const int64_t rows = (N + most - 1) / most;
+  auto whole = [&](int64_t n) { return (n + u.blocks_of - 1) / u.blocks_of * u.blocks_of; };
   if (gate_span >= rows) {
-    u.per_group = (gate_span + rows - 1) / rows;
+    u.per_group = whole((gate_span + rows - 1) / rows);
     u.rows = rows;
     u.count = gate_rows * u.per_group;
   } else {
     u.per_group = 0;
     u.rows = rows / gate_span * gate_span;
-    u.count = (N + u.rows - 1) / u.rows;
+    u.count = whole((N + u.rows - 1) / u.rows);
   }
   return u;
 }

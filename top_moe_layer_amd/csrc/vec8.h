@@ -18,27 +18,33 @@ struct Raw8<float> {
   f32x4 lo, hi;
 };
 
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_raw8(const T* p);
-template <>
-__device__ __forceinline__ Raw8<bf16_t> load_raw8<bf16_t>(const bf16_t* p) {
-  return Raw8<bf16_t>{*reinterpret_cast<const u32x4*>(p)};
+// 16 bytes to / from memory; NT: non-temporal, for data that this kernel reads
+// or writes once and that nothing reads again while it is still in the caches.
+template <bool NT, typename V>
+__device__ __forceinline__ V load_vec(const void* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  return *static_cast<const V*>(p);
 }
-template <>
-__device__ __forceinline__ Raw8<float> load_raw8<float>(const float* p) {
-  return Raw8<float>{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)};
+template <bool NT, typename V>
+__device__ __forceinline__ void store_vec(void* p, V v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  else *static_cast<V*>(p) = v;
 }
 
-template <typename T>
-__device__ __forceinline__ void store_raw8(T* p, const Raw8<T>& r);
-template <>
-__device__ __forceinline__ void store_raw8<bf16_t>(bf16_t* p, const Raw8<bf16_t>& r) {
-  *reinterpret_cast<u32x4*>(p) = r.q;
+template <typename T, bool NT = false>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* p) {
+  if constexpr (sizeof(T) == 2) return Raw8<T>{load_vec<NT, u32x4>(p)};
+  else return Raw8<T>{load_vec<NT, f32x4>(p), load_vec<NT, f32x4>(p + 4)};
 }
-template <>
-__device__ __forceinline__ void store_raw8<float>(float* p, const Raw8<float>& r) {
-  *reinterpret_cast<f32x4*>(p) = r.lo;
-  *reinterpret_cast<f32x4*>(p + 4) = r.hi;
+
+template <typename T, bool NT = false>
+__device__ __forceinline__ void store_raw8(T* p, const Raw8<T>& r) {
+  if constexpr (sizeof(T) == 2) {
+    store_vec<NT, u32x4>(p, r.q);
+  } else {
+    store_vec<NT, f32x4>(p, r.lo);
+    store_vec<NT, f32x4>(p + 4, r.hi);
+  }
 }
 
 template <typename T>
@@ -68,20 +74,18 @@ __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
 }
 
 // Rounded once to the dtype (nearest even).
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]);
-template <>
-__device__ __forceinline__ void store8<bf16_t>(bf16_t* p, const float (&v)[8]) {
-  u32x4 q;
+template <typename T, bool NT = false>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    u32x4 q;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = uint32_t(f32_to_bf16(v[2 * i])) | (uint32_t(f32_to_bf16(v[2 * i + 1])) << 16);
-  *reinterpret_cast<u32x4*>(p) = q;
-}
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
-  *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-  *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    for (int i = 0; i < 4; ++i)
+      q[i] = uint32_t(f32_to_bf16(v[2 * i])) | (uint32_t(f32_to_bf16(v[2 * i + 1])) << 16);
+    store_vec<NT, u32x4>(p, q);
+  } else {
+    store_vec<NT, f32x4>(p, f32x4{v[0], v[1], v[2], v[3]});
+    store_vec<NT, f32x4>(p + 4, f32x4{v[4], v[5], v[6], v[7]});
+  }
 }
 
 }  // namespace topmoe
