@@ -138,7 +138,7 @@ def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
         nbytes = moe_dispatch_workspace_bytes(N, E, k)
         wp, wn, ws = _scratch(nbytes, "moe_dispatch_fwd", dev, workspace)
     if xs is None:
-        xs = _empty((N * k, H), dtype=dt, device=dev)
+        xs = _empty(N * k, H, dtype=dt, device=dev)
     else:
         _is(xs, "xs", (N * k, H), dt, dev)
     offsets = _empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
@@ -173,7 +173,7 @@ def moe_dispatch_bwd(dxs: torch.Tensor, entry_row: torch.Tensor, *,
     dev, dt = dxs.device, dxs.dtype
     code = _code(dt)
     if dx is None:
-        dx = _empty((N, H), dtype=dt, device=dev)
+        dx = _empty(N, H, dtype=dt, device=dev)
     else:
         _is(dx, "dx", (N, H), dt, dev)
     _call("moe_dispatch_bwd", dev, stage_events, dxs.data_ptr(), entry_row.data_ptr(), N, H, k,
@@ -195,7 +195,7 @@ def moe_combine_fwd(ys: torch.Tensor, entry_row: torch.Tensor, alpha: torch.Tens
     if residual is not None:
         _is(residual, "residual", (N, H), dt, dev)
     if y is None:
-        y = _empty((N, H), dtype=dt, device=dev)
+        y = _empty(N, H, dtype=dt, device=dev)
     else:
         _is(y, "y", (N, H), dt, dev)
     _call("moe_combine_fwd", dev, stage_events, ys.data_ptr(), entry_row.data_ptr(),
@@ -415,16 +415,15 @@ def _pitched(t: torch.Tensor, name: str, shape, dt, dev) -> int:
     """Row pitch of a [R, C] tensor whose rows are contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape == shape and t.dtype is dt and t.is_contiguous() and t.device == dev:
+        return shape[1]
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev} (the library has no CPU path)")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dt:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dt}")
-    R, C = shape
-    if t.numel() == 0 or (R == 1 and t.stride(1) == 1):
-        return -(-C // 8) * 8
-    if t.stride(1) != 1 or t.stride(0) < C:
+    if t.stride(1) != 1 or t.stride(0) < shape[1]:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return t.stride(0)
 
@@ -435,7 +434,7 @@ def _need_act8(a: Act8, name: str, R: int, C: int, dev) -> None:
 
 
 def _new_act8(R: int, C: int, dev) -> Act8:
-    return Act8(_empty((R, C), dtype=torch.float8_e4m3fn, device=dev),
+    return Act8(_empty(R, C, dtype=torch.float8_e4m3fn, device=dev),
                 _empty((R, -(-C // B.ACT8_GROUP)), dtype=torch.uint8, device=dev))
 
 
@@ -469,7 +468,7 @@ def act8_unpack(q: torch.Tensor, scale: torch.Tensor, *, dtype: torch.dtype = to
     dev = q.device
     _need_act8(Act8(q, scale), "act8", R, C, dev)
     if x is None:
-        x = _empty((R, C), dtype=dtype, device=dev)
+        x = _empty(R, C, dtype=dtype, device=dev)
     code = _code(x.dtype)
     ld = _pitched(x, "x", (R, C), x.dtype, dev)
     _call("act8_unpack", dev, stage_events, q.data_ptr(), scale.data_ptr(), R, C, code,
@@ -488,7 +487,7 @@ def swiglu_act8_fwd(g: torch.Tensor, u: torch.Tensor, *, h: Optional[torch.Tenso
     ldg = _pitched(g, "g", (R, C), dt, dev)
     ldu = _pitched(u, "u", (R, C), dt, dev)
     if h is None:
-        h = _empty((R, C), dtype=dt, device=dev)
+        h = _empty(R, C, dtype=dt, device=dev)
     else:
         _is(h, "h", (R, C), dt, dev)
     g8, u8 = _new_act8(R, C, dev), _new_act8(R, C, dev)
@@ -513,7 +512,7 @@ def swiglu_act8_bwd(dh: torch.Tensor, g8: Act8, u8: Act8, *, with_h: bool = True
     if (dg is None) != (du is None):
         raise ValueError("dg and du go together")
     if dg is None:
-        dgu = _empty((R, 2 * C), dtype=dt, device=dev)
+        dgu = _empty(R, 2 * C, dtype=dt, device=dev)
         dg, du = dgu[:, :C], dgu[:, C:]
     lddg = _pitched(dg, "dg", (R, C), dt, dev)
     lddu = _pitched(du, "du", (R, C), dt, dev)

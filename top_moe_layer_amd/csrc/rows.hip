@@ -84,47 +84,52 @@ __global__ __launch_bounds__(256) void dispatch_count_kernel(const int32_t* __re
 
 // One block per chunk: every bucket's total and the count in earlier chunks
 // from the counts of all chunks, then the rank of each of its entries.  The
-// four wavefronts take a quarter of the chunk each, 64 entries at a time;
-// lanes of the same bucket find each other with one ballot per bit of it.
-__global__ __launch_bounds__(256) void dispatch_place_kernel(
+// wavefronts take an equal part of the chunk each, 64 entries at a time.
+constexpr int kPlaceWaves = 16;  // a chunk is a multiple of 1024 entries
+
+__global__ __launch_bounds__(64 * kPlaceWaves) void dispatch_place_kernel(
     const int32_t* __restrict__ idx, int64_t n, int chunk, int nchunk, int E, int bits, int cap,
     const int32_t* __restrict__ part, int32_t* __restrict__ offsets,
     int32_t* __restrict__ row_entry, int32_t* __restrict__ entry_row) {
+  constexpr int NT = 64 * kPlaceWaves;
   __shared__ int tot[kDispatchMaxExperts + 1], off[kDispatchMaxExperts + 1];
   __shared__ int tail[kDispatchMaxExperts + 1];
-  __shared__ int run[4][kDispatchMaxExperts + 1];  // next rank of each wavefront's entries
+  __shared__ int run[kPlaceWaves][kDispatchMaxExperts + 1];  // next rank of a wavefront's entries
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int B = E + 1;
-  for (int b = tid; b < B; b += 256) {
-    tot[b] = 0;
-    for (int w = 0; w < 4; ++w) run[w][b] = 0;
-  }
+  for (int b = tid; b < B; b += NT) tot[b] = tail[b] = 0;
+  for (int i = tid; i < kPlaceWaves * (kDispatchMaxExperts + 1); i += NT) (&run[0][0])[i] = 0;
   __syncthreads();
-  const int64_t quarter = chunk / 4;  // chunk is a multiple of 256
-  const int64_t w0 = int64_t(blockIdx.x) * chunk + wave * quarter;
-  const int64_t w1 = w0 + quarter < n ? w0 + quarter : n;
+  const int64_t share = chunk / kPlaceWaves;
+  const int64_t w0 = int64_t(blockIdx.x) * chunk + wave * share;
+  const int64_t w1 = w0 + share < n ? w0 + share : n;
   for (int64_t i = w0 + lane; i < w1; i += 64) atomicAdd(&run[wave][bucket_of(idx[i], E)], 1);
-  __syncthreads();
+  // totals, and counts before this chunk in tail[] (free until the scan)
   int shift = 0;
-  while ((1 << shift) < B && shift < 8) ++shift;  // lanes per chunk of counts
-  const int span = 1 << shift, slices = 256 >> shift;
-  // counts before this chunk go to tail[] first (free until the scan)
-  for (int b = tid; b < B; b += 256) tail[b] = 0;
-  __syncthreads();
+  while ((1 << shift) < B && shift < 8) ++shift;  // lanes along a chunk's counts
+  const int span = 1 << shift, slices = NT >> shift;
   for (int b = tid & (span - 1); b < B; b += span) {
     int all = 0, before = 0;
-    for (int c = tid >> shift; c < nchunk; c += slices) {
-      const int v = part[int64_t(c) * B + b];
-      all += v;
-      before += c < int(blockIdx.x) ? v : 0;
+    for (int c0 = tid >> shift; c0 < nchunk; c0 += slices * 8) {
+      int v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int c = c0 + u * slices;
+        v[u] = c < nchunk ? part[int64_t(c) * B + b] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        all += v[u];
+        before += c0 + u * slices < int(blockIdx.x) ? v[u] : 0;
+      }
     }
     atomicAdd(&tot[b], all);
     atomicAdd(&tail[b], before);
   }
   __syncthreads();
-  for (int b = tid; b < B; b += 256) {  // first rank of each wavefront's entries
+  for (int b = tid; b < B; b += NT) {  // first rank of each wavefront's entries
     int r = tail[b];
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kPlaceWaves; ++w) {
       const int c = run[w][b];
       run[w][b] = r;
       r += c;
@@ -436,9 +441,8 @@ hipError_t combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
 DispatchPlan plan_dispatch(int64_t n, int E) {
   DispatchPlan p;
   if (n <= kDispatchOne) return p;
-  int64_t c = (n + 255) / 256;           // at most 256 chunks
-  c = (c + 255) / 256 * 256;
-  p.chunk = c < 1024 ? 1024 : int(c);
+  const int64_t c = (n + 255) / 256;  // at most 256 chunks
+  p.chunk = int((c + 1023) / 1024 * 1024);
   p.nchunk = int((n + p.chunk - 1) / p.chunk);
   p.bytes = size_t(p.nchunk) * (E + 1) * sizeof(int32_t);
   return p;
@@ -465,7 +469,7 @@ hipError_t launch_dispatch_rows(const void* x, const int32_t* idx, int64_t N, in
   hipError_t e = launch_kernel(dispatch_count_kernel, dim3(p.nchunk), dim3(256), 0, first, idx, n,
                                p.chunk, E, part);
   if (e != hipSuccess) return e;
-  e = launch_kernel(dispatch_place_kernel, dim3(p.nchunk), dim3(256), 0, second, idx, n, p.chunk,
+  e = launch_kernel(dispatch_place_kernel, dim3(p.nchunk), dim3(64 * kPlaceWaves), 0, second, idx, n, p.chunk,
                     p.nchunk, E, bits, cap, part, offsets, row_entry, entry_row);
   if (e != hipSuccess) return e;
   rows.launched = true;
