@@ -494,6 +494,37 @@ int swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gscale, const uint8_t* uq,
                     void* dg, int64_t lddg, void* du, int64_t lddu, void* h, void* stream,
                     void* const* stage_events);
 
+/* The (g, u) that ffn_swiglu_fwd_train / moe_ffn_fwd_train left in `saved`, kept
+ * in 8 bits instead: keep8 copies them (and the MoE's routing) into `kept`,
+ * after which `saved` may be reused, and restore8 puts them, and h^T computed
+ * from them, into a backward workspace, from which ffn_swiglu_bwd_saved /
+ * moe_ffn_bwd with TOPMOE_MOE_BWD_SAVED run as after the training forward.
+ * Between the passes a layer then holds about 2 N k I bytes (2 + 1/16 an
+ * element pair) instead of its backward workspace.  The backward then computes
+ * from the 8-bit g and u (each within 2^-4 of its value, see act8_pack); y and
+ * the routing are as without it.
+ *   saved, workspace   *_bwd_workspace_bytes(), kept  *_keep8_bytes(): 256-byte
+ *   aligned.  kept holds, each part 256-byte aligned: the MoE's routing, g's
+ *   q [rows, I] (rows = N, or N * k in the experts' row order), u's q, g's
+ *   scale bytes [rows, I / 32], u's.
+ * Shape limits and statuses as for the backward; *_keep8_bytes return 0 for
+ * invalid shapes.  Stages: keep8 one, restore8 TOPMOE_RESTORE8_STAGES. */
+#define TOPMOE_RESTORE8_STAGES 2  /* 0 g, u (and routing), 1 h^T */
+size_t ffn_keep8_bytes(int64_t N, int64_t H, int64_t I, int dtype);
+int ffn_swiglu_keep8(const void* saved, size_t saved_bytes, int64_t N, int64_t H, int64_t I,
+                     int dtype, void* kept, size_t kept_bytes, void* stream,
+                     void* const* stage_events);
+int ffn_swiglu_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t H, int64_t I,
+                        int dtype, void* workspace, size_t workspace_bytes, void* stream,
+                        void* const* stage_events);
+size_t moe_keep8_bytes(int64_t N, int64_t H, int64_t I, int E, int k, int dtype);
+int moe_ffn_keep8(const void* saved, size_t saved_bytes, int64_t N, int64_t H, int64_t I, int E,
+                  int k, int dtype, void* kept, size_t kept_bytes, void* stream,
+                  void* const* stage_events);
+int moe_ffn_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t H, int64_t I, int E,
+                     int k, int dtype, void* workspace, size_t workspace_bytes, void* stream,
+                     void* const* stage_events);
+
 /* Human-readable text for a status code (static storage). */
 const char* topmoe_strerror(int status);
 

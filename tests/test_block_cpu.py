@@ -126,6 +126,27 @@ def test_act8_refusals():
     assert call("swiglu_act8_bwd", SWIGLU_BWD, du=FAKE, h=FAKE + 4) == B.ERR_BAD_ARG
 
 
+def test_keep8_refusals():
+    ffn = dict(src=FAKE, src_bytes=1 << 40, N=8, H=64, I=64, dtype=BF16, dst=FAKE, dst_bytes=0)
+    moe = dict(src=FAKE, src_bytes=1 << 40, N=8, H=64, I=64, E=4, k=2, dtype=BF16, dst=FAKE,
+               dst_bytes=0)
+    for base, names in ((ffn, ("ffn_swiglu_keep8", "ffn_swiglu_restore8")),
+                        (moe, ("moe_ffn_keep8", "moe_ffn_restore8"))):
+        for name in names:
+            assert call(name, base) == B.ERR_WORKSPACE_TOO_SMALL
+            assert call(name, base, dst_bytes=1 << 40, src_bytes=255) == B.ERR_WORKSPACE_TOO_SMALL
+            assert call(name, base, src=None) == B.ERR_NULL_ARG
+            assert call(name, base, dst=None) == B.ERR_NULL_ARG
+            assert call(name, base, dst_bytes=1 << 40, dst=FAKE + 128) == B.ERR_BAD_ARG
+            assert call(name, base, dst_bytes=1 << 40, src=FAKE + 64) == B.ERR_BAD_ARG
+            for over in (dict(I=96), dict(H=32), dict(N=-1)):
+                assert call(name, base, **over) == B.ERR_BAD_SHAPE, over
+            assert call(name, base, dtype=3) == B.ERR_UNSUPPORTED_DTYPE
+    n = 16384 * 6464  # a sixteenth of a byte of scales for each two bytes
+    assert 0 <= tm.ffn_keep8_bytes(16384, 2048, 6464, torch.bfloat16) - (2 * n + n // 16) <= 1024
+    assert tm.moe_keep8_bytes(8, 64, 96, 4, 2, torch.bfloat16) == 0
+
+
 def test_front_end_refusals():
     x, w = torch.zeros(4, 16), torch.zeros(16)
     idx = torch.zeros(4, 2, dtype=torch.int32)

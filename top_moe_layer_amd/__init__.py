@@ -20,6 +20,7 @@ from ._binding import (  # noqa: F401
     MOE_STAGE_NAMES,
     NORM_BWD_STAGES,
     NORM_BWD_STAGE_NAMES,
+    RESTORE8_STAGES,
     LIB_PATH,
     StageEvents,
     TopmoeError,
@@ -42,9 +43,11 @@ def __getattr__(name):
     if name in ("moe_dispatch_fwd", "moe_dispatch_bwd", "moe_combine_fwd", "moe_combine_bwd",
                 "moe_dispatch_workspace_bytes", "block_prenorm_fwd", "block_prenorm_bwd",
                 "block_postnorm_fwd", "block_postnorm_bwd", "block_norm_bwd_workspace_bytes",
-                "act8_pack", "act8_unpack", "swiglu_act8_fwd", "swiglu_act8_bwd", "Act8",
-                "MoeRows", "CombineGrads", "PrenormOutput", "PrenormGrads", "PostnormOutput",
-                "PostnormGrads", "SwigluAct8", "SwigluAct8Grads"):
+                "act8_pack", "act8_unpack", "swiglu_act8_fwd", "swiglu_act8_bwd",
+                "ffn_keep8_bytes", "moe_keep8_bytes", "ffn_swiglu_keep8", "ffn_swiglu_restore8",
+                "moe_ffn_keep8", "moe_ffn_restore8", "Act8", "MoeRows", "CombineGrads",
+                "PrenormOutput", "PrenormGrads", "PostnormOutput", "PostnormGrads", "SwigluAct8",
+                "SwigluAct8Grads"):
         from . import block
         globals()[name] = v = getattr(block, name)  # found without this function from now on
         return v

@@ -34,6 +34,7 @@ FFN_BWD_STAGES = 7
 MOE_BWD_STAGES = 12
 DISPATCH_STAGES = 2
 NORM_BWD_STAGES = 2
+RESTORE8_STAGES = 2
 DISPATCH_MAX_EXPERTS = 256
 DISPATCH_ONE = 32768
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
@@ -95,6 +96,12 @@ SIGNATURES = {
                                _vp, _vp]),
     "swiglu_act8_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _i64,
                                _vp, _vp, _vp]),
+    "ffn_keep8_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "ffn_swiglu_keep8": (_i32, [_vp, _sz, _i64, _i64, _i64, _i32, _vp, _sz, _vp, _vp]),
+    "ffn_swiglu_restore8": (_i32, [_vp, _sz, _i64, _i64, _i64, _i32, _vp, _sz, _vp, _vp]),
+    "moe_keep8_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32, _i32]),
+    "moe_ffn_keep8": (_i32, [_vp, _sz, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _sz, _vp, _vp]),
+    "moe_ffn_restore8": (_i32, [_vp, _sz, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _sz, _vp, _vp]),
     "topmoe_strerror": (ctypes.c_char_p, [_i32]),
     "topmoe_version": (_i32, []),
     "topmoe_set_tile_override": (_i32, [_i32, _vp]),

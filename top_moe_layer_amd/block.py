@@ -521,3 +521,70 @@ def swiglu_act8_bwd(dh: torch.Tensor, g8: Act8, u8: Act8, *, with_h: bool = True
           u8.q.data_ptr(), u8.scale.data_ptr(), dh.data_ptr(), R, C, code, dg.data_ptr(), lddg,
           du.data_ptr(), lddu, _ptr(h))
     return SwigluAct8Grads(dg, du, h)
+
+
+# ------------------------------------------------ the FFN's own activations in 8 bits
+def ffn_keep8_bytes(N: int, H: int, I: int, dtype: torch.dtype) -> int:
+    return int(B.lib().ffn_keep8_bytes(N, H, I, _dtype_code(dtype)))
+
+
+def moe_keep8_bytes(N: int, H: int, I: int, E: int, k: int, dtype: torch.dtype) -> int:
+    return int(B.lib().moe_keep8_bytes(N, H, I, E, k, _dtype_code(dtype)))
+
+
+def _keep8(name: str, src: torch.Tensor, sizes, need: int, dst: Optional[torch.Tensor], what: str,
+           events) -> torch.Tensor:
+    """``src`` (a byte buffer the entry point checks) into ``dst`` of ``need`` bytes."""
+    if need == 0:
+        B.check(B.ERR_BAD_SHAPE, name)
+    if dst is None:
+        dst = torch.empty(need, dtype=torch.uint8, device=src.device)
+    else:
+        _buffer(dst, what, need, src.device)
+    if not src.is_contiguous():
+        raise ValueError("the kept or saved buffer must be contiguous")
+    _call(name, src.device, events, src.data_ptr(), src.numel() * src.element_size(), *sizes,
+          dst.data_ptr(), dst.numel() * dst.element_size())
+    return dst
+
+
+@_on_kernel_stream
+def ffn_swiglu_keep8(saved: torch.Tensor, N: int, H: int, I: int, dtype: torch.dtype, *,
+                     kept: Optional[torch.Tensor] = None, stream=None,
+                     stage_events: Optional[B.StageEvents] = None) -> torch.Tensor:
+    """g and u of a training forward (ffn_swiglu_fwd(..., saved=saved)) in 8
+    bits: a byte buffer of ffn_keep8_bytes, after which ``saved`` is free."""
+    return _keep8("ffn_swiglu_keep8", saved, (N, H, I, _code(dtype)),
+                  ffn_keep8_bytes(N, H, I, dtype), kept, "kept", stage_events)
+
+
+@_on_kernel_stream
+def ffn_swiglu_restore8(kept: torch.Tensor, N: int, H: int, I: int, dtype: torch.dtype, *,
+                        workspace: Optional[torch.Tensor] = None, stream=None,
+                        stage_events: Optional[B.StageEvents] = None) -> torch.Tensor:
+    """A backward workspace from the kept bytes, for ffn_swiglu_bwd(...,
+    workspace=..., from_saved=True)."""
+    return _keep8("ffn_swiglu_restore8", kept, (N, H, I, _code(dtype)),
+                  int(B.lib().ffn_bwd_workspace_bytes(N, H, I, _code(dtype))), workspace,
+                  "workspace", stage_events)
+
+
+@_on_kernel_stream
+def moe_ffn_keep8(saved: torch.Tensor, N: int, H: int, I: int, E: int, k: int,
+                  dtype: torch.dtype, *, kept: Optional[torch.Tensor] = None, stream=None,
+                  stage_events: Optional[B.StageEvents] = None) -> torch.Tensor:
+    """As ffn_swiglu_keep8 for moe_ffn_fwd(..., saved=saved): the routing as it
+    is, g and u in 8 bits (moe_keep8_bytes)."""
+    return _keep8("moe_ffn_keep8", saved, (N, H, I, E, k, _code(dtype)),
+                  moe_keep8_bytes(N, H, I, E, k, dtype), kept, "kept", stage_events)
+
+
+@_on_kernel_stream
+def moe_ffn_restore8(kept: torch.Tensor, N: int, H: int, I: int, E: int, k: int,
+                     dtype: torch.dtype, *, workspace: Optional[torch.Tensor] = None, stream=None,
+                     stage_events: Optional[B.StageEvents] = None) -> torch.Tensor:
+    """A backward workspace from the kept bytes, for moe_ffn_bwd(...,
+    workspace=..., from_saved=True)."""
+    return _keep8("moe_ffn_restore8", kept, (N, H, I, E, k, _code(dtype)),
+                  int(B.lib().moe_bwd_workspace_bytes(N, H, I, E, k, _code(dtype))), workspace,
+                  "workspace", stage_events)

@@ -204,6 +204,88 @@ __global__ __launch_bounds__(256) void swiglu_act8_bwd_kernel(
   if (h != nullptr) store8<T, NT>(h + o, oh);
 }
 
+// ---- the (g, u) pairs of a training forward's workspace ----------------------
+// Eight pairs: 32 bytes of bf16 (g in the low halves), 64 of fp32.
+__device__ __forceinline__ void load_pairs8(const bf16_t* p, float (&g)[8], float (&u)[8]) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const u32x4 q = load_vec<true, u32x4>(p + 8 * w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) PairWord<bf16_t>::unpack(q[i], g[4 * w + i], u[4 * w + i]);
+  }
+}
+__device__ __forceinline__ void load_pairs8(const float* p, float (&g)[8], float (&u)[8]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const f32x4 q = load_vec<true, f32x4>(p + 4 * w);
+    g[2 * w] = q.x; u[2 * w] = q.y;
+    g[2 * w + 1] = q.z; u[2 * w + 1] = q.w;
+  }
+}
+
+// pairs [R, C] (C a multiple of 64) to g and u in 8 bits.
+template <typename T>
+__global__ __launch_bounds__(256) void pairs_pack_kernel(
+    const T* __restrict__ pairs, int64_t r0, uint32_t pieces, uint32_t pp, int C,
+    uint8_t* __restrict__ gq, uint8_t* __restrict__ gs, uint8_t* __restrict__ uq,
+    uint8_t* __restrict__ us) {
+  const Place a = place(r0, pieces, pp, C / 8);
+  const int64_t o = a.r * C + a.p * 8;
+  float g[8], u[8];
+  if (a.in) {
+    load_pairs8(pairs + 2 * o, g, u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = u[i] = 0.f;
+  }
+  uint32_t bg[2], bu[2];
+  const uint32_t sg = pack8(g, bg), su = pack8(u, bu);
+  if (!a.in) return;
+  store_q8(gq + o, bg);
+  store_q8(uq + o, bu);
+  if ((a.p & 3) == 0) {
+    gs[o / kAct8Group] = uint8_t(sg);
+    us[o / kAct8Group] = uint8_t(su);
+  }
+}
+
+// And back: the pairs, and h = SiLU(g) u of the kept values row-major.
+template <typename T>
+__global__ __launch_bounds__(256) void pairs_unpack_kernel(
+    const uint8_t* __restrict__ gq, const uint8_t* __restrict__ gs,
+    const uint8_t* __restrict__ uq, const uint8_t* __restrict__ us, int64_t r0, uint32_t pieces,
+    uint32_t pp, int C, T* __restrict__ pairs, T* __restrict__ h) {
+  const Place a = place(r0, pieces, pp, C / 8);
+  if (!a.in) return;
+  const int64_t o = a.r * C + a.p * 8;
+  uint32_t bg[2], bu[2];
+  load_q8(gq + o, bg);
+  load_q8(uq + o, bu);
+  float g[8], u[8], v[8];
+  unpack_q8(bg, scale_of(gs[o / kAct8Group]), g);
+  unpack_q8(bu, scale_of(us[o / kAct8Group]), u);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float gw[4], uw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      gw[i] = g[4 * w + i];
+      uw[i] = u[4 * w + i];
+    }
+    store_pairs4<T>(pairs, o + 4 * w, gw, uw);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = silu_mul(g[i], u[i]);
+  store8<T>(h + o, v);
+}
+
+// 16 bytes a thread.
+__global__ __launch_bounds__(256) void copy_kernel(const u32x4* __restrict__ src,
+                                                   u32x4* __restrict__ dst, int64_t n) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256)
+    dst[i] = src[i];
+}
+
 // Launches over slabs of rows of at most 2^30 pieces, so that piece numbers
 // stay in 32 bits and a grid within its limit of threads.
 template <typename F>
@@ -294,6 +376,33 @@ hipError_t launch_swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gs, const ui
   return dtype == TOPMOE_DTYPE_FP32
              ? swiglu_bwd<float>(gq, gs, uq, us, dh, R, C, dg, ldg, du, ldu, h, s)
              : swiglu_bwd<bf16_t>(gq, gs, uq, us, dh, R, C, dg, ldg, du, ldu, h, s);
+}
+
+hipError_t launch_pairs_pack(const void* pairs, int64_t R, int64_t C, int dtype, uint8_t* gq,
+                             uint8_t* gs, uint8_t* uq, uint8_t* us, const Launch& s) {
+  if (dtype == TOPMOE_DTYPE_FP32)
+    return TOPMOE_ACT8(pairs_pack_kernel<float>, static_cast<const float*>(pairs), r0, pieces, pp,
+                       int(C), gq, gs, uq, us);
+  return TOPMOE_ACT8(pairs_pack_kernel<bf16_t>, static_cast<const bf16_t*>(pairs), r0, pieces, pp,
+                     int(C), gq, gs, uq, us);
+}
+
+hipError_t launch_pairs_unpack(const uint8_t* gq, const uint8_t* gs, const uint8_t* uq,
+                               const uint8_t* us, int64_t R, int64_t C, int dtype, void* pairs,
+                               void* h, const Launch& s) {
+  if (dtype == TOPMOE_DTYPE_FP32)
+    return TOPMOE_ACT8(pairs_unpack_kernel<float>, gq, gs, uq, us, r0, pieces, pp, int(C),
+                       static_cast<float*>(pairs), static_cast<float*>(h));
+  return TOPMOE_ACT8(pairs_unpack_kernel<bf16_t>, gq, gs, uq, us, r0, pieces, pp, int(C),
+                     static_cast<bf16_t*>(pairs), static_cast<bf16_t*>(h));
+}
+
+hipError_t launch_copy(const void* src, void* dst, size_t bytes, const Launch& s) {
+  const int64_t n = int64_t(bytes / 16);
+  if (n == 0) return hipSuccess;
+  const int64_t grid = (n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096;
+  return launch_kernel(copy_kernel, dim3(unsigned(grid)), dim3(256), 0, s,
+                       static_cast<const u32x4*>(src), static_cast<u32x4*>(dst), n);
 }
 
 #undef TOPMOE_ACT8

@@ -65,6 +65,80 @@ int act8_shape(int64_t R, int64_t C) {
   if (R < 0 || R > kMaxRows || C <= 0 || C % 8 != 0 || C > kMaxRows) return TOPMOE_ERR_BAD_SHAPE;
   return TOPMOE_OK;
 }
+// A kept training forward: the routing (MoE), then g and u in 8 bits and their
+// scale bytes, each part 256-byte aligned.
+struct Keep8 {
+  size_t routing = 0, gq = 0, uq = 0, gs = 0, us = 0, total = 0;
+};
+Keep8 plan_keep8(size_t routing, int64_t rows, int64_t I) {
+  Keep8 k;
+  const size_t n = size_t(rows) * size_t(I);
+  k.routing = routing;
+  k.gq = align_up(routing);
+  k.uq = align_up(k.gq + n);
+  k.gs = align_up(k.uq + n);
+  k.us = align_up(k.gs + n / kAct8Group);
+  k.total = align_up(k.us + n / kAct8Group + 1);
+  return k;
+}
+
+// Stage 0: the workspace's routing and pairs into `kept`.
+int keep8(const Keep8& k, const void* saved, size_t off_gu, int64_t rows, int64_t I, int dtype,
+          void* kept, void* stream, void* const* stage_events) {
+  const char* sv = static_cast<const char*>(saved);
+  uint8_t* kp = static_cast<uint8_t*>(kept);
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch L = st.at(0);
+  Launch first = L, second = L;
+  const bool both = k.routing > 0 && rows > 0;
+  if (both) first.stop = second.start = nullptr;
+  if (k.routing > 0) TOPMOE_TRY(launch_copy(sv, kp, k.routing, first));
+  if (rows > 0)
+    TOPMOE_TRY(launch_pairs_pack(sv + off_gu, rows, I, dtype, kp + k.gq, kp + k.gs, kp + k.uq,
+                                 kp + k.us, second));
+  L.launched = first.launched || second.launched;
+  TOPMOE_TRY(st.close(L));
+  return TOPMOE_OK;
+}
+
+// Stage 0: the routing and the pairs from `kept`, and h row-major where the
+// backward will write [dg | du]; stage 1: h^T from it.
+int restore8(const Keep8& k, const void* kept, size_t off_gu, size_t off_h, size_t off_hT,
+             const GatherTransposeJobs& groups, int64_t rows, int64_t I, int dtype,
+             void* workspace, void* stream, void* const* stage_events) {
+  const uint8_t* kp = static_cast<const uint8_t*>(kept);
+  char* ws = static_cast<char*>(workspace);
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch l0 = st.at(0);
+  Launch first = l0, second = l0;
+  const bool both = k.routing > 0 && rows > 0;
+  if (both) first.stop = second.start = nullptr;
+  if (k.routing > 0) TOPMOE_TRY(launch_copy(kp, ws, k.routing, first));
+  if (rows > 0)
+    TOPMOE_TRY(launch_pairs_unpack(kp + k.gq, kp + k.gs, kp + k.uq, kp + k.us, rows, I, dtype,
+                                   ws + off_gu, ws + off_h, second));
+  l0.launched = first.launched || second.launched;
+  TOPMOE_TRY(st.close(l0));
+  const Launch l1 = st.at(1);
+  if (rows > 0) {
+    GatherTransposeJobs gj = groups;
+    gj.job[0] = GatherTransposeJob{ws + off_h, ws + off_hT, nullptr};
+    gj.n = 1;
+    TOPMOE_TRY(launch_gather_transpose(dtype, gj, gj.ldo, l1));
+  }
+  TOPMOE_TRY(st.close(l1));
+  return TOPMOE_OK;
+}
+
+// What keep8 / restore8 check of their two buffers.
+int keep8_buffers(const void* ws, size_t ws_bytes, size_t ws_need, const void* kept,
+                  size_t kept_bytes, size_t kept_need) {
+  if (!ws || !kept) return TOPMOE_ERR_NULL_ARG;
+  if (ws_bytes < ws_need || kept_bytes < kept_need) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(ws, 256) || !aligned(kept, 256)) return TOPMOE_ERR_BAD_ARG;
+  return TOPMOE_OK;
+}
+
 bool pitch_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0; }
 
 }  // namespace
@@ -344,6 +418,73 @@ int swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gscale, const uint8_t* uq,
                                     h, L));
   TOPMOE_TRY(st.close(L));
   return TOPMOE_OK;
+}
+
+size_t ffn_keep8_bytes(int64_t N, int64_t H, int64_t I, int dtype) {
+  FfnBwdPlan pl;
+  return plan_ffn_bwd(N, H, I, dtype, &pl) == TOPMOE_OK ? plan_keep8(0, N, I).total : 0;
+}
+
+int ffn_swiglu_keep8(const void* saved, size_t saved_bytes, int64_t N, int64_t H, int64_t I,
+                     int dtype, void* kept, size_t kept_bytes, void* stream,
+                     void* const* stage_events) {
+  FfnBwdPlan pl;
+  const int status = plan_ffn_bwd(N, H, I, dtype, &pl);
+  if (status != TOPMOE_OK) return status;
+  const Keep8 k = plan_keep8(0, N, I);
+  const int st = keep8_buffers(saved, saved_bytes, pl.total, kept, kept_bytes, k.total);
+  if (st != TOPMOE_OK) return st;
+  return keep8(k, saved, pl.off_gu, N, I, dtype, kept, stream, stage_events);
+}
+
+int ffn_swiglu_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t H, int64_t I,
+                        int dtype, void* workspace, size_t workspace_bytes, void* stream,
+                        void* const* stage_events) {
+  FfnBwdPlan pl;
+  const int status = plan_ffn_bwd(N, H, I, dtype, &pl);
+  if (status != TOPMOE_OK) return status;
+  const Keep8 k = plan_keep8(0, N, I);
+  const int st = keep8_buffers(workspace, workspace_bytes, pl.total, kept, kept_bytes, k.total);
+  if (st != TOPMOE_OK) return st;
+  GatherTransposeJobs gj{};
+  gj.E = 1; gj.k = 1; gj.C = int(I); gj.rows = N; gj.ldo = pl.ldk;
+  return restore8(k, kept, pl.off_gu, pl.off_dgdu, pl.off_hT, gj, N, I, dtype, workspace, stream,
+                  stage_events);
+}
+
+size_t moe_keep8_bytes(int64_t N, int64_t H, int64_t I, int E, int k, int dtype) {
+  MoeBwdPlan pl;
+  if (plan_moe_bwd(N, H, I, E, k, dtype, &pl) != TOPMOE_OK) return 0;
+  return plan_keep8(pl.off_wgT, pl.route.rows, I).total;
+}
+
+int moe_ffn_keep8(const void* saved, size_t saved_bytes, int64_t N, int64_t H, int64_t I, int E,
+                  int k, int dtype, void* kept, size_t kept_bytes, void* stream,
+                  void* const* stage_events) {
+  MoeBwdPlan pl;
+  const int status = plan_moe_bwd(N, H, I, E, k, dtype, &pl);
+  if (status != TOPMOE_OK) return status;
+  const Keep8 kp = plan_keep8(pl.off_wgT, pl.route.rows, I);
+  const int st = keep8_buffers(saved, saved_bytes, pl.total, kept, kept_bytes, kp.total);
+  if (st != TOPMOE_OK) return st;
+  return keep8(kp, saved, pl.off_gu, pl.route.rows, I, dtype, kept, stream, stage_events);
+}
+
+int moe_ffn_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t H, int64_t I, int E,
+                     int k, int dtype, void* workspace, size_t workspace_bytes, void* stream,
+                     void* const* stage_events) {
+  MoeBwdPlan pl;
+  const int status = plan_moe_bwd(N, H, I, E, k, dtype, &pl);
+  if (status != TOPMOE_OK) return status;
+  const Keep8 kp = plan_keep8(pl.off_wgT, pl.route.rows, I);
+  const int st = keep8_buffers(workspace, workspace_bytes, pl.total, kept, kept_bytes, kp.total);
+  if (st != TOPMOE_OK) return st;
+  GatherTransposeJobs gj{};  // grouped rows as they are, into the padded group columns
+  gj.offsets = reinterpret_cast<const int32_t*>(static_cast<char*>(workspace) +
+                                                pl.route.off_offsets);
+  gj.E = E; gj.k = k; gj.C = int(I); gj.rows = pl.route.rows; gj.ldo = pl.ldk;
+  return restore8(kp, kept, pl.off_gu, pl.off_dgdu, pl.off_hT, gj, pl.route.rows, I, dtype,
+                  workspace, stream, stage_events);
 }
 
 }  // extern "C"
