@@ -185,24 +185,36 @@ __global__ __launch_bounds__(256) void dispatch_copy_kernel(const T* __restrict_
 // of `copies` histograms by lane (up to 32, as many as the space holds), so
 // that the lanes of a wavefront that meet the same expert seldom add to the
 // same word.  The first pieces of the block's own tokens are loaded before the
-// counting.
+// counting.  A block's own entries (at most kSegs batches of 64) take a
+// wavefront a batch: the lanes of one bucket find each other by ballots, and
+// each batch's counts give the others their first ranks.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void dispatch_one_kernel(
     const T* __restrict__ x, const int32_t* __restrict__ idx, int n, int N, int tb, int hv, int H,
     int E, int k, int bits, int copies, int cap, T* __restrict__ xs,
     int32_t* __restrict__ offsets, int32_t* __restrict__ row_entry,
     int32_t* __restrict__ entry_row) {
-  constexpr int kPre = 6, kIn = 16;  // pieces and entries in flight per thread
+  constexpr int kPre = 6, kIn = 32;  // pieces and entries in flight per thread
+  constexpr int kOwn = kDispatchOne / 256 + kDispatchMaxExperts;  // tb * k <= n / 256 + k
+  constexpr int kWaves = NT / 64, kSegs = (kOwn + 63) / 64, kTurns = (kSegs + kWaves - 1) / kWaves;
   __shared__ int hist[2][kDispatchHist];  // [copies][B]: entries before the block's, from it on
-  __shared__ int tot[kDispatchMaxExperts + 1], run[kDispatchMaxExperts + 1];
+  __shared__ int tot[kDispatchMaxExperts + 1], before[kDispatchMaxExperts + 1];
   __shared__ int off[kDispatchMaxExperts + 1], tail[kDispatchMaxExperts + 1];
-  __shared__ int rows[kDispatchOne / 256 + kDispatchMaxExperts];  // tb * k <= n / 256 + k
-  const int tid = threadIdx.x, lane = tid & 63;
+  __shared__ int seg[kSegs][kDispatchMaxExperts + 1];
+  __shared__ int rows[kOwn];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int B = E + 1;
   const int t0 = blockIdx.x * tb, t1 = t0 + tb < N ? t0 + tb : N;
-  const int e0 = t0 * k, e1 = t1 * k;
+  const int e0 = t0 * k, own = (t1 - t0) * k;
+  const int segs = (own + 63) / 64;
   const int pieces = (t1 - t0) * hv;
   const T* xb = x + int64_t(t0) * H;
+  int ex[kTurns];  // this wavefront's own entries
+#pragma unroll
+  for (int q = 0; q < kTurns; ++q) {
+    const int i = (q * kWaves + wave) * 64 + lane;
+    ex[q] = i < own ? idx[e0 + i] : 0;
+  }
   Raw8<T> pre[kPre];
 #pragma unroll
   for (int u = 0; u < kPre; ++u) {  // a block's rows are consecutive: piece p is at 8 p
@@ -210,7 +222,19 @@ __global__ __launch_bounds__(NT) void dispatch_one_kernel(
     pre[u] = p < pieces ? load_raw8<T>(xb + int64_t(p) * 8) : zero_raw8<T>();
   }
   for (int i = tid; i < copies * B; i += NT) hist[0][i] = hist[1][i] = 0;
+  for (int i = tid; i < segs * (kDispatchMaxExperts + 1); i += NT) (&seg[0][0])[i] = 0;
   __syncthreads();
+  const uint64_t lt_mask = lane == 0 ? 0ull : (~0ull >> (64 - lane));
+  int rank[kTurns];  // within the batch
+#pragma unroll
+  for (int q = 0; q < kTurns; ++q) {
+    const int w = q * kWaves + wave;
+    const bool valid = w * 64 + lane < own;
+    const int b = valid ? bucket_of(ex[q], E) : 0;
+    const uint64_t peers = same_bucket(b, valid, bits);
+    rank[q] = __popcll(peers & lt_mask);
+    if (valid && rank[q] == 0) seg[w][b] = __popcll(peers);
+  }
   const int mine = (lane & (copies - 1)) * B;
   for (int i0 = tid; i0 < n; i0 += NT * kIn) {
     int e[kIn];
@@ -224,35 +248,32 @@ __global__ __launch_bounds__(NT) void dispatch_one_kernel(
   }
   __syncthreads();
   for (int b = tid; b < B; b += NT) {
-    int before = 0, after = 0;
+    int pre_b = 0, from_b = 0;
     for (int c = 0; c < copies; ++c) {
-      before += hist[0][c * B + b];
-      after += hist[1][c * B + b];
+      pre_b += hist[0][c * B + b];
+      from_b += hist[1][c * B + b];
     }
-    run[b] = before;
-    tot[b] = before + after;
+    before[b] = pre_b;
+    tot[b] = pre_b + from_b;
   }
   __syncthreads();
-  if (tid < 64) {
+  if (wave == 0) {
     scan_buckets(tot, E, cap, off, tail, lane);
     if (blockIdx.x == 0)
       for (int b = lane; b <= E; b += 64) offsets[b] = off[b];
-    __builtin_amdgcn_wave_barrier();
-    const uint64_t lt_mask = lane == 0 ? 0ull : (~0ull >> (64 - lane));
-    for (int base = e0; base < e1; base += 64) {
-      const int i = base + lane;
-      const bool valid = i < e1;
-      const int b = valid ? bucket_of(idx[i], E) : 0;
-      const uint64_t peers = same_bucket(b, valid, bits);
-      if (valid) {
-        const int r = row_of(b, run[b] + __popcll(peers & lt_mask), E, cap, tot, off, tail);
-        rows[i - e0] = r;
-        entry_row[i] = r;
-        row_entry[r < 0 ? -1 - r : r] = r < 0 ? -1 : i;
-      }
-      __builtin_amdgcn_wave_barrier();
-      if (valid && (peers & lt_mask) == 0ull) run[b] += __popcll(peers);
-      __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kTurns; ++q) {
+    const int w = q * kWaves + wave, i = w * 64 + lane;
+    if (i < own) {
+      const int b = bucket_of(ex[q], E);
+      int first = before[b];
+      for (int v = 0; v < w; ++v) first += seg[v][b];
+      const int r = row_of(b, first + rank[q], E, cap, tot, off, tail);
+      rows[i] = r;
+      entry_row[e0 + i] = r;
+      row_entry[r < 0 ? -1 - r : r] = r < 0 ? -1 : e0 + i;
     }
   }
   __syncthreads();
