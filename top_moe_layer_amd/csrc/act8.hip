@@ -314,7 +314,7 @@ hipError_t for_slabs(int64_t R, int64_t C, const Launch& s, F launch) {
   })
 // KERNEL<T, NT> by the outputs' bytes.
 #define TOPMOE_ACT8_NT(T, KERNEL, BYTES, ...)                     \
-  return (BYTES) > kNtBytes ? TOPMOE_ACT8((KERNEL<T, true>), __VA_ARGS__)  \
+  return (BYTES) >= kNtBytes ? TOPMOE_ACT8((KERNEL<T, true>), __VA_ARGS__)  \
                             : TOPMOE_ACT8((KERNEL<T, false>), __VA_ARGS__)
 
 namespace {

@@ -209,9 +209,13 @@ int dwr_chunks(int64_t N);
 hipError_t launch_dwr(const void* x, const float* dr, int64_t N, int H, int E, int dtype,
                       float* part, float* dWr, const Launch& s);
 
-// Outputs of more bytes than the Infinity Cache (256 MiB) holds are written
-// non-temporally: no reader would find them there.
-constexpr int64_t kNtBytes = int64_t(256) << 20;
+// Outputs from half the Infinity Cache (256 MiB) on are written
+// non-temporally where that was faster with a reader behind them: below, the
+// reader finds them in the cache (SwiGLU with 8-bit operands and a reader of h,
+// C = 6464: 101.9 against 103.5 us at 106 MB; 209.7 and 209.9 us at 212 MB, of
+// which its own 144.9 and 137.6); post norm and a reader of n, H = 2048: 20.3
+// against 20.6 us at 34 MB, 75.4 against 68.4 us at 134 MB.
+constexpr int64_t kNtBytes = int64_t(128) << 20;
 
 // ---- rows by expert and back (rows.hip)
 constexpr int kDispatchMaxExperts = 256;

@@ -67,8 +67,9 @@ __device__ __forceinline__ void load_f(const T* p, float (&v)[8]) {
 }
 
 // POST: the norm after the block with gate and residual (else r = y = x).
-// NEXT: the norm before the next block.
-template <typename T, int R, int V, bool POST, bool NEXT>
+// NEXT: the norm before the next block.  NT: non-temporal rows (see kNtBytes;
+// the rows read as well: 48.3 -> 45.7 us of the 16384 x 2048 post norm).
+template <typename T, int R, int V, bool POST, bool NEXT, bool NT>
 __global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
   __shared__ float slot[2][kWaves<R>];
   const int lane = int(threadIdx.x) % R, wave = int(threadIdx.x >> 6);
@@ -80,7 +81,7 @@ __global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int p = lane + v * R;
-    yr[v] = p < a.hv ? load_raw8<T>(y + p * 8) : zero_raw8<T>();
+    yr[v] = p < a.hv ? load_raw8<T, NT>(y + p * 8) : zero_raw8<T>();
   }
   const float inv_h = 1.0f / float(a.H);
   float rs[V][8];  // r
@@ -90,7 +91,7 @@ __global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * R;
-      res[v] = p < a.hv ? load_raw8<T>(rp + p * 8) : zero_raw8<T>();
+      res[v] = p < a.hv ? load_raw8<T, NT>(rp + p * 8) : zero_raw8<T>();
     }
     float rstd = 1.f;
     if (a.w != nullptr) {
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) rs[v][c] = fmaf(f[c], m[c], a.scale * q[c]);
-        store8<T>(out + p * 8, rs[v]);
+        store8<T, NT>(out + p * 8, rs[v]);
       } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) rs[v][c] = 0.f;
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
       load_f<T>(static_cast<const T*>(a.next_w) + p * 8, w);
 #pragma unroll
       for (int c = 0; c < 8; ++c) w[c] = rs[v][c] * rstd * w[c];
-      store8<T>(n + p * 8, w);
+      store8<T, NT>(n + p * 8, w);
     }
   }
 }
@@ -460,9 +461,14 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
 template <typename T, int R, int V>
 hipError_t fwd_flags(const NormFwd& a, bool post, bool next, int64_t rows, const Launch& L) {
   const dim3 grid(unsigned((rows + kSide<R> - 1) / kSide<R>)), block(kThreads<R>);
-  if (post && next) return launch_kernel(norm_fwd_kernel<T, R, V, true, true>, grid, block, 0, L, a);
-  if (post) return launch_kernel(norm_fwd_kernel<T, R, V, true, false>, grid, block, 0, L, a);
-  return launch_kernel(norm_fwd_kernel<T, R, V, false, true>, grid, block, 0, L, a);
+  const bool nt = a.N * a.H * int64_t(sizeof(T)) * (post && next ? 2 : 1) >= kNtBytes;
+#define TOPMOE_NORM_FWD(POST, NEXT)                                                               \
+  return nt ? launch_kernel(norm_fwd_kernel<T, R, V, POST, NEXT, true>, grid, block, 0, L, a) \
+            : launch_kernel(norm_fwd_kernel<T, R, V, POST, NEXT, false>, grid, block, 0, L, a)
+  if (post && next) TOPMOE_NORM_FWD(true, true);
+  if (post) TOPMOE_NORM_FWD(true, false);
+  TOPMOE_NORM_FWD(false, true);
+#undef TOPMOE_NORM_FWD
 }
 
 template <typename T>

@@ -160,8 +160,10 @@ __global__ __launch_bounds__(64 * kPlaceWaves) void dispatch_place_kernel(
 }
 
 // Token-major copy: each thread reads one piece of a token's row once and
-// writes it to the token's k rows (zeros to the rows of entries not kept).
-template <typename T>
+// writes it to the token's k rows (zeros to the rows of entries not kept).  NT:
+// x read non-temporally, from 96 MiB of rows on (with a reader of them: 70.4 ->
+// 66.8 us at 96 MiB, 94.9 -> 89.5 at 132; alone 24.5 -> 27.6 at 65).
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void dispatch_copy_kernel(const T* __restrict__ x,
                                                             const int32_t* __restrict__ entry_row,
                                                             int64_t t0, uint32_t pieces, int hv,
@@ -171,7 +173,7 @@ __global__ __launch_bounds__(256) void dispatch_copy_kernel(const T* __restrict_
   const uint32_t dt = g / uint32_t(hv);
   const int64_t t = t0 + dt;
   const int64_t h = int64_t(g - dt * uint32_t(hv)) * 8;
-  const Raw8<T> v = load_raw8<T>(x + t * H + h);
+  const Raw8<T> v = load_raw8<T, NT>(x + t * H + h);
   for (int j = 0; j < k; ++j) {
     const int r = entry_row[t * k + j];
     if (r >= 0) store_raw8<T>(xs + int64_t(r) * H + h, v);
@@ -299,8 +301,10 @@ __global__ void dispatch_empty_kernel(int E, int32_t* offsets) {
 // ---- back to tokens ---------------------------------------------------------
 // out[t] = residual[t] (or 0) + sum_j w[t, j] rows[entry_row[t, j]], the
 // combine (w = alpha) and the dispatch's gradient (w = 1).  A row id outside
-// [0, nrows) adds nothing.  Four slots' pieces are in flight at a time.
-template <typename T, bool WEIGHTED>
+// [0, nrows) adds nothing.  Four slots' pieces are in flight at a time.  NT:
+// rows read non-temporally, from 192 MiB of them on (just written, top-2, H =
+// 768: 155.5 -> 149.9 us with their writer at 192 MiB, 106.5 -> 108.8 at 132).
+template <typename T, bool WEIGHTED, bool NT>
 __global__ __launch_bounds__(256) void gather_sum_kernel(
     const T* __restrict__ rows, const int32_t* __restrict__ entry_row,
     const float* __restrict__ alpha, const T* residual, int64_t nrows, int64_t t0,
@@ -326,7 +330,7 @@ __global__ __launch_bounds__(256) void gather_sum_kernel(
       const int64_t r = j0 + u < k ? int64_t(er[j0 + u]) : -1;
       const bool use = r >= 0 && r < nrows;
       w[u] = !use ? 0.f : WEIGHTED ? alpha[t * k + j0 + u] : 1.f;
-      v[u] = use ? load_raw8<T>(rows + r * H + h) : zero_raw8<T>();
+      v[u] = use ? load_raw8<T, NT>(rows + r * H + h) : zero_raw8<T>();
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -341,9 +345,10 @@ __global__ __launch_bounds__(256) void gather_sum_kernel(
 
 // dys[row(i)] = alpha[i] dy[t] and dalpha[i] = dy[t] . ys[row(i)]: one
 // wavefront per entry, consecutive entries in a block, so that a token's k
-// wavefronts share its dy row in the caches; each row of ys is read once
-// (non-temporally: 16384 x 2048 bf16, k = 2: 58.5 -> 54.1 us, 6.2 TB/s).
-template <typename T>
+// wavefronts share its dy row in the caches; each row of ys is read once,
+// non-temporally, and dys written so when it is large (NT): 16384 x 2048 bf16,
+// k = 2: 66.3 -> 63.2 -> 54.0 us, 6.2 TB/s.
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(
     const T* __restrict__ dy, const T* __restrict__ ys, const int32_t* __restrict__ entry_row,
     const float* __restrict__ alpha, int64_t n, int64_t i0, int hv, int H, int k,
@@ -376,7 +381,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(
       dot = fmaf(fd[c], fs[c], dot);
       fd[c] *= a;
     }
-    store8<T>(o + p * 8, fd);
+    store8<T, NT>(o + p * 8, fd);
   }
   dot = wave_sum(dot);
   if (lane == 0) dalpha[i] = dot;
@@ -425,7 +430,9 @@ hipError_t dispatch_copy(const void* x, const int32_t* entry_row, int64_t N, int
   const int hv = H / 8;
   return for_slabs(N, slab_rows(hv), s, [&](int64_t t0, int64_t rows, const Launch& L) {
     const uint32_t pieces = uint32_t(rows * hv);
-    return launch_kernel(dispatch_copy_kernel<T>, dim3((pieces + 255) / 256), dim3(256), 0, L,
+    const auto kernel = N * k * H * int64_t(sizeof(T)) >= kNtBytes / 4 * 3
+                            ? dispatch_copy_kernel<T, true> : dispatch_copy_kernel<T, false>;
+    return launch_kernel(kernel, dim3((pieces + 255) / 256), dim3(256), 0, L,
                          static_cast<const T*>(x), entry_row, t0, pieces, hv, H, k,
                          static_cast<T*>(xs));
   });
@@ -438,7 +445,10 @@ hipError_t gather_sum(const void* rows, const int32_t* entry_row, const float* a
   const int hv = H / 8;
   return for_slabs(N, slab_rows(hv), s, [&](int64_t t0, int64_t m, const Launch& L) {
     const uint32_t pieces = uint32_t(m * hv);
-    return launch_kernel(gather_sum_kernel<T, WEIGHTED>, dim3((pieces + 255) / 256), dim3(256), 0,
+    const auto kernel = N * k * H * int64_t(sizeof(T)) >= kNtBytes / 2 * 3
+                            ? gather_sum_kernel<T, WEIGHTED, true>
+                            : gather_sum_kernel<T, WEIGHTED, false>;
+    return launch_kernel(kernel, dim3((pieces + 255) / 256), dim3(256), 0,
                          L, static_cast<const T*>(rows), entry_row, alpha,
                          static_cast<const T*>(residual), N * k, t0, pieces, hv, H, k,
                          static_cast<T*>(out));
@@ -451,7 +461,9 @@ hipError_t combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
                        const Launch& s) {
   const int64_t n = N * k;
   return for_slabs(n, int64_t(1) << 24, s, [&](int64_t i0, int64_t m, const Launch& L) {
-    return launch_kernel(combine_bwd_kernel<T>, dim3(unsigned((m + 3) / 4)), dim3(256), 0, L,
+    const auto kernel = n * H * int64_t(sizeof(T)) >= kNtBytes ? combine_bwd_kernel<T, true>
+                                                               : combine_bwd_kernel<T, false>;
+    return launch_kernel(kernel, dim3(unsigned((m + 3) / 4)), dim3(256), 0, L,
                          static_cast<const T*>(dy), static_cast<const T*>(ys), entry_row, alpha,
                          n, i0, H / 8, H, k, static_cast<T*>(dys), dalpha);
   });
