@@ -509,7 +509,7 @@ int swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gscale, const uint8_t* uq,
  *   scale bytes [rows, I / 32], u's.
  * Shape limits and statuses as for the backward; *_keep8_bytes return 0 for
  * invalid shapes.  Stages: keep8 one, restore8 TOPMOE_RESTORE8_STAGES. */
-#define TOPMOE_RESTORE8_STAGES 2  /* 0 g, u (and routing), 1 h^T */
+#define TOPMOE_RESTORE8_STAGES 2  /* 0 routing (dense: empty), 1 g, u and h^T */
 size_t ffn_keep8_bytes(int64_t N, int64_t H, int64_t I, int dtype);
 int ffn_swiglu_keep8(const void* saved, size_t saved_bytes, int64_t N, int64_t H, int64_t I,
                      int dtype, void* kept, size_t kept_bytes, void* stream,

@@ -16,6 +16,7 @@
 //                           (from the kept g, u; h for the down projection's
 //                            weight gradient)
 // Bound by memory.
+#include "act8_impl.h"
 #include "kernels.h"
 #include "vec8.h"
 
@@ -26,59 +27,6 @@ namespace topmoe {
 namespace {
 
 constexpr bool kNtLoad = true, kNtKeep = true;
-
-// Largest magnitude over the four lanes of a quad, as its fp32 bits (ordered
-// like the magnitudes).
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  uint32_t w = uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0xB1, 0xF, 0xF, false));  // lane ^ 1
-  v = v > w ? v : w;
-  w = uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, false));  // lane ^ 2
-  return v > w ? v : w;
-}
-
-// Eight channels of a group to 8 bytes and the group's scale byte.  Every lane
-// of the quad must take part (lanes past the row's end with zeros).
-__device__ __forceinline__ uint32_t pack8(const float (&x)[8], uint32_t (&q)[2]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
-    m = b < 0x7f800000u && b > m ? b : m;
-  }
-  m = quad_max(m);
-  // 448 = 1.75 * 2^8: the exponent less 8, one more for a fraction above 1.75
-  int e = int(m >> 23) - 135 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
-  e = e < -127 ? -127 : e;
-  const float inv = __uint_as_float(uint32_t(127 - e) << 23);  // 2^-e, e in [-127, 120]
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool fine = (__float_as_uint(x[i]) & 0x7fffffffu) < 0x7f800000u;
-    v[i] = fine ? x[i] * inv : __uint_as_float(0x7fc00000u);
-  }
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    int d = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * w], v[4 * w + 1], 0, false);
-    q[w] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * w + 2], v[4 * w + 3], d, true));
-  }
-  return uint32_t(e + 127);
-}
-
-// 2^(byte - 127) (a byte of 0 is the subnormal 2^-127; 255 is NaN).
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return byte == 0 ? __uint_as_float(0x00400000u)
-                   : byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
-}
-
-__device__ __forceinline__ void unpack_q8(const uint32_t (&q)[2], float s, float (&v)[8]) {
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    v[4 * w + 0] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 0) * s;
-    v[4 * w + 1] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 1) * s;
-    v[4 * w + 2] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 2) * s;
-    v[4 * w + 3] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 3) * s;
-  }
-}
 
 __device__ __forceinline__ void load_q8(const uint8_t* p, uint32_t (&q)[2]) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -223,7 +171,7 @@ __device__ __forceinline__ void load_pairs8(const float* p, float (&g)[8], float
   }
 }
 
-// pairs [R, C] (C a multiple of 64) to g and u in 8 bits.
+// pairs [R, C] (C a multiple of 64) to g and u in 8 bits (back: backward.hip).
 template <typename T>
 __global__ __launch_bounds__(256) void pairs_pack_kernel(
     const T* __restrict__ pairs, int64_t r0, uint32_t pieces, uint32_t pp, int C,
@@ -247,36 +195,6 @@ __global__ __launch_bounds__(256) void pairs_pack_kernel(
     gs[o / kAct8Group] = uint8_t(sg);
     us[o / kAct8Group] = uint8_t(su);
   }
-}
-
-// And back: the pairs, and h = SiLU(g) u of the kept values row-major.
-template <typename T>
-__global__ __launch_bounds__(256) void pairs_unpack_kernel(
-    const uint8_t* __restrict__ gq, const uint8_t* __restrict__ gs,
-    const uint8_t* __restrict__ uq, const uint8_t* __restrict__ us, int64_t r0, uint32_t pieces,
-    uint32_t pp, int C, T* __restrict__ pairs, T* __restrict__ h) {
-  const Place a = place(r0, pieces, pp, C / 8);
-  if (!a.in) return;
-  const int64_t o = a.r * C + a.p * 8;
-  uint32_t bg[2], bu[2];
-  load_q8(gq + o, bg);
-  load_q8(uq + o, bu);
-  float g[8], u[8], v[8];
-  unpack_q8(bg, scale_of(gs[o / kAct8Group]), g);
-  unpack_q8(bu, scale_of(us[o / kAct8Group]), u);
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    float gw[4], uw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      gw[i] = g[4 * w + i];
-      uw[i] = u[4 * w + i];
-    }
-    store_pairs4<T>(pairs, o + 4 * w, gw, uw);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = silu_mul(g[i], u[i]);
-  store8<T>(h + o, v);
 }
 
 // 16 bytes a thread.
@@ -385,16 +303,6 @@ hipError_t launch_pairs_pack(const void* pairs, int64_t R, int64_t C, int dtype,
                        int(C), gq, gs, uq, us);
   return TOPMOE_ACT8(pairs_pack_kernel<bf16_t>, static_cast<const bf16_t*>(pairs), r0, pieces, pp,
                      int(C), gq, gs, uq, us);
-}
-
-hipError_t launch_pairs_unpack(const uint8_t* gq, const uint8_t* gs, const uint8_t* uq,
-                               const uint8_t* us, int64_t R, int64_t C, int dtype, void* pairs,
-                               void* h, const Launch& s) {
-  if (dtype == TOPMOE_DTYPE_FP32)
-    return TOPMOE_ACT8(pairs_unpack_kernel<float>, gq, gs, uq, us, r0, pieces, pp, int(C),
-                       static_cast<float*>(pairs), static_cast<float*>(h));
-  return TOPMOE_ACT8(pairs_unpack_kernel<bf16_t>, gq, gs, uq, us, r0, pieces, pp, int(C),
-                     static_cast<bf16_t*>(pairs), static_cast<bf16_t*>(h));
 }
 
 hipError_t launch_copy(const void* src, void* dst, size_t bytes, const Launch& s) {

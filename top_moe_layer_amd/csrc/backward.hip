@@ -15,6 +15,7 @@
 //   router z-loss z_coef * mean_t lse_t^2 (upstream dz):  dr_e += z_coef dz 2 lse_t p_e / N
 //   (d lse / d r = p); an entry dropped by an expert capacity passes no d alpha.
 // Every float reduction runs in a fixed order, so results repeat bit for bit.
+#include "act8_impl.h"
 #include "device_common.h"
 #include "kernels.h"
 
@@ -122,31 +123,37 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeJobs jobs) {
 // row_g = entries[g] / k (entries NULL: g), scale_g = alpha_g[g] (NULL: 1).
 // Up to two sources (blockIdx.z) share the grouping.  Grid: x = 64-column
 // blocks of the padded width bound, y = C / 64.
+//
+// The group that holds padded columns pc0 .. pc0 + 63 into s_grp[4]: group (-1:
+// none), its first row, its row count, its first padded column.  Wavefront 0.
+__device__ __forceinline__ void find_group(const int32_t* offsets, int E, int64_t rows,
+                                           int64_t pc0, int lane, int* s_grp) {
+  const int G = offsets != nullptr ? E : 1;
+  int c = 0, o0 = 0;
+  if (lane < G) {
+    o0 = offsets != nullptr ? offsets[lane] : 0;
+    c = (offsets != nullptr ? offsets[lane + 1] : int(rows)) - o0;
+  }
+  const int kp = (c + 63) & ~63;
+  const int incl = wave_inclusive_scan(kp, lane);
+  if (lane == 0) s_grp[0] = -1;
+  __builtin_amdgcn_wave_barrier();
+  if (lane < G && pc0 >= incl - kp && pc0 < incl) {  // at most one group holds the block
+    s_grp[0] = lane;
+    s_grp[1] = o0;
+    s_grp[2] = c;
+    s_grp[3] = incl - kp;
+  }
+}
+
 template <typename T>
 __global__ __launch_bounds__(256) void gather_transpose_kernel(GatherTransposeJobs jobs) {
   using TT = TileT<T>;
   __shared__ __attribute__((aligned(16))) T tile[64 * TT::LD];
-  __shared__ int s_grp[4];  // group, its first row, its row count, its first padded column
+  __shared__ int s_grp[4];
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int64_t pc0 = int64_t(blockIdx.x) * 64;
-  if (tid < 64) {
-    const int G = jobs.offsets != nullptr ? jobs.E : 1;
-    int c = 0, o0 = 0;
-    if (lane < G) {
-      o0 = jobs.offsets != nullptr ? jobs.offsets[lane] : 0;
-      c = (jobs.offsets != nullptr ? jobs.offsets[lane + 1] : int(jobs.rows)) - o0;
-    }
-    const int kp = (c + 63) & ~63;
-    const int incl = wave_inclusive_scan(kp, lane);
-    if (lane == 0) s_grp[0] = -1;
-    __builtin_amdgcn_wave_barrier();
-    if (lane < G && pc0 >= incl - kp && pc0 < incl) {  // at most one group holds the block
-      s_grp[0] = lane;
-      s_grp[1] = o0;
-      s_grp[2] = c;
-      s_grp[3] = incl - kp;
-    }
-  }
+  if (tid < 64) find_group(jobs.offsets, jobs.E, jobs.rows, pc0, lane, s_grp);
   __syncthreads();
   if (s_grp[0] < 0) return;  // past the last group's padded columns
   const int gfirst = s_grp[1], cnt = s_grp[2], poff = s_grp[3];
@@ -185,6 +192,77 @@ __global__ __launch_bounds__(256) void gather_transpose_kernel(GatherTransposeJo
 #pragma unroll
     for (int w = 0; w < TT::V; ++w) v[w] = to_f32<T>(tile[TT::at(q * TT::V + w, h)]);
     st16<T>(dst + int64_t(h0 + h) * jobs.ldo + pc0 + q * TT::V, v);
+  }
+}
+
+// The kept g and u of grouped rows back into the pairs (g, u) [rows, C], and
+// h^T = (SiLU(g) u)^T in padded group columns, as the training forward's gate /
+// up projection leaves them: a 64 x 64 tile of h per block through LDS, eight
+// channels of a row per thread, two rows each.  Tiles go along the channels
+// first and in one contiguous share per XCD (blocks b, b + 8, ... run on one),
+// so that the halves of a 128-byte line of q meet in one L2.
+template <typename T>
+__global__ __launch_bounds__(256) void restore8_kernel(Restore8Job jb) {
+  using TT = TileT<T>;
+  __shared__ __attribute__((aligned(16))) T tile[64 * TT::LD];
+  __shared__ int s_grp[4];
+  const int tid = int(threadIdx.x), lane = tid & 63;
+  const int ct = jb.C / 64;
+  const int64_t t = int64_t(blockIdx.x & 7) * (gridDim.x / 8) + (blockIdx.x >> 3);
+  const int64_t pc0 = t / ct * 64;
+  if (pc0 >= jb.ldo) return;
+  if (tid < 64) find_group(jb.offsets, jb.E, jb.rows, pc0, lane, s_grp);
+  __syncthreads();
+  if (s_grp[0] < 0) return;  // past the last group's padded columns
+  const int gfirst = s_grp[1], cnt = s_grp[2], local0 = int(pc0) - s_grp[3];
+  const int h0 = int(t % ct) * 64;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int id = tid + 256 * i, l = id / 8, c0 = (id & 7) * 8;
+    float h[8];
+    if (local0 + l < cnt) {
+      const int64_t o = int64_t(gfirst + local0 + l) * jb.C + h0 + c0;
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 qg = *reinterpret_cast<const u32x2*>(jb.gq + o);
+      const u32x2 qu = *reinterpret_cast<const u32x2*>(jb.uq + o);
+      const uint32_t bg[2] = {qg.x, qg.y}, bu[2] = {qu.x, qu.y};
+      float g[8], u[8];
+      unpack_q8(bg, scale_of(jb.gs[o / kAct8Group]), g);
+      unpack_q8(bu, scale_of(jb.us[o / kAct8Group]), u);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float gw[4], uw[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gw[e] = g[4 * w + e];
+          uw[e] = u[4 * w + e];
+        }
+        store_pairs4<T>(jb.pairs, o + 4 * w, gw, uw);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = silu_mul(g[e], u[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = 0.f;
+    }
+#pragma unroll
+    for (int w = 0; w < 8 / TT::V; ++w) {
+      float v[TT::V];
+#pragma unroll
+      for (int e = 0; e < TT::V; ++e) v[e] = h[TT::V * w + e];
+      st16<T>(&tile[TT::piece(l, c0 / TT::V + w)], v);
+    }
+  }
+  __syncthreads();
+  T* dst = static_cast<T*>(jb.hT);
+#pragma unroll
+  for (int i = 0; i < TT::PER; ++i) {
+    const int id = tid + 256 * i;
+    const int h = id / TT::CPR, q = id - h * TT::CPR;
+    float v[TT::V];
+#pragma unroll
+    for (int w = 0; w < TT::V; ++w) v[w] = to_f32<T>(tile[TT::at(q * TT::V + w, h)]);
+    st16<T>(dst + int64_t(h0 + h) * jb.ldo + pc0 + q * TT::V, v);
   }
 }
 
@@ -456,6 +534,14 @@ hipError_t launch_transpose(int dtype, const TransposeJobs& jobs, int max_tiles,
   if (dtype == TOPMOE_DTYPE_FP32)
     return launch_kernel(transpose_kernel<float>, grid, dim3(256), 0, s, jobs);
   return launch_kernel(transpose_kernel<bf16_t>, grid, dim3(256), 0, s, jobs);
+}
+
+hipError_t launch_restore8(int dtype, const Restore8Job& job, const Launch& s) {
+  if (job.rows <= 0) return hipSuccess;
+  const dim3 grid(unsigned((job.ldo / 64 * (job.C / 64) + 7) / 8 * 8));
+  if (dtype == TOPMOE_DTYPE_FP32)
+    return launch_kernel(restore8_kernel<float>, grid, dim3(256), 0, s, job);
+  return launch_kernel(restore8_kernel<bf16_t>, grid, dim3(256), 0, s, job);
 }
 
 hipError_t launch_gather_transpose(int dtype, const GatherTransposeJobs& jobs, int64_t ldo,

@@ -101,31 +101,21 @@ int keep8(const Keep8& k, const void* saved, size_t off_gu, int64_t rows, int64_
   return TOPMOE_OK;
 }
 
-// Stage 0: the routing and the pairs from `kept`, and h row-major where the
-// backward will write [dg | du]; stage 1: h^T from it.
-int restore8(const Keep8& k, const void* kept, size_t off_gu, size_t off_h, size_t off_hT,
-             const GatherTransposeJobs& groups, int64_t rows, int64_t I, int dtype,
+// Stage 0: the routing from `kept` (empty for the dense FFN); stage 1: the pairs
+// and h^T.
+int restore8(const Keep8& k, const void* kept, size_t off_gu, size_t off_hT,
+             const int32_t* offsets, int E, int64_t rows, int64_t I, int64_t ldk, int dtype,
              void* workspace, void* stream, void* const* stage_events) {
   const uint8_t* kp = static_cast<const uint8_t*>(kept);
   char* ws = static_cast<char*>(workspace);
   const Stages st{stage_events, static_cast<hipStream_t>(stream)};
   const Launch l0 = st.at(0);
-  Launch first = l0, second = l0;
-  const bool both = k.routing > 0 && rows > 0;
-  if (both) first.stop = second.start = nullptr;
-  if (k.routing > 0) TOPMOE_TRY(launch_copy(kp, ws, k.routing, first));
-  if (rows > 0)
-    TOPMOE_TRY(launch_pairs_unpack(kp + k.gq, kp + k.gs, kp + k.uq, kp + k.us, rows, I, dtype,
-                                   ws + off_gu, ws + off_h, second));
-  l0.launched = first.launched || second.launched;
+  if (k.routing > 0) TOPMOE_TRY(launch_copy(kp, ws, k.routing, l0));
   TOPMOE_TRY(st.close(l0));
   const Launch l1 = st.at(1);
-  if (rows > 0) {
-    GatherTransposeJobs gj = groups;
-    gj.job[0] = GatherTransposeJob{ws + off_h, ws + off_hT, nullptr};
-    gj.n = 1;
-    TOPMOE_TRY(launch_gather_transpose(dtype, gj, gj.ldo, l1));
-  }
+  const Restore8Job job{kp + k.gq, kp + k.gs, kp + k.uq, kp + k.us, ws + off_gu, ws + off_hT,
+                        offsets, E, int(I), rows, ldk};
+  TOPMOE_TRY(launch_restore8(dtype, job, l1));
   TOPMOE_TRY(st.close(l1));
   return TOPMOE_OK;
 }
@@ -446,10 +436,8 @@ int ffn_swiglu_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t 
   const Keep8 k = plan_keep8(0, N, I);
   const int st = keep8_buffers(workspace, workspace_bytes, pl.total, kept, kept_bytes, k.total);
   if (st != TOPMOE_OK) return st;
-  GatherTransposeJobs gj{};
-  gj.E = 1; gj.k = 1; gj.C = int(I); gj.rows = N; gj.ldo = pl.ldk;
-  return restore8(k, kept, pl.off_gu, pl.off_dgdu, pl.off_hT, gj, N, I, dtype, workspace, stream,
-                  stage_events);
+  return restore8(k, kept, pl.off_gu, pl.off_hT, nullptr, 1, N, I, pl.ldk, dtype, workspace,
+                  stream, stage_events);
 }
 
 size_t moe_keep8_bytes(int64_t N, int64_t H, int64_t I, int E, int k, int dtype) {
@@ -479,11 +467,9 @@ int moe_ffn_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t H, 
   const Keep8 kp = plan_keep8(pl.off_wgT, pl.route.rows, I);
   const int st = keep8_buffers(workspace, workspace_bytes, pl.total, kept, kept_bytes, kp.total);
   if (st != TOPMOE_OK) return st;
-  GatherTransposeJobs gj{};  // grouped rows as they are, into the padded group columns
-  gj.offsets = reinterpret_cast<const int32_t*>(static_cast<char*>(workspace) +
-                                                pl.route.off_offsets);
-  gj.E = E; gj.k = k; gj.C = int(I); gj.rows = pl.route.rows; gj.ldo = pl.ldk;
-  return restore8(kp, kept, pl.off_gu, pl.off_dgdu, pl.off_hT, gj, pl.route.rows, I, dtype,
+  const int32_t* offsets = reinterpret_cast<const int32_t*>(static_cast<char*>(workspace) +
+                                                            pl.route.off_offsets);
+  return restore8(kp, kept, pl.off_gu, pl.off_hT, offsets, E, pl.route.rows, I, pl.ldk, dtype,
                   workspace, stream, stage_events);
 }
 

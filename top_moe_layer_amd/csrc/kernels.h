@@ -316,13 +316,20 @@ hipError_t launch_swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gs, const ui
                                   int dtype, void* dg, int64_t ldg, void* du, int64_t ldu, void* h,
                                   const Launch& s);
 
-// The (g, u) pairs [R, C] of a training forward's workspace to 8 bits and back
-// (and h = SiLU(g) u [R, C] of the kept values); a copy of whole 16-byte words.
+// The (g, u) pairs [R, C] of a training forward's workspace to 8 bits; back, as
+// the pairs and h^T in padded group columns (offsets as for the gathered
+// transposes); a copy of whole 16-byte words.
 hipError_t launch_pairs_pack(const void* pairs, int64_t R, int64_t C, int dtype, uint8_t* gq,
                              uint8_t* gs, uint8_t* uq, uint8_t* us, const Launch& s);
-hipError_t launch_pairs_unpack(const uint8_t* gq, const uint8_t* gs, const uint8_t* uq,
-                               const uint8_t* us, int64_t R, int64_t C, int dtype, void* pairs,
-                               void* h, const Launch& s);
+struct Restore8Job {
+  const uint8_t *gq, *gs, *uq, *us;
+  void* pairs;             // [rows, C]
+  void* hT;                // [C, ldo]
+  const int32_t* offsets;  // [E + 1] or NULL: one group of `rows`
+  int E, C;
+  int64_t rows, ldo;
+};
+hipError_t launch_restore8(int dtype, const Restore8Job& job, const Launch& s);
 hipError_t launch_copy(const void* src, void* dst, size_t bytes, const Launch& s);
 
 }  // namespace topmoe
