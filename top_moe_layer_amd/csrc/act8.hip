@@ -15,7 +15,10 @@
 //   dg = dh u s (1 + g (1 - s)),  du = dh g s,  h = g s u,  s = sigmoid(g)
 //                           (from the kept g, u; h for the down projection's
 //                            weight gradient)
-// Bound by memory.
+// Bound by memory: 16384 x 6464 bf16 on an MI355X, forward 137 us (854 MB, 6.2
+// TB/s), backward 180 us (1.07 GB, 5.9 TB/s), no byte moved twice.  Inputs are
+// read and kept bytes written non-temporally, the bytes being read again only
+// in the backward pass: 147 us with neither, 144 with h alone written so.
 #include "act8_impl.h"
 #include "kernels.h"
 #include "vec8.h"
