@@ -519,6 +519,60 @@ def test_deterministic_streams_and_graph(env, N, H, E, k, dt):
         torch.randn(1 << 16, device=dev).sum().item()
 
 
+def test_gpu_refusals(env):
+    """Calls that the front end or the library turns down before anything is launched."""
+    dev, tm = env
+    from top_moe_layer_amd import TopmoeError
+
+    x, w = torch.zeros(4, 64, device=dev), torch.zeros(64, device=dev)
+    idx = torch.zeros(4, 2, dtype=torch.int32, device=dev)
+    odd = torch.zeros(4 * 64 + 1, device=dev)[1:].view(4, 64)  # 4 bytes off its allocation
+    g8 = tm.act8_pack(x)
+    bad = [
+        (ValueError, lambda: tm.block_prenorm_fwd(x.t(), torch.zeros(4, device=dev))),
+        (ValueError, lambda: tm.block_prenorm_fwd(x, w[:32])),
+        (TypeError, lambda: tm.block_prenorm_fwd(x, w.to(torch.bfloat16))),
+        (TypeError, lambda: tm.block_prenorm_fwd(x.half(), w.half())),
+        (ValueError, lambda: tm.block_prenorm_fwd(x, w.cpu())),
+        (TopmoeError, lambda: tm.block_prenorm_fwd(odd, w)),
+        (TopmoeError, lambda: tm.block_prenorm_fwd(x, w, eps=0.0)),
+        (TopmoeError, lambda: tm.block_prenorm_fwd(x[:, :60].contiguous(), w[:60].contiguous())),
+        (ValueError, lambda: tm.block_postnorm_fwd(x, x, gate=torch.zeros(3, 64, device=dev))),
+        (ValueError, lambda: tm.block_postnorm_fwd(x, x, gate=torch.zeros(4, device=dev))),
+        (ValueError, lambda: tm.block_postnorm_fwd(x, x[:2])),
+        (ValueError, lambda: tm.block_postnorm_bwd(x, x, dn=x)),
+        (TypeError, lambda: tm.block_postnorm_bwd(x, x, w)),  # no rstd
+        (ValueError, lambda: tm.block_prenorm_bwd(x, x, w, torch.zeros(4, device=dev),
+                                                  workspace=torch.zeros(8, device=dev))),
+        (TypeError, lambda: tm.moe_dispatch_fwd(x, idx.long(), 4)),
+        (ValueError, lambda: tm.moe_dispatch_fwd(x, idx[:2], 4)),
+        (ValueError, lambda: tm.moe_dispatch_fwd(x, idx[:, 0], 4)),
+        (TopmoeError, lambda: tm.moe_dispatch_fwd(x, idx, 0)),
+        (TopmoeError, lambda: tm.moe_dispatch_fwd(x, idx, 10 ** 12)),
+        (TopmoeError, lambda: tm.moe_dispatch_fwd(x, idx, 1)),  # k > E
+        (TopmoeError, lambda: tm.moe_dispatch_fwd(x, idx, 4, capacity_factor=-1.0)),
+        (TopmoeError, lambda: tm.moe_dispatch_fwd(odd, idx, 4)),
+        (ValueError, lambda: tm.moe_combine_fwd(x, idx, torch.zeros(4, 2, device=dev))),  # 8 rows
+        (TypeError, lambda: tm.moe_combine_fwd(torch.zeros(8, 64, device=dev), idx,
+                                               torch.zeros(4, 2, device=dev).half())),
+        (ValueError, lambda: tm.act8_pack(x.t())),
+        (ValueError, lambda: tm.act8_pack(x.view(2, 2, 64))),
+        (ValueError, lambda: tm.act8_pack(x[:1].expand(4, 64))),
+        (TopmoeError, lambda: tm.act8_pack(x[:, :60])),
+        (TopmoeError, lambda: tm.act8_pack(x[:, 2:34])),  # rows that begin off 16 bytes
+        (ValueError, lambda: tm.act8_unpack(g8.q, g8.scale[:, :1])),
+        (TypeError, lambda: tm.act8_unpack(g8.q.view(torch.uint8), g8.scale)),
+        (ValueError, lambda: tm.swiglu_act8_bwd(x, g8, g8, dg=x)),
+        (TopmoeError, lambda: tm.ffn_swiglu_keep8(x, 4, 64, 64, torch.float32)),  # too small
+        (TopmoeError, lambda: tm.ffn_swiglu_keep8(x, 4, 64, 60, torch.float32)),
+    ]
+    for i, (err, call) in enumerate(bad):
+        with pytest.raises(err):
+            call()
+            raise AssertionError(f"call {i} was taken")
+    torch.cuda.synchronize()
+
+
 def test_stage_events(env):
     dev, tm = env
     for N in (16, 40000):  # one launch, three launches

@@ -7,7 +7,6 @@ from __future__ import annotations
 
 import functools
 import inspect
-from dataclasses import dataclass
 from typing import NamedTuple, Optional
 
 import torch
@@ -133,6 +132,8 @@ def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
         raise ValueError("topk_idx must be a [N, k] tensor")
     k = topk_idx.shape[1]
     _is(topk_idx, "topk_idx", (N, k), torch.int32, dev)
+    if not 1 <= E <= B.DISPATCH_MAX_EXPERTS:
+        B.check(B.ERR_BAD_SHAPE, "moe_dispatch_fwd")
     wp = wn = ws = None
     if workspace is not None or N * k > B.DISPATCH_ONE:
         nbytes = moe_dispatch_workspace_bytes(N, E, k)
@@ -141,7 +142,7 @@ def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
         xs = _empty(N * k, H, dtype=dt, device=dev)
     else:
         _is(xs, "xs", (N * k, H), dt, dev)
-    offsets = _empty(max(E, 0) + 1, dtype=torch.int32, device=dev)
+    offsets = _empty(E + 1, dtype=torch.int32, device=dev)
     row_entry = _empty(N * k, dtype=torch.int32, device=dev)
     entry_row = torch.empty_like(topk_idx)
     _call("moe_dispatch_fwd", dev, stage_events, x.data_ptr(), topk_idx.data_ptr(), N, H, E, k,

@@ -29,7 +29,7 @@ namespace topmoe {
 
 namespace {
 
-constexpr bool kNtLoad = true, kNtKeep = true;
+constexpr bool kNtLoad = true, kNtKeep = true;  // non-temporal, see above
 
 __device__ __forceinline__ void load_q8(const uint8_t* p, uint32_t (&q)[2]) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

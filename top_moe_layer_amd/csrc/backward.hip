@@ -220,8 +220,9 @@ __global__ __launch_bounds__(256) void restore8_kernel(Restore8Job jb) {
   for (int i = 0; i < 2; ++i) {
     const int id = tid + 256 * i, l = id / 8, c0 = (id & 7) * 8;
     float h[8];
-    if (local0 + l < cnt) {
-      const int64_t o = int64_t(gfirst + local0 + l) * jb.C + h0 + c0;
+    const int64_t row = int64_t(gfirst) + local0 + l;
+    if (local0 + l < cnt && row >= 0 && row < jb.rows) {  // (offsets come from the kept bytes)
+      const int64_t o = row * jb.C + h0 + c0;
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
       const u32x2 qg = *reinterpret_cast<const u32x2*>(jb.gq + o);
       const u32x2 qu = *reinterpret_cast<const u32x2*>(jb.uq + o);
