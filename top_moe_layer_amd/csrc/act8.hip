@@ -9,8 +9,9 @@
 // element that is not finite is stored as NaN and takes no part in the scale:
 // a diverged activation stays visible in the gradients.
 //
-// One thread moves 8 channels; the four threads of a group find its largest
-// magnitude with two lane exchanges.  SwiGLU with its two operands kept:
+// One thread moves 16 bytes of an activation, 8 bf16 or 4 fp32 channels; the
+// four or eight threads of a group find its largest magnitude with two or three
+// lane exchanges.  SwiGLU with its two operands kept:
 //   h  = SiLU(g) u          (from g, u as they came)
 //   dg = dh u s (1 + g (1 - s)),  du = dh g s,  h = g s u,  s = sigmoid(g)
 //                           (from the kept g, u; h for the down projection's
@@ -21,7 +22,7 @@
 // in the backward pass: 147 us with neither, 144 with h alone written so.
 #include "act8_impl.h"
 #include "kernels.h"
-#include "vec8.h"
+#include "vec16.h"
 
 #include "../../include/topmoe.h"
 
@@ -31,57 +32,63 @@ namespace {
 
 constexpr bool kNtLoad = true, kNtKeep = true;  // non-temporal, see above
 
-__device__ __forceinline__ void load_q8(const uint8_t* p, uint32_t (&q)[2]) {
+__device__ __forceinline__ void load_q(const uint8_t* p, uint32_t (&q)[2]) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   const u32x2 v = load_vec<kNtLoad, u32x2>(p);
   q[0] = v.x;
   q[1] = v.y;
 }
-__device__ __forceinline__ void store_q8(uint8_t* p, const uint32_t (&q)[2]) {
+__device__ __forceinline__ void load_q(const uint8_t* p, uint32_t (&q)[1]) {
+  q[0] = load_vec<kNtLoad, uint32_t>(p);
+}
+__device__ __forceinline__ void store_q(uint8_t* p, const uint32_t (&q)[2]) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   store_vec<kNtKeep, u32x2>(p, u32x2{q[0], q[1]});
+}
+__device__ __forceinline__ void store_q(uint8_t* p, const uint32_t (&q)[1]) {
+  store_vec<kNtKeep, uint32_t>(p, q[0]);
 }
 
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
 }
 
-// The thread's row and piece: pieces of 8 channels, a row's pieces padded to
-// whole groups (pp = 4 ceil(C / 32)), so that a quad of lanes is one group.
+// The thread's row and piece: pieces of E channels, a row's pieces padded to
+// whole groups (pp = ceil(C / 32) groups of L lanes).
+template <typename T>
 struct Place {
+  static constexpr int E = kE<T>, L = kGroupLanes<kE<T>>;
   int64_t r;
   int p;
   bool any, in;  // any: within the launch's rows; in: and within the row
+  uint32_t groups;
+  __device__ __forceinline__ Place(int64_t r0, uint32_t pieces, uint32_t pp, int C) {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t dr = i / pp;
+    r = r0 + dr;
+    p = int(i - dr * pp);
+    any = i < pieces;
+    in = any && p < C / E;
+    groups = pp / L;
+  }
+  __device__ __forceinline__ int64_t at(int64_t pitch) const { return r * pitch + int64_t(p) * E; }
+  __device__ __forceinline__ int64_t group() const { return r * groups + p / L; }
+  __device__ __forceinline__ bool first() const { return any && p % L == 0; }
 };
-__device__ __forceinline__ Place place(int64_t r0, uint32_t pieces, uint32_t pp, int cv) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t dr = i / pp;
-  Place a;
-  a.r = r0 + dr;
-  a.p = int(i - dr * pp);
-  a.any = i < pieces;
-  a.in = a.any && a.p < cv;
-  return a;
-}
-
-template <typename T>
-__device__ __forceinline__ void load_or_zero(const T* p, bool in, float (&v)[8]) {
-  const Raw8<T> raw = in ? load_raw8<T, kNtLoad>(p) : zero_raw8<T>();
-  unpack8(raw, v);
-}
 
 template <typename T>
 __global__ __launch_bounds__(256) void act8_pack_kernel(const T* __restrict__ x, int64_t ldx,
                                                         int64_t r0, uint32_t pieces, uint32_t pp,
                                                         int C, uint8_t* __restrict__ q,
                                                         uint8_t* __restrict__ scale) {
-  const Place a = place(r0, pieces, pp, C / 8);
-  float v[8];
-  load_or_zero<T>(x + a.r * ldx + a.p * 8, a.in, v);
-  uint32_t b[2];
-  const uint32_t s = pack8(v, b);
-  if (a.in) store_q8(q + a.r * C + a.p * 8, b);
-  if (a.any && (a.p & 3) == 0) scale[a.r * (pp / 4) + a.p / 4] = uint8_t(s);
+  const Place<T> a(r0, pieces, pp, C);
+  constexpr int E = kE<T>;
+  float v[E];
+  unpack(load_piece_if<kNtLoad>(a.in, x + a.at(ldx)), v);
+  uint32_t b[E / 4];
+  const uint32_t s = pack_q<E>(v, b);
+  if (a.in) store_q(q + a.at(C), b);
+  if (a.first()) scale[a.group()] = uint8_t(s);
 }
 
 template <typename T, bool NT>
@@ -90,13 +97,14 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const uint8_t* __restr
                                                           int64_t r0, uint32_t pieces,
                                                           uint32_t pp, int C, T* __restrict__ x,
                                                           int64_t ldx) {
-  const Place a = place(r0, pieces, pp, C / 8);
+  const Place<T> a(r0, pieces, pp, C);
+  constexpr int E = kE<T>;
   if (!a.in) return;
-  uint32_t b[2];
-  load_q8(q + a.r * C + a.p * 8, b);
-  float v[8];
-  unpack_q8(b, scale_of(scale[a.r * (pp / 4) + a.p / 4]), v);
-  store8<T, NT>(x + a.r * ldx + a.p * 8, v);
+  uint32_t b[E / 4];
+  load_q(q + a.at(C), b);
+  float v[E];
+  unpack_q<E>(b, scale_of(scale[a.group()]), v);
+  store_piece<NT>(x + a.at(ldx), v);
 }
 
 template <typename T, bool NT>
@@ -104,24 +112,24 @@ __global__ __launch_bounds__(256) void swiglu_act8_fwd_kernel(
     const T* __restrict__ g, const T* __restrict__ u, int64_t ldg, int64_t ldu, int64_t r0,
     uint32_t pieces, uint32_t pp, int C, T* __restrict__ h, uint8_t* __restrict__ gq, uint8_t* __restrict__ gs,
     uint8_t* __restrict__ uq, uint8_t* __restrict__ us) {
-  const Place a = place(r0, pieces, pp, C / 8);
-  float vg[8], vu[8], vh[8];
-  load_or_zero<T>(g + a.r * ldg + a.p * 8, a.in, vg);
-  load_or_zero<T>(u + a.r * ldu + a.p * 8, a.in, vu);
-  uint32_t bg[2], bu[2];
-  const uint32_t sg = pack8(vg, bg), su = pack8(vu, bu);
-  const int64_t o = a.r * C + a.p * 8;
+  const Place<T> a(r0, pieces, pp, C);
+  constexpr int E = kE<T>;
+  float vg[E], vu[E], vh[E];
+  unpack(load_piece_if<kNtLoad>(a.in, g + a.at(ldg)), vg);
+  unpack(load_piece_if<kNtLoad>(a.in, u + a.at(ldu)), vu);
+  uint32_t bg[E / 4], bu[E / 4];
+  const uint32_t sg = pack_q<E>(vg, bg), su = pack_q<E>(vu, bu);
+  const int64_t o = a.at(C);
   if (a.in) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) vh[i] = silu_mul(vg[i], vu[i]);
-    store8<T, NT>(h + o, vh);
-    store_q8(gq + o, bg);
-    store_q8(uq + o, bu);
+    for (int i = 0; i < E; ++i) vh[i] = silu_mul(vg[i], vu[i]);
+    store_piece<NT>(h + o, vh);
+    store_q(gq + o, bg);
+    store_q(uq + o, bu);
   }
-  if (a.any && (a.p & 3) == 0) {
-    const int64_t i = a.r * (pp / 4) + a.p / 4;
-    gs[i] = uint8_t(sg);
-    us[i] = uint8_t(su);
+  if (a.first()) {
+    gs[a.group()] = uint8_t(sg);
+    us[a.group()] = uint8_t(su);
   }
 }
 
@@ -131,33 +139,34 @@ __global__ __launch_bounds__(256) void swiglu_act8_bwd_kernel(
     const uint8_t* __restrict__ uq, const uint8_t* __restrict__ us, const T* __restrict__ dh,
     int64_t r0, uint32_t pieces, uint32_t pp, int C, T* __restrict__ dg,
     int64_t ldg, T* __restrict__ du, int64_t ldu, T* __restrict__ h) {
-  const Place a = place(r0, pieces, pp, C / 8);
+  const Place<T> a(r0, pieces, pp, C);
+  constexpr int E = kE<T>;
   if (!a.in) return;
-  const int64_t o = a.r * C + a.p * 8, si = a.r * (pp / 4) + a.p / 4;
-  uint32_t bg[2], bu[2];
-  load_q8(gq + o, bg);
-  load_q8(uq + o, bu);
-  float vg[8], vu[8], vd[8];
-  const Raw8<T> raw = load_raw8<T, kNtLoad>(dh + o);
-  unpack_q8(bg, scale_of(gs[si]), vg);
-  unpack_q8(bu, scale_of(us[si]), vu);
-  unpack8(raw, vd);
-  float og[8], ou[8], oh[8];
+  const int64_t o = a.at(C), si = a.group();
+  uint32_t bg[E / 4], bu[E / 4];
+  load_q(gq + o, bg);
+  load_q(uq + o, bu);
+  float vg[E], vu[E], vd[E];
+  const u32x4 raw = load_piece<kNtLoad>(dh + o);
+  unpack_q<E>(bg, scale_of(gs[si]), vg);
+  unpack_q<E>(bu, scale_of(us[si]), vu);
+  unpack(raw, vd);
+  float og[E], ou[E], oh[E];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < E; ++i) {
     const float s = sigmoid(vg[i]), gsig = vg[i] * s;
     ou[i] = vd[i] * gsig;
     oh[i] = gsig * vu[i];
     og[i] = vd[i] * vu[i] * (s * (1.0f + vg[i] * (1.0f - s)));
   }
-  store8<T, NT>(dg + a.r * ldg + a.p * 8, og);
-  store8<T, NT>(du + a.r * ldu + a.p * 8, ou);
-  if (h != nullptr) store8<T, NT>(h + o, oh);
+  store_piece<NT>(dg + a.at(ldg), og);
+  store_piece<NT>(du + a.at(ldu), ou);
+  if (h != nullptr) store_piece<NT>(h + o, oh);
 }
 
 // ---- the (g, u) pairs of a training forward's workspace ----------------------
-// Eight pairs: 32 bytes of bf16 (g in the low halves), 64 of fp32.
-__device__ __forceinline__ void load_pairs8(const bf16_t* p, float (&g)[8], float (&u)[8]) {
+// A thread's pairs: 32 bytes, g in the low halves of bf16's words.
+__device__ __forceinline__ void load_pairs(const bf16_t* p, float (&g)[8], float (&u)[8]) {
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const u32x4 q = load_vec<true, u32x4>(p + 8 * w);
@@ -165,9 +174,9 @@ __device__ __forceinline__ void load_pairs8(const bf16_t* p, float (&g)[8], floa
     for (int i = 0; i < 4; ++i) PairWord<bf16_t>::unpack(q[i], g[4 * w + i], u[4 * w + i]);
   }
 }
-__device__ __forceinline__ void load_pairs8(const float* p, float (&g)[8], float (&u)[8]) {
+__device__ __forceinline__ void load_pairs(const float* p, float (&g)[4], float (&u)[4]) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < 2; ++w) {
     const f32x4 q = load_vec<true, f32x4>(p + 4 * w);
     g[2 * w] = q.x; u[2 * w] = q.y;
     g[2 * w + 1] = q.z; u[2 * w + 1] = q.w;
@@ -180,23 +189,24 @@ __global__ __launch_bounds__(256) void pairs_pack_kernel(
     const T* __restrict__ pairs, int64_t r0, uint32_t pieces, uint32_t pp, int C,
     uint8_t* __restrict__ gq, uint8_t* __restrict__ gs, uint8_t* __restrict__ uq,
     uint8_t* __restrict__ us) {
-  const Place a = place(r0, pieces, pp, C / 8);
-  const int64_t o = a.r * C + a.p * 8;
-  float g[8], u[8];
+  const Place<T> a(r0, pieces, pp, C);
+  constexpr int E = kE<T>;
+  const int64_t o = a.at(C);
+  float g[E], u[E];
   if (a.in) {
-    load_pairs8(pairs + 2 * o, g, u);
+    load_pairs(pairs + 2 * o, g, u);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = u[i] = 0.f;
+    for (int i = 0; i < E; ++i) g[i] = u[i] = 0.f;
   }
-  uint32_t bg[2], bu[2];
-  const uint32_t sg = pack8(g, bg), su = pack8(u, bu);
+  uint32_t bg[E / 4], bu[E / 4];
+  const uint32_t sg = pack_q<E>(g, bg), su = pack_q<E>(u, bu);
   if (!a.in) return;
-  store_q8(gq + o, bg);
-  store_q8(uq + o, bu);
-  if ((a.p & 3) == 0) {
-    gs[o / kAct8Group] = uint8_t(sg);
-    us[o / kAct8Group] = uint8_t(su);
+  store_q(gq + o, bg);
+  store_q(uq + o, bu);
+  if (a.first()) {
+    gs[a.group()] = uint8_t(sg);
+    us[a.group()] = uint8_t(su);
   }
 }
 
@@ -209,9 +219,9 @@ __global__ __launch_bounds__(256) void copy_kernel(const u32x4* __restrict__ src
 
 // Launches over slabs of rows of at most 2^30 pieces, so that piece numbers
 // stay in 32 bits and a grid within its limit of threads.
-template <typename F>
+template <typename T, typename F>
 hipError_t for_slabs(int64_t R, int64_t C, const Launch& s, F launch) {
-  const uint32_t pp = uint32_t((C + kAct8Group - 1) / kAct8Group * 4);
+  const uint32_t pp = uint32_t((C + kAct8Group - 1) / kAct8Group * Place<T>::L);
   int64_t slab = (int64_t(1) << 30) / pp;
   if (slab < 1) slab = 1;
   for (int64_t r0 = 0; r0 < R; r0 += slab) {
@@ -229,19 +239,19 @@ hipError_t for_slabs(int64_t R, int64_t C, const Launch& s, F launch) {
 
 }  // namespace
 
-#define TOPMOE_ACT8(KERNEL, ...)                                                                 \
-  for_slabs(R, C, s, [&](dim3 grid, int64_t r0, uint32_t pieces, uint32_t pp, const Launch& L) { \
-    return launch_kernel(KERNEL, grid, dim3(256), 0, L, __VA_ARGS__);                            \
+#define TOPMOE_ACT8(T, KERNEL, ...)                                                                \
+  for_slabs<T>(R, C, s, [&](dim3 grid, int64_t r0, uint32_t pieces, uint32_t pp, const Launch& L) { \
+    return launch_kernel(KERNEL, grid, dim3(256), 0, L, __VA_ARGS__);                              \
   })
 // KERNEL<T, NT> by the outputs' bytes.
-#define TOPMOE_ACT8_NT(T, KERNEL, BYTES, ...)                     \
-  return (BYTES) >= kNtBytes ? TOPMOE_ACT8((KERNEL<T, true>), __VA_ARGS__)  \
-                            : TOPMOE_ACT8((KERNEL<T, false>), __VA_ARGS__)
+#define TOPMOE_ACT8_NT(T, KERNEL, BYTES, ...)                                 \
+  return (BYTES) >= kNtBytes ? TOPMOE_ACT8(T, (KERNEL<T, true>), __VA_ARGS__) \
+                             : TOPMOE_ACT8(T, (KERNEL<T, false>), __VA_ARGS__)
 
 namespace {
 
 template <typename T>
-hipError_t unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C, void* x,
+hipError_t unpack_typed(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C, void* x,
                   int64_t ldx, const Launch& s) {
   TOPMOE_ACT8_NT(T, act8_unpack_kernel, R * C * int64_t(sizeof(T)), q, scale, r0, pieces, pp,
                  int(C), static_cast<T*>(x), ldx);
@@ -270,16 +280,16 @@ hipError_t swiglu_bwd(const uint8_t* gq, const uint8_t* gs, const uint8_t* uq, c
 hipError_t launch_act8_pack(const void* x, int64_t ldx, int64_t R, int64_t C, int dtype,
                             uint8_t* q, uint8_t* scale, const Launch& s) {
   if (dtype == TOPMOE_DTYPE_FP32)
-    return TOPMOE_ACT8(act8_pack_kernel<float>, static_cast<const float*>(x), ldx, r0, pieces, pp,
+    return TOPMOE_ACT8(float, act8_pack_kernel<float>, static_cast<const float*>(x), ldx, r0, pieces, pp,
                        int(C), q, scale);
-  return TOPMOE_ACT8(act8_pack_kernel<bf16_t>, static_cast<const bf16_t*>(x), ldx, r0, pieces, pp,
+  return TOPMOE_ACT8(bf16_t, act8_pack_kernel<bf16_t>, static_cast<const bf16_t*>(x), ldx, r0, pieces, pp,
                      int(C), q, scale);
 }
 
 hipError_t launch_act8_unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C,
                               int dtype, void* x, int64_t ldx, const Launch& s) {
-  return dtype == TOPMOE_DTYPE_FP32 ? unpack<float>(q, scale, R, C, x, ldx, s)
-                                    : unpack<bf16_t>(q, scale, R, C, x, ldx, s);
+  return dtype == TOPMOE_DTYPE_FP32 ? unpack_typed<float>(q, scale, R, C, x, ldx, s)
+                                    : unpack_typed<bf16_t>(q, scale, R, C, x, ldx, s);
 }
 
 hipError_t launch_swiglu_act8_fwd(const void* g, int64_t ldg, const void* u, int64_t ldu,
@@ -302,9 +312,9 @@ hipError_t launch_swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gs, const ui
 hipError_t launch_pairs_pack(const void* pairs, int64_t R, int64_t C, int dtype, uint8_t* gq,
                              uint8_t* gs, uint8_t* uq, uint8_t* us, const Launch& s) {
   if (dtype == TOPMOE_DTYPE_FP32)
-    return TOPMOE_ACT8(pairs_pack_kernel<float>, static_cast<const float*>(pairs), r0, pieces, pp,
+    return TOPMOE_ACT8(float, pairs_pack_kernel<float>, static_cast<const float*>(pairs), r0, pieces, pp,
                        int(C), gq, gs, uq, us);
-  return TOPMOE_ACT8(pairs_pack_kernel<bf16_t>, static_cast<const bf16_t*>(pairs), r0, pieces, pp,
+  return TOPMOE_ACT8(bf16_t, pairs_pack_kernel<bf16_t>, static_cast<const bf16_t*>(pairs), r0, pieces, pp,
                      int(C), gq, gs, uq, us);
 }
 

@@ -228,8 +228,8 @@ __global__ __launch_bounds__(256) void restore8_kernel(Restore8Job jb) {
       const u32x2 qu = *reinterpret_cast<const u32x2*>(jb.uq + o);
       const uint32_t bg[2] = {qg.x, qg.y}, bu[2] = {qu.x, qu.y};
       float g[8], u[8];
-      unpack_q8(bg, scale_of(jb.gs[o / kAct8Group]), g);
-      unpack_q8(bu, scale_of(jb.us[o / kAct8Group]), u);
+      unpack_q<8>(bg, scale_of(jb.gs[o / kAct8Group]), g);
+      unpack_q<8>(bu, scale_of(jb.us[o / kAct8Group]), u);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         float gw[4], uw[4];

@@ -41,6 +41,8 @@ int kept_entries(double capacity_factor, int64_t N, int k, int E) {
 }
 
 // ---- norms
+int pieces(int64_t H, int dtype) { return int(H / (dtype == TOPMOE_DTYPE_FP32 ? 4 : 8)); }
+
 int norm_shape(int64_t N, int64_t H, int64_t gate_rows) {
   if (N < 0 || N > kMaxRows) return TOPMOE_ERR_BAD_SHAPE;
   if (H <= 0 || H % 8 != 0 || H > kNormMaxH) return TOPMOE_ERR_BAD_SHAPE;
@@ -227,7 +229,7 @@ int block_prenorm_fwd(const void* x, const void* w, int64_t N, int64_t H, float 
     return TOPMOE_ERR_BAD_ARG;
   NormFwd a{};
   a.y = x; a.next_w = w; a.n = n; a.next_rstd = rstd;
-  a.N = N; a.H = int(H); a.hv = int(H / 8); a.eps = eps; a.gate_span = 1;
+  a.N = N; a.H = int(H); a.hv = pieces(H, dtype); a.eps = eps; a.gate_span = 1;
   const Stages st{stage_events, static_cast<hipStream_t>(stream)};
   const Launch L = st.at(0);
   TOPMOE_TRY(launch_norm_fwd(a, false, true, dtype, L));
@@ -237,7 +239,13 @@ int block_prenorm_fwd(const void* x, const void* w, int64_t N, int64_t H, float 
 
 size_t block_norm_bwd_workspace_bytes(int64_t N, int64_t H, int64_t gate_rows) {
   if (norm_shape(N, H, gate_rows) != TOPMOE_OK) return 0;
-  return norm_bwd_bytes(plan_norm_units(N, H, gate_rows, span_of(N, gate_rows)), H);
+  size_t most = 0;  // of the two types
+  for (int dtype : {TOPMOE_DTYPE_FP32, TOPMOE_DTYPE_BF16}) {
+    const NormUnits u = plan_norm_units(N, pieces(H, dtype), gate_rows, span_of(N, gate_rows));
+    const size_t b = norm_bwd_bytes(u, H);
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 int block_prenorm_bwd(const void* dn, const void* x, const void* w, const float* rstd,
@@ -250,14 +258,14 @@ int block_prenorm_bwd(const void* dn, const void* x, const void* w, const float*
   if (!w || !dw || !workspace || (N > 0 && (!dn || !x || !rstd || !dx))) return TOPMOE_ERR_NULL_ARG;
   NormBwd a{};
   a.gate_span = span_of(N, 1);
-  a.units = plan_norm_units(N, H, 1, a.gate_span);
+  a.units = plan_norm_units(N, pieces(H, dtype), 1, a.gate_span);
   if (workspace_bytes < norm_bwd_bytes(a.units, H)) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(dn, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(rstd, 4) ||
       !aligned(dresidual, 16) || !aligned(dx, 16) || !aligned(dw, 16) || !aligned(workspace, 256))
     return TOPMOE_ERR_BAD_ARG;
   a.dout = dresidual; a.dn = dn; a.out = x; a.next_w = w; a.next_rstd = rstd;
   a.dy = dx; a.dnext_w = dw; a.part_next = static_cast<float*>(workspace);
-  a.N = N; a.gate_rows = 1; a.H = int(H); a.hv = int(H / 8);
+  a.N = N; a.gate_rows = 1; a.H = int(H); a.hv = pieces(H, dtype);
   const Stages st{stage_events, static_cast<hipStream_t>(stream)};
   const Launch rows = st.at(0), sums = st.at(1);
   TOPMOE_TRY(launch_norm_bwd(a, false, true, dtype, rows, sums));
@@ -287,7 +295,7 @@ int block_postnorm_fwd(const void* y, const void* residual, const void* w, const
   NormFwd a{};
   a.y = y; a.residual = residual; a.w = w; a.gate = gate; a.next_w = next_w;
   a.out = out; a.n = n; a.rstd = rstd; a.next_rstd = next_rstd;
-  a.N = N; a.H = int(H); a.hv = int(H / 8); a.gate_mode = gate_mode;
+  a.N = N; a.H = int(H); a.hv = pieces(H, dtype); a.gate_mode = gate_mode;
   a.gate_span = span_of(N, gate_mode == kGateChannel ? gate_rows : 1);
   a.scale = residual_scale; a.eps = eps;
   const Stages st{stage_events, static_cast<hipStream_t>(stream)};
@@ -320,7 +328,7 @@ int block_postnorm_bwd(const void* dout, const void* dn, const void* y, const vo
   NormBwd a{};
   a.gate_rows = channel ? gate_rows : 1;
   a.gate_span = span_of(N, a.gate_rows);
-  a.units = plan_norm_units(N, H, a.gate_rows, a.gate_span);
+  a.units = plan_norm_units(N, pieces(H, dtype), a.gate_rows, a.gate_span);
   if (workspace_bytes < norm_bwd_bytes(a.units, H)) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(dout, 16) || !aligned(dn, 16) || !aligned(y, 16) || !aligned(out, 16) ||
       !aligned(w, 16) || !aligned(gate, channel ? 16 : 4) || !aligned(next_w, 16) ||
@@ -334,7 +342,7 @@ int block_postnorm_bwd(const void* dout, const void* dn, const void* y, const vo
   float* part = static_cast<float*>(workspace);
   a.part = w || channel ? part : nullptr;
   a.part_next = part + size_t(a.units.count / a.units.blocks_of) * size_t(H);
-  a.N = N; a.H = int(H); a.hv = int(H / 8); a.gate_mode = gate_mode; a.scale = residual_scale;
+  a.N = N; a.H = int(H); a.hv = pieces(H, dtype); a.gate_mode = gate_mode; a.scale = residual_scale;
   const Stages st{stage_events, static_cast<hipStream_t>(stream)};
   const Launch rows = st.at(0), sums = st.at(1);
   TOPMOE_TRY(launch_norm_bwd(a, true, next_w != nullptr, dtype, rows, sums));

@@ -262,7 +262,7 @@ struct NormFwd {
   float* next_rstd;      // [N]
   int64_t N, t0;         // t0: first row of this launch
   int64_t gate_span;     // tokens that share a gate row
-  int H, hv, gate_mode;  // hv = H / 8
+  int H, hv, gate_mode;  // hv: 16-byte pieces of a row
   float scale, eps;
 };
 hipError_t launch_norm_fwd(const NormFwd& a, bool post, bool next, int dtype, const Launch& s);
@@ -275,7 +275,7 @@ struct NormUnits {
   int64_t per_group = 0, count = 0;
   int blocks_of = 1;
 };
-NormUnits plan_norm_units(int64_t N, int64_t H, int64_t gate_rows, int64_t gate_span);
+NormUnits plan_norm_units(int64_t N, int64_t hv, int64_t gate_rows, int64_t gate_span);
 struct NormBwd {
   const void* dout;         // [N, H] or NULL: 0
   const void* dn;           // [N, H]

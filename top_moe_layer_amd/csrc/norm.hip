@@ -12,7 +12,7 @@
 //   dy   = rstd_y * (b - yh * mean(b * yh))  (no norm: b)
 //   dw   = sum_t gate * dr * yh,   dgate = the sum of w * dr * yh over what shares the gate
 //
-// R threads per row, V pieces of 8 channels each: a block of R / 64 wavefronts,
+// R threads per row, V pieces of 16 bytes each: a block of R / 64 wavefronts,
 // or for narrow rows a wavefront or a part of one, 256 / R rows a block.  The
 // row stays in registers between its statistics and its use, so every tensor
 // is read once and written once.  Bound by memory: post norm with a channel
@@ -29,7 +29,7 @@
 // hold whole groups, whose dgate they then write themselves (the partial sums
 // are of gate * dr * yh).
 #include "kernels.h"
-#include "vec8.h"
+#include "vec16.h"
 
 #include "../../include/topmoe.h"
 
@@ -65,8 +65,8 @@ __device__ __forceinline__ float row_sum(float v, float (&slot)[2][W], int& turn
 }
 
 template <typename T>
-__device__ __forceinline__ void load_f(const T* p, float (&v)[8]) {
-  unpack8(load_raw8<T>(p), v);
+__device__ __forceinline__ void load_f(const T* p, float (&v)[kE<T>]) {
+  unpack(load_piece(p), v);
 }
 
 // POST: the norm after the block with gate and residual (else r = y = x).
@@ -74,37 +74,38 @@ __device__ __forceinline__ void load_f(const T* p, float (&v)[8]) {
 // the rows read as well: 48.3 -> 45.7 us of the 16384 x 2048 post norm).
 template <typename T, int R, int V, bool POST, bool NEXT, bool NT>
 __global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
+  constexpr int E = kE<T>;
   __shared__ float slot[2][kWaves<R>];
   const int lane = int(threadIdx.x) % R, wave = int(threadIdx.x >> 6);
   const int64_t t = a.t0 + int64_t(blockIdx.x) * kSide<R> + int(threadIdx.x) / R;
   if (kSide<R> > 1 && t >= a.N) return;
   int turn = 0;
   const T* y = static_cast<const T*>(a.y) + t * a.H;
-  Raw8<T> yr[V];
+  u32x4 yr[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int p = lane + v * R;
-    yr[v] = p < a.hv ? load_raw8<T, NT>(y + p * 8) : zero_raw8<T>();
+    yr[v] = load_piece_if<NT>(p < a.hv, y + p * E);
   }
   const float inv_h = 1.0f / float(a.H);
-  float rs[V][8];  // r
+  float rs[V][E];  // r
   if constexpr (POST) {
-    Raw8<T> res[V];
+    u32x4 res[V];
     const T* rp = static_cast<const T*>(a.residual) + t * a.H;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * R;
-      res[v] = p < a.hv ? load_raw8<T, NT>(rp + p * 8) : zero_raw8<T>();
+      res[v] = load_piece_if<NT>(p < a.hv, rp + p * E);
     }
     float rstd = 1.f;
     if (a.w != nullptr) {
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float f[8];
-        unpack8(yr[v], f);
+        float f[E];
+        unpack(yr[v], f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) s = fmaf(f[c], f[c], s);
+        for (int c = 0; c < E; ++c) s = fmaf(f[c], f[c], s);
       }
       rstd = 1.0f / sqrtf(row_sum<R>(s, slot, turn, wave) * inv_h + a.eps);
       if (lane == 0) a.rstd[t] = rstd;
@@ -117,43 +118,43 @@ __global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * R;
-      float f[8], q[8];
-      unpack8(yr[v], f);
-      unpack8(res[v], q);
+      float f[E], q[E];
+      unpack(yr[v], f);
+      unpack(res[v], q);
       if (p < a.hv) {
-        float m[8];
+        float m[E];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) m[c] = rstd * gt;
+        for (int c = 0; c < E; ++c) m[c] = rstd * gt;
         if (a.w != nullptr) {
-          float w[8];
-          load_f<T>(static_cast<const T*>(a.w) + p * 8, w);
+          float w[E];
+          load_f<T>(static_cast<const T*>(a.w) + p * E, w);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) m[c] *= w[c];
+          for (int c = 0; c < E; ++c) m[c] *= w[c];
         }
         if (gp != nullptr) {
-          float g[8];
-          load_f<T>(gp + p * 8, g);
+          float g[E];
+          load_f<T>(gp + p * E, g);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) m[c] *= g[c];
+          for (int c = 0; c < E; ++c) m[c] *= g[c];
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) rs[v][c] = fmaf(f[c], m[c], a.scale * q[c]);
-        store8<T, NT>(out + p * 8, rs[v]);
+        for (int c = 0; c < E; ++c) rs[v][c] = fmaf(f[c], m[c], a.scale * q[c]);
+        store_piece<NT>(out + p * E, rs[v]);
       } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) rs[v][c] = 0.f;
+        for (int c = 0; c < E; ++c) rs[v][c] = 0.f;
       }
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) unpack8(yr[v], rs[v]);
+    for (int v = 0; v < V; ++v) unpack(yr[v], rs[v]);
   }
   if constexpr (NEXT) {
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) s = fmaf(rs[v][c], rs[v][c], s);
+      for (int c = 0; c < E; ++c) s = fmaf(rs[v][c], rs[v][c], s);
     const float rstd = 1.0f / sqrtf(row_sum<R>(s, slot, turn, wave) * inv_h + a.eps);
     if (lane == 0) a.next_rstd[t] = rstd;
     T* n = static_cast<T*>(a.n) + t * a.H;
@@ -161,39 +162,39 @@ __global__ __launch_bounds__(kThreads<R>) void norm_fwd_kernel(NormFwd a) {
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * R;
       if (p >= a.hv) continue;
-      float w[8];
-      load_f<T>(static_cast<const T*>(a.next_w) + p * 8, w);
+      float w[E];
+      load_f<T>(static_cast<const T*>(a.next_w) + p * E, w);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) w[c] = rs[v][c] * rstd * w[c];
-      store8<T, NT>(n + p * 8, w);
+      for (int c = 0; c < E; ++c) w[c] = rs[v][c] * rstd * w[c];
+      store_piece<NT>(n + p * E, w);
     }
   }
 }
 
 // What one row of the backward pass reads, as loaded.
-template <typename T, int V, bool POST, bool NEXT>
+template <int V>
 struct BwdRow {
-  Raw8<T> dout[V], y[V], out[V], dn[V];
+  u32x4 dout[V], y[V], out[V], dn[V];
   float rstd, next_rstd, gate;  // gate: of a token gate
 };
 
 template <typename T, int R, int V, bool POST, bool NEXT>
 __device__ __forceinline__ void load_row(const NormBwd& a, int64_t t, int lane,
-                                         BwdRow<T, V, POST, NEXT>& r) {
+                                         BwdRow<V>& r) {
+  constexpr int E = kE<T>;
   const int64_t row = t * a.H;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int p = lane + v * R;
     const bool in = p < a.hv;
-    const int64_t at = row + p * 8;
+    const int64_t at = row + p * E;
     if constexpr (NEXT) {
-      r.out[v] = in ? load_raw8<T, true>(static_cast<const T*>(a.out) + at) : zero_raw8<T>();
-      r.dn[v] = in ? load_raw8<T, true>(static_cast<const T*>(a.dn) + at) : zero_raw8<T>();
+      r.out[v] = load_piece_if<true>(in, static_cast<const T*>(a.out) + at);
+      r.dn[v] = load_piece_if<true>(in, static_cast<const T*>(a.dn) + at);
     }
-    r.dout[v] = in && a.dout != nullptr ? load_raw8<T, true>(static_cast<const T*>(a.dout) + at)
-                                        : zero_raw8<T>();
+    r.dout[v] = load_piece_if<true>(in && a.dout != nullptr, static_cast<const T*>(a.dout) + at);
     if constexpr (POST)
-      r.y[v] = in ? load_raw8<T, true>(static_cast<const T*>(a.y) + at) : zero_raw8<T>();
+      r.y[v] = load_piece_if<true>(in, static_cast<const T*>(a.y) + at);
   }
   if constexpr (NEXT) r.next_rstd = a.next_rstd[t];
   if constexpr (POST) {
@@ -210,7 +211,7 @@ __device__ __forceinline__ void load_row(const NormBwd& a, int64_t t, int lane,
 // side by side in a block of narrow rows add their sums to one partial row.
 template <typename T, int R, int V, bool POST, bool NEXT, bool FLUSH, bool PRE>
 __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
-  constexpr int G = kSide<R>;
+  constexpr int E = kE<T>, G = kSide<R>;
   __shared__ float slot[2][kWaves<R>];
   const int wave = int(threadIdx.x >> 6), side = int(threadIdx.x) / R;
   const int lane = int(threadIdx.x) % R;
@@ -231,18 +232,17 @@ __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
   const bool any = r0 < r1;  // a block's last units may have no rows
   const T* cgate = POST && any && a.gate_mode == kGateChannel
                        ? static_cast<const T*>(a.gate) + group * a.H : nullptr;
-  Raw8<T> w[V], nw[V], cg[V];  // PRE: post and next weight, the current group's gate
-  auto hold = [&](Raw8<T>(&r)[V], const void* from) {
+  u32x4 w[V], nw[V], cg[V];  // PRE: post and next weight, the current group's gate
+  auto hold = [&](u32x4(&r)[V], const void* from) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * R;
-      r[v] = from != nullptr && p < a.hv ? load_raw8<T>(static_cast<const T*>(from) + p * 8)
-                                         : zero_raw8<T>();
+      r[v] = load_piece_if(from != nullptr && p < a.hv, static_cast<const T*>(from) + p * E);
     }
   };
-  auto held = [&](const Raw8<T>& r, const void* from, int p, float(&f)[8]) {
-    if constexpr (PRE) unpack8(r, f);
-    else unpack8(p < a.hv ? load_raw8<T>(static_cast<const T*>(from) + p * 8) : zero_raw8<T>(), f);
+  auto held = [&](const u32x4& r, const void* from, int p, float(&f)[E]) {
+    if constexpr (PRE) unpack(r, f);
+    else unpack(load_piece_if(p < a.hv, static_cast<const T*>(from) + p * E), f);
   };
   if constexpr (PRE) {
     if constexpr (NEXT) hold(nw, a.next_w);
@@ -251,36 +251,36 @@ __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
       hold(cg, cgate);
     }
   }
-  float sg[V][8], sn[V][8];   // sums for dgate and dw (of the current group), dw_next
-  float sw[FLUSH ? V : 1][8];  // for dw, of the finished groups
+  float sg[V][E], sn[V][E];   // sums for dgate and dw (of the current group), dw_next
+  float sw[FLUSH ? V : 1][E];  // for dw, of the finished groups
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < E; ++c) {
       sg[v][c] = sn[v][c] = 0.f;
       if constexpr (FLUSH) sw[v][c] = 0.f;
     }
 
-  BwdRow<T, V, POST, NEXT> cur;
-  if (PRE && any) load_row<T, R>(a, r0, lane, cur);
+  BwdRow<V> cur;
+  if (PRE && any) load_row<T, R, V, POST, NEXT>(a, r0, lane, cur);
   int64_t left = FLUSH ? a.gate_span : 0;  // rows to the end of the group
   for (int64_t t = r0; t < r1; ++t) {
-    BwdRow<T, V, POST, NEXT> nxt;
-    if constexpr (PRE) load_row<T, R>(a, t + 1 < r1 ? t + 1 : t, lane, nxt);
-    else load_row<T, R>(a, t, lane, cur);
-    float dr[V][8];
+    BwdRow<V> nxt;
+    if constexpr (PRE) load_row<T, R, V, POST, NEXT>(a, t + 1 < r1 ? t + 1 : t, lane, nxt);
+    else load_row<T, R, V, POST, NEXT>(a, t, lane, cur);
+    float dr[V][E];
 #pragma unroll
-    for (int v = 0; v < V; ++v) unpack8(cur.dout[v], dr[v]);
+    for (int v = 0; v < V; ++v) unpack(cur.dout[v], dr[v]);
     if constexpr (NEXT) {
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float rh[8], av[8], wv[8];
-        unpack8(cur.out[v], rh);
-        unpack8(cur.dn[v], av);
+        float rh[E], av[E], wv[E];
+        unpack(cur.out[v], rh);
+        unpack(cur.dn[v], av);
         held(nw[v], a.next_w, lane + v * R, wv);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < E; ++c) {
           rh[c] *= cur.next_rstd;
           sn[v][c] = fmaf(av[c], rh[c], sn[v][c]);
           s = fmaf(av[c] * wv[c], rh[c], s);
@@ -289,12 +289,12 @@ __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
       const float m = row_sum<R>(s, slot, turn, wave) * inv_h;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float rh[8], av[8], wv[8];
-        unpack8(cur.out[v], rh);
-        unpack8(cur.dn[v], av);
+        float rh[E], av[E], wv[E];
+        unpack(cur.out[v], rh);
+        unpack(cur.dn[v], av);
         held(nw[v], a.next_w, lane + v * R, wv);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < E; ++c)
           dr[v][c] += cur.next_rstd * (av[c] * wv[c] - rh[c] * cur.next_rstd * m);
       }
     }
@@ -302,34 +302,34 @@ __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int p = lane + v * R;
-        if (p < a.hv) store8<T>(static_cast<T*>(a.dy) + t * a.H + p * 8, dr[v]);
+        if (p < a.hv) store_piece(static_cast<T*>(a.dy) + t * a.H + p * E, dr[v]);
       }
     } else {
       float s = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int p = lane + v * R;
-        float q[8], yh[8], g[8];
-        unpack8(cur.y[v], yh);
+        float q[E], yh[E], g[E];
+        unpack(cur.y[v], yh);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < E; ++c) {
           q[c] = a.scale * dr[v][c];
           yh[c] *= cur.rstd;
           sg[v][c] = fmaf(dr[v][c] * cur.gate, yh[c], sg[v][c]);
         }
-        if (p < a.hv) store8<T>(static_cast<T*>(a.dresidual) + t * a.H + p * 8, q);
+        if (p < a.hv) store_piece(static_cast<T*>(a.dresidual) + t * a.H + p * E, q);
         if (a.w != nullptr) {  // from here dr is b without a token gate
           held(w[v], a.w, p, g);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) dr[v][c] *= g[c];
+          for (int c = 0; c < E; ++c) dr[v][c] *= g[c];
         }
         if (cgate != nullptr) {
           held(cg[v], cgate, p, g);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) dr[v][c] *= g[c];
+          for (int c = 0; c < E; ++c) dr[v][c] *= g[c];
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) s = fmaf(dr[v][c], yh[c], s);
+        for (int c = 0; c < E; ++c) s = fmaf(dr[v][c], yh[c], s);
       }
       float m = 0.f;
       if (a.w != nullptr || a.gate_mode == kGateToken) {
@@ -342,27 +342,27 @@ __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int p = lane + v * R;
-        float yh[8];
-        unpack8(cur.y[v], yh);
+        float yh[E];
+        unpack(cur.y[v], yh);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) yh[c] = k * (dr[v][c] - yh[c] * cur.rstd * m);
-        if (p < a.hv) store8<T>(static_cast<T*>(a.dy) + t * a.H + p * 8, yh);
+        for (int c = 0; c < E; ++c) yh[c] = k * (dr[v][c] - yh[c] * cur.rstd * m);
+        if (p < a.hv) store_piece(static_cast<T*>(a.dy) + t * a.H + p * E, yh);
       }
       if constexpr (FLUSH) {
         if (--left == 0) {  // the group ends
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             const int p = lane + v * R;
-            float g[8], q[8];
+            float g[E], q[E];
             held(cg[v], cgate, p, g);
             if (a.w != nullptr) held(w[v], a.w, p, q);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < E; ++c) {
               sw[v][c] = fmaf(g[c], sg[v][c], sw[v][c]);
               q[c] = a.w != nullptr ? q[c] * sg[v][c] : sg[v][c];
               sg[v][c] = 0.f;
             }
-            if (p < a.hv) store8<T>(static_cast<T*>(a.dgate) + group * a.H + p * 8, q);
+            if (p < a.hv) store_piece(static_cast<T*>(a.dgate) + group * a.H + p * E, q);
           }
           left = a.gate_span;
           ++group;
@@ -374,28 +374,28 @@ __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
     if constexpr (PRE) cur = nxt;
   }
   // One partial row per block: the units' sums added in order.
-  __shared__ float sums[G > 1 ? G - 1 : 1][G > 1 ? R * V * 8 : 1];
-  auto out = [&](float(&acc)[V][8], float* part) {
+  __shared__ float sums[G > 1 ? G - 1 : 1][G > 1 ? R * V * E : 1];
+  auto out = [&](float(&acc)[V][E], float* part) {
     if constexpr (G > 1) {
       __syncthreads();
       if (side > 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-          for (int c = 0; c < 8; ++c) sums[side - 1][(v * 8 + c) * R + lane] = acc[v][c];
+          for (int c = 0; c < E; ++c) sums[side - 1][(v * E + c) * R + lane] = acc[v][c];
       }
       __syncthreads();
       if (side > 0) return;
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          for (int g = 0; g < G - 1; ++g) acc[v][c] += sums[g][(v * 8 + c) * R + lane];
+        for (int c = 0; c < E; ++c)
+          for (int g = 0; g < G - 1; ++g) acc[v][c] += sums[g][(v * E + c) * R + lane];
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = lane + v * R;
-      if (p < a.hv) store8<float>(part + int64_t(blockIdx.x) * a.H + p * 8, acc[v]);
+      if (p < a.hv) store_f32(part + int64_t(blockIdx.x) * a.H + p * E, acc[v]);
     }
   };
   if constexpr (POST) {
@@ -484,7 +484,7 @@ hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
     if (t0 + slab < N) L.stop = nullptr;
     a.t0 = t0;
     const int64_t rows = t0 + slab < N ? slab : N - t0;
-    hipError_t e;
+    hipError_t e = hipErrorInvalidValue;
     // Pieces in use by all lanes, two or more loads in flight each, and few
     // barriers: against 4 wavefronts for every H above 512 and one below,
     // the bytes of 16384 x 2048 take 50 / 46 (H = 2048: 256 x 1 against 128 x 2),
@@ -496,7 +496,8 @@ hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
     else if (a.hv <= 256) e = fwd_flags<T, 128, 2>(a, post, next, rows, L);
     else if (a.hv <= 512) e = fwd_flags<T, 256, 2>(a, post, next, rows, L);
     else if (a.hv <= 1024) e = fwd_flags<T, 256, 4>(a, post, next, rows, L);
-    else e = fwd_flags<T, 512, 4>(a, post, next, rows, L);
+    else if (kE<T> == 8 || a.hv <= 2048) e = fwd_flags<T, 512, 4>(a, post, next, rows, L);
+    else if constexpr (kE<T> == 4) e = fwd_flags<T, 1024, 4>(a, post, next, rows, L);
     if (e != hipSuccess) return e;
     s.launched = true;
   }
@@ -523,7 +524,7 @@ template <typename T>
 hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
                      const Launch& sums) {
   if (a.units.count > 0) {
-    hipError_t e;
+    hipError_t e = hipErrorInvalidValue;
     // One piece a thread leaves registers for the next row's (H = 2048: 94 ->
     // 82 us); 128 threads for H = 1024 against 64 with two pieces: 81 / 88 us.
     if (a.hv <= 16) e = bwd_flags<T, 16, 1, true>(a, post, next, rows);
@@ -532,8 +533,9 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
     else if (a.hv <= 128) e = bwd_flags<T, 128, 1, true>(a, post, next, rows);
     else if (a.hv <= 256) e = bwd_flags<T, 256, 1, true>(a, post, next, rows);
     else if (a.hv <= 512) e = bwd_flags<T, 512, 1, true>(a, post, next, rows);
-    else if (a.hv <= 1024) e = bwd_flags<T, 1024, 1, false>(a, post, next, rows);
-    else e = bwd_flags<T, 1024, 2, false>(a, post, next, rows);
+    else if (a.hv <= 1024) e = bwd_flags<T, 1024, 1, kE<T> == 4>(a, post, next, rows);
+    else if (kE<T> == 8 || a.hv <= 2048) e = bwd_flags<T, 1024, 2, false>(a, post, next, rows);
+    else if constexpr (kE<T> == 4) e = bwd_flags<T, 1024, 4, false>(a, post, next, rows);
     if (e != hipSuccess) return e;
   }
   // The roles of the sums; neighbouring ones share a launch (a grid has at
@@ -569,18 +571,18 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
 
 // Units of one launch: about as many as the chip holds at once (256 CUs x 12 to
 // 16 wavefronts, of which a wider row's block takes more), each of at least one
-// row.  H = 2048: 1024 units 77.6 us, 512 76.6, 768 77.7; H = 512: 4096 87.4,
+// row.  bf16, H = 2048: 1024 units 77.6 us, 512 76.6, 768 77.7; H = 512: 4096 87.4,
 // 3072 79.6, 2048 79.0 (pre norm 61.4, 61.2, 62.9); H = 768: 2048 83.4, 1024 90.9.
-NormUnits plan_norm_units(int64_t N, int64_t H, int64_t gate_rows, int64_t gate_span) {
+NormUnits plan_norm_units(int64_t N, int64_t hv, int64_t gate_rows, int64_t gate_span) {
   NormUnits u;
   // units side by side in a block: kSide of the backward's threads per row
-  u.blocks_of = H <= 128 ? 16 : H <= 256 ? 8 : H <= 512 ? 4 : 1;
+  u.blocks_of = hv <= 16 ? 16 : hv <= 32 ? 8 : hv <= 64 ? 4 : 1;
   if (N <= 0) {  // no units: the sums are of nothing
     u.per_group = u.blocks_of;
     return u;
   }
-  const int64_t most = H <= 512 ? 768 * u.blocks_of : H <= 1024 ? 2048 : H <= 2048 ? 1024
-                       : H <= 4096 ? 512 : 256;
+  const int64_t most = hv <= 64 ? 768 * u.blocks_of : hv <= 128 ? 2048 : hv <= 256 ? 1024
+                       : hv <= 512 ? 512 : 256;
   const int64_t rows = (N + most - 1) / most;
   auto whole = [&](int64_t n) { return (n + u.blocks_of - 1) / u.blocks_of * u.blocks_of; };
   if (gate_span >= rows) {

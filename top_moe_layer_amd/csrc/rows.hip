@@ -21,7 +21,7 @@
 // kernel), back 13 us (5.6 TB/s); combine gradient of 16384 x 2048, k = 2,
 // 54 us (6.2 TB/s), all moving no more than each input and output once.
 #include "kernels.h"
-#include "vec8.h"
+#include "vec16.h"
 
 #include "../../include/topmoe.h"
 
@@ -169,21 +169,20 @@ __global__ __launch_bounds__(64 * kPlaceWaves) void dispatch_place_kernel(
 // writes it to the token's k rows (zeros to the rows of entries not kept).  NT:
 // x read non-temporally, from 96 MiB of rows on (with a reader of them: 70.4 ->
 // 66.8 us at 96 MiB, 94.9 -> 89.5 at 132; alone 24.5 -> 27.6 at 65).
-template <typename T, bool NT>
-__global__ __launch_bounds__(256) void dispatch_copy_kernel(const T* __restrict__ x,
+template <bool NT>
+__global__ __launch_bounds__(256) void dispatch_copy_kernel(const u32x4* __restrict__ x,
                                                             const int32_t* __restrict__ entry_row,
                                                             int64_t t0, uint32_t pieces, int hv,
-                                                            int H, int k, T* __restrict__ xs) {
+                                                            int k, u32x4* __restrict__ xs) {
   const uint32_t g = blockIdx.x * 256u + threadIdx.x;
   if (g >= pieces) return;
-  const uint32_t dt = g / uint32_t(hv);
+  const uint32_t dt = g / uint32_t(hv), p = g - dt * uint32_t(hv);
   const int64_t t = t0 + dt;
-  const int64_t h = int64_t(g - dt * uint32_t(hv)) * 8;
-  const Raw8<T> v = load_raw8<T, NT>(x + t * H + h);
+  const u32x4 v = load_piece<NT>(x + t * hv + p);
   for (int j = 0; j < k; ++j) {
     const int r = entry_row[t * k + j];
-    if (r >= 0) store_raw8<T>(xs + int64_t(r) * H + h, v);
-    else store_raw8<T>(xs + int64_t(-1 - r) * H + h, zero_raw8<T>());
+    if (r >= 0) xs[int64_t(r) * hv + p] = v;
+    else xs[int64_t(-1 - r) * hv + p] = u32x4{0u, 0u, 0u, 0u};
   }
 }
 
@@ -200,10 +199,10 @@ __global__ __launch_bounds__(256) void dispatch_copy_kernel(const T* __restrict_
 // 32768 entries the counting takes about 5.5 us, 33 MB from L2 on all CUs, and
 // the rows' loads run under it; one copy of the histogram instead of 32 costs
 // another 5 us, 8 or 64 nothing.
-template <typename T, int NT>
+template <int NT>
 __global__ __launch_bounds__(NT) void dispatch_one_kernel(
-    const T* __restrict__ x, const int32_t* __restrict__ idx, int n, int N, int tb, int hv, int H,
-    int E, int k, int bits, int copies, int cap, T* __restrict__ xs,
+    const u32x4* __restrict__ x, const int32_t* __restrict__ idx, int n, int N, int tb, int hv,
+    int E, int k, int bits, int copies, int cap, u32x4* __restrict__ xs,
     int32_t* __restrict__ offsets, int32_t* __restrict__ row_entry,
     int32_t* __restrict__ entry_row) {
   constexpr int kPre = NT == 1024 ? 6 : 2, kIn = NT == 1024 ? 32 : 4;  // in flight per thread:
@@ -222,18 +221,18 @@ __global__ __launch_bounds__(NT) void dispatch_one_kernel(
   const int e0 = t0 * k, own = (t1 - t0) * k;
   const int segs = (own + 63) / 64;
   const int pieces = (t1 - t0) * hv;
-  const T* xb = x + int64_t(t0) * H;
+  const u32x4* xb = x + int64_t(t0) * hv;  // the block's rows are consecutive
   int ex[kTurns];  // this wavefront's own entries
 #pragma unroll
   for (int q = 0; q < kTurns; ++q) {
     const int i = (q * kWaves + wave) * 64 + lane;
     ex[q] = i < own ? idx[e0 + i] : 0;
   }
-  Raw8<T> pre[kPre];
+  u32x4 pre[kPre];
 #pragma unroll
-  for (int u = 0; u < kPre; ++u) {  // a block's rows are consecutive: piece p is at 8 p
+  for (int u = 0; u < kPre; ++u) {
     const int p = tid + u * NT;
-    pre[u] = p < pieces ? load_raw8<T>(xb + int64_t(p) * 8) : zero_raw8<T>();
+    pre[u] = load_piece_if(p < pieces, xb + p);
   }
   for (int i = tid; i < copies * B; i += NT) hist[0][i] = hist[1][i] = 0;
   for (int i = tid; i < segs * (kDispatchMaxExperts + 1); i += NT) (&seg[0][0])[i] = 0;
@@ -291,19 +290,18 @@ __global__ __launch_bounds__(NT) void dispatch_one_kernel(
     }
   }
   __syncthreads();
-  auto put = [&](int p, const Raw8<T>& v) {
-    const int t = p / hv;
-    const int64_t h = int64_t(p - t * hv) * 8;
+  auto put = [&](int g, u32x4 v) {
+    const int t = g / hv, p = g - t * hv;
     for (int j = 0; j < k; ++j) {
       const int r = rows[t * k + j];
-      if (r >= 0) store_raw8<T>(xs + int64_t(r) * H + h, v);
-      else store_raw8<T>(xs + int64_t(-1 - r) * H + h, zero_raw8<T>());
+      if (r >= 0) xs[int64_t(r) * hv + p] = v;
+      else xs[int64_t(-1 - r) * hv + p] = u32x4{0u, 0u, 0u, 0u};
     }
   };
 #pragma unroll
   for (int u = 0; u < kPre; ++u)
     if (tid + u * NT < pieces) put(tid + u * NT, pre[u]);
-  for (int p = tid + kPre * NT; p < pieces; p += NT) put(p, load_raw8<T>(xb + int64_t(p) * 8));
+  for (int g = tid + kPre * NT; g < pieces; g += NT) put(g, load_piece(xb + g));
 }
 
 __global__ void dispatch_empty_kernel(int E, int32_t* offsets) {
@@ -321,38 +319,34 @@ __global__ __launch_bounds__(256) void gather_sum_kernel(
     const T* __restrict__ rows, const int32_t* __restrict__ entry_row,
     const float* __restrict__ alpha, const T* residual, int64_t nrows, int64_t t0,
     uint32_t pieces, int hv, int H, int k, T* out) {
+  constexpr int E = kE<T>;
   const uint32_t g = blockIdx.x * 256u + threadIdx.x;
   if (g >= pieces) return;
   const uint32_t dt = g / uint32_t(hv);
   const int64_t t = t0 + dt;
-  const int64_t h = int64_t(g - dt * uint32_t(hv)) * 8;
-  float acc[8];
-  if (residual != nullptr) {
-    unpack8(load_raw8<T>(residual + t * H + h), acc);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  }
+  const int64_t h = int64_t(g - dt * uint32_t(hv)) * E;
+  float acc[E];
+  unpack(load_piece_if(residual != nullptr, residual + t * H + h), acc);
   const int32_t* er = entry_row + t * k;
   for (int j0 = 0; j0 < k; j0 += 4) {
-    Raw8<T> v[4];
+    u32x4 v[4];
     float w[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int64_t r = j0 + u < k ? int64_t(er[j0 + u]) : -1;
       const bool use = r >= 0 && r < nrows;
       w[u] = !use ? 0.f : WEIGHTED ? alpha[t * k + j0 + u] : 1.f;
-      v[u] = use ? load_raw8<T, NT>(rows + r * H + h) : zero_raw8<T>();
+      v[u] = load_piece_if<NT>(use, rows + r * H + h);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      float f[8];
-      unpack8(v[u], f);
+      float f[E];
+      unpack(v[u], f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = WEIGHTED ? fmaf(w[u], f[i], acc[i]) : acc[i] + f[i];
+      for (int i = 0; i < E; ++i) acc[i] = WEIGHTED ? fmaf(w[u], f[i], acc[i]) : acc[i] + f[i];
     }
   }
-  store8<T>(out + t * H + h, acc);
+  store_piece(out + t * H + h, acc);
 }
 
 // dys[row(i)] = alpha[i] dy[t] and dalpha[i] = dy[t] . ys[row(i)]: one
@@ -376,7 +370,8 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(
   }
   T* o = dys + row * H;
   if (r < 0) {
-    for (int p = lane; p < hv; p += 64) store_raw8<T>(o + p * 8, zero_raw8<T>());
+    for (int p = lane; p < hv; p += 64)
+      *reinterpret_cast<u32x4*>(o + p * kE<T>) = u32x4{0u, 0u, 0u, 0u};
     if (lane == 0) dalpha[i] = 0.f;
     return;
   }
@@ -385,15 +380,15 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(
   const float a = alpha[i];
   float dot = 0.f;
   for (int p = lane; p < hv; p += 64) {
-    float fd[8], fs[8];
-    unpack8(load_raw8<T>(d + p * 8), fd);
-    unpack8(load_raw8<T, true>(s + p * 8), fs);
+    float fd[kE<T>], fs[kE<T>];
+    unpack(load_piece(d + p * kE<T>), fd);
+    unpack(load_piece<true>(s + p * kE<T>), fs);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < kE<T>; ++c) {
       dot = fmaf(fd[c], fs[c], dot);
       fd[c] *= a;
     }
-    store8<T, NT>(o + p * 8, fd);
+    store_piece<NT>(o + p * kE<T>, fd);
   }
   dot = wave_sum(dot);
   if (lane == 0) dalpha[i] = dot;
@@ -419,34 +414,29 @@ hipError_t for_slabs(int64_t N, int64_t slab, const Launch& L, F launch) {
   return hipSuccess;
 }
 
-template <typename T>
-hipError_t dispatch_one(const void* x, const int32_t* idx, int64_t N, int H, int E, int k,
-                        int bits, int cap, void* xs, int32_t* offsets, int32_t* row_entry,
+hipError_t dispatch_one(const u32x4* x, const int32_t* idx, int64_t N, int hv, int E, int k,
+                        int bits, int cap, u32x4* xs, int32_t* offsets, int32_t* row_entry,
                         int32_t* entry_row, const Launch& s) {
   const int tb = int((N + 255) / 256);
   int copies = N * k <= kDispatchFew ? 4 : 32;
   while (copies * (E + 1) > kDispatchHist) copies /= 2;
   const dim3 grid(unsigned((N + tb - 1) / tb));
-#define TOPMOE_LAUNCH_ONE(NT)                                                               \
-  return launch_kernel(dispatch_one_kernel<T, NT>, grid, dim3(NT), 0, s,                      \
-                       static_cast<const T*>(x), idx, int(N * k), int(N), tb, H / 8, H, E, k, \
-                       bits, copies, cap, static_cast<T*>(xs), offsets, row_entry, entry_row)
+#define TOPMOE_LAUNCH_ONE(NT)                                                                    \
+  return launch_kernel(dispatch_one_kernel<NT>, grid, dim3(NT), 0, s, x, idx, int(N * k), int(N), \
+                       tb, hv, E, k, bits, copies, cap, xs, offsets, row_entry, entry_row)
   if (N * k <= kDispatchFew) TOPMOE_LAUNCH_ONE(256);
   TOPMOE_LAUNCH_ONE(1024);
 #undef TOPMOE_LAUNCH_ONE
 }
 
-template <typename T>
-hipError_t dispatch_copy(const void* x, const int32_t* entry_row, int64_t N, int H, int k,
-                         void* xs, const Launch& s) {
-  const int hv = H / 8;
+hipError_t dispatch_copy(const u32x4* x, const int32_t* entry_row, int64_t N, int hv, int k,
+                         u32x4* xs, const Launch& s) {
   return for_slabs(N, slab_rows(hv), s, [&](int64_t t0, int64_t rows, const Launch& L) {
     const uint32_t pieces = uint32_t(rows * hv);
-    const auto kernel = N * k * H * int64_t(sizeof(T)) >= kNtBytes / 4 * 3
-                            ? dispatch_copy_kernel<T, true> : dispatch_copy_kernel<T, false>;
-    return launch_kernel(kernel, dim3((pieces + 255) / 256), dim3(256), 0, L,
-                         static_cast<const T*>(x), entry_row, t0, pieces, hv, H, k,
-                         static_cast<T*>(xs));
+    const auto kernel = N * k * hv * 16 >= kNtBytes / 4 * 3 ? dispatch_copy_kernel<true>
+                                                            : dispatch_copy_kernel<false>;
+    return launch_kernel(kernel, dim3((pieces + 255) / 256), dim3(256), 0, L, x, entry_row, t0,
+                         pieces, hv, k, xs);
   });
 }
 
@@ -454,7 +444,7 @@ template <typename T, bool WEIGHTED>
 hipError_t gather_sum(const void* rows, const int32_t* entry_row, const float* alpha,
                       const void* residual, int64_t N, int H, int k, void* out,
                       const Launch& s) {
-  const int hv = H / 8;
+  const int hv = H / kE<T>;
   return for_slabs(N, slab_rows(hv), s, [&](int64_t t0, int64_t m, const Launch& L) {
     const uint32_t pieces = uint32_t(m * hv);
     const auto kernel = N * k * H * int64_t(sizeof(T)) >= kNtBytes / 2 * 3
@@ -477,7 +467,7 @@ hipError_t combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
                                                                : combine_bwd_kernel<T, false>;
     return launch_kernel(kernel, dim3(unsigned((m + 3) / 4)), dim3(256), 0, L,
                          static_cast<const T*>(dy), static_cast<const T*>(ys), entry_row, alpha,
-                         n, i0, H / 8, H, k, static_cast<T*>(dys), dalpha);
+                         n, i0, H / kE<T>, H, k, static_cast<T*>(dys), dalpha);
   });
 }
 
@@ -499,15 +489,15 @@ hipError_t launch_dispatch_rows(const void* x, const int32_t* idx, int64_t N, in
                                 const Launch& rows, const Launch& copy) {
   const int64_t n = N * k;
   const DispatchPlan p = plan_dispatch(n, E);
-  const bool f32 = dtype == TOPMOE_DTYPE_FP32;
   if (n == 0) return launch_kernel(dispatch_empty_kernel, dim3(1), dim3(256), 0, rows, E, offsets);
   int bits = 0;
   while ((E >> bits) != 0) ++bits;
+  // rows only move: pieces of 16 bytes whatever the type
+  const int hv = H / (dtype == TOPMOE_DTYPE_FP32 ? 4 : 8);
+  const u32x4* xp = static_cast<const u32x4*>(x);
+  u32x4* op = static_cast<u32x4*>(xs);
   if (p.nchunk == 0)
-    return f32 ? dispatch_one<float>(x, idx, N, H, E, k, bits, cap, xs, offsets, row_entry,
-                                     entry_row, copy)
-               : dispatch_one<bf16_t>(x, idx, N, H, E, k, bits, cap, xs, offsets, row_entry,
-                                      entry_row, copy);
+    return dispatch_one(xp, idx, N, hv, E, k, bits, cap, op, offsets, row_entry, entry_row, copy);
   Launch first = rows, second = rows;
   first.stop = nullptr;
   second.start = nullptr;
@@ -518,8 +508,7 @@ hipError_t launch_dispatch_rows(const void* x, const int32_t* idx, int64_t N, in
                     p.nchunk, E, bits, cap, part, offsets, row_entry, entry_row);
   if (e != hipSuccess) return e;
   rows.launched = true;
-  return f32 ? dispatch_copy<float>(x, entry_row, N, H, k, xs, copy)
-             : dispatch_copy<bf16_t>(x, entry_row, N, H, k, xs, copy);
+  return dispatch_copy(xp, entry_row, N, hv, k, op, copy);
 }
 
 hipError_t launch_gather_sum(const void* rows, const int32_t* entry_row, const float* alpha,
