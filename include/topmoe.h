@@ -360,8 +360,10 @@ int moe_ffn_bwd(const void* x, const float* Wr, const void* Wg, const void* Wu,
 #define TOPMOE_DISPATCH_STAGES 2  /* 0 rows of the entries (empty in the one-launch
                                      dispatch), 1 copy                             */
 #define TOPMOE_DISPATCH_MAX_EXPERTS 256
-#define TOPMOE_DISPATCH_ONE 32768  /* most entries (N * k) of the one-launch dispatch,
-                                      which needs no workspace                     */
+/* The one-launch dispatch, which needs no workspace: at most TOPMOE_DISPATCH_ONE
+ * entries (N * k), and x and xs together below TOPMOE_DISPATCH_ONE_BYTES. */
+#define TOPMOE_DISPATCH_ONE 32768
+#define TOPMOE_DISPATCH_ONE_BYTES ((int64_t)128 << 20)
 
 /* Workspace needed by moe_dispatch_fwd: counts per chunk of entries.  Returns
  * 0 for invalid sizes (and at least 256 for valid ones). */
@@ -376,7 +378,7 @@ size_t moe_dispatch_workspace_bytes(int64_t N, int E, int k);
  *   entry_row [N, k]    int32 output: the entry's row, or -1 - row if not kept
  *   workspace           at least moe_dispatch_workspace_bytes(N, E, k) bytes,
  *                       256-byte aligned; contents on entry ignored.  Not used,
- *                       and may be NULL, up to TOPMOE_DISPATCH_ONE entries. */
+ *                       and may be NULL, in the one-launch dispatch. */
 int moe_dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t H, int E, int k,
                      float capacity_factor, int dtype, void* xs, int32_t* expert_offsets,
                      int32_t* row_entry, int32_t* entry_row, void* workspace,

@@ -70,6 +70,8 @@ def test_rows_refusals(name):
         for cf in (-1.0, NAN, INF):
             assert call(name, base, cf=cf) == B.ERR_BAD_ARG
         need = tm.moe_dispatch_workspace_bytes(32768, 4, 2)
+        # few entries of long rows take three launches as well: 1024 * 3 * 2^15 * 2 bytes
+        assert call(name, base, N=1024, H=1 << 15) == B.ERR_WORKSPACE_TOO_SMALL
         assert call(name, base, ws_bytes=64 * 4) == B.ERR_WORKSPACE_TOO_SMALL
         assert call(name, base, ws=None) == B.ERR_NULL_ARG
         for p, off in (("x", 8), ("xs", 8), ("idx", 2), ("off", 1), ("entry_row", 2), ("ws", 64)):

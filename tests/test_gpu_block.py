@@ -46,6 +46,7 @@ ROUTES = [  # N, H, E, k, capacity factor, share of padding tokens, one expert t
     (16384, 8, 7, 2, 1.0, 0.1, False),   # the last one-launch size
     (128, 16, 256, 256, 0.0, 0.0, False),
     (16385, 8, 7, 2, 1.0, 0.1, False),   # the first with three launches
+    (90, 131072, 4, 3, 1.0, 0.1, False),  # few entries of long rows: bf16 one launch, fp32 three
     (700, 104, 5, 2, 0.0, 0.0, False),
     (700, 104, 5, 2, 0.01, 0.3, True),
     (3001, 16, 64, 6, 1.25, 0.05, False),

@@ -37,6 +37,7 @@ NORM_BWD_STAGES = 2
 RESTORE8_STAGES = 2
 DISPATCH_MAX_EXPERTS = 256
 DISPATCH_ONE = 32768
+DISPATCH_ONE_BYTES = 128 << 20
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 ACT8_GROUP = 32
 

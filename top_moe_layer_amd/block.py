@@ -135,7 +135,8 @@ def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
     if not 1 <= E <= B.DISPATCH_MAX_EXPERTS:
         B.check(B.ERR_BAD_SHAPE, "moe_dispatch_fwd")
     wp = wn = ws = None
-    if workspace is not None or N * k > B.DISPATCH_ONE:
+    if (workspace is not None or N * k > B.DISPATCH_ONE or
+            N * (k + 1) * H * x.element_size() >= B.DISPATCH_ONE_BYTES):
         nbytes = moe_dispatch_workspace_bytes(N, E, k)
         wp, wn, ws = _scratch(nbytes, "moe_dispatch_fwd", dev, workspace)
     if xs is None:

@@ -12,7 +12,9 @@
 using namespace topmoe;
 
 static_assert(kDispatchMaxExperts == TOPMOE_DISPATCH_MAX_EXPERTS, "expert limit");
-static_assert(kDispatchOne == TOPMOE_DISPATCH_ONE, "one-launch limit");
+static_assert(kDispatchOne == TOPMOE_DISPATCH_ONE &&
+                  kDispatchOneBytes == TOPMOE_DISPATCH_ONE_BYTES,
+              "one-launch limits");
 static_assert(kAct8Group == TOPMOE_ACT8_GROUP, "scale group");
 static_assert(kGateNone == TOPMOE_GATE_NONE && kGateChannel == TOPMOE_GATE_CHANNEL &&
                   kGateToken == TOPMOE_GATE_TOKEN,
@@ -150,7 +152,8 @@ int moe_dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t 
   if (E < 1 || E > kDispatchMaxExperts || k > E) return TOPMOE_ERR_BAD_SHAPE;
   const int status = rows_shape(N, H, k);
   if (status != TOPMOE_OK) return status;
-  const size_t need = plan_dispatch(N * k, E).bytes;
+  const bool one = dispatch_in_one(N, H, k, dtype == TOPMOE_DTYPE_FP32 ? 4 : 2);
+  const size_t need = one ? 0 : plan_dispatch(N * k, E).bytes;
   if (!expert_offsets || (need > 0 && !workspace) ||
       (N > 0 && (!x || !topk_idx || !xs || !row_entry || !entry_row)))
     return TOPMOE_ERR_NULL_ARG;

@@ -219,14 +219,20 @@ constexpr int64_t kNtBytes = int64_t(128) << 20;
 
 // ---- rows by expert and back (rows.hip)
 constexpr int kDispatchMaxExperts = 256;
-// Most entries (N * k) of the one-launch dispatch.  In it every block counts
-// all of them, which three launches do once: bf16, top-2 of 8, H = 256 / 768 /
-// 2048, one launch against three: 12.5 / 17.7 / 40.3 against 19.6 / 20.0 /
-// 40.2 us at 32768 entries, 18.7 / 33.4 / 85.4 against 19.3 / 30.5 / 72.9 at
-// 65536.
+// Most entries (N * k) and bytes (of x and xs) of the one-launch dispatch.  In
+// it every block counts all entries, which three launches do once, and all
+// blocks load and then store at the same time.  bf16, one launch against
+// three: top-2 of 8, H = 256 / 768, 12.5 / 17.7 against 19.6 / 20.0 us at 32768
+// entries, 18.7 / 33.4 against 19.3 / 30.5 at 65536; 8192 entries of 16 experts,
+// H = 4096, k = 4: 17.1 against 20.4 us (80 MiB), 42.1 against 37.7 at H = 8192
+// (160 MiB); k = 1: 31.1 against 30.2 (128 MiB), 64.3 against 49.6 (256 MiB).
 constexpr int kDispatchOne = 32768;
-// Chunks of entries counted by one block each (none in the one-launch
-// dispatch) and the bytes of their counts [nchunk, E + 1].
+constexpr int64_t kDispatchOneBytes = int64_t(128) << 20;
+inline bool dispatch_in_one(int64_t N, int64_t H, int k, int elem) {
+  return N * k <= kDispatchOne && N * (k + 1) * H * elem < kDispatchOneBytes;
+}
+// Otherwise: chunks of entries counted by one block each, and the bytes of
+// their counts [nchunk, E + 1].
 struct DispatchPlan {
   int chunk = 0, nchunk = 0;
   size_t bytes = 0;

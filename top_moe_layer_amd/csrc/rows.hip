@@ -475,7 +475,7 @@ hipError_t combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
 
 DispatchPlan plan_dispatch(int64_t n, int E) {
   DispatchPlan p;
-  if (n <= kDispatchOne) return p;
+  if (n <= 0) return p;
   const int64_t c = (n + 255) / 256;  // at most 256 chunks
   p.chunk = int((c + 1023) / 1024 * 1024);
   p.nchunk = int((n + p.chunk - 1) / p.chunk);
@@ -496,7 +496,7 @@ hipError_t launch_dispatch_rows(const void* x, const int32_t* idx, int64_t N, in
   const int hv = H / (dtype == TOPMOE_DTYPE_FP32 ? 4 : 8);
   const u32x4* xp = static_cast<const u32x4*>(x);
   u32x4* op = static_cast<u32x4*>(xs);
-  if (p.nchunk == 0)
+  if (dispatch_in_one(N, H, k, dtype == TOPMOE_DTYPE_FP32 ? 4 : 2))
     return dispatch_one(xp, idx, N, hv, E, k, bits, cap, op, offsets, row_entry, entry_row, copy);
   Launch first = rows, second = rows;
   first.stop = nullptr;
