@@ -504,20 +504,35 @@ hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
   return hipSuccess;
 }
 
+template <typename T, int R, int V, bool POST, bool NEXT, bool PRE>
+hipError_t bwd_kernel(const NormBwd& a, const Launch& L) {
+  const dim3 grid(static_cast<unsigned>(a.units.count / a.units.blocks_of)), block(kThreads<R>);
+  if constexpr (POST) {
+    if (a.units.per_group == 0)
+      return launch_kernel(norm_bwd_kernel<T, R, V, POST, NEXT, true, PRE>, grid, block, 0, L, a);
+  }
+  return launch_kernel(norm_bwd_kernel<T, R, V, POST, NEXT, false, PRE>, grid, block, 0, L, a);
+}
+
 template <typename T, int R, int V, bool PRE>
 hipError_t bwd_flags(const NormBwd& a, bool post, bool next, const Launch& L) {
-  const dim3 grid(static_cast<unsigned>(a.units.count / a.units.blocks_of));
-  const dim3 block(kThreads<R>);
-#define TOPMOE_NORM_BWD(POST, NEXT, FLUSH) \
-  return launch_kernel(norm_bwd_kernel<T, R, V, POST, NEXT, FLUSH, PRE>, grid, block, 0, L, a)
-  if (!post) TOPMOE_NORM_BWD(false, true, false);
-  if (a.units.per_group == 0) {
-    if (next) TOPMOE_NORM_BWD(true, true, true);
-    TOPMOE_NORM_BWD(true, false, true);
+  if (!post) return bwd_kernel<T, R, V, false, true, PRE>(a, L);
+  if (next) return bwd_kernel<T, R, V, true, true, PRE>(a, L);
+  return bwd_kernel<T, R, V, true, false, PRE>(a, L);
+}
+
+// Rows of 513 to 1024 pieces.  Both norms of eight channels a piece leave 1024
+// threads no registers for the next row (H = 8192: 93 us loading each row when
+// it is needed, 84 with spilled registers, 79 with 512 threads).
+template <typename T>
+hipError_t bwd_upto_1024(const NormBwd& a, bool post, bool next, const Launch& L) {
+  if constexpr (kE<T> == 4) {
+    return bwd_flags<T, 1024, 1, true>(a, post, next, L);
+  } else {
+    if (post && next) return bwd_kernel<T, 512, 2, true, true, true>(a, L);
+    if (post) return bwd_kernel<T, 1024, 1, true, false, true>(a, L);
+    return bwd_kernel<T, 1024, 1, false, true, true>(a, L);
   }
-  if (next) TOPMOE_NORM_BWD(true, true, false);
-  TOPMOE_NORM_BWD(true, false, false);
-#undef TOPMOE_NORM_BWD
 }
 
 template <typename T>
@@ -533,7 +548,7 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
     else if (a.hv <= 128) e = bwd_flags<T, 128, 1, true>(a, post, next, rows);
     else if (a.hv <= 256) e = bwd_flags<T, 256, 1, true>(a, post, next, rows);
     else if (a.hv <= 512) e = bwd_flags<T, 512, 1, true>(a, post, next, rows);
-    else if (a.hv <= 1024) e = bwd_flags<T, 1024, 1, kE<T> == 4>(a, post, next, rows);
+    else if (a.hv <= 1024) e = bwd_upto_1024<T>(a, post, next, rows);
     else if (kE<T> == 8 || a.hv <= 2048) e = bwd_flags<T, 1024, 2, false>(a, post, next, rows);
     else if constexpr (kE<T> == 4) e = bwd_flags<T, 1024, 4, false>(a, post, next, rows);
     if (e != hipSuccess) return e;
