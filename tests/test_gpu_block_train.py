@@ -330,6 +330,20 @@ def test_moe_keep8(env, N, H, I, E, k, cf, dt):
         assert eq(t.grad, ref)
 
 
+def test_keep8_no_tokens(env):
+    dev, tm = env
+    H, I, E = 64, 64, 4
+    leaf = lambda *s: torch.randn(*s, device=dev).requires_grad_()
+    x = torch.empty(0, H, device=dev).requires_grad_()
+    L = [x, leaf(I, H), leaf(I, H), leaf(H, I)]
+    tm.swiglu_ffn(*L, keep_activations="act8").sum().backward()
+    M = [x, leaf(E, H), leaf(E, I, H), leaf(E, I, H), leaf(E, H, I)]
+    y, aux = tm.moe_ffn(*M, 2, 0.01, keep_activations="act8")[:2]
+    (y.sum() + aux.sum()).backward()
+    torch.cuda.synchronize()
+    assert all(not t.grad.any() for t in L + M)
+
+
 def test_keep8_holds_less(env):
     """What a training forward holds until the backward."""
     dev, tm = env

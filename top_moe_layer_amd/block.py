@@ -16,7 +16,8 @@ from .ops import _buffer, _dtype_code, _need, _ptr, _torch_stream
 
 
 # The current stream's handle without a Stream object (0.1 us a call instead of 2.8).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _empty = torch.empty
 _CODES = {torch.float32: B.DTYPE_FP32, torch.bfloat16: B.DTYPE_BF16}
 
@@ -249,6 +250,7 @@ class PostnormGrads(NamedTuple):
     dnext_w: Optional[torch.Tensor]
 
 
+@functools.lru_cache(maxsize=256)  # of three numbers; 0.5 us of a 14 us call
 def block_norm_bwd_workspace_bytes(N: int, H: int, gate_rows: int = 1) -> int:
     return int(B.lib().block_norm_bwd_workspace_bytes(N, H, gate_rows))
 

@@ -207,9 +207,13 @@ __device__ __forceinline__ void load_row(const NormBwd& a, int64_t t, int lane,
 // column sums in registers.  FLUSH: units of whole gate groups.  PRE: the
 // weights stay in registers, and the next row's loads are issued before a
 // row's sums, so that they run under its barriers; the widest rows have no
-// registers left for that and load what they need when they need it.  The units
+// registers left for that and load what they need when they need it.  The
+// residual's gradient, which nobody reads before the block's own backward pass
+// is through, is written non-temporally (NT) once it and dy fill half the
+// Infinity Cache (16384 x 2048 bf16: 80.0 -> 77.3 us, with readers of both
+// behind 124.3 -> 119.4, at half the rows 67.5 -> 69.1; dy as well: 86.9).  The units
 // side by side in a block of narrow rows add their sums to one partial row.
-template <typename T, int R, int V, bool POST, bool NEXT, bool FLUSH, bool PRE>
+template <typename T, int R, int V, bool POST, bool NEXT, bool FLUSH, bool PRE, bool NT>
 __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
   constexpr int E = kE<T>, G = kSide<R>;
   __shared__ float slot[2][kWaves<R>];
@@ -317,7 +321,7 @@ __global__ __launch_bounds__(kThreads<R>) void norm_bwd_kernel(NormBwd a) {
           yh[c] *= cur.rstd;
           sg[v][c] = fmaf(dr[v][c] * cur.gate, yh[c], sg[v][c]);
         }
-        if (p < a.hv) store_piece(static_cast<T*>(a.dresidual) + t * a.H + p * E, q);
+        if (p < a.hv) store_piece<NT>(static_cast<T*>(a.dresidual) + t * a.H + p * E, q);
         if (a.w != nullptr) {  // from here dr is b without a token gate
           held(w[v], a.w, p, g);
 #pragma unroll
@@ -507,11 +511,18 @@ hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
 template <typename T, int R, int V, bool POST, bool NEXT, bool PRE>
 hipError_t bwd_kernel(const NormBwd& a, const Launch& L) {
   const dim3 grid(static_cast<unsigned>(a.units.count / a.units.blocks_of)), block(kThreads<R>);
+#define TOPMOE_NORM_BWD(FLUSH, NT) \
+  return launch_kernel(norm_bwd_kernel<T, R, V, POST, NEXT, FLUSH, PRE, NT>, grid, block, 0, L, a)
   if constexpr (POST) {
-    if (a.units.per_group == 0)
-      return launch_kernel(norm_bwd_kernel<T, R, V, POST, NEXT, true, PRE>, grid, block, 0, L, a);
+    const bool nt = 2 * a.N * a.H * int64_t(sizeof(T)) >= kNtBytes;
+    if (a.units.per_group == 0) {
+      if (nt) TOPMOE_NORM_BWD(true, true);
+      TOPMOE_NORM_BWD(true, false);
+    }
+    if (nt) TOPMOE_NORM_BWD(false, true);
   }
-  return launch_kernel(norm_bwd_kernel<T, R, V, POST, NEXT, false, PRE>, grid, block, 0, L, a);
+  TOPMOE_NORM_BWD(false, false);
+#undef TOPMOE_NORM_BWD
 }
 
 template <typename T, int R, int V, bool PRE>
@@ -586,8 +597,9 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
 
 // Units of one launch: about as many as the chip holds at once (256 CUs x 12 to
 // 16 wavefronts, of which a wider row's block takes more), each of at least one
-// row.  bf16, H = 2048: 1024 units 77.6 us, 512 76.6, 768 77.7; H = 512: 4096 87.4,
-// 3072 79.6, 2048 79.0 (pre norm 61.4, 61.2, 62.9); H = 768: 2048 83.4, 1024 90.9.
+// row.  bf16, post norm (pre norm): H = 2048, 1024 units 77.6 us, 512 76.6, 768
+// 77.7; H = 512, 1024 blocks of four 87.4 (61.4), 768 79.6 (61.2), 512 79.0
+// (62.9); H = 768, 2048 units 83.4, 1024 90.9.
 NormUnits plan_norm_units(int64_t N, int64_t hv, int64_t gate_rows, int64_t gate_span) {
   NormUnits u;
   // units side by side in a block: kSide of the backward's threads per row
