@@ -200,6 +200,7 @@ POST = [  # gate shape as a function of (N, H), post norm, next norm, residual s
     (lambda N, H: (N, H), True, False, 1.0),
     (lambda N, H: (N // 3, 1, H) if N % 3 == 0 else (1, 1, H), True, True, 1.0),
     (lambda N, H: (3, H) if N % 3 == 0 else (1, H), False, True, 0.0),
+    (lambda N, H: (N, H), True, True, 1.0),
 ]
 
 
@@ -258,13 +259,28 @@ def test_postnorm(env, N, H, which, dt):
     postnorm_case(env, N, H, dt, which)
 
 
-@pytest.mark.parametrize("N,H,which", [(4200, 40, 3), (4200, 40, 8), (4200, 40, 7), (4200, 520, 9),
-                                       (3000, 16, 5), (2049, 64, 0)])
+@pytest.mark.parametrize("N,H,which", [
+    (4200, 40, 3), (4200, 520, 9), (3000, 16, 5), (2049, 64, 0), (60000, 16, 3), (49998, 40, 9),
+    (30000, 104, 8), (25001, 200, 0), (9000, 512, 5), (8199, 1000, 9), (3300, 2048, 3),
+    (1701, 4096, 9), (900, 6008, 3), (700, 8200, 5), (700, 16384, 0)])
 def test_postnorm_many_rows(env, N, H, which):
-    """Units of several rows: within a gate's group, and several groups to a unit."""
+    """Units of several rows within a gate's group (or without one), in every layout of threads."""
     announce(f"postnorm N={N} H={H} case {which}")
     postnorm_case(env, N, H, "fp32", which)
     postnorm_case(env, N, H, "bf16", which)
+
+
+@pytest.mark.parametrize("N,H,which,dt", [
+    (60000, 16, 7, "fp32"), (150000, 16, 8, "bf16"), (60000, 104, 7, "bf16"), (30000, 200, 10, "bf16"),
+    (9000, 512, 10, "fp32"), (8199, 1000, 8, "bf16"), (8199, 1000, 10, "fp32"),
+    (3300, 2048, 8, "bf16"), (1700, 4096, 10, "bf16"), (1700, 3000, 10, "fp32"),
+    (900, 6008, 8, "bf16"), (900, 6008, 7, "bf16"), (900, 6008, 10, "fp32"),
+    (700, 16384, 10, "bf16"), (700, 8200, 10, "fp32")])
+def test_postnorm_units_of_whole_gate_groups(env, N, H, which, dt):
+    """More rows than units, each gate row shared by one token or three: units that hold whole
+    groups, in every layout of threads, with and without the next norm."""
+    announce(f"postnorm N={N} H={H} case {which} {dt}")
+    postnorm_case(env, N, H, dt, which)
 
 
 def test_postnorm_in_place_and_gradient_of_n_alone(env):

@@ -492,8 +492,9 @@ hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
     // Pieces in use by all lanes, two or more loads in flight each, and few
     // barriers: against 4 wavefronts for every H above 512 and one below,
     // the bytes of 16384 x 2048 take 50 / 46 (H = 2048: 256 x 1 against 128 x 2),
-    // 83 / 50 (768), 83 / 48 (256) and 273 / 81 us (64).
-    if (a.hv <= 16) e = fwd_flags<T, 16, 1>(a, post, next, rows, L);
+    // 83 / 50 (768), 83 / 48 (256) and 273 / 50 us (64).
+    if (a.hv <= 8) e = fwd_flags<T, 8, 1>(a, post, next, rows, L);
+    else if (a.hv <= 16) e = fwd_flags<T, 16, 1>(a, post, next, rows, L);
     else if (a.hv <= 32) e = fwd_flags<T, 32, 1>(a, post, next, rows, L);
     else if (a.hv <= 64) e = fwd_flags<T, 64, 1>(a, post, next, rows, L);
     else if (a.hv <= 128) e = fwd_flags<T, 64, 2>(a, post, next, rows, L);
@@ -553,7 +554,8 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
     hipError_t e = hipErrorInvalidValue;
     // One piece a thread leaves registers for the next row's (H = 2048: 94 ->
     // 82 us); 128 threads for H = 1024 against 64 with two pieces: 81 / 88 us.
-    if (a.hv <= 16) e = bwd_flags<T, 16, 1, true>(a, post, next, rows);
+    if (a.hv <= 8) e = bwd_flags<T, 8, 1, true>(a, post, next, rows);
+    else if (a.hv <= 16) e = bwd_flags<T, 16, 1, true>(a, post, next, rows);
     else if (a.hv <= 32) e = bwd_flags<T, 32, 1, true>(a, post, next, rows);
     else if (a.hv <= 64) e = bwd_flags<T, 64, 1, true>(a, post, next, rows);
     else if (a.hv <= 128) e = bwd_flags<T, 128, 1, true>(a, post, next, rows);
@@ -603,7 +605,7 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
 NormUnits plan_norm_units(int64_t N, int64_t hv, int64_t gate_rows, int64_t gate_span) {
   NormUnits u;
   // units side by side in a block: kSide of the backward's threads per row
-  u.blocks_of = hv <= 16 ? 16 : hv <= 32 ? 8 : hv <= 64 ? 4 : 1;
+  u.blocks_of = hv <= 8 ? 32 : hv <= 16 ? 16 : hv <= 32 ? 8 : hv <= 64 ? 4 : 1;
   if (N <= 0) {  // no units: the sums are of nothing
     u.per_group = u.blocks_of;
     return u;
