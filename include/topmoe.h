@@ -414,7 +414,7 @@ int moe_combine_bwd(const void* dy, const void* ys, const int32_t* entry_row, co
  *   n  = next_w * r / sqrt(mean(r^2) + eps), of the unrounded r, rounded once
  * H is a multiple of 8 with 8 <= H <= 16384; N < 2^31; eps positive and finite;
  * weights and gates have x's dtype; tensor pointers are 16-byte aligned (a
- * token gate, its gradient and the float32 arrays: 4-byte).  Outputs must not
+ * token gate and its gradient: their element's size; float32 arrays: 4-byte).  Outputs must not
  * alias inputs or each other, except where said.  With N == 0 tensors of that
  * size may be NULL; weight gradients are then zero. */
 #define TOPMOE_NORM_BWD_STAGES 2  /* 0 rows, 1 sums over the tokens (forwards: one stage) */

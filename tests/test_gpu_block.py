@@ -293,6 +293,25 @@ def test_postnorm_in_place_and_gradient_of_n_alone(env):
     assert got.out.data_ptr() == out.data_ptr() and torch.equal(got.out, want.out)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_token_gate_off_its_allocation(env, dt):
+    """The gate of a batch's later tokens: values one by one, at any element's offset."""
+    dev, tm = env
+    d = DT[dt]
+    y, res = rnd(1, 9, 64, dt=d).to(dev), rnd(2, 9, 64, dt=d).to(dev)
+    gate, dout = rnd(3, 9, 1, dt=d).to(dev), rnd(4, 9, 64, dt=d).to(dev)
+    for first in (1, 2, 3):
+        cut = [t[first:] for t in (y, res, gate, dout)]
+        o = tm.block_postnorm_fwd(cut[0], cut[1], gate=cut[2])
+        want = tm.block_postnorm_fwd(y, res, gate=gate)
+        b = tm.block_postnorm_bwd(cut[3], cut[0], gate=cut[2])
+        whole = tm.block_postnorm_bwd(dout, y, gate=gate)
+        torch.cuda.synchronize()
+        assert torch.equal(o.out, want.out[first:])
+        for name in ("dy", "dresidual", "dgate"):
+            assert torch.equal(getattr(b, name), getattr(whole, name)[first:]), name
+
+
 def test_norm_infinite_row_stays_in_its_row(env):
     """A row that holds an infinity or NaN gives NaN there and nothing elsewhere."""
     dev, tm = env

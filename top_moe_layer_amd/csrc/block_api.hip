@@ -54,6 +54,12 @@ int norm_shape(int64_t N, int64_t H, int64_t gate_rows) {
   return TOPMOE_OK;
 }
 
+// Alignment of a gate and its gradient: rows of pieces, or values one by one.
+size_t gate_align(int gate_mode, int dtype) {
+  if (gate_mode == kGateChannel) return 16;
+  return dtype == TOPMOE_DTYPE_FP32 ? 4 : 2;
+}
+
 // Tokens that share a row of the gate (the whole batch for the other modes).
 int64_t span_of(int64_t N, int64_t gate_rows) {
   const int64_t s = gate_rows > 0 ? N / gate_rows : N;
@@ -292,7 +298,7 @@ int block_postnorm_fwd(const void* y, const void* residual, const void* w, const
     return TOPMOE_ERR_NULL_ARG;
   if (!(eps > 0.f) || isinf(eps) || !isfinite(residual_scale)) return TOPMOE_ERR_BAD_ARG;
   if (!aligned(y, 16) || !aligned(residual, 16) || !aligned(w, 16) ||
-      !aligned(gate, gate_mode == kGateChannel ? 16 : 4) || !aligned(next_w, 16) ||
+      !aligned(gate, gate_align(gate_mode, dtype)) || !aligned(next_w, 16) ||
       !aligned(out, 16) || !aligned(rstd, 4) || !aligned(n, 16) || !aligned(next_rstd, 4))
     return TOPMOE_ERR_BAD_ARG;
   NormFwd a{};
@@ -334,9 +340,9 @@ int block_postnorm_bwd(const void* dout, const void* dn, const void* y, const vo
   a.units = plan_norm_units(N, pieces(H, dtype), a.gate_rows, a.gate_span);
   if (workspace_bytes < norm_bwd_bytes(a.units, H)) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(dout, 16) || !aligned(dn, 16) || !aligned(y, 16) || !aligned(out, 16) ||
-      !aligned(w, 16) || !aligned(gate, channel ? 16 : 4) || !aligned(next_w, 16) ||
+      !aligned(w, 16) || !aligned(gate, gate_align(gate_mode, dtype)) || !aligned(next_w, 16) ||
       !aligned(rstd, 4) || !aligned(next_rstd, 4) || !aligned(dy, 16) || !aligned(dresidual, 16) ||
-      !aligned(dw, 16) || !aligned(dgate, channel ? 16 : 4) || !aligned(dnext_w, 16) ||
+      !aligned(dw, 16) || !aligned(dgate, gate_align(gate_mode, dtype)) || !aligned(dnext_w, 16) ||
       !aligned(workspace, 256))
     return TOPMOE_ERR_BAD_ARG;
   a.dout = dout; a.dn = dn; a.y = y; a.out = out; a.w = w; a.gate = gate; a.next_w = next_w;

@@ -17,8 +17,8 @@
 // row stays in registers between its statistics and its use, so every tensor
 // is read once and written once.  Bound by memory: post norm with a channel
 // gate and the next norm, 16384 x 2048 bf16 on an MI355X, 46 us forward (268
-// MB, 5.8 TB/s) and 80 us backward (402 MB; rows 74 us with their partial sums
-// at 5.7 TB/s, then the sums).
+// MB, 5.8 TB/s) and 78 us backward (402 MB; rows 71 us with their partial sums
+// at 5.9 TB/s, then the sums).
 //
 // Column sums of the backward pass (dw, dgate, dw_next) are taken in two fixed
 // steps without atomics: each unit of consecutive rows sums its own rows in
@@ -480,8 +480,9 @@ hipError_t fwd_flags(const NormFwd& a, bool post, bool next, int64_t rows, const
 
 template <typename T>
 hipError_t fwd_typed(NormFwd a, bool post, bool next, const Launch& s) {
-  // rows of one launch: at most 2^22, so that a grid keeps below 2^32 threads
-  const int64_t slab = int64_t(1) << 22, N = a.N;
+  // rows of one launch: at most 2^21, so that a grid of 1024 threads a row keeps
+  // below 2^32 threads
+  const int64_t slab = int64_t(1) << 21, N = a.N;
   for (int64_t t0 = 0; t0 < N; t0 += slab) {
     Launch L = s;
     if (t0 > 0) L.start = nullptr;
@@ -614,7 +615,9 @@ NormUnits plan_norm_units(int64_t N, int64_t hv, int64_t gate_rows, int64_t gate
                        : hv <= 512 ? 512 : 256;
   const int64_t rows = (N + most - 1) / most;
   auto whole = [&](int64_t n) { return (n + u.blocks_of - 1) / u.blocks_of * u.blocks_of; };
-  if (gate_span >= rows) {
+  // A gate group as long as a unit is a unit of one whole group, which needs no
+  // sums of its own.
+  if (gate_span > rows || gate_rows == 1) {
     u.per_group = whole((gate_span + rows - 1) / rows);
     u.rows = rows;
     u.count = gate_rows * u.per_group;
