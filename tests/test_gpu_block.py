@@ -201,6 +201,7 @@ POST = [  # gate shape as a function of (N, H), post norm, next norm, residual s
     (lambda N, H: (N // 3, 1, H) if N % 3 == 0 else (1, 1, H), True, True, 1.0),
     (lambda N, H: (3, H) if N % 3 == 0 else (1, H), False, True, 0.0),
     (lambda N, H: (N, H), True, True, 1.0),
+    (lambda N, H: (N // 48, H) if N % 48 == 0 else (1, H), True, True, 1.0),
 ]
 
 
@@ -281,6 +282,17 @@ def test_postnorm_units_of_whole_gate_groups(env, N, H, which, dt):
     groups, in every layout of threads, with and without the next norm."""
     announce(f"postnorm N={N} H={H} case {which} {dt}")
     postnorm_case(env, N, H, dt, which)
+
+
+@pytest.mark.parametrize("N,H,which", [
+    (1200, 200, 8), (600, 768, 8), (4800, 768, 11), (4800, 768, 9), (1536, 4096, 11),
+    (768, 16384, 11), (1800, 768, 8), (2304, 1000, 9), (15360, 200, 11), (960, 64, 7),
+    (4110, 16, 8), (24960, 1000, 11)])
+def test_postnorm_many_gate_rows(env, N, H, which):
+    """Gate rows of few units each, and so many that each is a unit of its own."""
+    announce(f"postnorm N={N} H={H} case {which}")
+    postnorm_case(env, N, H, "fp32", which)
+    postnorm_case(env, N, H, "bf16", which)
 
 
 def test_postnorm_in_place_and_gradient_of_n_alone(env):

@@ -424,6 +424,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
   const int role = a.first_role + int(blockIdx.y);
   const float* part = (role == 1 ? a.part_next : a.part) + (in ? h : 0);
   const int64_t per_group = a.units.per_group / a.units.blocks_of;
+  const uint32_t per = uint32_t(per_group);  // (fewer than 2^32 units)
   int64_t u0 = 0, u1 = a.units.count / a.units.blocks_of;
   if (role >= 2) {
     u0 = int64_t(role - 2) * per_group;
@@ -435,15 +436,24 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
   const T* gate = static_cast<const T*>(a.gate) + (in ? h : 0);
   float acc = 0.f;
   for (int64_t u = u0 + s; u < u1; u += 32 * 8) {
-    float v[8], g[8];
+    float v[8];
+    T g[8];  // converted only after all loads are on their way
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t x = u + i * 32;
       v[i] = x < u1 ? part[x * a.H] : 0.f;
-      g[i] = gated && x < u1 ? to_f32<T>(gate[(x / per_group) * a.H]) : 1.f;
+    }
+    if (gated) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t x = u + i * 32 < u1 ? u + i * 32 : u1 - 1;
+        g[i] = gate[int64_t(uint32_t(x) / per) * a.H];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = u + i * 32 < u1 ? v[i] * to_f32<T>(g[i]) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc = fmaf(v[i], g[i], acc);
+    for (int i = 0; i < 8; ++i) acc += v[i];
   }
   sm[s][col] = acc;
   __syncthreads();
@@ -463,6 +473,32 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
   }
   if (role == 0 && a.dw != nullptr)
     static_cast<T*>(a.dw)[h] = from_f32<T>(one ? acc * to_f32<T>(gate[0]) : acc);
+}
+
+// dgate of many rows from few units each: a thread per value, its units' sums
+// added in order, eight loads in flight.  In a launch of its own from 2^16 values
+// on: 128 rows, 4096 x 16384 bf16, 286 -> 114 us; 32 rows, 16384 x 2048, 68 ->
+// 61; for 8 rows of 2048 the launch would cost more than it saves (21 / 22).
+constexpr int kFewUnits = 32;
+constexpr int64_t kManyValues = int64_t(1) << 16;
+
+template <typename T>
+__global__ __launch_bounds__(256) void norm_gate_sums_kernel(NormBwd a) {
+  const int h = int(blockIdx.x) * 256 + int(threadIdx.x);
+  if (h >= a.H) return;
+  const int64_t g = a.first_role - 2 + int64_t(blockIdx.y);
+  const int units = int(a.units.per_group / a.units.blocks_of);
+  const float* part = a.part + g * units * a.H + h;
+  float acc = 0.f;
+  for (int u = 0; u < units; u += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = u + i < units ? part[int64_t(u + i) * a.H] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc += v[i];
+  }
+  const float w = a.w != nullptr ? to_f32<T>(static_cast<const T*>(a.w)[h]) : 1.f;
+  static_cast<T*>(a.dgate)[g * a.H + h] = from_f32<T>(acc * w);
 }
 
 template <typename T, int R, int V>
@@ -574,20 +610,26 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
   const int64_t gates = channel && a.gate_rows > 1 ? a.gate_rows : 0;
   const int64_t first = first_role ? 0 : next ? 1 : 2;
   const int64_t end = gates > 0 ? 2 + gates : next ? 2 : first_role ? 1 : 0;
+  const bool few = a.units.count > 0 && gates * a.H >= kManyValues &&
+                   a.units.per_group <= kFewUnits * a.units.blocks_of;
   Launch L = sums;
   for (int64_t r = first; r < end;) {
     if (r == 1 && !next) {
       r = 2;
       continue;
     }
-    int64_t stop = r == 0 && !next ? 1 : end;
+    int64_t stop = r == 0 && !next ? 1 : r < 2 && few && end > 2 ? 2 : end;
     if (stop - r > 65535) stop = r + 65535;
     L.stop = stop == end ? sums.stop : nullptr;
     NormBwd b = a;
     b.first_role = int(r);
+    const unsigned roles = unsigned(stop - r);
     const hipError_t e =
-        launch_kernel(norm_reduce_kernel<T>, dim3(unsigned((a.H + 31) / 32), unsigned(stop - r)),
-                      dim3(1024), 0, L, b);
+        r >= 2 && few
+            ? launch_kernel(norm_gate_sums_kernel<T>, dim3(unsigned((a.H + 255) / 256), roles),
+                            dim3(256), 0, L, b)
+            : launch_kernel(norm_reduce_kernel<T>, dim3(unsigned((a.H + 31) / 32), roles),
+                            dim3(1024), 0, L, b);
     if (e != hipSuccess) return e;
     sums.launched = true;
     L.start = nullptr;
@@ -615,15 +657,17 @@ NormUnits plan_norm_units(int64_t N, int64_t hv, int64_t gate_rows, int64_t gate
                        : hv <= 512 ? 512 : 256;
   const int64_t rows = (N + most - 1) / most;
   auto whole = [&](int64_t n) { return (n + u.blocks_of - 1) / u.blocks_of * u.blocks_of; };
-  // A gate group as long as a unit is a unit of one whole group, which needs no
-  // sums of its own.
-  if (gate_span > rows || gate_rows == 1) {
+  // Units of whole groups need no sums for the gate: for groups no longer than a
+  // unit (16384 x 2048, 1024 gate rows: 241 -> 47 us), and for enough groups to
+  // fill the chip by themselves (512 gate rows: 64 -> 51; 256: 62 -> 73).
+  const bool fill = gate_rows >= 512 && gate_rows >= 128 * u.blocks_of;
+  if (gate_rows == 1 || (gate_span > rows && !fill)) {
     u.per_group = whole((gate_span + rows - 1) / rows);
     u.rows = rows;
     u.count = gate_rows * u.per_group;
   } else {
     u.per_group = 0;
-    u.rows = rows / gate_span * gate_span;
+    u.rows = gate_span > rows ? gate_span : rows / gate_span * gate_span;
     u.count = whole((N + u.rows - 1) / u.rows);
   }
   return u;
