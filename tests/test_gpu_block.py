@@ -49,6 +49,10 @@ ROUTES = [  # N, H, E, k, capacity factor, share of padding tokens, one expert t
     (90, 131072, 4, 3, 1.0, 0.1, False),  # few entries of long rows: bf16 one launch, fp32 three
     (700, 104, 5, 2, 0.0, 0.0, False),
     (700, 104, 5, 2, 0.01, 0.3, True),
+    (701, 200, 5, 2, 0.0, 0.1, False),  # parts of a wavefront a row, or a whole one
+    (61, 128, 6, 3, 1.0, 0.1, False),
+    (61, 256, 6, 3, 1.0, 0.1, False),
+    (61, 264, 6, 3, 1.0, 0.1, False),
     (3001, 16, 64, 6, 1.25, 0.05, False),
     (2500, 8, 256, 4, 1.0, 0.0, True),
     (40000, 8, 2, 1, 0.0, 0.0, False),

@@ -349,18 +349,19 @@ __global__ __launch_bounds__(256) void gather_sum_kernel(
   store_piece(out + t * H + h, acc);
 }
 
-// dys[row(i)] = alpha[i] dy[t] and dalpha[i] = dy[t] . ys[row(i)]: one
-// wavefront per entry, consecutive entries in a block, so that a token's k
-// wavefronts share its dy row in the caches; each row of ys is read once,
-// non-temporally, and dys written so when it is large (NT): 16384 x 2048 bf16,
-// k = 2: 66.3 -> 63.2 -> 54.0 us, 6.2 TB/s.
-template <typename T, bool NT>
+// dys[row(i)] = alpha[i] dy[t] and dalpha[i] = dy[t] . ys[row(i)]: a wavefront,
+// or for rows of few pieces a part of one, R lanes per entry, consecutive
+// entries in a block, so that a token's k entries share its dy row in the
+// caches; each row of ys is read once, non-temporally, and dys written so when
+// it is large (NT): 16384 x 2048 bf16, k = 2: 66.3 -> 63.2 -> 54.0 us, 6.2 TB/s.
+// Fewer lanes: 32768 tokens, k = 8, H = 64, 128, 256: 71, 78, 89 -> 24, 28, 57 us.
+template <typename T, bool NT, int R>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(
     const T* __restrict__ dy, const T* __restrict__ ys, const int32_t* __restrict__ entry_row,
     const float* __restrict__ alpha, int64_t n, int64_t i0, int hv, int H, int k,
     T* __restrict__ dys, float* __restrict__ dalpha) {
-  const int lane = threadIdx.x & 63;
-  const int64_t i = i0 + int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int lane = int(threadIdx.x) % R;
+  const int64_t i = i0 + int64_t(blockIdx.x) * (256 / R) + int(threadIdx.x) / R;
   if (i >= n) return;
   const int64_t r = entry_row[i];
   const int64_t row = r < 0 ? -1 - r : r;
@@ -370,7 +371,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(
   }
   T* o = dys + row * H;
   if (r < 0) {
-    for (int p = lane; p < hv; p += 64)
+    for (int p = lane; p < hv; p += R)
       *reinterpret_cast<u32x4*>(o + p * kE<T>) = u32x4{0u, 0u, 0u, 0u};
     if (lane == 0) dalpha[i] = 0.f;
     return;
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(
   const T* s = ys + row * H;
   const float a = alpha[i];
   float dot = 0.f;
-  for (int p = lane; p < hv; p += 64) {
+  for (int p = lane; p < hv; p += R) {
     float fd[kE<T>], fs[kE<T>];
     unpack(load_piece(d + p * kE<T>), fd);
     unpack(load_piece<true>(s + p * kE<T>), fs);
@@ -390,7 +391,8 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(
     }
     store_piece<NT>(o + p * kE<T>, fd);
   }
-  dot = wave_sum(dot);
+#pragma unroll
+  for (int o = R / 2; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
   if (lane == 0) dalpha[i] = dot;
 }
 
@@ -457,15 +459,16 @@ hipError_t gather_sum(const void* rows, const int32_t* entry_row, const float* a
   });
 }
 
-template <typename T>
+template <typename T, int R>
 hipError_t combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
                        const float* alpha, int64_t N, int H, int k, void* dys, float* dalpha,
                        const Launch& s) {
   const int64_t n = N * k;
   return for_slabs(n, int64_t(1) << 24, s, [&](int64_t i0, int64_t m, const Launch& L) {
-    const auto kernel = n * H * int64_t(sizeof(T)) >= kNtBytes ? combine_bwd_kernel<T, true>
-                                                               : combine_bwd_kernel<T, false>;
-    return launch_kernel(kernel, dim3(unsigned((m + 3) / 4)), dim3(256), 0, L,
+    const auto kernel = n * H * int64_t(sizeof(T)) >= kNtBytes ? combine_bwd_kernel<T, true, R>
+                                                               : combine_bwd_kernel<T, false, R>;
+    constexpr int side = 256 / R;
+    return launch_kernel(kernel, dim3(unsigned((m + side - 1) / side)), dim3(256), 0, L,
                          static_cast<const T*>(dy), static_cast<const T*>(ys), entry_row, alpha,
                          n, i0, H / kE<T>, H, k, static_cast<T*>(dys), dalpha);
   });
@@ -524,9 +527,17 @@ hipError_t launch_gather_sum(const void* rows, const int32_t* entry_row, const f
 hipError_t launch_moe_combine_bwd(const void* dy, const void* ys, const int32_t* entry_row,
                                   const float* alpha, int64_t N, int H, int k, int dtype,
                                   void* dys, float* dalpha, const Launch& s) {
-  return dtype == TOPMOE_DTYPE_FP32
-             ? combine_bwd<float>(dy, ys, entry_row, alpha, N, H, k, dys, dalpha, s)
-             : combine_bwd<bf16_t>(dy, ys, entry_row, alpha, N, H, k, dys, dalpha, s);
+#define TOPMOE_COMBINE_BWD(T, R) \
+  return combine_bwd<T, R>(dy, ys, entry_row, alpha, N, H, k, dys, dalpha, s)
+  if (dtype == TOPMOE_DTYPE_FP32) {
+    if (H <= 64) TOPMOE_COMBINE_BWD(float, 16);
+    if (H <= 128) TOPMOE_COMBINE_BWD(float, 32);
+    TOPMOE_COMBINE_BWD(float, 64);
+  }
+  if (H <= 128) TOPMOE_COMBINE_BWD(bf16_t, 16);
+  if (H <= 256) TOPMOE_COMBINE_BWD(bf16_t, 32);
+  TOPMOE_COMBINE_BWD(bf16_t, 64);
+#undef TOPMOE_COMBINE_BWD
 }
 
 }  // namespace topmoe
