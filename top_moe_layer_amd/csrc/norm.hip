@@ -572,12 +572,15 @@ hipError_t bwd_flags(const NormBwd& a, bool post, bool next, const Launch& L) {
 
 // Rows of 513 to 1024 pieces.  Both norms of eight channels a piece leave 1024
 // threads no registers for the next row (H = 8192: 93 us loading each row when
-// it is needed, 84 with spilled registers, 79 with 512 threads).
+// it is needed, 84 with spilled registers, 79 with 512 threads), 768 threads
+// have them (H = 4200: 93 -> 84 us, 5944: 84 -> 81; with one norm, or between
+// the other widths' threads, as many idle lanes less gave nothing).
 template <typename T>
 hipError_t bwd_upto_1024(const NormBwd& a, bool post, bool next, const Launch& L) {
   if constexpr (kE<T> == 4) {
     return bwd_flags<T, 1024, 1, true>(a, post, next, L);
   } else {
+    if (post && next && a.hv <= 768) return bwd_kernel<T, 768, 1, true, true, true>(a, L);
     if (post && next) return bwd_kernel<T, 512, 2, true, true, true>(a, L);
     if (post) return bwd_kernel<T, 1024, 1, true, false, true>(a, L);
     return bwd_kernel<T, 1024, 1, false, true, true>(a, L);
