@@ -486,7 +486,8 @@ def test_no_tokens(env):
     p = tm.block_prenorm_fwd(e(0, 16), w)
     b = tm.block_prenorm_bwd(e(0, 16), e(0, 16), w, p.rstd)
     assert p.n.shape == (0, 16) and b.dw.abs().max() == 0
-    for gate in (None, torch.ones(16, device=dev), torch.ones(3, 16, device=dev), e(0, 1), e(0, 16)):
+    for gate in (None, torch.ones(16, device=dev), torch.ones(3, 16, device=dev), e(0, 1), e(0, 16),
+                 torch.ones(70000, 16, device=dev)):
         q = tm.block_postnorm_fwd(e(0, 16), e(0, 16), w, gate=gate, next_w=w)
         b = tm.block_postnorm_bwd(e(0, 16), e(0, 16), w, rstd=q.rstd, gate=gate, dn=e(0, 16),
                                   out=q.out, next_w=w, next_rstd=q.next_rstd)

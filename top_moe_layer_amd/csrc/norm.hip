@@ -486,7 +486,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void norm_gate_sums_kernel(NormBwd a) {
   const int h = int(blockIdx.x) * 256 + int(threadIdx.x);
   if (h >= a.H) return;
-  const int64_t g = a.first_role - 2 + int64_t(blockIdx.y);
+  const int64_t g = blockIdx.y;
   const int units = int(a.units.per_group / a.units.blocks_of);
   const float* part = a.part + g * units * a.H + h;
   float acc = 0.f;
@@ -606,8 +606,9 @@ hipError_t bwd_typed(const NormBwd& a, bool post, bool next, const Launch& rows,
     else if constexpr (kE<T> == 4) e = bwd_flags<T, 1024, 4, false>(a, post, next, rows);
     if (e != hipSuccess) return e;
   }
-  // The roles of the sums; neighbouring ones share a launch (a grid has at
-  // most 65535 rows).
+  // The roles of the sums; neighbouring ones share a launch.  With tokens there
+  // are fewer than 4096 gate rows (see plan_norm_units: more are written by units
+  // of whole groups); an empty batch's may be more than a grid has rows.
   const bool channel = post && a.gate_mode == kGateChannel && a.units.per_group > 0;
   const bool first_role = post && (a.dw != nullptr || (channel && a.gate_rows == 1));
   const int64_t gates = channel && a.gate_rows > 1 ? a.gate_rows : 0;
