@@ -424,7 +424,6 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
   const int role = a.first_role + int(blockIdx.y);
   const float* part = (role == 1 ? a.part_next : a.part) + (in ? h : 0);
   const int64_t per_group = a.units.per_group / a.units.blocks_of;
-  const uint32_t per = uint32_t(per_group);  // (fewer than 2^32 units)
   int64_t u0 = 0, u1 = a.units.count / a.units.blocks_of;
   if (role >= 2) {
     u0 = int64_t(role - 2) * per_group;
@@ -434,6 +433,9 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
   const bool gated = role == 0 && a.gate_mode == kGateChannel && a.units.per_group > 0 &&
                      a.gate_rows > 1;
   const T* gate = static_cast<const T*>(a.gate) + (in ? h : 0);
+  // x / per_group as x * ceil(2^28 / per_group) >> 28, exact for both below 2^14:
+  // plans of several gate rows that get here have fewer than 2^13 blocks.
+  const uint64_t magic = gated ? ((1u << 28) + uint32_t(per_group) - 1) / uint32_t(per_group) : 0;
   float acc = 0.f;
   for (int64_t u = u0 + s; u < u1; u += 32 * 8) {
     float v[8];
@@ -447,7 +449,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormBwd a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t x = u + i * 32 < u1 ? u + i * 32 : u1 - 1;
-        g[i] = gate[int64_t(uint32_t(x) / per) * a.H];
+        g[i] = gate[int64_t(uint32_t(x) * magic >> 28) * a.H];
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = u + i * 32 < u1 ? v[i] * to_f32<T>(g[i]) : 0.f;
