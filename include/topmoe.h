@@ -78,10 +78,11 @@ extern "C" {
 #define TOPMOE_ERR_WORKSPACE_TOO_SMALL  -4  /* workspace_bytes < *_workspace_bytes()  */
 #define TOPMOE_ERR_HIP                  -5  /* a HIP runtime call or launch failed    */
 #define TOPMOE_ERR_BAD_ARG              -6  /* aux_coef, z_coef or capacity_factor negative or not
-                                               finite; aux_grad, z_grad or residual_scale not
-                                               finite; eps not positive and finite; unknown
-                                               flag bits or gate mode; misaligned pointer; a
-                                               launch-shape override that is not instantiated */
+                                               finite; a negative capacity; aux_grad, z_grad
+                                               or residual_scale not finite; eps not positive
+                                               and finite; unknown flag bits or gate mode;
+                                               misaligned pointer; a launch-shape override
+                                               that is not instantiated */
 #define TOPMOE_ERR_SCRATCH_TOO_SMALL    -7  /* moe_ffn_fwd_noalloc: the problem's workspace
                                                exceeds the fixed scratch */
 
@@ -164,8 +165,10 @@ size_t moe_workspace_bytes(int64_t N, int64_t H, int64_t I, int E, int k, int dt
  *   aux_coef             router_aux_loss_coef (>= 0); 0 gives aux = 0 exactly,
  *                        which is also the module's value outside training
  *   z_coef               router z-loss coefficient (>= 0); 0 gives z_loss = 0
- *   capacity_factor      expert capacity factor (>= 0); 0 = no capacity (dropless,
- *                        the pages' module); a capacity of N or more drops nothing
+ *   capacity_factor      expert capacity factor (>= 0), of which the float's own
+ *                        value counts (the float nearest 1.2 lies above it); 0 =
+ *                        no capacity (dropless, the pages' module); a capacity of
+ *                        N or more drops nothing
  *   flags                0, or TOPMOE_MOE_RAW_TOPK_WEIGHTS and / or TOPMOE_MOE_EVAL
  *   y        [N, H]      output (dtype): y_t = residual_t (or 0) + the sum over
  *                        the selected (and kept) experts in ascending expert id
@@ -345,9 +348,9 @@ int moe_ffn_bwd(const void* x, const float* Wr, const void* Wg, const void* Wu,
  *
  * Entry i = t * k + j is slot j of token t.  Its rank is the number of earlier
  * entries of the same expert (a token may name an expert twice: two entries).
- * An expert keeps its first C = ceil(capacity_factor * N * k / E) entries (all
- * of them for capacity_factor 0); an entry whose topk_idx is outside [0, E)
- * -- a padding token's -1 -- is kept by none.  Kept entries take the rows
+ * An expert keeps its first C entries (all of them without a capacity); an
+ * entry whose topk_idx is outside [0, E) -- a padding token's -1 -- is kept by
+ * none.  Kept entries take the rows
  * [0, expert_offsets[E]), grouped by ascending expert and in rank order; the
  * others take the rows behind them, by (expert, rank), those without an expert
  * last, and their rows hold zeros.  Every row of the [N * k, H] outputs is
@@ -372,6 +375,10 @@ size_t moe_dispatch_workspace_bytes(int64_t N, int E, int k);
 /* xs[row(i)] = x[t].
  *   x        [N, H]     tokens (dtype)
  *   topk_idx [N, k]     int32 experts
+ *   capacity_factor     C = ceil(capacity_factor * N * k / E) of the float's own
+ *                       value, in double; 0 = no capacity.  The float nearest
+ *                       1.2 lies above it: where such a product should be a
+ *                       whole number, give C itself (moe_dispatch_fwd_capacity)
  *   xs       [N*k, H]   output (dtype): the rows by expert, zeros behind them
  *   expert_offsets [E+1] int32 output: first row of each expert; [E]: kept rows
  *   row_entry [N*k]     int32 output: the entry of each kept row, then -1
@@ -383,6 +390,12 @@ int moe_dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t 
                      float capacity_factor, int dtype, void* xs, int32_t* expert_offsets,
                      int32_t* row_entry, int32_t* entry_row, void* workspace,
                      size_t workspace_bytes, void* stream, void* const* stage_events);
+/* The same with C itself: capacity >= 0 entries an expert, 0 = no capacity. */
+int moe_dispatch_fwd_capacity(const void* x, const int32_t* topk_idx, int64_t N, int64_t H, int E,
+                              int k, int64_t capacity, int dtype, void* xs,
+                              int32_t* expert_offsets, int32_t* row_entry, int32_t* entry_row,
+                              void* workspace, size_t workspace_bytes, void* stream,
+                              void* const* stage_events);
 /* dx[t] = the sum over t's kept entries, in slot order, of dxs[entry_row]
  * (fp32, rounded once).  dxs [N*k, H], entry_row [N, k] as the dispatch wrote
  * it, dx [N, H].  One stage. */

@@ -1,5 +1,7 @@
 """Refusals of the block operators that need no GPU: the C ABI validates on the
 host before anything is launched, the torch front end before that."""
+import math
+
 import pytest
 import torch
 
@@ -159,3 +161,32 @@ def test_front_end_refusals():
             f()
     with pytest.raises(TypeError):
         tm.act8_pack([1.0])
+
+
+@pytest.mark.parametrize("factor", [1.2, 0.6, 1.6, 1.1, 0.7, 1.25, 0.01, 1e-300, 5.0, 1e308])
+def test_capacity_of_a_factor(factor):
+    """Whole-number products of factors that 32 bits do not hold stay whole (1.2 as a float lies
+    above 1.2)."""
+    from top_moe_layer_amd import block
+
+    for N, E, k in ((50, 10, 2), (500, 8, 2), (1000, 10, 1), (33, 5, 3), (1 << 20, 64, 8)):
+        n = N * k
+        c = factor * n / E
+        assert (block._capacity(factor, N, E, k) or n) == (min(math.ceil(c), n) if c < n else n)
+    assert block._capacity(1.2, 50, 10, 2) == 12
+    assert block._capacity(0.0, 50, 10, 2) == 0
+    for bad in (-1.0, NAN, INF):
+        with pytest.raises(tm.TopmoeError):
+            block._capacity(bad, 50, 10, 2)
+
+
+def test_capacity_refusals():
+    base = {("capacity" if n == "cf" else n): (0 if n == "cf" else v) for n, v in DISPATCH.items()}
+    name = "moe_dispatch_fwd_capacity"
+    assert call(name, base) == B.ERR_WORKSPACE_TOO_SMALL
+    assert call(name, base, capacity=1 << 40) == B.ERR_WORKSPACE_TOO_SMALL
+    assert call(name, base, capacity=-1) == B.ERR_BAD_ARG
+    assert call(name, base, capacity=-(1 << 40)) == B.ERR_BAD_ARG
+    assert call(name, base, dtype=2) == B.ERR_UNSUPPORTED_DTYPE
+    assert call(name, base, E=0) == B.ERR_BAD_SHAPE
+    assert call(name, base, xs=None) == B.ERR_NULL_ARG

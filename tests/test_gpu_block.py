@@ -92,6 +92,33 @@ def test_dispatch(env, N, H, E, k, cf, pad, one, dt):
     assert torch.equal(bits(o.xs.cpu()), bits(want))
 
 
+@pytest.mark.parametrize("N,E,k,cf", [(50, 10, 2, 1.2), (50, 10, 2, 0.6), (500, 8, 2, 1.2),
+                                      (500, 8, 2, 1.6), (17000, 10, 2, 1.1)])
+def test_dispatch_capacity_factors_between_floats(env, N, E, k, cf):
+    """Factors whose product is a whole number, and which a float exceeds: the C entry point takes
+    the float's own value, the front end the factor it is given."""
+    dev, tm = env
+    from top_moe_layer_amd import _binding as B
+
+    announce(f"dispatch capacity N={N} E={E} k={k} factor {cf}")
+    g = torch.Generator().manual_seed(N)
+    idx = torch.where(torch.rand(N, k, generator=g) < 0.7, 1, 3).to(torch.int32)
+    x, on = rnd(1, N, 8).to(dev), idx.to(dev)
+    o = tm.moe_dispatch_fwd(x, on, E, capacity_factor=cf)
+    torch.cuda.synchronize()
+    want = R.rows_of(idx.tolist(), E, cf)
+    assert (o.expert_offsets.tolist(), o.row_entry.tolist(), o.entry_row.flatten().tolist()) == want
+    ws = torch.empty(tm.moe_dispatch_workspace_bytes(N, E, k), dtype=torch.uint8, device=dev)
+    single = float(torch.tensor(cf, dtype=torch.float32))
+    st = B.lib().moe_dispatch_fwd(x.data_ptr(), on.data_ptr(), N, 8, E, k, cf, B.DTYPE_FP32,
+                                  o.xs.data_ptr(), o.expert_offsets.data_ptr(),
+                                  o.row_entry.data_ptr(), o.entry_row.data_ptr(), ws.data_ptr(),
+                                  ws.numel(), torch.cuda.current_stream().cuda_stream, None)
+    torch.cuda.synchronize()
+    assert st == B.OK
+    assert o.expert_offsets.tolist() == R.rows_of(idx.tolist(), E, single)[0] != want[0]
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("N,H,E,k,cf,pad,one", [r for r in ROUTES if r[0] * r[1] * r[3] < 1 << 21])
 def test_back_to_tokens(env, N, H, E, k, cf, pad, one, dt):

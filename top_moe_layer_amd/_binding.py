@@ -80,6 +80,8 @@ SIGNATURES = {
     "moe_dispatch_workspace_bytes": (_sz, [_i64, _i32, _i32]),
     "moe_dispatch_fwd": (_i32, [_vp, _vp, _i64, _i64, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp,
                                 _vp, _sz, _vp, _vp]),
+    "moe_dispatch_fwd_capacity": (_i32, [_vp, _vp, _i64, _i64, _i32, _i32, _i64, _i32, _vp, _vp,
+                                         _vp, _vp, _vp, _sz, _vp, _vp]),
     "moe_dispatch_bwd": (_i32, [_vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp]),
     "moe_combine_fwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp]),
     "moe_combine_bwd": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),

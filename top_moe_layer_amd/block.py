@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import functools
 import inspect
+import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -116,6 +117,17 @@ def moe_dispatch_workspace_bytes(N: int, E: int, k: int) -> int:
     return int(B.lib().moe_dispatch_workspace_bytes(N, E, k))
 
 
+def _capacity(factor: float, N: int, E: int, k: int) -> int:
+    """Entries an expert keeps, ceil(factor * N * k / E) as Python evaluates it
+    (the C entry point's float would take 1.2 for a little more); 0: all."""
+    if factor == 0.0:
+        return 0
+    if not 0.0 < factor < math.inf:
+        B.check(B.ERR_BAD_ARG, "moe_dispatch_fwd")
+    c = factor * N * k / E
+    return max(math.ceil(c), 1) if c < N * k else 0
+
+
 @_on_kernel_stream
 def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
                      capacity_factor: float = 0.0, xs: Optional[torch.Tensor] = None,
@@ -124,8 +136,9 @@ def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
     """The tokens' rows sorted by expert (stable: ascending token within an
     expert).  x [..., H]; topk_idx [N, k] int32, entries outside [0, E) (a
     padding token's -1) belong to no expert.  ``capacity_factor`` > 0 keeps
-    the first ceil(factor * N * k / E) entries of each expert.  Entries not
-    kept have zero rows behind the experts' (from expert_offsets[E])."""
+    the first ceil(capacity_factor * N * k / E) entries of each expert, in
+    Python's floats.  Entries not kept have zero rows behind the experts'
+    (from expert_offsets[E])."""
     dev, dt = x.device, x.dtype
     code = _code(dt)
     N, H = _rows(x, "x")
@@ -135,6 +148,7 @@ def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
     _is(topk_idx, "topk_idx", (N, k), torch.int32, dev)
     if not 1 <= E <= B.DISPATCH_MAX_EXPERTS:
         B.check(B.ERR_BAD_SHAPE, "moe_dispatch_fwd")
+    cap = _capacity(float(capacity_factor), N, E, k)
     wp = wn = ws = None
     if (workspace is not None or N * k > B.DISPATCH_ONE or
             N * (k + 1) * H * x.element_size() >= B.DISPATCH_ONE_BYTES):
@@ -147,8 +161,8 @@ def moe_dispatch_fwd(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *,
     offsets = _empty(E + 1, dtype=torch.int32, device=dev)
     row_entry = _empty(N * k, dtype=torch.int32, device=dev)
     entry_row = torch.empty_like(topk_idx)
-    _call("moe_dispatch_fwd", dev, stage_events, x.data_ptr(), topk_idx.data_ptr(), N, H, E, k,
-          float(capacity_factor), code, xs.data_ptr(), offsets.data_ptr(), row_entry.data_ptr(),
+    _call("moe_dispatch_fwd_capacity", dev, stage_events, x.data_ptr(), topk_idx.data_ptr(), N, H,
+          E, k, cap, code, xs.data_ptr(), offsets.data_ptr(), row_entry.data_ptr(),
           entry_row.data_ptr(), wp, wn or 0)
     return MoeRows(xs, offsets, row_entry, entry_row)
 

@@ -66,7 +66,7 @@ const char* topmoe_strerror(int status) {
              "of moe_ffn_fwd_noalloc (TOPMOE_NOALLOC_SCRATCH_BYTES, 64 MiB)";
     case TOPMOE_ERR_BAD_ARG:
       return "invalid argument (aux_coef, z_coef or capacity_factor negative or not finite, "
-             "aux_grad, z_grad or residual_scale not finite, eps not positive and finite, an "
+             "a negative capacity, aux_grad, z_grad or residual_scale not finite, eps not positive and finite, an "
              "unknown gate mode, unknown flag bits, a misaligned pointer, or a launch-shape "
              "override that is not instantiated)";
   }

@@ -35,11 +35,46 @@ int rows_shape(int64_t N, int64_t H, int k) {
   return TOPMOE_OK;
 }
 
-// Entries an expert keeps: ceil(capacity_factor * N * k / E); INT32_MAX = all.
-int kept_entries(double capacity_factor, int64_t N, int k, int E) {
-  if (capacity_factor <= 0.0) return INT32_MAX;
-  const double c = ceil(capacity_factor * double(N) * double(k) / double(E));
+// Entries an expert keeps, INT32_MAX = all, -1 = no such capacity: of a factor
+// ceil(factor * N * k / E), of the float's own value, or the capacity itself.
+int kept_entries(float factor, int64_t N, int k, int E) {
+  if (!nonneg_finite(factor)) return -1;
+  if (factor == 0.f) return INT32_MAX;
+  const double c = ceil(double(factor) * double(N) * double(k) / double(E));
   return c >= double(N) * double(k) ? INT32_MAX : int(c);
+}
+int kept_entries(int64_t capacity, int64_t, int, int) {
+  return capacity < 0 ? -1 : capacity == 0 || capacity > kMaxRows ? INT32_MAX : int(capacity);
+}
+
+template <typename Capacity>
+int dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t H, int E, int k,
+                 Capacity capacity, int dtype, void* xs, int32_t* expert_offsets,
+                 int32_t* row_entry, int32_t* entry_row, void* workspace, size_t workspace_bytes,
+                 void* stream, void* const* stage_events) {
+  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
+  if (E < 1 || E > kDispatchMaxExperts || k > E) return TOPMOE_ERR_BAD_SHAPE;
+  const int status = rows_shape(N, H, k);
+  if (status != TOPMOE_OK) return status;
+  const bool one = dispatch_in_one(N, H, k, dtype == TOPMOE_DTYPE_FP32 ? 4 : 2);
+  const size_t need = one ? 0 : plan_dispatch(N * k, E).bytes;
+  if (!expert_offsets || (need > 0 && !workspace) ||
+      (N > 0 && (!x || !topk_idx || !xs || !row_entry || !entry_row)))
+    return TOPMOE_ERR_NULL_ARG;
+  const int cap = kept_entries(capacity, N, k, E);
+  if (cap < 0) return TOPMOE_ERR_BAD_ARG;
+  if (need > 0 && workspace_bytes < need) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(topk_idx, 4) || !aligned(expert_offsets, 4) ||
+      !aligned(row_entry, 4) || !aligned(entry_row, 4) || !aligned(workspace, 256))
+    return TOPMOE_ERR_BAD_ARG;
+  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
+  const Launch rows = st.at(0), copy = st.at(1);
+  TOPMOE_TRY(launch_dispatch_rows(x, topk_idx, N, int(H), E, k, cap, dtype, xs, expert_offsets,
+                                  row_entry, entry_row, static_cast<int32_t*>(workspace), rows,
+                                  copy));
+  TOPMOE_TRY(st.close(rows));
+  TOPMOE_TRY(st.close(copy));
+  return TOPMOE_OK;
 }
 
 // ---- norms
@@ -154,29 +189,17 @@ int moe_dispatch_fwd(const void* x, const int32_t* topk_idx, int64_t N, int64_t 
                      float capacity_factor, int dtype, void* xs, int32_t* expert_offsets,
                      int32_t* row_entry, int32_t* entry_row, void* workspace,
                      size_t workspace_bytes, void* stream, void* const* stage_events) {
-  if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
-  if (E < 1 || E > kDispatchMaxExperts || k > E) return TOPMOE_ERR_BAD_SHAPE;
-  const int status = rows_shape(N, H, k);
-  if (status != TOPMOE_OK) return status;
-  const bool one = dispatch_in_one(N, H, k, dtype == TOPMOE_DTYPE_FP32 ? 4 : 2);
-  const size_t need = one ? 0 : plan_dispatch(N * k, E).bytes;
-  if (!expert_offsets || (need > 0 && !workspace) ||
-      (N > 0 && (!x || !topk_idx || !xs || !row_entry || !entry_row)))
-    return TOPMOE_ERR_NULL_ARG;
-  if (!nonneg_finite(capacity_factor)) return TOPMOE_ERR_BAD_ARG;
-  if (need > 0 && workspace_bytes < need) return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
-  if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(topk_idx, 4) || !aligned(expert_offsets, 4) ||
-      !aligned(row_entry, 4) || !aligned(entry_row, 4) || !aligned(workspace, 256))
-    return TOPMOE_ERR_BAD_ARG;
-  const Stages st{stage_events, static_cast<hipStream_t>(stream)};
-  const Launch rows = st.at(0), copy = st.at(1);
-  TOPMOE_TRY(launch_dispatch_rows(x, topk_idx, N, int(H), E, k,
-                                  kept_entries(capacity_factor, N, k, E), dtype, xs,
-                                  expert_offsets, row_entry, entry_row,
-                                  static_cast<int32_t*>(workspace), rows, copy));
-  TOPMOE_TRY(st.close(rows));
-  TOPMOE_TRY(st.close(copy));
-  return TOPMOE_OK;
+  return dispatch_fwd(x, topk_idx, N, H, E, k, capacity_factor, dtype, xs, expert_offsets,
+                      row_entry, entry_row, workspace, workspace_bytes, stream, stage_events);
+}
+
+int moe_dispatch_fwd_capacity(const void* x, const int32_t* topk_idx, int64_t N, int64_t H, int E,
+                              int k, int64_t capacity, int dtype, void* xs,
+                              int32_t* expert_offsets, int32_t* row_entry, int32_t* entry_row,
+                              void* workspace, size_t workspace_bytes, void* stream,
+                              void* const* stage_events) {
+  return dispatch_fwd(x, topk_idx, N, H, E, k, capacity, dtype, xs, expert_offsets, row_entry,
+                      entry_row, workspace, workspace_bytes, stream, stage_events);
 }
 
 int moe_dispatch_bwd(const void* dxs, const int32_t* entry_row, int64_t N, int64_t H, int k,
