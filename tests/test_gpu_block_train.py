@@ -361,6 +361,45 @@ def test_keep8_holds_less(env):
     assert held["act8"] * 4 < held[True]
 
 
+@pytest.mark.parametrize("kind", ["dense", "moe"])
+def test_keep8_released_by_the_backward(env, kind):
+    """The kept bytes are a saved tensor of the graph: gone after its backward while the output
+    still holds it, there again for a second pass where the graph is retained, seen by hooks."""
+    dev, tm = env
+    announce(f"kept bytes after the backward, {kind}")
+    N, H, I, E, k = 512, 256, 704, 4, 2
+    d = torch.bfloat16
+    if kind == "dense":
+        shapes, kept = ((N, H), (I, H), (I, H), (H, I)), tm.ffn_keep8_bytes(N, H, I, d)
+        run = lambda L: tm.swiglu_ffn(*L, keep_activations="act8")
+    else:
+        shapes = ((N, H), (E, H), (E, I, H), (E, I, H), (E, H, I))
+        kept = tm.moe_keep8_bytes(N, H, I, E, k, d)
+        run = lambda L: tm.moe_ffn(*L, k, 0.0, keep_activations="act8")[0]
+    L = [rnd(i, *s, dt=torch.float32 if s == (E, H) else d, scale=0.1).to(dev).requires_grad_()
+         for i, s in enumerate(shapes)]
+    dy = rnd(9, N, H, dt=d).to(dev)
+    for t in L:
+        t.grad = torch.zeros_like(t)  # so that the gradients take no new memory
+    seen = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: seen.append(t.numel()) or t, lambda t: t):
+        y = run(L)
+    assert kept in seen
+    y = run(L)
+    y.backward(dy, retain_graph=True)
+    first = [t.grad.clone() for t in L]
+    for t in L:
+        t.grad.zero_()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    y.backward(dy)
+    torch.cuda.synchronize()
+    assert before - torch.cuda.memory_allocated() >= kept
+    assert all(eq(t.grad, g) for t, g in zip(L, first))
+    with pytest.raises(RuntimeError):
+        y.backward(dy)
+
+
 def test_keep8_captured(env):
     """The training step with kept bytes in a graph, replayed over new inputs."""
     dev, tm = env

@@ -29,10 +29,8 @@ def _keep_mode(keep_activations) -> int:
 class _SwiGLUFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, Wg, Wu, Wd, residual, keep):
-        ctx.save_for_backward(x, Wg, Wu, Wd)
         ctx.has_residual = residual is not None
-        ctx.saved = ctx.kept = None
-        saved = None
+        ctx.saved = saved = kept = None
         if keep and any(ctx.needs_input_grad[:4]):
             H, I = x.shape[-1], Wg.shape[0]
             N = x.numel() // H
@@ -40,18 +38,19 @@ class _SwiGLUFunction(torch.autograd.Function):
             saved = torch.empty(max(nb, 256), dtype=torch.uint8, device=x.device)
         y = ops.ffn_swiglu_fwd(x, Wg, Wu, Wd, residual=residual, saved=saved)
         if saved is not None and keep == 2:
-            ctx.kept = block.ffn_swiglu_keep8(saved, N, H, I, x.dtype)
+            kept = block.ffn_swiglu_keep8(saved, N, H, I, x.dtype)
         else:
             ctx.saved = saved
+        ctx.save_for_backward(x, Wg, Wu, Wd, kept)  # released by the backward, as the inputs are
         return y
 
     @staticmethod
     def backward(ctx, dy):
-        x, Wg, Wu, Wd = ctx.saved_tensors
+        x, Wg, Wu, Wd, kept = ctx.saved_tensors
         saved = ctx.saved
-        if ctx.kept is not None:
+        if kept is not None:
             H, I = x.shape[-1], Wg.shape[0]
-            saved = block.ffn_swiglu_restore8(ctx.kept, x.numel() // H, H, I, x.dtype)
+            saved = block.ffn_swiglu_restore8(kept, x.numel() // H, H, I, x.dtype)
         g = ops.ffn_swiglu_bwd(x, Wg, Wu, Wd, dy.contiguous(), workspace=saved,
                                from_saved=saved is not None)
         ctx.saved = None
@@ -74,8 +73,7 @@ class _MoEFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, Wr, Wg, Wu, Wd, residual, k, aux_coef, z_coef, capacity_factor,
                 norm_topk_prob, keep):
-        ctx.saved = ctx.kept = None
-        saved = None
+        ctx.saved = saved = kept = None
         if keep and any(ctx.needs_input_grad[:5]):
             H, (E, I) = x.shape[-1], Wg.shape[:2]
             N = x.numel() // H
@@ -86,10 +84,10 @@ class _MoEFunction(torch.autograd.Function):
                               capacity_factor=capacity_factor, return_lists=False,
                               saved=saved)
         if saved is not None and keep == 2:
-            ctx.kept = block.moe_ffn_keep8(saved, N, H, I, E, k, x.dtype)
+            kept = block.moe_ffn_keep8(saved, N, H, I, E, k, x.dtype)
         else:
             ctx.saved = saved
-        ctx.save_for_backward(x, Wr, Wg, Wu, Wd)
+        ctx.save_for_backward(x, Wr, Wg, Wu, Wd, kept)
         ctx.cfg = (k, aux_coef, z_coef, capacity_factor, norm_topk_prob, residual is not None)
         z = out.z_loss if out.z_loss is not None else torch.zeros(1, dtype=torch.float32,
                                                                    device=x.device)
@@ -98,7 +96,7 @@ class _MoEFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy, daux, dz, _didx, _dalpha):
-        x, Wr, Wg, Wu, Wd = ctx.saved_tensors
+        x, Wr, Wg, Wu, Wd, kept = ctx.saved_tensors
         k, aux_coef, z_coef, capacity_factor, norm, has_res = ctx.cfg
         if dy is None:
             dy = torch.zeros_like(x)
@@ -108,9 +106,9 @@ class _MoEFunction(torch.autograd.Function):
         aux_grad = f32(daux) if daux is not None else 0.0
         z_grad = f32(dz) if dz is not None else 0.0
         saved = ctx.saved
-        if ctx.kept is not None:
+        if kept is not None:
             H, (E, I) = x.shape[-1], Wg.shape[:2]
-            saved = block.moe_ffn_restore8(ctx.kept, x.numel() // H, H, I, E, k, x.dtype)
+            saved = block.moe_ffn_restore8(kept, x.numel() // H, H, I, E, k, x.dtype)
         g = ops.moe_ffn_bwd(x, Wr, Wg, Wu, Wd, dy.contiguous(), k, aux_coef, aux_grad=aux_grad,
                             norm_topk_prob=norm, z_coef=z_coef, z_grad=z_grad,
                             capacity_factor=capacity_factor, workspace=saved,
