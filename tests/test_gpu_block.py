@@ -480,6 +480,33 @@ def test_swiglu_act8(env, Rn, C, halves, dt):
     assert torch.equal(bits(du), bits(b.du.contiguous()))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_swiglu_act8_far_products(env, dt):
+    """g * u past the range of 32 bits where SiLU(g) * u is within it; and of operands
+    that 8 bits hold exactly the forward's and the backward's h are the same bits."""
+    dev, tm = env
+    announce(f"swiglu_act8 products past the range, {dt}")
+    d, half = DT[dt], R.half_step(DT[dt])
+    g, u = torch.zeros(3, 32), torch.zeros(3, 32)
+    g[0], u[0] = -50.0, 1e37
+    g[0, 1], u[0, 1] = -40.0, -3e38
+    g[1], u[1] = 30.0, 1e37
+    g[2], u[2] = -80.0, 1e-3
+    g, u = g.to(d), u.to(d)
+    o = tm.swiglu_act8_fwd(g.to(dev), u.to(dev))
+    (h, tol), = R.silu_terms(g.double(), u.double())
+    assert bool(h.isfinite().all())
+    R.check("h", o.h, h, half * h.abs() + tol)
+    grid = torch.arange(-448, 449, 32, dtype=torch.float32)
+    grid = grid[:28].reshape(1, 28) / 64  # multiples of 1/2 up to 7: four bits
+    g, u = grid.repeat(2, 1)[:, :24].to(d).to(dev), grid.flip(1).repeat(2, 1)[:, :24].to(d).to(dev)
+    o = tm.swiglu_act8_fwd(g, u)
+    assert torch.equal(tm.act8_unpack(*o.g8, dtype=d), g)
+    b = tm.swiglu_act8_bwd(torch.ones_like(g), o.g8, o.u8)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(o.h), bits(b.h))
+
+
 def test_swiglu_act8_diverged(env):
     """A value that is not finite is NaN in its own gradients and nowhere else."""
     dev, tm = env

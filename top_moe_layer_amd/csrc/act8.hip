@@ -52,6 +52,8 @@ __device__ __forceinline__ void store_q(uint8_t* p, const uint32_t (&q)[1]) {
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
 }
+// SiLU(g) first: g * u may pass fp32's range where SiLU(g) * u does not.
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
 
 // The thread's row and piece: pieces of E channels, a row's pieces padded to
 // whole groups (pp = ceil(C / 32) groups of L lanes).
@@ -122,7 +124,7 @@ __global__ __launch_bounds__(256) void swiglu_act8_fwd_kernel(
   const int64_t o = a.at(C);
   if (a.in) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) vh[i] = silu_mul(vg[i], vu[i]);
+    for (int i = 0; i < E; ++i) vh[i] = silu(vg[i]) * vu[i];
     store_piece<NT>(h + o, vh);
     store_q(gq + o, bg);
     store_q(uq + o, bu);
