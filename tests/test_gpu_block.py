@@ -337,6 +337,58 @@ def test_postnorm_in_place_and_gradient_of_n_alone(env):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("which", [i for i, c in enumerate(POST) if c[2]])
+@pytest.mark.parametrize("N,H", [(3, 40), (99, 768), (3000, 104), (3, 8200)])
+def test_postnorm_gradient_of_n_alone(env, N, H, which, dt):
+    """No dout: against the formula, and the bits of a dout of zeros."""
+    dev, tm = env
+    announce(f"postnorm gradient of n alone N={N} H={H} case {which} {dt}")
+    gate_shape, norm, _, scale = POST[which]
+    d, half = DT[dt], R.half_step(DT[dt])
+    shape = gate_shape(N, H)
+    y, res, dn = rnd(1, N, H, dt=d, scale=0.7), rnd(2, N, H, dt=d, scale=2.0), rnd(3, N, H, dt=d)
+    w = rnd(4, H, dt=d) + 1 if norm else None
+    gate = rnd(5, *shape, dt=d) if shape else None
+    next_w = rnd(6, H, dt=d) + 1
+    to = lambda t: None if t is None else t.to(dev)
+    o = tm.block_postnorm_fwd(to(y), to(res), to(w), gate=to(gate), next_w=to(next_w),
+                              residual_scale=scale)
+    kw = dict(rstd=o.rstd, gate=to(gate), dn=to(dn), out=o.out, next_w=to(next_w),
+              next_rstd=o.next_rstd, residual_scale=scale)
+    b = tm.block_postnorm_bwd(None, to(y), to(w), **kw)
+    zero = tm.block_postnorm_bwd(torch.zeros(N, H, dtype=d, device=dev), to(y), to(w), **kw)
+    torch.cuda.synchronize()
+    cpu = lambda t: None if t is None else t.cpu()
+    args = (None, dn, y, o.out.cpu(), w, gate, next_w, cpu(o.rstd), cpu(o.next_rstd), scale)
+    ref, mag = R.postnorm_bwd(*args), R.postnorm_bwd(*args, mag=True)
+    for name in ("dy", "dresidual", "dw", "dgate", "dnext_w"):
+        got = getattr(b, name)
+        assert (got is None) == (ref[name] is None), name
+        if got is None:
+            continue
+        chain = 2 * depth(H) + 16 + (N if name in ("dw", "dgate", "dnext_w") else 0)
+        R.check(name, got, ref[name], half * ref[name].abs() + chain * R.U32 * mag[name])
+        assert torch.equal(bits(got), bits(getattr(zero, name))), name
+
+
+def test_postnorm_bwd_needs_a_gradient(env):
+    dev, tm = env
+    x, w = torch.zeros(4, 64, device=dev), torch.zeros(64, device=dev)
+    with pytest.raises(TypeError):
+        tm.block_postnorm_bwd(None, x)
+    with pytest.raises(TypeError):
+        tm.block_postnorm_bwd(None, x, w, rstd=torch.zeros(4, device=dev))
+    with pytest.raises(TypeError):
+        tm.block_postnorm_bwd(x, None)
+    with pytest.raises(ValueError):
+        tm.block_postnorm_bwd(x.cpu(), x)
+    side = torch.cuda.Stream()
+    b = tm.block_postnorm_bwd(stream=side, y=x, dout=x)
+    side.synchronize()
+    assert not b.dy.any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
 def test_token_gate_off_its_allocation(env, dt):
     """The gate of a batch's later tokens: values one by one, at any element's offset."""
     dev, tm = env

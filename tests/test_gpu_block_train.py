@@ -95,6 +95,26 @@ def test_functions_are_their_entry_points(env):
         tm.swiglu_act8(rnd(1, 4, 7).to(dev))
 
 
+def test_postnorm_gradient_of_n_alone_takes_no_zeros(env):
+    """A loss of n alone: no tensor of zeros is made for the gradient of out."""
+    dev, tm = env
+    N, H = 4096, 512
+    y, res, w = (t.to(dev).requires_grad_() for t in (rnd(1, N, H), rnd(2, N, H), 1 + rnd(3, H)))
+    dn = rnd(4, N, H).to(dev)
+    n = tm.block_postnorm(y, res, w, next_w=w)[1]
+    for t in (y, res, w):
+        t.grad = torch.zeros_like(t)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    n.backward(dn)
+    torch.cuda.synchronize()
+    # dy, dresidual and the partial sums (2 * 2048 units * H floats, once more as much as a
+    # tensor of the rows), but no third tensor of the rows beside the small ones
+    rows, sums = N * H * 4, tm.block_norm_bwd_workspace_bytes(N, H)
+    assert torch.cuda.max_memory_allocated() - before < 2.9 * rows + sums
+
+
 # ------------------------------------------------------------ a block of its own experts
 def block_forward(P, k, E, cf, ops, act8):
     """One pre- and post-normed MoE block whose experts are the caller's own

@@ -216,7 +216,7 @@ class _PostnormFunction(torch.autograd.Function):
         y, w, gate, next_w, out, rstd, next_rstd = ctx.saved_tensors
         if dout is None and dn is None:
             return (None,) * 7
-        dout = torch.zeros_like(y) if dout is None else dout.contiguous()
+        dout = None if dout is None else dout.contiguous()  # None: the gradient of n alone
         if dn is None:  # n was not used: its norm has no gradient
             next_w = out = next_rstd = None
         else:

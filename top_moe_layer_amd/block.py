@@ -23,16 +23,18 @@ _empty = torch.empty
 _CODES = {torch.float32: B.DTYPE_FP32, torch.bfloat16: B.DTYPE_BF16}
 
 
-def _on_kernel_stream(fn):
+def _on_kernel_stream(fn=None, *, of: int = 0):
     """Call ``fn`` with the stream its kernels run on as torch's current
     stream: ``stream`` (an object or a raw handle; ``fn`` itself never sees
-    it) or, by default, the current stream of the first argument's device,
-    where ``fn`` is called as it is."""
-    name = next(iter(inspect.signature(fn).parameters))
+    it) or, by default, the current stream of the device of its argument
+    ``of``, where ``fn`` is called as it is."""
+    if fn is None:
+        return functools.partial(_on_kernel_stream, of=of)
+    name = list(inspect.signature(fn).parameters)[of]
 
     @functools.wraps(fn)
     def wrapped(*args, stream=None, **kw):
-        t = args[0] if args else kw.get(name)
+        t = args[of] if len(args) > of else kw.get(name)
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{fn.__name__}: {name} must be a torch.Tensor")
         if not t.is_cuda:
@@ -369,21 +371,22 @@ def block_postnorm_fwd(y: torch.Tensor, residual: torch.Tensor, w: Optional[torc
     return PostnormOutput(out, rstd, n, next_rstd)
 
 
-@_on_kernel_stream
-def block_postnorm_bwd(dout: torch.Tensor, y: torch.Tensor,
+@_on_kernel_stream(of=1)
+def block_postnorm_bwd(dout: Optional[torch.Tensor], y: torch.Tensor,
                        w: Optional[torch.Tensor] = None, *, rstd: Optional[torch.Tensor] = None,
                        gate: Optional[torch.Tensor] = None, dn: Optional[torch.Tensor] = None,
                        out: Optional[torch.Tensor] = None, next_w: Optional[torch.Tensor] = None,
                        next_rstd: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
                        workspace: Optional[torch.Tensor] = None,
                        stream=None, stage_events: Optional[B.StageEvents] = None) -> PostnormGrads:
-    """Gradients of block_postnorm_fwd for dout (and, with ``next_w``, dn):
-    dy, dresidual (y's shape), dw, dnext_w [H] and dgate (the gate's shape).
-    ``rstd``, ``out`` and ``next_rstd`` as the forward returned them."""
+    """Gradients of block_postnorm_fwd for dout (and, with ``next_w``, dn; dout
+    None is then the gradient of n alone): dy, dresidual (y's shape), dw,
+    dnext_w [H] and dgate (the gate's shape).  ``rstd``, ``out`` and ``next_rstd`` as the forward returned them."""
     dev, dt = y.device, y.dtype
     code = _code(dt)
     N, H = _rows(y, "y")
-    _is(dout, "dout", y.shape, dt, dev)
+    if dout is not None or next_w is None:
+        _is(dout, "dout", y.shape, dt, dev)
     if w is not None:
         _is(w, "w", (H,), dt, dev)
         _is(rstd, "rstd", (N,), torch.float32, dev)
@@ -402,7 +405,7 @@ def block_postnorm_bwd(dout: torch.Tensor, y: torch.Tensor,
     dw = new(w) if w is not None else None
     dnext_w = new(next_w) if next_w is not None else None
     dgate = new(gate) if gate is not None else None
-    _call("block_postnorm_bwd", dev, stage_events, dout.data_ptr(), _ptr(dn), y.data_ptr(),
+    _call("block_postnorm_bwd", dev, stage_events, _ptr(dout), _ptr(dn), y.data_ptr(),
           _ptr(out), _ptr(w), _ptr(gate), _ptr(next_w), _ptr(rstd), _ptr(next_rstd), N, H, mode,
           gate_rows, float(residual_scale), code, dy.data_ptr(), dresidual.data_ptr(), _ptr(dw),
           _ptr(dgate), _ptr(dnext_w), wp, wn)
