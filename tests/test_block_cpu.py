@@ -190,3 +190,33 @@ def test_capacity_refusals():
     assert call(name, base, dtype=2) == B.ERR_UNSUPPORTED_DTYPE
     assert call(name, base, E=0) == B.ERR_BAD_SHAPE
     assert call(name, base, xs=None) == B.ERR_NULL_ARG
+
+
+def test_gate_shapes():
+    """Rows of a gate belong to runs of consecutive tokens; what broadcasting would read otherwise
+    is refused."""
+    from top_moe_layer_amd import block
+
+    H, dt, dev = 64, torch.float32, torch.device("cpu")
+
+    def gate(shape, *lead):
+        y = torch.zeros(*lead, H)
+        return block._gate(torch.zeros(shape), y.shape, y.numel() // H, H, dt, dev)
+
+    channel = lambda rows: (B.GATE_CHANNEL, rows)
+    token = (B.GATE_TOKEN, 1)
+    for shape, lead, want in [
+            ((H,), (2, 4), channel(1)), ((2, H), (2, 4), channel(2)), ((4, H), (2, 4), channel(4)),
+            ((1, H), (8,), channel(1)), ((2, 1, H), (2, 4), channel(2)), ((1, 1, H), (2, 4), channel(1)),
+            ((4, 1, H), (2, 4), channel(4)), ((2, 4, H), (2, 4), channel(8)), ((1, 4, H), (1, 4), channel(4)),
+            ((2, 1, H), (8,), channel(2)), ((2, 4, H), (8,), channel(8)), ((2, 3, 1, H), (2, 3, 4), channel(6)),
+            ((2, 1, 1, H), (2, 3, 4), channel(2)), ((2, 1, 4, H), (2, 1, 4), channel(8)),
+            ((1, H), (), channel(1)), ((1, 1, H), (), channel(1)), ((0, 1, H), (0, 4), channel(0)),
+            ((8, 1), (8,), token), ((2, 4, 1), (2, 4), token), ((8, 1), (2, 4), token),
+            ((1, 1), (1,), token), ((0, 1), (0,), token)]:
+        assert gate(shape, *lead) == want, (shape, lead)
+    for shape, lead in [((1, 4, H), (2, 4)), ((1, 4, H), (8,)), ((4, 2, H), (2, 4)),
+                        ((2, 1, 4, H), (2, 3, 4)), ((1, 3, 1, H), (2, 3, 4)), ((3, H), (2, 4)),
+                        ((4, 2, 1), (2, 4)), ((1, 4, 1), (2, 4)), ((4,), (4,))]:
+        with pytest.raises(ValueError):
+            gate(shape, *lead)

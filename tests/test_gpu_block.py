@@ -388,6 +388,28 @@ def test_postnorm_bwd_needs_a_gradient(env):
     assert not b.dy.any()
 
 
+def test_gate_row_per_position_is_refused(env):
+    """A gate that torch would broadcast over the batch, not taken for runs of tokens."""
+    dev, tm = env
+    B, S, H = 2, 4, 64
+    y, res, w = rnd(1, B, S, H).to(dev), rnd(2, B, S, H).to(dev), rnd(3, H).to(dev)
+    pos = rnd(4, 1, S, H).to(dev)
+    o = tm.block_postnorm_fwd(y, res, w)
+    for call in (lambda: tm.block_postnorm_fwd(y, res, w, gate=pos),
+                 lambda: tm.block_postnorm_bwd(y, y, w, rstd=o.rstd, gate=pos),
+                 lambda: tm.block_postnorm(y, res, w, gate=pos),
+                 lambda: tm.block_postnorm_fwd(y, res, w, gate=rnd(5, S, B, 1).to(dev))):
+        with pytest.raises(ValueError, match="gate"):
+            call()
+    got = tm.block_postnorm_fwd(y, res, gate=pos.expand(B, S, H).contiguous())
+    one = tm.block_postnorm_fwd(y[:1], res[:1], gate=pos)
+    torch.cuda.synchronize()
+    want = res.double() + pos.double() * y.double()
+    mag = (res.abs() + (pos * y).abs()).double().cpu()
+    R.check("out", got.out, want.cpu(), 4 * R.U32 * mag)
+    assert torch.equal(one.out, got.out[:1])
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 def test_token_gate_off_its_allocation(env, dt):
     """The gate of a batch's later tokens: values one by one, at any element's offset."""

@@ -316,7 +316,19 @@ def block_prenorm_bwd(dn: torch.Tensor, x: torch.Tensor, w: torch.Tensor, rstd: 
     return PrenormGrads(dx, dw)
 
 
-def _gate(gate: Optional[torch.Tensor], N: int, H: int, dt, dev):
+def _rows_in_order(lead, of) -> bool:
+    """Whether a gate's rows, leading dimensions ``lead``, belong to runs of
+    consecutive tokens of a tensor with leading dimensions ``of`` whichever way
+    one reads them: one dimension of rows (then only ones), the tensor's own
+    dimensions up to one of them, or, beside a tensor of another rank, rows
+    none of which stands behind a 1 that could be broadcast over."""
+    n = len(lead)
+    while n and lead[n - 1] == 1:
+        n -= 1
+    return n <= 1 or (lead[:n] == of[:n] if len(lead) == len(of) else 1 not in lead[:n])
+
+
+def _gate(gate: Optional[torch.Tensor], y_shape, N: int, H: int, dt, dev):
     """(gate_mode, gate_rows) of a gate [H], [G, H] / [B, 1, H] (N a multiple
     of the rows) or [..., 1] with one value per token."""
     if gate is None:
@@ -326,13 +338,17 @@ def _gate(gate: Optional[torch.Tensor], N: int, H: int, dt, dev):
     shape = tuple(gate.shape)
     _is(gate, "gate", shape, dt, dev)
     if len(shape) > 1 and shape[-1] == 1 and gate.numel() == N:
-        return B.GATE_TOKEN, 1
+        if len(shape) != len(y_shape) or _rows_in_order(shape[:-1], tuple(y_shape[:-1])):
+            return B.GATE_TOKEN, 1
     if shape and shape[-1] == H:
         rows = gate.numel() // H
-        if (rows and N % rows == 0) or (rows == 0 and N == 0):
+        if ((rows and N % rows == 0) or (rows == 0 and N == 0)) and (
+                len(shape) < 3 or rows == 0 or _rows_in_order(shape[:-1], tuple(y_shape[:-1]))):
             return B.GATE_CHANNEL, rows
     raise ValueError(f"gate has shape {shape}; expected ({H},), (G, {H}) with G dividing the {N} "
-                     f"tokens, or one value per token in a last dimension of 1")
+                     f"tokens, or one value per token in a last dimension of 1, with rows in the "
+                     f"order of the tokens {tuple(y_shape[:-1])} (a row per position is expanded "
+                     f"over the batch first)")
 
 
 @_on_kernel_stream
@@ -344,8 +360,10 @@ def block_postnorm_fwd(y: torch.Tensor, residual: torch.Tensor, w: Optional[torc
     """After a block with output y [..., H]: out = residual_scale * residual +
     gate * w * y / rms(y), without the norm where ``w`` is None, and with
     ``next_w`` the next block's norm n = next_w * out / rms(out) in the same
-    pass.  ``gate``: [H], [G, H] (each row for N / G consecutive tokens) or
-    one value per token [..., 1].  ``out`` may be the residual itself."""
+    pass.  ``gate``: [H]; [G, H], each row for N / G consecutive tokens, as
+    [B, 1, H] is for y [B, S, H]; or one value per token [..., 1].  Gates are
+    not broadcast: a [1, S, H], a row per position, is refused unless B is 1.
+    ``out`` may be the residual itself."""
     dev, dt = y.device, y.dtype
     code = _code(dt)
     N, H = _rows(y, "y")
@@ -354,7 +372,7 @@ def block_postnorm_fwd(y: torch.Tensor, residual: torch.Tensor, w: Optional[torc
         _is(w, "w", (H,), dt, dev)
     if next_w is not None:
         _is(next_w, "next_w", (H,), dt, dev)
-    mode, gate_rows = _gate(gate, N, H, dt, dev)
+    mode, gate_rows = _gate(gate, y.shape, N, H, dt, dev)
     if out is None:
         out = torch.empty_like(y)
     else:
@@ -397,7 +415,7 @@ def block_postnorm_bwd(dout: Optional[torch.Tensor], y: torch.Tensor,
         _is(next_rstd, "next_rstd", (N,), torch.float32, dev)
     elif dn is not None:
         raise ValueError("dn needs next_w")
-    mode, gate_rows = _gate(gate, N, H, dt, dev)
+    mode, gate_rows = _gate(gate, y.shape, N, H, dt, dev)
     nbytes = block_norm_bwd_workspace_bytes(N, H, gate_rows)
     wp, wn, ws = _scratch(nbytes, "block_postnorm_bwd", dev, workspace)
     new = torch.empty_like
