@@ -95,6 +95,16 @@ def test_functions_are_their_entry_points(env):
         tm.swiglu_act8(rnd(1, 4, 7).to(dev))
 
 
+def test_swiglu_act8_operands_of_one_shape(env):
+    """As many values in another shape are not an operand."""
+    dev, tm = env
+    g = rnd(1, 2, 3, 64).to(dev)
+    for u in (rnd(2, 3, 2, 64), rnd(2, 6, 64), rnd(2, 2, 6, 32)):
+        with pytest.raises(ValueError, match="shape"):
+            tm.swiglu_act8(g, u.to(dev))
+    assert tm.swiglu_act8(g, rnd(2, 2, 3, 64).to(dev)).shape == g.shape
+
+
 def test_postnorm_gradient_of_n_alone_takes_no_zeros(env):
     """A loss of n alone: no tensor of zeros is made for the gradient of out."""
     dev, tm = env

@@ -248,6 +248,8 @@ class _SwigluAct8Function(torch.autograd.Function):
             gu = g.reshape(-1, 2 * C)
             g2, u2 = gu[:, :C], gu[:, C:]
         else:
+            if u.shape != g.shape:
+                raise ValueError(f"u has shape {tuple(u.shape)}, expected g's {tuple(g.shape)}")
             g2, u2 = g.reshape(-1, C), u.reshape(-1, C)
         o = block.swiglu_act8_fwd(g2, u2)
         ctx.save_for_backward(*o.g8, *o.u8)
