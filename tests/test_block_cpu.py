@@ -220,3 +220,23 @@ def test_gate_shapes():
                         ((4, 2, 1), (2, 4)), ((1, 4, 1), (2, 4)), ((4,), (4,))]:
         with pytest.raises(ValueError):
             gate(shape, *lead)
+
+
+def test_too_few_stage_events():
+    """Every entry point's stage count, and the refusal of events for fewer."""
+    from top_moe_layer_amd import block, ops
+
+    class Events(B.StageEvents):
+        def __init__(self, stages):  # no events are made
+            self.stages, self.n, self.arr = stages, 2 * stages, None
+
+    assert set(block._STAGES) <= set(B.SIGNATURES)
+    for name in ("block_prenorm_bwd", "moe_dispatch_fwd_capacity", "ffn_swiglu_restore8", "act8_pack"):
+        stages = block._STAGES.get(name, 1)
+        with pytest.raises(ValueError, match="stages"):
+            block._call(name, torch.device("cuda", 0), Events(stages - 1))
+    for stages in (B.FFN_STAGES, B.MOE_STAGES, B.FFN_BWD_STAGES, B.MOE_BWD_STAGES):
+        with pytest.raises(ValueError, match="stages"):
+            ops._events(Events(stages - 1), stages)
+        assert ops._events(Events(stages), stages).value is None
+    assert ops._events(None, 2) is None

@@ -768,3 +768,18 @@ def test_stage_events(env):
     ev = tm.StageEvents(tm.NORM_BWD_STAGES)
     tm.block_prenorm_bwd(x, x, w, p.rstd, stage_events=ev)
     assert all(v > 0 for v in ev.elapsed_ms())
+
+
+def test_stage_events_of_another_call(env):
+    """Events for fewer stages than the call has are refused."""
+    dev, tm = env
+    x, w = rnd(1, 16, 64).to(dev), torch.ones(64, device=dev)
+    idx = route(1, 16, 4, 1, 0.0, False).to(dev)
+    p = tm.block_prenorm_fwd(x, w)
+    with pytest.raises(ValueError, match="stages"):
+        tm.block_prenorm_bwd(x, x, w, p.rstd, stage_events=tm.StageEvents(1))
+    with pytest.raises(ValueError, match="stages"):
+        tm.moe_dispatch_fwd(x, idx, 4, stage_events=tm.StageEvents(1))
+    one = tm.StageEvents(1)
+    tm.block_prenorm_fwd(x, w, stage_events=one)
+    assert one.elapsed_ms()[0] > 0

@@ -263,6 +263,13 @@ class StageEvents:
     def ptr(self):
         return ctypes.cast(self.arr, ctypes.c_void_p)
 
+    def for_stages(self, stages: int):
+        """The events for a call of so many stages, which uses two of each: fewer would be read
+        past their end."""
+        if self.stages < stages:
+            raise ValueError(f"stage_events has {self.stages} stages, the call {stages}")
+        return self.ptr
+
     def elapsed_ms(self):
         """Kernel milliseconds of each stage of the last recorded call (waits for it)."""
         out = []

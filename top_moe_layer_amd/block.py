@@ -88,13 +88,17 @@ def _scratch(nbytes: int, what: str, dev, ws: Optional[torch.Tensor]):
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
-def _events(e: Optional[B.StageEvents]):
-    return None if e is None else e.ptr
+# Entry points of more than one stage.
+_STAGES = {"moe_dispatch_fwd_capacity": B.DISPATCH_STAGES, "block_prenorm_bwd": B.NORM_BWD_STAGES,
+           "block_postnorm_bwd": B.NORM_BWD_STAGES, "ffn_swiglu_restore8": B.RESTORE8_STAGES,
+           "moe_ffn_restore8": B.RESTORE8_STAGES}
 
 
 def _call(name: str, dev, events, *args) -> None:
     """The C entry point, on torch's current stream of ``dev``."""
-    st = getattr(B.lib(), name)(*args, _raw_stream(dev.index), _events(events))
+    if events is not None:
+        events = events.for_stages(_STAGES.get(name, 1))
+    st = getattr(B.lib(), name)(*args, _raw_stream(dev.index), events)
     if st != B.OK:
         raise B.TopmoeError(st, name)
 

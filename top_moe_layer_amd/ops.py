@@ -88,6 +88,10 @@ def _buffer(t: torch.Tensor, name: str, nbytes: int, device) -> torch.Tensor:
     return t
 
 
+def _events(e: Optional[B.StageEvents], stages: int):
+    return None if e is None else e.for_stages(stages)
+
+
 def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
     if ws is None:
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -135,7 +139,7 @@ def ffn_swiglu_fwd(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torc
     if nbytes == 0:
         B.check(B.ERR_BAD_SHAPE, "ffn_swiglu_fwd")
     ws = _workspace(nbytes, dev, workspace)
-    evp = stage_events.ptr if stage_events is not None else None
+    evp = _events(stage_events, B.FFN_STAGES)
     if saved is not None:
         _buffer(saved, "saved", B.raw_ffn_bwd_workspace_bytes(N, H, I, code), dev)
         st = B.raw_ffn_swiglu_fwd_train(_ptr(xf), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(rf), _ptr(y),
@@ -226,7 +230,7 @@ def moe_ffn_fwd(x: torch.Tensor, Wr: torch.Tensor, Wg: torch.Tensor, Wu: torch.T
             float(aux_coef), float(z_coef), float(capacity_factor), flags, code, _ptr(y),
             _ptr(topk_idx), _ptr(alpha), _ptr(aux_loss), _ptr(z_loss), _ptr(expert_offsets),
             _ptr(sorted_token_ids), _ptr(ws), ws.numel() * ws.element_size())
-    evp = stage_events.ptr if stage_events is not None else None
+    evp = _events(stage_events, B.MOE_STAGES)
     if saved is not None:
         _buffer(saved, "saved", B.raw_moe_bwd_workspace_bytes(N, H, I, E, k, code), dev)
         st = B.raw_moe_ffn_fwd_train(*args, _ptr(saved), saved.numel() * saved.element_size(),
@@ -298,7 +302,7 @@ def ffn_swiglu_bwd(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torc
     st = fn(_ptr(xf), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(dyf), _ptr(dx),
             _ptr(dWg), _ptr(dWu), _ptr(dWd), N, H, I, code, _ptr(ws),
             ws.numel() * ws.element_size(), _stream(dev, stream),
-            stage_events.ptr if stage_events is not None else None)
+            _events(stage_events, B.FFN_BWD_STAGES))
     B.check(st, "ffn_swiglu_bwd")
     return FfnGrads(dx.view(x.shape), dWg, dWu, dWd)
 
@@ -357,6 +361,6 @@ def moe_ffn_bwd(x: torch.Tensor, Wr: torch.Tensor, Wg: torch.Tensor, Wu: torch.T
                            float(z_coef), float(capacity_factor), flags, code,
                            _ptr(dx), _ptr(dWr), _ptr(dWg), _ptr(dWu), _ptr(dWd), _ptr(ws),
                            ws.numel() * ws.element_size(), _stream(dev, stream),
-                           stage_events.ptr if stage_events is not None else None)
+                           _events(stage_events, B.MOE_BWD_STAGES))
     B.check(st, "moe_ffn_bwd")
     return MoeGrads(dx.view(x.shape), dWr, dWg, dWu, dWd)
