@@ -116,14 +116,6 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeJobs jobs) {
   }
 }
 
-// Padded group columns: group e's rows (offsets[e] .. offsets[e+1]) sit at
-// columns poff_e .. poff_e + c_e of a [C][ldo] matrix, poff_e = sum over
-// earlier groups of c rounded up to 64, and columns c_e .. round64(c_e) are
-// zero.  out[c][poff_e + i] = scale_g * in[row_g][c] with g = offsets[e] + i,
-// row_g = entries[g] / k (entries NULL: g), scale_g = alpha_g[g] (NULL: 1).
-// Up to two sources (blockIdx.z) share the grouping.  Grid: x = 64-column
-// blocks of the padded width bound, y = C / 64.
-//
 // The group that holds padded columns pc0 .. pc0 + 63 into s_grp[4]: group (-1:
 // none), its first row, its row count, its first padded column.  Wavefront 0.
 __device__ __forceinline__ void find_group(const int32_t* offsets, int E, int64_t rows,
@@ -146,6 +138,13 @@ __device__ __forceinline__ void find_group(const int32_t* offsets, int E, int64_
   }
 }
 
+// Padded group columns: group e's rows (offsets[e] .. offsets[e+1]) sit at
+// columns poff_e .. poff_e + c_e of a [C][ldo] matrix, poff_e = sum over
+// earlier groups of c rounded up to 64, and columns c_e .. round64(c_e) are
+// zero.  out[c][poff_e + i] = scale_g * in[row_g][c] with g = offsets[e] + i,
+// row_g = entries[g] / k (entries NULL: g), scale_g = alpha_g[g] (NULL: 1).
+// Up to two sources (blockIdx.z) share the grouping.  Grid: x = 64-column
+// blocks of the padded width bound, y = C / 64.
 template <typename T>
 __global__ __launch_bounds__(256) void gather_transpose_kernel(GatherTransposeJobs jobs) {
   using TT = TileT<T>;
