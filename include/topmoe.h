@@ -484,9 +484,12 @@ int block_postnorm_bwd(const void* dout, const void* dn, const void* y, const vo
  * ceil(C / 32)] (a row's last group may be shorter): value = q * 2^(byte -
  * 127).  The exponent is the smallest of at least -127 for which the group's
  * largest finite magnitude is at most 448 * 2^e (no element saturates; zeros
- * have byte 0), and q is rounded to nearest even.  An element that is not
- * finite is kept as NaN and takes no part in the scale.  (A value next to the
- * dtype's largest may round up past it, and then unpacks to infinity.)
+ * have byte 0), and q is rounded to nearest even: a finite x is kept within
+ * max(2^-4 |x|, 2^-10 * 2^e), the second where it lies below e4m3's normal
+ * numbers, 2^-6 * 2^e; one up to 2^-10 * 2^e, some 2^-18 of its group's largest,
+ * is kept as 0.  An element that is not finite is kept as NaN and takes no part
+ * in the scale.  (A value next to the dtype's largest may round up past it, and
+ * then unpacks to infinity.)
  * C is a positive multiple of 8 below 2^31, R < 2^31; row pitches (ld*, in
  * elements) are multiples of 8, at least C; q and scale are dense.  Tensor
  * pointers 16-byte aligned, q 8-byte.  Outputs must not alias inputs or each
@@ -516,8 +519,8 @@ int swiglu_act8_bwd(const uint8_t* gq, const uint8_t* gscale, const uint8_t* uq,
  * moe_ffn_bwd with TOPMOE_MOE_BWD_SAVED run as after the training forward.
  * Between the passes a layer then holds about 2 N k I bytes (2 + 1/16 an
  * element pair) instead of its backward workspace.  The backward then computes
- * from the 8-bit g and u (each within 2^-4 of its value, see act8_pack); y and
- * the routing are as without it.
+ * from the 8-bit g and u, each as near its value as act8_pack's; y and the
+ * routing are as without it.
  *   saved, workspace   *_bwd_workspace_bytes(), kept  *_keep8_bytes(): 256-byte
  *   aligned.  kept holds, each part 256-byte aligned: the MoE's routing, g's
  *   q [rows, I] (rows = N, or N * k in the experts' row order), u's q, g's

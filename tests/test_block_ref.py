@@ -78,3 +78,22 @@ def test_act8_scales():
     assert float(v[1, 0]) == 448.0 and float(v[1, 39]) == 448.0  # 449 / 2 = 224.5 -> 224
     assert torch.isnan(v[2, 4]) and float(v[2, 3]) == -448.0
     assert torch.isnan(v[4, 5]) and abs(float(v[4, 6]) / 3.0e38 - 1) <= 2.0 ** -4
+
+
+def test_act8_error_bound():
+    """A kept value is within max(2^-4 |x|, 2^-10 2^e) of x: relative where e4m3's numbers are
+    normal, absolute below, where 2^-4 |x| alone does not hold and small elements become 0."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(64, 96, generator=g, dtype=torch.float64).float().double()
+    x = x * torch.exp2(-torch.randint(0, 30, x.shape, generator=g).double())  # within one group
+    x[5] *= 2.0 ** -100
+    codes, scale, v = R.act8(x)
+    unit = torch.exp2(scale.double() - 127).repeat_interleave(32, 1)
+    err = (v - x).abs()
+    assert bool((err <= torch.maximum(2.0 ** -4 * x.abs(), 2.0 ** -10 * unit)).all())
+    assert bool((err > 2.0 ** -4 * x.abs()).any())
+    assert torch.equal(v == 0, x.abs() <= 2.0 ** -10 * unit)
+    group = x.abs().reshape(64, 3, 32).amax(-1).repeat_interleave(32, 1)
+    lost = v == 0
+    assert bool(lost.any()) and bool((x.abs()[lost] <= 2.0 ** -17 * group[lost]).all())
+    assert bool((v[x.abs() > 2.0 ** -17 * group] != 0).all())
