@@ -125,6 +125,52 @@ def test_postnorm_gradient_of_n_alone_takes_no_zeros(env):
     assert torch.cuda.max_memory_allocated() - before < 2.9 * rows + sums
 
 
+def functions(dev, tm, dt):
+    """Every Function with its leaves: name -> (leaves, call)."""
+    N, H, I, E, k = 40, 64, 64, 4, 2
+    d = DT[dt]
+    leaf = lambda seed, *s, t=d, scale=0.5: rnd(seed, *s, dt=t, scale=scale).to(dev).requires_grad_()
+    idx = torch.randint(-1, E, (N, k), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    idx = idx.to(dev)
+    er = tm.moe_dispatch_fwd(torch.zeros(N, H, dtype=d, device=dev), idx, E).entry_row
+    x, w, f32 = leaf(1, N, H), leaf(2, H), torch.float32
+    ffn = [leaf(3, I, H), leaf(4, I, H), leaf(5, H, I)]
+    moe = [leaf(6, E, H, t=f32), leaf(7, E, I, H), leaf(8, E, I, H), leaf(9, E, H, I)]
+    ys, alpha, w2, gate = leaf(10, N * k, H), leaf(11, N, k, t=f32), leaf(12, H), leaf(13, H)
+    out = {
+        "prenorm": ([x, w], lambda: tm.block_prenorm(x, w)),
+        "postnorm": ([x, w, gate], lambda: tm.block_postnorm(x, x, w, gate=gate)),
+        "postnorm n": ([x, w, w2], lambda: tm.block_postnorm(x, x, w, next_w=w2)[1]),
+        "dispatch": ([x], lambda: tm.moe_dispatch(x, idx, E).xs),
+        "combine": ([ys, alpha, x], lambda: tm.moe_combine(ys, er, alpha, x)),
+        "swiglu": ([ys], lambda: tm.swiglu_act8(ys)),
+    }
+    for keep in (False, True, "act8"):
+        out[f"ffn {keep}"] = ([x, *ffn], lambda keep=keep: tm.swiglu_ffn(x, *ffn, x, keep_activations=keep))
+        out[f"moe {keep}"] = ([x, *moe], lambda keep=keep: tm.moe_ffn(x, *moe, k, 0.0, keep_activations=keep)[0])
+    return out
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_upstream_gradients_at_any_offset(env, dt):
+    """The gradient of a piece of a concatenation begins at any element, that of a sum is expanded
+    from one value: both as a tensor of their own."""
+    dev, tm = env
+    one = torch.ones(1, dtype=DT[dt], device=dev)
+    for name, (leaves, call) in functions(dev, tm, dt).items():
+        announce(f"gradient at an odd offset: {name} {dt}")
+        y = call()
+        dy = rnd(20, *y.shape, dt=DT[dt]).to(dev)
+        want = torch.autograd.grad(y, leaves, dy)
+        y = call()
+        cat = torch.cat([one, y.flatten()])
+        got = torch.autograd.grad(cat, leaves, torch.cat([one, dy.flatten()]))
+        assert all(eq(a, b) for a, b in zip(got, want)), name
+        want = torch.autograd.grad(call(), leaves, torch.ones_like(dy))
+        got = torch.autograd.grad(call().sum(), leaves)
+        assert all(eq(a, b) for a, b in zip(got, want)), name
+
+
 # ------------------------------------------------------------ a block of its own experts
 def block_forward(P, k, E, cf, ops, act8):
     """One pre- and post-normed MoE block whose experts are the caller's own

@@ -26,6 +26,13 @@ def _keep_mode(keep_activations) -> int:
     return 2 if keep_activations == "act8" else int(bool(keep_activations))
 
 
+def _grad(t: torch.Tensor) -> torch.Tensor:
+    """An upstream gradient as the kernels take it: contiguous, and 16-byte
+    aligned, which a piece of a larger one (of a concatenation, say) need not be."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _SwiGLUFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, Wg, Wu, Wd, residual, keep):
@@ -51,7 +58,7 @@ class _SwiGLUFunction(torch.autograd.Function):
         if kept is not None:
             H, I = x.shape[-1], Wg.shape[0]
             saved = block.ffn_swiglu_restore8(kept, x.numel() // H, H, I, x.dtype)
-        g = ops.ffn_swiglu_bwd(x, Wg, Wu, Wd, dy.contiguous(), workspace=saved,
+        g = ops.ffn_swiglu_bwd(x, Wg, Wu, Wd, _grad(dy), workspace=saved,
                                from_saved=saved is not None)
         ctx.saved = None
         return g.dx, g.dWg, g.dWu, g.dWd, (dy if ctx.has_residual else None), None
@@ -111,7 +118,7 @@ class _MoEFunction(torch.autograd.Function):
         if kept is not None:
             H, (E, I) = x.shape[-1], Wg.shape[:2]
             saved = block.moe_ffn_restore8(kept, x.numel() // H, H, I, E, k, x.dtype)
-        g = ops.moe_ffn_bwd(x, Wr, Wg, Wu, Wd, dy.contiguous(), k, aux_coef, aux_grad=aux_grad,
+        g = ops.moe_ffn_bwd(x, Wr, Wg, Wu, Wd, _grad(dy), k, aux_coef, aux_grad=aux_grad,
                             norm_topk_prob=norm, z_coef=z_coef, z_grad=z_grad,
                             capacity_factor=capacity_factor, workspace=saved,
                             from_saved=saved is not None)
@@ -146,7 +153,7 @@ class _DispatchFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dxs, _off, _re, _er):
         entry_row, = ctx.saved_tensors
-        dx = block.moe_dispatch_bwd(dxs.contiguous(), entry_row)
+        dx = block.moe_dispatch_bwd(_grad(dxs), entry_row)
         return dx.view(ctx.shape), None, None, None
 
 
@@ -169,7 +176,7 @@ class _CombineFunction(torch.autograd.Function):
         ys, entry_row, alpha = ctx.saved_tensors
         dys = dalpha = None
         if ctx.needs_input_grad[0] or ctx.needs_input_grad[2]:
-            dys, dalpha = block.moe_combine_bwd(dy.contiguous(), ys, entry_row, alpha)
+            dys, dalpha = block.moe_combine_bwd(_grad(dy), ys, entry_row, alpha)
         return dys, None, dalpha, dy if ctx.needs_input_grad[3] else None
 
 
@@ -192,7 +199,7 @@ class _PrenormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dn):
         x, w, rstd = ctx.saved_tensors
-        g = block.block_prenorm_bwd(dn.contiguous(), x, w, rstd)
+        g = block.block_prenorm_bwd(_grad(dn), x, w, rstd)
         return g.dx, g.dw, None
 
 
@@ -218,11 +225,11 @@ class _PostnormFunction(torch.autograd.Function):
         y, w, gate, next_w, out, rstd, next_rstd = ctx.saved_tensors
         if dout is None and dn is None:
             return (None,) * 7
-        dout = None if dout is None else dout.contiguous()  # None: the gradient of n alone
+        dout = None if dout is None else _grad(dout)  # None: the gradient of n alone
         if dn is None:  # n was not used: its norm has no gradient
             next_w = out = next_rstd = None
         else:
-            dn = dn.contiguous()
+            dn = _grad(dn)
         g = block.block_postnorm_bwd(dout, y, w, rstd=rstd, gate=gate, dn=dn, out=out,
                                      next_w=next_w, next_rstd=next_rstd, residual_scale=ctx.scale)
         return g.dy, g.dresidual, g.dw, g.dgate, g.dnext_w, None, None
@@ -264,7 +271,7 @@ class _SwigluAct8Function(torch.autograd.Function):
         R, C = gq.shape
         dgu = torch.empty((R, 2 * C) if ctx.fused else (2, R, C), dtype=dh.dtype, device=dh.device)
         dg, du = (dgu[:, :C], dgu[:, C:]) if ctx.fused else (dgu[0], dgu[1])
-        block.swiglu_act8_bwd(dh.reshape(R, C).contiguous(), block.Act8(gq, gs),
+        block.swiglu_act8_bwd(_grad(dh.reshape(R, C)), block.Act8(gq, gs),
                               block.Act8(uq, us), with_h=False, dg=dg, du=du)
         if ctx.fused:
             return dgu.view(ctx.shape), None
