@@ -171,6 +171,51 @@ def test_upstream_gradients_at_any_offset(env, dt):
         assert all(eq(a, b) for a, b in zip(got, want)), name
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_functions_captured(env, dt):
+    """Forward and backward of every Function in one graph, replayed over new inputs."""
+    dev, tm = env
+    fs = functions(dev, tm, dt)
+    leaves = list({id(t): t for l, _ in fs.values() for t in l}.values())
+    ups = {n: rnd(30, *call().shape, dt=DT[dt]).to(dev) for n, (_, call) in fs.items()}
+
+    def step():
+        res = []
+        for name, (l, call) in fs.items():
+            y = call()
+            # (a residual's gradient is the upstream gradient itself, which is cleared below)
+            res += [t.clone() for t in (y.detach(), *torch.autograd.grad(y, l, ups[name]))]
+        return res
+
+    first = [t.detach().clone() for t in leaves]
+    second = [torch.randn_like(t) * 0.5 for t in first]
+    want = {}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.no_grad():
+        for name, src in (("2", second), ("1", first)):
+            for t, v in zip(leaves, src):
+                t.copy_(v)
+            with torch.enable_grad():
+                want[name] = [t.clone() for t in step()]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for r in range(4):
+        name, src = ("1", first) if r % 2 == 0 else ("2", second)
+        with torch.no_grad():
+            for t, v in zip(leaves, src):
+                t.copy_(v)
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(eq(a, b) for a, b in zip(outs, want[name])), r
+        assert all(eq(a, b) for a, b in zip(step(), want[name]))  # eager work between the replays
+
+
 # ------------------------------------------------------------ a block of its own experts
 def block_forward(P, k, E, cf, ops, act8):
     """One pre- and post-normed MoE block whose experts are the caller's own
