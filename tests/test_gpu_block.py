@@ -700,6 +700,54 @@ def test_deterministic_streams_and_graph(env, N, H, E, k, dt):
         torch.randn(1 << 16, device=dev).sum().item()
 
 
+def test_two_streams_at_once(env):
+    """Two passes of different inputs in flight at the same time."""
+    dev, tm = env
+    a, b = (block_inputs(dev, seed, 16500, 104, 16, 2, "bf16") for seed in (40, 60))
+    want = [block_pass(tm, t, 16, 1.0) for t in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in want]
+    for turn in range(3):
+        got = []
+        for t, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                got.append(block_pass(tm, t, 16, 1.0))
+        torch.cuda.synchronize()
+        assert all(same(x, y) for x, y in zip(got, want)), turn
+
+
+@pytest.mark.parametrize("N,H,G", [(20000, 64, 1), (100, 768, 4), (4096, 64, 4096)])
+def test_buffers_of_the_caller(env, N, H, G):
+    """Workspaces and outputs given, with other bytes in them, one workspace for calls in turn."""
+    dev, tm = env
+    announce(f"given buffers N={N} H={H} gate rows {G}")
+    E, k = 8, 2
+    x, dn, y = (rnd(i, N, H).to(dev) for i in range(3))
+    w, gate, idx = rnd(3, H).to(dev), rnd(4, G, H).to(dev), route(5, N, E, k, 0.1, False).to(dev)
+    nan = lambda *s: torch.full(s, math.nan, device=dev)
+    size = max(tm.moe_dispatch_workspace_bytes(N, E, k), tm.block_norm_bwd_workspace_bytes(N, H),
+               tm.block_norm_bwd_workspace_bytes(N, H, G))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device=dev)
+    d = tm.moe_dispatch_fwd(x, idx, E, xs=nan(N * k, H), workspace=ws)
+    p = tm.block_prenorm_fwd(x, w, n=nan(N, H))
+    b = tm.block_prenorm_bwd(dn, x, w, p.rstd, workspace=ws)
+    o = tm.block_postnorm_fwd(y, x, w, gate=gate, next_w=w, out=nan(N, H))
+    kw = dict(rstd=o.rstd, gate=gate, dn=dn, out=o.out, next_w=w, next_rstd=o.next_rstd)
+    q = tm.block_postnorm_bwd(dn, y, w, workspace=ws, **kw)
+    back = tm.moe_dispatch_bwd(d.xs, d.entry_row, dx=nan(N, H))
+    alpha = torch.rand(N, k, device=dev)
+    c = tm.moe_combine_fwd(d.xs, d.entry_row, alpha, y=nan(N, H))
+    torch.cuda.synchronize()
+    got = [*d, *p, *b, *o, *q, back, c]
+    d = tm.moe_dispatch_fwd(x, idx, E)
+    p = tm.block_prenorm_fwd(x, w)
+    o = tm.block_postnorm_fwd(y, x, w, gate=gate, next_w=w)
+    want = [*d, *p, *tm.block_prenorm_bwd(dn, x, w, p.rstd), *o, *tm.block_postnorm_bwd(dn, y, w, **kw),
+            tm.moe_dispatch_bwd(d.xs, d.entry_row), tm.moe_combine_fwd(d.xs, d.entry_row, alpha)]
+    torch.cuda.synchronize()
+    assert same(got, want)
+
+
 def test_gpu_refusals(env):
     """Calls that the front end or the library turns down before anything is launched."""
     dev, tm = env
