@@ -425,11 +425,13 @@ int moe_combine_bwd(const void* dy, const void* ys, const int32_t* entry_row, co
  *   yh = y / sqrt(mean(y^2) + eps) with a post norm, y without (w NULL)
  *   r  = residual_scale * residual + gate * w * yh,    out = r rounded once
  *   n  = next_w * r / sqrt(mean(r^2) + eps), of the unrounded r, rounded once
+ * The sum of the squares is fp32 too: a row whose sum passes its range (one
+ * element beyond about 1.8e19 does) has rstd 0, as one with an infinity has.
  * H is a multiple of 8 with 8 <= H <= 16384; N < 2^31; eps positive and finite;
  * weights and gates have x's dtype; tensor pointers are 16-byte aligned (a
- * token gate and its gradient: their element's size; float32 arrays: 4-byte).  Outputs must not
- * alias inputs or each other, except where said.  With N == 0 tensors of that
- * size may be NULL; weight gradients are then zero. */
+ * token gate and its gradient: their element's size; float32 arrays: 4-byte).
+ * Outputs must not alias inputs or each other, except where said.  With N == 0
+ * tensors of that size may be NULL; weight gradients are then zero. */
 #define TOPMOE_NORM_BWD_STAGES 2  /* 0 rows, 1 sums over the tokens (forwards: one stage) */
 /* gate_mode: none (1); a value per channel, in gate_rows rows [gate_rows, H]
  * of which row t / (N / gate_rows) belongs to token t (gate_rows divides N: 1

@@ -442,6 +442,26 @@ def test_norm_infinite_row_stays_in_its_row(env):
     assert float(n[3][torch.arange(72) != 5].abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_norm_squares_past_the_range(env, dt):
+    """A finite row whose squares' sum is infinite in 32 bits: rstd 0, zeros, no gradient of its
+    own, and the others' bits as without it."""
+    dev, tm = env
+    d = DT[dt]
+    x, w, dn, dres = rnd(1, 9, 72, dt=d), rnd(2, 72, dt=d), rnd(3, 9, 72, dt=d), rnd(4, 9, 72, dt=d)
+    on = [t.to(dev) for t in (x, w, dn, dres)]
+    clean = tm.block_prenorm_fwd(on[0], on[1])
+    x[3, 5] = 1e20
+    on[0] = x.to(dev)
+    o = tm.block_prenorm_fwd(on[0], on[1])
+    b = tm.block_prenorm_bwd(on[2], on[0], on[1], o.rstd, dresidual=on[3])
+    torch.cuda.synchronize()
+    others = torch.arange(9) != 3
+    assert float(o.rstd[3]) == 0.0 and not o.n[3].any()
+    assert torch.equal(o.n.cpu()[others], clean.n.cpu()[others])
+    assert torch.equal(b.dx[3], on[3][3]) and bool(b.dw.isfinite().all())
+
+
 # ------------------------------------------------------------ 8 bits
 ACT = [(1, 8), (3, 24), (5, 32), (7, 40), (33, 200), (64, 256), (13, 1000), (100, 2432), (2, 16384)]
 
