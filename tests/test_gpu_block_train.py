@@ -451,6 +451,31 @@ def test_moe_keep8(env, N, H, I, E, k, cf, dt):
         assert eq(t.grad, ref)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_keep8_products_next_to_the_range(env, dt):
+    """g * u within the range of 32 bits before they are kept and past it as kept (-59 and 1.07 *
+    2^122 as -60 and 1.125 * 2^122), SiLU(g) * u far within: the down weights' gradient is finite,
+    the formula's to half a step of the type, one of it and one of the products (see silu_terms)."""
+    dev, tm = env
+    N, H, I = 3, 64, 64
+    d = DT[dt]
+    x = torch.zeros(N, H, dtype=d)
+    x[:, 0] = 1.0
+    Wg, Wu = torch.zeros(I, H, dtype=d), torch.zeros(I, H, dtype=d)
+    Wg[:, 0], Wu[:, 0] = -59.0, 1.07 * 2.0 ** 122
+    Wd = torch.ones(H, I, dtype=d)
+    L = [t.to(dev).requires_grad_() for t in (x, Wg, Wu, Wd)]
+    y = tm.swiglu_ffn(*L, keep_activations="act8")
+    assert bool(y.isfinite().all())
+    y.backward(torch.ones_like(y))
+    torch.cuda.synchronize()
+    (h, tol), = R.silu_terms(torch.tensor([-60.0], dtype=torch.float64),
+                             torch.tensor([1.125 * 2.0 ** 122], dtype=torch.float64))
+    want = torch.full((H, I), float(N * h), dtype=torch.float64)
+    # h^T is rounded to the type, then three of them are added and rounded once more
+    R.check("dWd", L[3].grad, want, N * tol + (2 * R.half_step(d) + 4 * R.U32) * want.abs())
+
+
 def test_keep8_no_tokens(env):
     dev, tm = env
     H, I, E = 64, 64, 4

@@ -49,12 +49,6 @@ __device__ __forceinline__ void store_q(uint8_t* p, const uint32_t (&q)[1]) {
   store_vec<kNtKeep, uint32_t>(p, q[0]);
 }
 
-__device__ __forceinline__ float sigmoid(float g) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
-}
-// SiLU(g) first: g * u may pass fp32's range where SiLU(g) * u does not.
-__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
-
 // The thread's row and piece: pieces of E channels, a row's pieces padded to
 // whole groups (pp = ceil(C / 32) groups of L lanes).
 template <typename T>

@@ -1,5 +1,5 @@
 // Values in 8 bits: a thread's channels to and from e4m3 with their group's
-// scale byte (the format is described in act8.hip).
+// scale byte (the format is described in act8.hip), and SiLU of them.
 #pragma once
 
 #include "device_common.h"
@@ -71,5 +71,11 @@ __device__ __forceinline__ void unpack_q(const uint32_t (&q)[E / 4], float s, fl
     v[4 * w + 3] = __builtin_amdgcn_cvt_f32_fp8(int(q[w]), 3) * s;
   }
 }
+
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
+}
+// SiLU(g) first: g * u may pass fp32's range where SiLU(g) * u does not.
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
 
 }  // namespace topmoe

@@ -240,7 +240,7 @@ __global__ __launch_bounds__(256) void restore8_kernel(Restore8Job jb) {
         store_pairs4<T>(jb.pairs, o + 4 * w, gw, uw);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = silu_mul(g[e], u[e]);
+      for (int e = 0; e < 8; ++e) h[e] = silu(g[e]) * u[e];
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = 0.f;
