@@ -601,6 +601,26 @@ def test_swiglu_act8_far_products(env, dt):
     assert torch.equal(bits(o.h), bits(b.h))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_swiglu_act8_bwd_far_products(env, dt):
+    """dh * u past the range of 32 bits where dh * u * SiLU'(g) is within it."""
+    dev, tm = env
+    announce(f"swiglu_act8 gradients past the range, {dt}")
+    d, half = DT[dt], R.half_step(DT[dt])
+    g, u, dh = (torch.zeros(3, 32) for _ in range(3))
+    g[0], u[0], dh[0] = -50.0, 1e37, 100.0
+    g[1], u[1], dh[1] = -30.0, -3e38, 2.0
+    g[2], u[2], dh[2] = 20.0, 1e37, 0.5
+    g, u, dh = g.to(d), u.to(d), dh.to(d)
+    o = tm.swiglu_act8_fwd(g.to(dev), u.to(dev))
+    b = tm.swiglu_act8_bwd(dh.to(dev), o.g8, o.u8)
+    torch.cuda.synchronize()
+    terms = R.silu_terms(R.act8(g)[2], R.act8(u)[2], dh.double())
+    for name, (ref, tol) in zip(("h", "dg", "du"), terms):
+        assert bool((ref.abs() < 3e38).all())
+        R.check(name, getattr(b, name), ref, half * ref.abs() + tol)
+
+
 def test_swiglu_act8_diverged(env):
     """A value that is not finite is NaN in its own gradients and nowhere else."""
     dev, tm = env

@@ -153,7 +153,7 @@ __global__ __launch_bounds__(256) void swiglu_act8_bwd_kernel(
     const float s = sigmoid(vg[i]), gsig = vg[i] * s;
     ou[i] = vd[i] * gsig;
     oh[i] = gsig * vu[i];
-    og[i] = vd[i] * vu[i] * (s * (1.0f + vg[i] * (1.0f - s)));
+    og[i] = vd[i] * (vu[i] * s * (1.0f + vg[i] * (1.0f - s)));  // dh * u may pass the range
   }
   store_piece<NT>(dg + a.at(ldg), og);
   store_piece<NT>(du + a.at(ldu), ou);
