@@ -545,6 +545,81 @@ int moe_ffn_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t H, 
                      int k, int dtype, void* workspace, size_t workspace_bytes, void* stream,
                      void* const* stage_events);
 
+/* ---- products of rows by expert ------------------------------------------
+ * A linear layer of the caller's own experts between the dispatch and the
+ * combine above (the nn.Linear of lesson 13, section 0, one per expert): rows
+ * grouped by expert times each expert's matrix, and its gradients.
+ *   y[r]  = w_e x[r]   for the rows r in [expert_offsets[e], expert_offsets[e+1])
+ *   dx[r] = w_e^T dy[r];   dw_e = the sum over e's rows of dy[r] x[r]^T
+ * Sums are fp32, each result rounded once to the dtype.  Rows behind
+ * expert_offsets[E] belong to no expert: theirs of y and dx are zeros, and they
+ * add nothing to dw; they are not read.  An expert without rows has dw = 0.
+ * Every element of y, dx and dw is written, from the same sums in the same
+ * order at every call.
+ *   x [R, K], dy, y [R, O], dx [R, K]: row pitches in elements, multiples of 8
+ *   up to 2^21, rows that do not overlap; w, dw [E, O, K] dense, in the dtype;
+ *   expert_offsets [E + 1], from 0 on and not decreasing, on the device (other
+ *   values give other rows, but no access outside the tensors); NULL with
+ *   E == 1: one matrix for all rows.
+ * K and O are positive multiples of 8 up to 2^20, R < 2^31, E <= 256; tensor
+ * pointers 16-byte aligned.  Outputs must not alias inputs or each other.  With
+ * R == 0 tensors of that size may be NULL. */
+#define TOPMOE_LINEAR_MAX_EXPERTS 256
+#define TOPMOE_LINEAR_BWD_STAGES 2  /* 0 dx, 1 dw (forward: one stage) */
+int moe_linear_fwd(const void* x, int64_t ldx, const void* w, const int32_t* expert_offsets,
+                   int64_t R, int64_t K, int64_t O, int E, int dtype, void* y, int64_t ldy,
+                   void* stream, void* const* stage_events);
+/* dx NULL: not wanted (w may be NULL as well); dw NULL: not wanted (x may be). */
+int moe_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                   const int32_t* expert_offsets, int64_t R, int64_t K, int64_t O, int E,
+                   int dtype, void* dx, int64_t lddx, void* dw, void* stream,
+                   void* const* stage_events);
+
+/* ---- matrices and rows in 4 bits ------------------------------------------
+ * Groups of 32 consecutive channels of a row (the last may be shorter) with one
+ * scale: q holds e2m1 values (OCP microscaling fp4: 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and negatives) of x / 2^e, rounded to nearest, ties to the even code, two a
+ * byte, the first in the low half; scale the byte e + 127, e being the smallest
+ * integer (at least -127) for which the group's largest magnitude is at most
+ * 6 * 2^e (448 * 2^e in the 8-bit format above).  A value is thus kept within
+ * max(x / 6, 2^e / 4) of itself.  A group with an element that is not finite has the
+ * scale byte 255 and reads back as NaN.  Read back, 4 * 2^126 and more are
+ * infinite.
+ *   x [R, C] with a row pitch in elements (a multiple of 8); q [R, C / 2] and
+ *   scale [R, ceil(C / 32)] bytes, dense (an [E, O, K] matrix: R = E * O rows).
+ * C is a positive multiple of 8, R and C < 2^31; x 16-byte, q 4-byte aligned. */
+#define TOPMOE_MX4_GROUP 32
+int mx4_pack(const void* x, int64_t ldx, int64_t R, int64_t C, int dtype, uint8_t* q,
+             uint8_t* scale, void* stream, void* const* stage_events);
+int mx4_unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C, int dtype, void* x,
+               int64_t ldx, void* stream, void* const* stage_events);
+/* moe_linear_fwd with each expert's matrix in 4 bits (wq [E, O, K / 2], w_scale
+ * [E, O, K / 32]) and the rows as
+ *   TOPMOE_ROWS_PLAIN  x [R, K] in the dtype of y
+ *   TOPMOE_ROWS_ACT8   act8_pack's q [R, K] (ldx ignored) and x_scale [R, K / 32]
+ *   TOPMOE_ROWS_MX4    mx4_pack's  q [R, K / 2] and x_scale
+ * The product is that of the values the bytes stand for; y has the dtype.  Sums
+ * are fp32; with 8-bit rows and y in bf16 the matrix instructions add eight
+ * products at a time with 14 bits below the largest of them.  A scale byte of 255
+ * is NaN.  K is a multiple of 32, so that every group is whole; x and wq 16-byte
+ * aligned; the rest as for moe_linear_fwd. */
+#define TOPMOE_ROWS_PLAIN 0
+#define TOPMOE_ROWS_ACT8 1
+#define TOPMOE_ROWS_MX4 2
+int mx4_linear_fwd(const void* x, int64_t ldx, const uint8_t* x_scale, int rows,
+                   const uint8_t* wq, const uint8_t* w_scale, const int32_t* expert_offsets,
+                   int64_t R, int64_t K, int64_t O, int E, int dtype, void* y, int64_t ldy,
+                   void* stream, void* const* stage_events);
+/* dx of it for frozen matrices (adapters trained around them): dx[r] = w_e^T
+ * dy[r].  The matrices are turned into bf16 (exact) in the workspace first.
+ * mx4_linear_bwd_workspace_bytes returns 0 for invalid sizes. */
+#define TOPMOE_MX4_BWD_STAGES 2  /* 0 matrices to bf16, 1 dx */
+size_t mx4_linear_bwd_workspace_bytes(int64_t K, int64_t O, int E);
+int mx4_linear_bwd(const void* dy, int64_t lddy, const uint8_t* wq, const uint8_t* w_scale,
+                   const int32_t* expert_offsets, int64_t R, int64_t K, int64_t O, int E,
+                   int dtype, void* dx, int64_t lddx, void* workspace, size_t workspace_bytes,
+                   void* stream, void* const* stage_events);
+
 /* Human-readable text for a status code (static storage). */
 const char* topmoe_strerror(int status);
 

@@ -21,6 +21,10 @@ from ._binding import (  # noqa: F401
     NORM_BWD_STAGES,
     NORM_BWD_STAGE_NAMES,
     RESTORE8_STAGES,
+    LINEAR_BWD_STAGES,
+    LINEAR_BWD_STAGE_NAMES,
+    MX4_BWD_STAGES,
+    MX4_BWD_STAGE_NAMES,
     LIB_PATH,
     StageEvents,
     TopmoeError,
@@ -51,8 +55,14 @@ def __getattr__(name):
         from . import block
         globals()[name] = v = getattr(block, name)  # found without this function from now on
         return v
+    if name in ("moe_linear_fwd", "moe_linear_bwd", "MoeLinearGrads", "Mx4", "mx4_pack",
+                "mx4_unpack", "mx4_linear_fwd", "mx4_linear_bwd",
+                "mx4_linear_bwd_workspace_bytes"):
+        from . import linear
+        globals()[name] = v = getattr(linear, name)
+        return v
     if name in ("swiglu_ffn", "moe_ffn", "moe_dispatch", "moe_combine", "block_prenorm",
-                "block_postnorm", "swiglu_act8"):
+                "block_postnorm", "swiglu_act8", "moe_linear", "mx4_linear"):
         from . import autograd
         return getattr(autograd, name)
     raise AttributeError(name)

@@ -40,6 +40,11 @@ DISPATCH_ONE = 32768
 DISPATCH_ONE_BYTES = 128 << 20
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 ACT8_GROUP = 32
+LINEAR_MAX_EXPERTS = 256
+LINEAR_BWD_STAGES = 2
+MX4_BWD_STAGES = 2
+MX4_GROUP = 32
+ROWS_PLAIN, ROWS_ACT8, ROWS_MX4 = 0, 1, 2
 
 FFN_STAGE_NAMES = ["gateup_gemm", "down_gemm"]
 MOE_STAGE_NAMES = ["router", "permute", "gateup_gemm", "down_gemm", "combine"]
@@ -49,6 +54,8 @@ MOE_BWD_STAGE_NAMES = ["router", "permute", "transpose_w", "transpose_act", "gu_
                        "dx_gemm", "router_bwd", "dx_combine", "dwr", "dwgu_gemm", "dwd_gemm"]
 DISPATCH_STAGE_NAMES = ["rows", "copy"]
 NORM_BWD_STAGE_NAMES = ["rows", "sums"]
+LINEAR_BWD_STAGE_NAMES = ["dx", "dw"]
+MX4_BWD_STAGE_NAMES = ["unpack", "dx"]
 
 # Every function include/topmoe.h declares, with its ctypes signature.
 _vp, _i64, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -105,6 +112,17 @@ SIGNATURES = {
     "moe_keep8_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32, _i32]),
     "moe_ffn_keep8": (_i32, [_vp, _sz, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _sz, _vp, _vp]),
     "moe_ffn_restore8": (_i32, [_vp, _sz, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _sz, _vp, _vp]),
+    "moe_linear_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp,
+                              _vp]),
+    "moe_linear_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp,
+                              _i64, _vp, _vp, _vp]),
+    "mx4_pack": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "mx4_unpack": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp]),
+    "mx4_linear_fwd": (_i32, [_vp, _i64, _vp, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32,
+                              _vp, _i64, _vp, _vp]),
+    "mx4_linear_bwd_workspace_bytes": (_sz, [_i64, _i64, _i32]),
+    "mx4_linear_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64,
+                              _vp, _sz, _vp, _vp]),
     "topmoe_strerror": (ctypes.c_char_p, [_i32]),
     "topmoe_version": (_i32, []),
     "topmoe_set_tile_override": (_i32, [_i32, _vp]),

@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import block, ops
+from . import block, linear, ops
 
 
 def _keep_mode(keep_activations) -> int:
@@ -185,6 +185,50 @@ def moe_combine(ys: torch.Tensor, entry_row: torch.Tensor, alpha: torch.Tensor,
     """Differentiable moe_combine_fwd: gradients to ``ys``, ``alpha`` and
     ``residual``."""
     return _CombineFunction.apply(ys, entry_row, alpha, residual)
+
+
+# ------------------------------------------------------------ products by expert
+class _LinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, expert_offsets):
+        y = linear.moe_linear_fwd(x, w, expert_offsets)
+        ctx.save_for_backward(x if ctx.needs_input_grad[1] else None, w, expert_offsets)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, expert_offsets = ctx.saved_tensors
+        dx, dw = linear.moe_linear_bwd(_grad(dy), x, w, expert_offsets,
+                                       need_dx=ctx.needs_input_grad[0],
+                                       need_dw=ctx.needs_input_grad[1])
+        return dx, dw, None
+
+
+def moe_linear(x: torch.Tensor, w: torch.Tensor,
+               expert_offsets: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable moe_linear_fwd: gradients to ``x`` and ``w``."""
+    return _LinearFunction.apply(x, w, expert_offsets)
+
+
+class _Mx4LinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, q, scale, expert_offsets):
+        ctx.save_for_backward(q, scale, expert_offsets)
+        return linear.mx4_linear_fwd(x, linear.Mx4(q, scale), expert_offsets)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        q, scale, expert_offsets = ctx.saved_tensors
+        return linear.mx4_linear_bwd(_grad(dy), linear.Mx4(q, scale), expert_offsets), None, None, None
+
+
+def mx4_linear(x: torch.Tensor, w: linear.Mx4,
+               expert_offsets: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable mx4_linear_fwd of a plain x over frozen 4-bit matrices (as
+    adapters are trained around them): gradients to ``x``."""
+    return _Mx4LinearFunction.apply(x, w.q, w.scale, expert_offsets)
 
 
 # ------------------------------------------------------------ norms

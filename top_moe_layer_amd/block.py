@@ -91,7 +91,8 @@ def _scratch(nbytes: int, what: str, dev, ws: Optional[torch.Tensor]):
 # Entry points of more than one stage.
 _STAGES = {"moe_dispatch_fwd_capacity": B.DISPATCH_STAGES, "block_prenorm_bwd": B.NORM_BWD_STAGES,
            "block_postnorm_bwd": B.NORM_BWD_STAGES, "ffn_swiglu_restore8": B.RESTORE8_STAGES,
-           "moe_ffn_restore8": B.RESTORE8_STAGES}
+           "moe_ffn_restore8": B.RESTORE8_STAGES, "moe_linear_bwd": B.LINEAR_BWD_STAGES,
+           "mx4_linear_bwd": B.MX4_BWD_STAGES}
 
 
 def _call(name: str, dev, events, *args) -> None:

@@ -21,8 +21,6 @@
 // read and kept bytes written non-temporally, the bytes being read again only
 // in the backward pass: 147 us with neither, 144 with h alone written so.
 #include "act8_impl.h"
-#include "kernels.h"
-#include "vec16.h"
 
 #include "../../include/topmoe.h"
 
@@ -48,29 +46,6 @@ __device__ __forceinline__ void store_q(uint8_t* p, const uint32_t (&q)[2]) {
 __device__ __forceinline__ void store_q(uint8_t* p, const uint32_t (&q)[1]) {
   store_vec<kNtKeep, uint32_t>(p, q[0]);
 }
-
-// The thread's row and piece: pieces of E channels, a row's pieces padded to
-// whole groups (pp = ceil(C / 32) groups of L lanes).
-template <typename T>
-struct Place {
-  static constexpr int E = kE<T>, L = kGroupLanes<kE<T>>;
-  int64_t r;
-  int p;
-  bool any, in;  // any: within the launch's rows; in: and within the row
-  uint32_t groups;
-  __device__ __forceinline__ Place(int64_t r0, uint32_t pieces, uint32_t pp, int C) {
-    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-    const uint32_t dr = i / pp;
-    r = r0 + dr;
-    p = int(i - dr * pp);
-    any = i < pieces;
-    in = any && p < C / E;
-    groups = pp / L;
-  }
-  __device__ __forceinline__ int64_t at(int64_t pitch) const { return r * pitch + int64_t(p) * E; }
-  __device__ __forceinline__ int64_t group() const { return r * groups + p / L; }
-  __device__ __forceinline__ bool first() const { return any && p % L == 0; }
-};
 
 template <typename T>
 __global__ __launch_bounds__(256) void act8_pack_kernel(const T* __restrict__ x, int64_t ldx,
@@ -211,26 +186,6 @@ __global__ __launch_bounds__(256) void copy_kernel(const u32x4* __restrict__ src
                                                    u32x4* __restrict__ dst, int64_t n) {
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256)
     dst[i] = src[i];
-}
-
-// Launches over slabs of rows of at most 2^30 pieces, so that piece numbers
-// stay in 32 bits and a grid within its limit of threads.
-template <typename T, typename F>
-hipError_t for_slabs(int64_t R, int64_t C, const Launch& s, F launch) {
-  const uint32_t pp = uint32_t((C + kAct8Group - 1) / kAct8Group * Place<T>::L);
-  int64_t slab = (int64_t(1) << 30) / pp;
-  if (slab < 1) slab = 1;
-  for (int64_t r0 = 0; r0 < R; r0 += slab) {
-    Launch L = s;
-    if (r0 > 0) L.start = nullptr;
-    if (r0 + slab < R) L.stop = nullptr;
-    const int64_t rows = r0 + slab < R ? slab : R - r0;
-    const uint32_t pieces = uint32_t(rows * pp);
-    const hipError_t e = launch(dim3((pieces + 255) / 256), r0, pieces, pp, L);
-    if (e != hipSuccess) return e;
-    s.launched = true;
-  }
-  return hipSuccess;
 }
 
 }  // namespace

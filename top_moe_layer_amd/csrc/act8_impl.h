@@ -1,8 +1,11 @@
 // Values in 8 bits: a thread's channels to and from e4m3 with their group's
-// scale byte (the format is described in act8.hip), and SiLU of them.
+// scale byte (the format is described in act8.hip), and SiLU of them.  Places
+// of threads in rows of groups, and launches over many rows, also for 4 bits.
 #pragma once
 
 #include "device_common.h"
+#include "kernels.h"
+#include "vec16.h"
 
 namespace topmoe {
 
@@ -77,5 +80,48 @@ __device__ __forceinline__ float sigmoid(float g) {
 }
 // SiLU(g) first: g * u may pass fp32's range where SiLU(g) * u does not.
 __device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
+
+// The thread's row and piece: pieces of E channels, a row's pieces padded to
+// whole groups (pp = ceil(C / 32) groups of L lanes).
+template <typename T>
+struct Place {
+  static constexpr int E = kE<T>, L = kGroupLanes<kE<T>>;
+  int64_t r;
+  int p;
+  bool any, in;  // any: within the launch's rows; in: and within the row
+  uint32_t groups;
+  __device__ __forceinline__ Place(int64_t r0, uint32_t pieces, uint32_t pp, int C) {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t dr = i / pp;
+    r = r0 + dr;
+    p = int(i - dr * pp);
+    any = i < pieces;
+    in = any && p < C / E;
+    groups = pp / L;
+  }
+  __device__ __forceinline__ int64_t at(int64_t pitch) const { return r * pitch + int64_t(p) * E; }
+  __device__ __forceinline__ int64_t group() const { return r * groups + p / L; }
+  __device__ __forceinline__ bool first() const { return any && p % L == 0; }
+};
+
+// Launches over slabs of rows of at most 2^30 pieces, so that piece numbers
+// stay in 32 bits and a grid within its limit of threads.
+template <typename T, typename F>
+hipError_t for_slabs(int64_t R, int64_t C, const Launch& s, F launch) {
+  const uint32_t pp = uint32_t((C + kAct8Group - 1) / kAct8Group * Place<T>::L);
+  int64_t slab = (int64_t(1) << 30) / pp;
+  if (slab < 1) slab = 1;
+  for (int64_t r0 = 0; r0 < R; r0 += slab) {
+    Launch L = s;
+    if (r0 > 0) L.start = nullptr;
+    if (r0 + slab < R) L.stop = nullptr;
+    const int64_t rows = r0 + slab < R ? slab : R - r0;
+    const uint32_t pieces = uint32_t(rows * pp);
+    const hipError_t e = launch(dim3((pieces + 255) / 256), r0, pieces, pp, L);
+    if (e != hipSuccess) return e;
+    s.launched = true;
+  }
+  return hipSuccess;
+}
 
 }  // namespace topmoe
