@@ -17,6 +17,8 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSide = int64_t(1) << 20, kMaxPitch = int64_t(1) << 21;
+// Rows of all experts' matrices: what a launch's threads number in 32 bits.
+constexpr int64_t kMaxOut = int64_t(1) << 25;
 
 bool known_dtype(int dtype) {
   return dtype == TOPMOE_DTYPE_FP32 || dtype == TOPMOE_DTYPE_BF16;
@@ -28,6 +30,7 @@ int linear_shape(int64_t R, int64_t K, int64_t O, int E, const int32_t* offsets,
   if (R < 0 || R > kMaxRows || K <= 0 || K % step != 0 || K > kMaxSide) return TOPMOE_ERR_BAD_SHAPE;
   if (O <= 0 || O % 8 != 0 || O > kMaxSide) return TOPMOE_ERR_BAD_SHAPE;
   if (E < 1 || E > kMmMaxExperts || (!offsets && E != 1)) return TOPMOE_ERR_BAD_SHAPE;
+  if (int64_t(E) * O > kMaxOut) return TOPMOE_ERR_BAD_SHAPE;
   return TOPMOE_OK;
 }
 
@@ -161,7 +164,7 @@ int mx4_linear_fwd(const void* x, int64_t ldx, const uint8_t* x_scale, int rows,
 
 size_t mx4_linear_bwd_workspace_bytes(int64_t K, int64_t O, int E) {
   if (K <= 0 || K % kMx4Group != 0 || K > kMaxSide || O <= 0 || O % 8 != 0 || O > kMaxSide ||
-      E < 1 || E > kMmMaxExperts)
+      E < 1 || E > kMmMaxExperts || int64_t(E) * O > kMaxOut)
     return 0;
   return align_up(size_t(E) * size_t(O) * size_t(K) * 2);
 }
@@ -173,7 +176,7 @@ int mx4_linear_bwd(const void* dy, int64_t lddy, const uint8_t* wq, const uint8_
   if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
   const int status = linear_shape(R, K, O, E, expert_offsets, kMx4Group);
   if (status != TOPMOE_OK) return status;
-  if (int64_t(E) * O > kMaxRows || !pitch_ok(lddy, O) || !pitch_ok(lddx, K))
+  if (!pitch_ok(lddy, O) || !pitch_ok(lddx, K))
     return TOPMOE_ERR_BAD_SHAPE;
   if (!wq || !w_scale || !workspace || (R > 0 && (!dy || !dx))) return TOPMOE_ERR_NULL_ARG;
   if (workspace_bytes < mx4_linear_bwd_workspace_bytes(K, O, E))

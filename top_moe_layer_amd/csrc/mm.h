@@ -44,12 +44,12 @@ struct MmParams {
 constexpr int kMmMaxExperts = 256;
 constexpr int kMx4Group = 32;  // channels that share a scale
 
-// Rows an expert has on average (the host does not know how they are spread).
+// Rows an expert has on average (the host does not know how they are spread),
+// and tiles of BM x BN that they then make.
 inline int64_t mm_rows_each(const MmParams& p) { return (p.R + p.E - 1) / p.E; }
-// Whether the kernel for few rows takes a product: up to `most` rows an expert,
-// and a grid within its limit of threads.
-inline bool mm_few(const MmParams& p, int64_t most) {
-  return mm_rows_each(p) <= most && (int64_t(p.N) + 31) / 32 * (p.E + 1) * 512 < (int64_t(1) << 31);
+inline int64_t mm_tiles(const MmParams& p, int64_t bm, int64_t bn) {
+  const int64_t experts = p.E < p.R ? p.E : p.R;
+  return (mm_rows_each(p) + bm - 1) / bm * experts * ((p.N + bn - 1) / bn);
 }
 
 hipError_t launch_mm_bf16(MmLayout layout, const MmParams& p, const Launch& s);

@@ -56,11 +56,17 @@ __device__ __forceinline__ u32x2 read_tr(const char* lds) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                        (__attribute__((address_space(3))) s16x4*)lds));
 }
-__device__ __forceinline__ const char* scalar_ptr(const char* p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
-  return reinterpret_cast<const char*>((uint64_t(hi) << 32) | lo);
+// a's lanes 32-63 change places with b's lanes 0-31; a's odd rows of 16 lanes
+// with b's even ones.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -87,15 +93,39 @@ __device__ __forceinline__ f32x16 mfma_f32(u32x4 a, u32x4 b, f32x16 c) {
                                              0);
   return c;
 }
-// FA: 0 e4m3 (eight registers), 4 e2m1 (four); byte SEL of the scales.
-template <int FA, int SEL>
-__device__ __forceinline__ f32x16 mfma_mx(u32x4 a0, u32x4 a1, u32x4 b, f32x16 c, uint32_t sa,
-                                          uint32_t sb) {
-  const i32x8 x = {int(a0[0]), int(a0[1]), int(a0[2]), int(a0[3]),
-                   int(a1[0]), int(a1[1]), int(a1[2]), int(a1[3])};
-  const i32x8 y = {int(b[0]), int(b[1]), int(b[2]), int(b[3]), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, FA, 4, SEL, int(sa), SEL,
-                                                         int(sb));
+// e2m1 by a format FY: 0 e4m3 (eight registers), 4 e2m1 (four); byte SEL of the
+// scales.  In assembly: through the builtin the compiler keeps the accumulators
+// apart from the results, about 100 registers more, which spill.  So the waits
+// are this code's own: two states between a vector instruction that wrote an
+// operand and this one, and settle() before anything but another of these reads
+// or writes an accumulator.
+template <int FY, int SEL>
+__device__ __forceinline__ void mfma_mx(u32x4 a, u32x4 b0, u32x4 b1, f32x16& c, uint32_t sa,
+                                        uint32_t sb) {
+  if constexpr (FY == 4) {
+    if constexpr (SEL == 0)
+      asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+          : "+v"(c) : "v"(a), "v"(b0), "v"(sa), "v"(sb));
+    else if constexpr (SEL == 1)
+      asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+          : "+v"(c) : "v"(a), "v"(b0), "v"(sa), "v"(sb));
+    else if constexpr (SEL == 2)
+      asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+          : "+v"(c) : "v"(a), "v"(b0), "v"(sa), "v"(sb));
+    else
+      asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+          : "+v"(c) : "v"(a), "v"(b0), "v"(sa), "v"(sb));
+  } else {
+    const i32x8 y = {int(b0[0]), int(b0[1]), int(b0[2]), int(b0[3]),
+                     int(b1[0]), int(b1[1]), int(b1[2]), int(b1[3])};
+    static_assert(SEL < 2, "two sub-steps");
+    if constexpr (SEL == 0)
+      asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0] cbsz:4"
+          : "+v"(c) : "v"(a), "v"(y), "v"(sa), "v"(sb));
+    else
+      asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4"
+          : "+v"(c) : "v"(a), "v"(y), "v"(sa), "v"(sb));
+  }
 }
 // Two e2m1 / e4m3 values times a scale as two bf16 (exact; a product outside
 // bf16's range becomes infinite, or rounds on its subnormals).
@@ -142,24 +172,22 @@ __device__ __forceinline__ float scale_f32(uint32_t byte) {
                    : byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
 }
 
-// n scale bytes (1, 2 or 4) from kb on of a row of KB, 2^0 behind its end.
+// n words of scale bytes from kb on of a row of KB, zeros (2^-127) behind its end.
 template <int n>
-__device__ __forceinline__ uint32_t scale_bytes(const uint8_t* row, int kb, int KB) {
-  if (kb + n <= KB) {
-    if constexpr (n == 4) {
-      typedef uint32_t __attribute__((aligned(1))) w;
-      return *reinterpret_cast<const w*>(row + kb);
-    } else if constexpr (n == 2) {
-      typedef uint16_t __attribute__((aligned(1))) w;
-      return *reinterpret_cast<const w*>(row + kb);
-    } else {
-      return row[kb];
-    }
-  }
-  uint32_t v = 0;
+__device__ __forceinline__ void scale_words(const uint8_t* row, int kb, int KB, uint32_t (&w)[n]) {
+  typedef uint32_t __attribute__((aligned(1))) any;
+  if (kb + 4 * n <= KB) {
 #pragma unroll
-  for (int i = 0; i < n; ++i) v |= uint32_t(kb + i < KB ? row[kb + i] : 127) << (8 * i);
-  return v;
+    for (int i = 0; i < n; ++i) w[i] = *reinterpret_cast<const any*>(row + kb + 4 * i);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (kb + 4 * i + j < KB) w[i] |= uint32_t(row[kb + 4 * i + j]) << (8 * j);
+  }
 }
 
 // The offsets' expert e, held inside [0, R] so that no row outside is touched
@@ -224,14 +252,31 @@ __device__ __forceinline__ RowTile row_tile(int t, const int (&o)[5], int incl, 
   return r;
 }
 
-// Elements of a K slice.
-constexpr int slice_of(int fa, int fb) {
-  return fa == kMmF32 ? 32 : fb == kMmE2m1 ? (fa == kMmE2m1 ? 256 : 128) : 64;
+// The expert with the rank-th most rows (ties by number), so that the longest
+// sums start first; beyond 64 experts, where tiles are many and no expert's rows
+// are a large part of all, just the rank-th.
+__device__ __forceinline__ int by_rows(const int32_t* offsets, int E, int64_t R, int rank,
+                                       int lane) {
+  if (offsets == nullptr || E > 64) return rank;
+  const int rows = lane < E ? offset_at(offsets, lane + 1, E, R) - offset_at(offsets, lane, E, R)
+                            : -1;
+  int mine = 0;
+  for (int e = 0; e < E; ++e) {
+    const int other = __builtin_amdgcn_readlane(rows, e);
+    mine += other > rows || (other == rows && e < lane) ? 1 : 0;
+  }
+  return __ffsll((long long)__ballot(lane < E && mine == rank)) - 1;
 }
 
-template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int S>
+// Elements of a K slice of Q sub-steps (an e2m1 matrix beside bf16 has four:
+// a lane's 16 bytes).
+constexpr int slice_of(int fa, int fb, int Q) {
+  return Q * (fa == kMmF32 ? 8 : fb == kMmE2m1 ? 64 : 16);
+}
+
+template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int Q, int S>
 struct Shape {
-  static constexpr int KS = slice_of(FA, FB);
+  static constexpr int KS = slice_of(FA, FB, Q);
   static constexpr bool TA = LAYOUT == kMmTN, TB = LAYOUT != kMmNT;  // rows across K
   static constexpr int RBA = TA ? BM * mm_bits(FA) / 8 : KS * mm_bits(FA) / 8;  // bytes of an LDS row
   static constexpr int RBB = TB ? BN * mm_bits(FB) / 8 : KS * mm_bits(FB) / 8;
@@ -256,23 +301,23 @@ __device__ __forceinline__ int swz_t(int row) {
   return BITS == 16 ? (row & 3) * 4 : ((row >> 2) & 1) * 8;
 }
 
-template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN, (Shape<LAYOUT, FA, FB, OT, BM, BN, WM, WN, S>::WAVES))
+template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int Q, int S>
+__global__ __launch_bounds__(64 * WM * WN, (Shape<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>::WAVES))
 void mm_kernel(MmParams p) {
-  using Z = Shape<LAYOUT, FA, FB, OT, BM, BN, WM, WN, S>;
+  using Z = Shape<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>;
   constexpr int KS = Z::KS, NW = Z::NW, RBA = Z::RBA, RBB = Z::RBB, STAGE = Z::STAGE;
   constexpr bool TA = Z::TA, TB = Z::TB, TN_ = LAYOUT == kMmTN;
   constexpr bool MX = FB == kMmE2m1, F32 = FA == kMmF32, WQ = FB == kMmE2m1Bf;
   constexpr bool SA = mm_scaled(FA), SB = mm_scaled(FB);
   constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
-  constexpr int Q = MX ? KS / 64 : F32 ? 4 : 4;       // sub-steps of a slice
   constexpr int NS = FA == kMmF32Split ? 3 : 1;       // bf16 parts of a row's element
   constexpr int PA = FA == kMmE4m3 || FA == kMmF32Split ? 2 : 1;  // 16-byte pieces of a fragment
   constexpr int SBYTES = MX ? Q : 1;                  // a lane's scales of a slice
   constexpr int LA = Z::LA, LB = Z::LB;
   constexpr int ESA = mm_bits(FA) / 8, ESB = mm_bits(FB) / 8;  // 0 for e2m1
-  static_assert(WTM % 32 == 0 && WTN % 32 == 0 && Q % 2 == 0, "tile shape");
-  static_assert(S * STAGE <= 156 * 1024 && (S - 1) * (LA + LB) < 64, "ring");
+  static_assert(WTM % 32 == 0 && WTN % 32 == 0 && (Q == 2 || Q == 4) && (!WQ || Q == 4), "tile shape");
+  static_assert(!(SA || SB) || S * KS / 32 <= 16, "scales of a round");
+  static_assert((S == 3 || S == 4) && S * STAGE <= 160 * 1024 && (S - 1) * (LA + LB) < 64, "ring");
   static_assert(!TA || FA == kMmBf16 || FA == kMmF32, "transposed rows");
   static_assert(!TB || FB == kMmBf16 || FB == kMmF32, "transposed matrix");
   static_assert(!TA || RBA % 256 == 0, "transposing reads take whole 256-byte windows");
@@ -280,186 +325,207 @@ void mm_kernel(MmParams p) {
   // One object per slot, so that reads of one are known not to touch another.
   __shared__ __attribute__((aligned(1024))) char ring0[STAGE];
   __shared__ __attribute__((aligned(1024))) char ring1[STAGE];
-  __shared__ __attribute__((aligned(1024))) char ring2[S > 2 ? STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char ring2[STAGE];
+  __shared__ __attribute__((aligned(1024))) char ring3[S > 3 ? STAGE : 16];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 31, fg = lane >> 5;
   const int wm = (wid / WN) * WTM, wn = (wid % WN) * WTN;
   const int nt = (p.N + BN - 1) / BN;
-
-  // ---- the block's tile.  Blocks go to the 8 XCDs round robin: XCD x takes
-  // the x-th eighth of the tiles, in groups of GM row tiles, column by column,
-  // so that blocks running together share rows and matrix panels in its L2.
-  constexpr int GM = 8;
-  int e, row0, rows, n0, KT, krow0 = 0, K = p.K;
-  {
-    const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
-    int mt, col;
-    if constexpr (TN_) {
-      const int mts = (p.M + BM - 1) / BM, per_e = mts * nt;
-      const int share = (per_e + 7) >> 3;  // of an expert's tiles
-      e = j / share;
-      const int t = x * share + (j - e * share);
-      if (e >= p.E || t >= per_e) return;
-      const int first = t / (GM * nt) * GM, in = t - first * nt;
-      const int gsz = mts - first < GM ? mts - first : GM;
-      mt = first + in % gsz;
-      col = in / gsz;
-      row0 = mt * BM;
-      rows = p.M - row0 < BM ? p.M - row0 : BM;
-      int o0 = 0, o1 = int(p.R);
-      if (p.offsets != nullptr) {
-        o0 = offset_at(p.offsets, e, p.E, p.R);
-        o1 = offset_at(p.offsets, e + 1, p.E, p.R);
-      }
-      krow0 = __builtin_amdgcn_readfirstlane(o0);
-      K = __builtin_amdgcn_readfirstlane(o1 > o0 ? o1 - o0 : 0);
-    } else {
-      int o[5], incl = 0, last = 0, mts;
-      if (p.offsets != nullptr) mts = row_tiles<BM>(p.offsets, p.E, p.R, lane, o, incl, last);
-      else mts = int((p.R + BM - 1) / BM);
-      const int total = mts * nt, share = (total + 7) >> 3;  // at most the grid
-      const int t = x * share + j;
-      if (j >= share || t >= total) return;
-      const int first = t / (GM * nt) * GM, in = t - first * nt;
-      const int gsz = mts - first < GM ? mts - first : GM;
-      mt = first + in % gsz;
-      col = in / gsz;
-      if (p.offsets != nullptr) {
-        const RowTile r = row_tile<BM>(mt, o, incl, last, p.E, p.R, lane);
-        e = r.e;
-        row0 = r.row0;
-        rows = r.rows;
-      } else {
-        e = 0;
-        row0 = mt * BM;
-        rows = p.R - row0 < BM ? int(p.R - row0) : BM;
-      }
-    }
-    n0 = __builtin_amdgcn_readfirstlane(col * BN);
-    e = __builtin_amdgcn_readfirstlane(e);
-    row0 = __builtin_amdgcn_readfirstlane(row0);
-    rows = __builtin_amdgcn_readfirstlane(rows);
-    KT = (K + KS - 1) / KS;
-    if (!TN_ && e == p.E && p.offsets != nullptr) KT = 0;  // rows of no expert
-  }
-  const int cols = p.N - n0 < BN ? p.N - n0 : BN;
-
-  // ---- load sources: scalar bases and the lanes' offsets from them
   const int64_t pitch_a = TA ? p.lda * ESA : p.lda * mm_bits(FA) / 8;
   const int64_t pitch_b = TN_ ? p.ldb * ESB
                               : TB ? int64_t(p.N) * ESB : int64_t(p.K) * mm_bits(FB) / 8;
-  const char* base_a = static_cast<const char*>(p.A);
-  const char* base_b = static_cast<const char*>(p.B);
-  if constexpr (TA) base_a += krow0 * pitch_a + int64_t(row0) * ESA;
-  else base_a += row0 * pitch_a;
-  if constexpr (TN_) base_b += krow0 * pitch_b + int64_t(n0) * ESB;
-  else if constexpr (TB) base_b += int64_t(e) * p.K * pitch_b + int64_t(n0) * ESB;
-  else base_b += (int64_t(e) * p.N + n0) * pitch_b;
-  base_a = scalar_ptr(base_a);
-  base_b = scalar_ptr(base_b);
-  uint32_t off_a[LA], off_b[LB];
-  // The lane's chunk of a row along K is the same in all its loads: NW loads on,
-  // rows have moved by a multiple of the swizzle's period.
-  const int chunk_a = ((lane * 16 % RBA) / 16) ^ swz<RBA>((wid * 1024 + lane * 16) / RBA);
-  const int chunk_b = ((lane * 16 % RBB) / 16) ^ swz<RBB>((wid * 1024 + lane * 16) / RBB);
-#pragma unroll
-  for (int i = 0; i < LA; ++i) {
-    const int at = (wid + NW * i) * 1024 + lane * 16, r = at / RBA, c = (at % RBA) / 16;
-    if constexpr (TA) {
-      const int ch = c ^ swz_t<mm_bits(FA)>(r);
-      off_a[i] = ch * 16 < rows * ESA ? uint32_t(r * pitch_a) + ch * 16 : kBeyond;
-    } else {
-      off_a[i] = uint32_t(r * pitch_a) + chunk_a * 16;
-    }
+
+  // ---- the block's tiles.  Blocks go to the 8 XCDs round robin: XCD x takes
+  // the x-th eighth of the tiles (TN: of each expert's), in groups of GM row
+  // tiles, column by column, so that blocks running together share rows and
+  // matrix panels in its L2.  NT, NN: the grid's blocks of an XCD take its
+  // tiles in turn; TN, where an expert's rows are the length of its tiles: a
+  // block a tile.
+  constexpr int GM = 8;
+  struct Tile {
+    const char *a, *b;          // first bytes of the tile's rows and columns
+    const uint8_t *sa, *sb;     // and of their scales
+    int e, row0, n0, rows, cols, K, KT;  // KT: slices, whole rounds of the ring
+  };
+  const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+  int o[5], incl = 0, last = 0, mts, share, total, mine;
+  if constexpr (TN_) {
+    mts = (p.M + BM - 1) / BM;
+    total = mts * nt;
+    share = (total + 7) >> 3;
+    mine = local / share < p.E && xcd * share + local % share < total ? 1 : 0;
+  } else {
+    if (p.offsets != nullptr) mts = row_tiles<BM>(p.offsets, p.E, p.R, lane, o, incl, last);
+    else mts = int((p.R + BM - 1) / BM);
+    total = mts * nt;  // at most the tiles the grid was planned for
+    share = (total + 7) >> 3;
+    const int end = total - xcd * share < share ? total - xcd * share : share;
+    const int blocks = gridDim.x >> 3;
+    mine = local < end ? (end - local + blocks - 1) / blocks : 0;
   }
-#pragma unroll
-  for (int i = 0; i < LB; ++i) {
-    const int at = (wid + NW * i) * 1024 + lane * 16, r = at / RBB, c = (at % RBB) / 16;
-    if constexpr (TB) {
-      const int ch = c ^ swz_t<mm_bits(FB)>(r);
-      off_b[i] = ch * 16 < cols * ESB ? uint32_t(r * pitch_b) + ch * 16 : kBeyond;
+  mine = __builtin_amdgcn_readfirstlane(mine);
+  if (mine <= 0) return;
+  auto tile = [&](int i) {
+    Tile t;
+    int at;
+    if constexpr (TN_) at = xcd * share + local % share;
+    else at = xcd * share + local + i * int(gridDim.x >> 3);
+    const int first = at / (GM * nt) * GM, in = at - first * nt;
+    const int gsz = mts - first < GM ? mts - first : GM;
+    const int mt = first + in % gsz;
+    t.n0 = __builtin_amdgcn_readfirstlane(in / gsz * BN);
+    t.cols = p.N - t.n0 < BN ? p.N - t.n0 : BN;
+    int krow0 = 0;
+    if constexpr (TN_) {
+      t.e = __builtin_amdgcn_readfirstlane(by_rows(p.offsets, p.E, p.R, local / share, lane));
+      t.row0 = mt * BM;
+      t.rows = p.M - t.row0 < BM ? p.M - t.row0 : BM;
+      int o0 = 0, o1 = int(p.R);
+      if (p.offsets != nullptr) {
+        o0 = offset_at(p.offsets, t.e, p.E, p.R);
+        o1 = offset_at(p.offsets, t.e + 1, p.E, p.R);
+      }
+      krow0 = __builtin_amdgcn_readfirstlane(o0);
+      t.K = __builtin_amdgcn_readfirstlane(o1 > o0 ? o1 - o0 : 0);
+    } else if (p.offsets != nullptr) {
+      const RowTile r = row_tile<BM>(mt, o, incl, last, p.E, p.R, lane);
+      t.e = __builtin_amdgcn_readfirstlane(r.e);
+      t.row0 = r.row0;
+      t.rows = r.rows;
+      t.K = t.e == p.E ? 0 : p.K;  // rows of no expert: a product over nothing
     } else {
-      off_b[i] = uint32_t(r * pitch_b) + chunk_b * 16;
+      t.e = 0;
+      t.row0 = mt * BM;
+      t.rows = p.R - t.row0 < BM ? int(p.R - t.row0) : BM;
+      t.K = p.K;
     }
-  }
-  // Slice kt into a slot; one past the last is all zeros (an empty buffer), so
-  // that the loop has no special cases.  Across K the slice's last row ends
-  // the buffer; along K lanes past K load from beyond it.
-  auto issue = [&](int kt, char* slot) {
-    const int left = K - kt * KS > 0 ? K - kt * KS : 0;  // elements
-    const int take = left < KS ? left : KS;
-    const uint32_t rec_a =
-        TA ? uint32_t((take - 1) * pitch_a + rows * ESA)
-           : uint32_t((rows - 1) * pitch_a) + uint32_t(int64_t(left) * mm_bits(FA) / 8);
-    const uint32_t rec_b =
-        TB ? uint32_t((take - 1) * pitch_b + cols * ESB)
-           : uint32_t((cols - 1) * pitch_b) + uint32_t(int64_t(left) * mm_bits(FB) / 8);
-    const auto ra = buffer(base_a + (TA ? kt * KS * pitch_a : int64_t(kt) * RBA), left ? rec_a : 0u);
-    const auto rb = buffer(base_b + (TB ? kt * KS * pitch_b : int64_t(kt) * RBB), left ? rec_b : 0u);
-    const bool in_a = TA || chunk_a * 128 < take * mm_bits(FA);
-    const bool in_b = TB || chunk_b * 128 < take * mm_bits(FB);
-#pragma unroll
-    for (int i = 0; i < LA; ++i) {
-      const int blk = wid + NW * i;
-      if (Z::ABYTES / 1024 % NW != 0 && blk >= Z::ABYTES / 1024) break;
-      dma16(ra, slot + blk * 1024, in_a ? off_a[i] : kBeyond);
-    }
-#pragma unroll
-    for (int i = 0; i < LB; ++i) {
-      const int blk = wid + NW * i;
-      if (Z::BBYTES / 1024 % NW != 0 && blk >= Z::BBYTES / 1024) break;
-      dma16(rb, slot + Z::ABYTES + blk * 1024, in_b ? off_b[i] : kBeyond);
-    }
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    const int slices = (t.K + KS - 1) / KS;
+    t.KT = slices > S ? (slices + S - 1) / S * S : S;
+    t.a = static_cast<const char*>(p.A);
+    t.b = static_cast<const char*>(p.B);
+    if constexpr (TA) t.a += krow0 * pitch_a + int64_t(t.row0) * ESA;
+    else t.a += t.row0 * pitch_a;
+    if constexpr (TN_) t.b += krow0 * pitch_b + int64_t(t.n0) * ESB;
+    else if constexpr (TB) t.b += int64_t(t.e) * p.K * pitch_b + int64_t(t.n0) * ESB;
+    else t.b += (int64_t(t.e) * p.N + t.n0) * pitch_b;
+    t.sa = SA ? p.As + int64_t(t.row0) * (p.K / 32) : nullptr;
+    t.sb = SB ? p.Bs + (int64_t(t.e) * p.N + t.n0) * (p.K / 32) : nullptr;
+    return t;
   };
 
-  // ---- scales: a lane's bytes of its rows and columns, fetched a slice ahead
-  const int KB = p.K / 32;
-  const uint8_t* sbase_a = nullptr;
-  const uint8_t* sbase_b = nullptr;
-  uint32_t soff_a[SA ? TM : 1], soff_b[SB ? TN : 1];
-  if constexpr (SA) {
-    sbase_a = reinterpret_cast<const uint8_t*>(
-        scalar_ptr(reinterpret_cast<const char*>(p.As) + int64_t(row0) * KB));
+  // ---- loads.  Wavefront w fills the 1 KB blocks w, w + NW, ... of each
+  // operand's part of a slot; a lane's 16-byte chunk of the LDS row is the same
+  // in all of them (rows move by a multiple of the swizzle's period).
+  const int row_a = (wid * 1024 + lane * 16) / RBA, row_b = (wid * 1024 + lane * 16) / RBB;
+  const int chunk_a = ((lane * 16 % RBA) / 16) ^ (TA ? swz_t<mm_bits(FA)>(row_a) : swz<RBA>(row_a));
+  const int chunk_b = ((lane * 16 % RBB) / 16) ^ (TB ? swz_t<mm_bits(FB)>(row_b) : swz<RBB>(row_b));
+  static_assert(TA ? (mm_bits(FA) == 16 ? NW * 1024 / RBA % 4 == 0 : NW * 1024 / RBA % 8 == 0)
+                   : NW * 4 % (RBA / 16) == 0, "one chunk a lane");
+  static_assert(TB ? (mm_bits(FB) == 16 ? NW * 1024 / RBB % 4 == 0 : NW * 1024 / RBB % 8 == 0)
+                   : NW * 4 % (RBB / 16) == 0, "one chunk a lane");
+  uint32_t off_a[LA], off_b[LB];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int r = wm + 32 * i + fr;
-      soff_a[i] = uint32_t(r < rows ? r : rows - 1) * uint32_t(KB);
-    }
-  }
-  if constexpr (SB) {
-    sbase_b = reinterpret_cast<const uint8_t*>(
-        scalar_ptr(reinterpret_cast<const char*>(p.Bs) + (int64_t(e) * p.N + n0) * KB));
+  for (int i = 0; i < LA; ++i)
+    off_a[i] = uint32_t((row_a + i * NW * 1024 / RBA) * pitch_a) + chunk_a * 16;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int c = wn + 32 * j + fr;
-      soff_b[j] = uint32_t(c < cols ? c : cols - 1) * uint32_t(KB);
+  for (int i = 0; i < LB; ++i)
+    off_b[i] = uint32_t((row_b + i * NW * 1024 / RBB) * pitch_b) + chunk_b * 16;
+  // Slice kt of a tile into a slot, in Q parts, one under each sub-step's matrix
+  // instructions; one past the tile's last is all zeros (an empty buffer).
+  // Across K the slice's last row ends the buffer and lanes past the last
+  // column load from beyond it; along K it ends with the last row, and lanes
+  // past K load from beyond.
+  auto issue = [&](const Tile& t, int kt, char* slot, int part) {
+    int w = wid;  // opaque, so that the slots' addresses are added up here, not kept
+    asm volatile("" : "+s"(w));
+    const int left = t.K - kt * KS > 0 ? t.K - kt * KS : 0;  // elements
+    const int take = left < KS ? left : KS;
+    const uint32_t rec_a =
+        TA ? uint32_t((take - 1) * pitch_a + t.rows * ESA)
+           : uint32_t((t.rows - 1) * pitch_a) + uint32_t(int64_t(left) * mm_bits(FA) / 8);
+    const uint32_t rec_b =
+        TB ? uint32_t((take - 1) * pitch_b + t.cols * ESB)
+           : uint32_t((t.cols - 1) * pitch_b) + uint32_t(int64_t(left) * mm_bits(FB) / 8);
+    const auto ra = buffer(t.a + (TA ? kt * KS * pitch_a : int64_t(kt) * RBA), left ? rec_a : 0u);
+    const auto rb = buffer(t.b + (TB ? kt * KS * pitch_b : int64_t(kt) * RBB), left ? rec_b : 0u);
+    const bool in_a = TA ? chunk_a * 16 < t.rows * ESA : chunk_a * 128 < take * mm_bits(FA);
+    const bool in_b = TB ? chunk_b * 16 < t.cols * ESB : chunk_b * 128 < take * mm_bits(FB);
+#pragma unroll
+    for (int l = part * (LA + LB) / Q; l < (part + 1) * (LA + LB) / Q; ++l) {
+      const int i = l < LA ? l : l - LA, blk = w + NW * i;
+      if (l < LA) {
+        if (Z::ABYTES / 1024 % NW == 0 || blk < Z::ABYTES / 1024)
+          dma16(ra, slot + blk * 1024, in_a ? off_a[i] : kBeyond);
+      } else {
+        if (Z::BBYTES / 1024 % NW == 0 || blk < Z::BBYTES / 1024)
+          dma16(rb, slot + Z::ABYTES + blk * 1024, in_b ? off_b[i] : kBeyond);
+      }
     }
-  }
-  uint32_t next_a[SA ? TM : 1], next_b[SB ? TN : 1];  // of the slice behind the current one
-  uint32_t sc_a[SA ? TM : 1], sc_b[SB ? TN : 1];      // of the current one
-  auto fetch_scales = [&](int kt) {
-    const int kb = MX ? kt * (KS / 32) + fg * SBYTES : kt * 2 + fg;
+  };
+  auto issue_all = [&](const Tile& t, int kt, char* slot) {
+#pragma unroll
+    for (int part = 0; part < Q; ++part) issue(t, kt, slot, part);
+  };
+
+  // ---- scales: those of a round of S slices go through registers into LDS (a
+  // row or column a thread), a round ahead, and a lane reads the bytes of its
+  // rows and columns slice by slice.
+  constexpr int NTHR = 64 * NW, SROWS = (SA ? BM : 0) + (SB ? BN : 0);
+  constexpr int SW = (S * KS / 32 + 3) / 4, SP = SW > 2 ? 16 : 8;  // words of a row; its bytes in LDS
+  constexpr int SR = (SROWS + NTHR - 1) / NTHR;                    // rows of a thread
+  __shared__ __attribute__((aligned(16))) char s_scale[SROWS > 0 ? 2 * SROWS * SP : 16];
+  uint32_t sword[SR > 0 ? SR : 1][SW];
+  int sturn = 0;  // the half of s_scale that the current round reads
+  auto fetch_scales = [&](const Tile& t, int kt) {
+    const int KB = t.K / 32;
+#pragma unroll
+    for (int i = 0; i < SR; ++i) {
+      const int x = tid + NTHR * i, c = SA ? x - BM : x;
+      const uint8_t* row = nullptr;
+      if (SA && x < BM) row = t.sa + uint32_t(x < t.rows ? x : t.rows - 1) * uint32_t(KB);
+      else if (SB) row = t.sb + uint32_t(c < t.cols ? c : t.cols - 1) * uint32_t(KB);
+      if (x < SROWS) scale_words<SW>(row, kt * (KS / 32), KB, sword[i]);
+    }
+  };
+  auto keep_scales = [&](int half) {
+#pragma unroll
+    for (int i = 0; i < SR; ++i) {
+      const int x = tid + NTHR * i;
+#pragma unroll
+      for (int w = 0; w < SW; ++w)
+        if (x < SROWS)
+          *reinterpret_cast<uint32_t*>(s_scale + half * SROWS * SP + x * SP + 4 * w) = sword[i][w];
+    }
+  };
+  uint32_t sc_a[SA ? TM : 1], sc_b[SB ? TN : 1];  // of the current slice
+  uint32_t nx_a[SA ? TM : 1], nx_b[SB ? TN : 1];  // of the next one
+  auto read_scales = [&](int half, int slice) {
+    typedef typename std::conditional<SBYTES == 4, uint32_t, typename std::conditional<
+                                      SBYTES == 2, uint16_t, uint8_t>::type>::type word;
+    const char* at = s_scale + half * SROWS * SP + fr * SP + fg * SBYTES + slice * (KS / 32);
     if constexpr (SA) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) next_a[i] = scale_bytes<SBYTES>(sbase_a + soff_a[i], kb, KB);
+      for (int i = 0; i < TM; ++i)
+        nx_a[i] = *reinterpret_cast<const word*>(at + wm * SP + 32 * i * SP);
     }
     if constexpr (SB) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) next_b[j] = scale_bytes<SBYTES>(sbase_b + soff_b[j], kb, KB);
+      for (int j = 0; j < TN; ++j)
+        nx_b[j] = *reinterpret_cast<const word*>(at + (wn + (SA ? BM : 0)) * SP + 32 * j * SP);
     }
   };
   auto take_scales = [&]() {
     if constexpr (SA) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-        sc_a[i] = MX ? next_a[i] : __float_as_uint(scale_f32(next_a[i]));
+      for (int i = 0; i < TM; ++i) sc_a[i] = MX ? nx_a[i] : __float_as_uint(scale_f32(nx_a[i]));
     }
     if constexpr (SB) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-        sc_b[j] = MX ? next_b[j] : __float_as_uint(scale_f32(next_b[j]));
+      for (int j = 0; j < TN; ++j) sc_b[j] = MX ? nx_b[j] : __float_as_uint(scale_f32(nx_b[j]));
     }
   };
 
@@ -474,9 +540,11 @@ void mm_kernel(MmParams p) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       if constexpr (!TA) {
-        const int r = wm + 32 * i + fr, z = swz<RBA>(fr);
-        const char* row = slot + r * RBA;
-        auto chunk = [&](int c) { return *reinterpret_cast<const u32x4*>(row + ((c ^ z) << 4)); };
+        const int z = swz<RBA>(fr);
+        const char* row = slot + (wm + fr) * RBA;
+        auto chunk = [&](int c) {
+          return *reinterpret_cast<const u32x4*>(row + ((c ^ z) << 4) + 32 * i * RBA);
+        };
         if constexpr (FA == kMmBf16) {
           fa[buf][i][0] = chunk(WQ ? 4 * fg + q : 2 * q + fg);
         } else if constexpr (FA == kMmF32) {
@@ -487,7 +555,7 @@ void mm_kernel(MmParams p) {
           fa[buf][i][1] = chunk(c + 1);
         } else if constexpr (FA == kMmE4m3Bf) {
           const u32x2 v = *reinterpret_cast<const u32x2*>(row + (((2 * fg + (q >> 1)) ^ z) << 4) +
-                                                          8 * (q & 1));
+                                                          8 * (q & 1) + 32 * i * RBA);
           fa[buf][i][0] = u32x4{v.x, v.y, 0u, 0u};
         } else if constexpr (FA == kMmE4m3) {
           fa[buf][i][0] = chunk(2 * q + fg);
@@ -515,9 +583,11 @@ void mm_kernel(MmParams p) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       if constexpr (!TB) {
-        const int r = wn + 32 * j + fr, z = swz<RBB>(fr);
-        const char* row = slot + r * RBB;
-        auto chunk = [&](int c) { return *reinterpret_cast<const u32x4*>(row + ((c ^ z) << 4)); };
+        const int z = swz<RBB>(fr);
+        const char* row = slot + (wn + fr) * RBB;
+        auto chunk = [&](int c) {
+          return *reinterpret_cast<const u32x4*>(row + ((c ^ z) << 4) + 32 * j * RBB);
+        };
         if constexpr (WQ) {
           if (q == 0) raw_b[j] = chunk(fg);
         } else if constexpr (MX) {
@@ -548,13 +618,17 @@ void mm_kernel(MmParams p) {
     }
   };
 
+  // The matrix's columns are the instructions' rows, so that a lane ends with
+  // runs of four columns of one row.
   f32x16 acc[TM][TN];
+  auto clear = [&]() {
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+      for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  };
   auto mma = [&](auto qc, int buf) {
     constexpr int q = decltype(qc)::value;
 #pragma unroll
@@ -567,37 +641,53 @@ void mm_kernel(MmParams p) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         if constexpr (MX) {
-          acc[i][j] = mfma_mx<FA == kMmE4m3 ? 0 : 4, q>(fa[buf][i][0], fa[buf][i][PA - 1],
-                                                        fb[buf][j], acc[i][j], sc_a[i], sc_b[j]);
+          mfma_mx<FA == kMmE4m3 ? 0 : 4, q>(fb[buf][j], fa[buf][i][0], fa[buf][i][PA - 1],
+                                            acc[i][j], sc_b[j], sc_a[i]);
         } else if constexpr (F32) {
-          acc[i][j] = mfma_f32(part[0], fb[buf][j], acc[i][j]);
+          acc[i][j] = mfma_f32(fb[buf][j], part[0], acc[i][j]);
         } else {
           // the smallest part first
 #pragma unroll
-          for (int s = NS - 1; s >= 0; --s) acc[i][j] = mfma_bf16(part[s], fb[buf][j], acc[i][j]);
+          for (int s = NS - 1; s >= 0; --s) acc[i][j] = mfma_bf16(fb[buf][j], part[s], acc[i][j]);
         }
       }
     }
   };
-  // One slice, read from `cur`; the fragments of the next one's first sub-step
-  // come from `nxt` under the last one's matrix instructions.
-  auto step = [&](int kt, char* cur, const char* nxt) {
-    if constexpr (SA || SB) fetch_scales(kt + 1 < KT ? kt + 1 : kt);
+  // One slice, read from `cur`, while slice `kt` of tile t goes into `free`, the
+  // slot read before; the fragments of the next slice's first sub-step come
+  // from `nxt` under the last one's matrix instructions.  `slice`: its number in
+  // the round; the round's last puts the next round's scales away.  `stored`:
+  // the stores of a tile before may still be under way behind the loads that
+  // are waited for.
+  constexpr int NST = sizeof(OT) == 2 ? TM * TN * 2 : TM * TN * 4;  // stores of a whole tile
+  constexpr int BEHIND = (S - 2) * Z::LMIN, BEHIND_ST = BEHIND + NST < 63 ? BEHIND + NST : 63;
+  auto step = [&](const char* cur, const char* nxt, char* free, const Tile& t, int kt, int slice,
+                  bool stored) {
     auto sub = [&](auto qc) {
       constexpr int q = decltype(qc)::value;
+      __builtin_amdgcn_sched_barrier(0);
       if constexpr (q + 1 < Q) {
         load_a(cur, q + 1, (q + 1) & 1);
         load_b(cur, q + 1, (q + 1) & 1);
+        issue(t, kt, free, q);
         convert_b(q + 1, (q + 1) & 1);
         mma(qc, q & 1);
       } else {
-        wait_loads<(S - 2) * Z::LMIN>();
+        issue(t, kt, free, q);
+        if constexpr (SROWS > 0) {
+          if (slice + 1 == S) {
+            sturn ^= 1;
+            keep_scales(sturn);
+          }
+        }
+        if (stored) wait_loads<BEHIND_ST>();
+        else wait_loads<BEHIND>();
         slot_barrier();
-        issue(kt + S, cur);
+        if constexpr (SROWS > 0) read_scales(sturn, slice + 1 == S ? 0 : slice + 1);
         load_a(nxt, 0, 0);
         load_b(nxt, 0, 0);
         mma(qc, q & 1);
-        take_scales();
+        if constexpr (SROWS > 0) take_scales();
         convert_b(0, 0);
       }
     };
@@ -607,76 +697,162 @@ void mm_kernel(MmParams p) {
       sub(std::integral_constant<int, 2>{});
       sub(std::integral_constant<int, 3>{});
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  if (KT > 0) {
-    issue(0, ring0);
-    issue(1, ring1);
-    if constexpr (S > 2) issue(2, ring2);
-    if constexpr (SA || SB) fetch_scales(0);
-    wait_loads<(S - 1) * Z::LMIN>();
-    slot_barrier();
-    load_a(ring0, 0, 0);
-    load_b(ring0, 0, 0);
-    take_scales();
-    convert_b(0, 0);
-    int kt = 0;
-    for (; kt + S <= KT; kt += S) {
-      step(kt, ring0, ring1);
-      if constexpr (S == 2) {
-        step(kt + 1, ring1, ring0);
-      } else {
-        step(kt + 1, ring1, ring2);
-        step(kt + 2, ring2, ring0);
-      }
-    }
-    if (kt < KT) step(kt, ring0, ring1);
-    if constexpr (S > 2) {
-      if (kt + 1 < KT) step(kt + 1, ring1, ring2);
-    }
-    wait_loads<0>();  // no load into LDS outlives the block
-  }
 
-  // ---- epilogue: lane (fr, fg), register v holds row 8 (v / 4) + 4 fg + v % 4,
-  // column fr of a 32 x 32 piece; four rows of a column are transposed inside a
-  // lane quad, so that a lane stores four columns of a row.
-  const int q4 = fr & 3, cl = wn + (fr & ~3);
-  OT* out = static_cast<OT*>(p.C);
-  const int64_t ldc = TN_ ? p.N : p.ldc;
-  const int64_t first = TN_ ? int64_t(e) * p.M + row0 : int64_t(row0);
+  // Every scaled instruction has been issued, then at least the 19 states that
+  // the longest of them takes, then the accumulators are read.
+  auto settle = [&]() {
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+    for (int t = 0; t < 2 * TM * TN; ++t) {
+      if (t == TM * TN) asm volatile("s_nop 15\n\ts_nop 15" : "+v"(acc[0][0]));
+      asm volatile("" : "+v"(acc[t / TN % TM][t % TN]));
+    }
+  };
+
+  // ---- a tile's results.  Lane (fr, fg), register v of a 32 x 32 piece: row
+  // fr, column 8 (v / 4) + 4 fg + v % 4.  bf16: two swaps of half-wavefronts and
+  // of rows of 16 lanes bring the 32 columns of a row to four lanes, 16 bytes in
+  // each.
+  auto put = [&](const Tile& t, auto whole_tile) {
+    constexpr bool whole = decltype(whole_tile)::value;
+    const int64_t ldc = TN_ ? p.N : p.ldc;
+    const int64_t first = TN_ ? int64_t(t.e) * p.M + t.row0 : int64_t(t.row0);
+    OT* out = static_cast<OT*>(p.C) + first * ldc + t.n0;
+    // opaque, so that no address is kept for the whole block
+    int r0 = wm + (sizeof(OT) == 2 ? lane & 15 : fr);
+    int c0 = wn + (sizeof(OT) == 2 ? 8 * (((lane >> 4) & 1) * 2 + fg) : 4 * fg);
+    asm volatile("" : "+v"(r0), "+v"(c0));
 #pragma unroll
-    for (int vq = 0; vq < 4; ++vq) {
-      const int r = wm + 32 * i + 8 * vq + 4 * fg + q4;
-      OT* o = out + (first + r) * ldc + n0 + cl;
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        float b[4];
+        const f32x16& d = acc[i][j];
+        if constexpr (sizeof(OT) == 2) {
+          uint32_t w[8];  // columns 8 (k / 2) + 4 fg + 2 (k % 2) ..
 #pragma unroll
-        for (int w = 0; w < 4; ++w) b[w] = acc[i][j][4 * vq + w];
-        quad_transpose(b, q4);
-        if (r < rows && cl + 32 * j < cols) store4<OT>(o + 32 * j, b);
+          for (int k = 0; k < 8; ++k)
+            w[k] = __builtin_bit_cast(
+                uint32_t, bf16x2{static_cast<__bf16>(d[2 * k]), static_cast<__bf16>(d[2 * k + 1])});
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            swap32(w[k], w[2 + k]);      // lanes 0-31: columns 0-7, 32-63: 8-15
+            swap32(w[4 + k], w[6 + k]);  // 16-23, 24-31
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) swap16(w[k], w[4 + k]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // rows 0-15, 16-31 of the piece
+            const int r = r0 + 32 * i + 16 * h, c = c0 + 32 * j;
+            if (whole || (r < t.rows && c < t.cols))
+              *reinterpret_cast<u32x4*>(out + (uint32_t(r) * uint32_t(ldc) + uint32_t(c))) =
+                  u32x4{w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = r0 + 32 * i, c = c0 + 32 * j + 8 * q;
+            if (whole || (r < t.rows && c < t.cols))
+              *reinterpret_cast<f32x4*>(out + (uint32_t(r) * uint32_t(ldc) + uint32_t(c))) =
+                  f32x4{d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+          }
+        }
       }
     }
+  };
+
+  // ---- the ring runs on from tile to tile: under a tile's last slices the
+  // first ones of the next are loaded, and they arrive under its stores.
+  char* const ring[4] = {ring0, ring1, ring2, S > 3 ? ring3 : ring0};
+  Tile cur = tile(0);
+#pragma unroll
+  for (int s = 0; s + 1 < S; ++s) issue_all(cur, s, ring[s]);
+  if constexpr (SROWS > 0) {
+    fetch_scales(cur, 0);
+    keep_scales(0);
   }
+  wait_loads<BEHIND>();
+  slot_barrier();
+  if constexpr (SROWS > 0) read_scales(0, 0);
+  load_a(ring0, 0, 0);
+  load_b(ring0, 0, 0);
+  if constexpr (SROWS > 0) take_scales();
+  convert_b(0, 0);
+  bool stored = false;
+  for (int i = 0; i < mine; ++i) {
+    Tile nxt = cur;
+    if (i + 1 < mine) nxt = tile(i + 1);
+    else nxt.K = 0;  // nothing is loaded any more
+    clear();
+    for (int kt = 0; kt < cur.KT; kt += S) {
+      const bool over = kt + S >= cur.KT;
+      const bool st = stored && kt == 0;
+      if constexpr (SROWS > 0) fetch_scales(over ? nxt : cur, over ? 0 : kt + S);
+      step(ring0, ring1, ring[S - 1], cur, kt + S - 1, 0, st);
+      Tile src = cur;
+      if (over) src = nxt;
+      const int at = over ? 0 : kt + S;
+      if constexpr (S == 3) {
+        step(ring1, ring2, ring0, src, at, 1, false);
+        step(ring2, ring0, ring1, src, at + 1, 2, false);
+      } else {
+        step(ring1, ring2, ring0, src, at, 1, st);
+        step(ring2, ring3, ring1, src, at + 1, 2, false);
+        step(ring3, ring0, ring2, src, at + 2, 3, false);
+      }
+    }
+    if constexpr (MX) settle();
+    if (cur.rows == BM && cur.cols == BN) {
+      put(cur, std::true_type{});
+      stored = true;
+    } else {
+      put(cur, std::false_type{});
+      stored = false;
+    }
+    cur = nxt;
+  }
+  wait_loads<0>();  // no load into LDS outlives the block
 }
 
-template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int S>
+// Blocks of a kernel that are on the device at once, asked once per device.
+template <typename K>
+int resident(K kernel, int threads, int (&cached)[64]) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (cached[dev] == 0) {
+    int cus = 0, per_cu = 0;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+        cus <= 0)
+      cus = 256;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kernel, threads, 0) != hipSuccess ||
+        per_cu <= 0)
+      per_cu = 1;
+    cached[dev] = cus * per_cu;
+  }
+  return cached[dev];
+}
+
+template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int Q, int S>
 hipError_t launch_tile(const MmParams& p, const Launch& s) {
+  using Z = Shape<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>;
   const int64_t nt = (p.N + BN - 1) / BN;
+  auto kernel = mm_kernel<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>;
   int64_t grid;
   if (LAYOUT == kMmTN) {
     grid = 8 * int64_t(p.E) * (((p.M + BM - 1) / BM * nt + 7) / 8);
   } else {
     // row tiles at most: every expert's last one, and that of the rows of none, may be partial
     const int64_t full = p.R / BM, parts = p.offsets == nullptr ? 1 : int64_t(p.E) + 1;
-    const int64_t mts = full + (parts < p.R ? parts : p.R);
-    grid = (mts * nt + 7) / 8 * 8;
+    const int64_t tiles = (full + (parts < p.R ? parts : p.R)) * nt;
+    if (tiles > 0x7fffffff) return hipErrorInvalidValue;
+    static int cached[64] = {};
+    const int64_t cap = resident(kernel, 64 * Z::NW, cached) / 8 * 8;
+    grid = (tiles + 7) / 8 * 8;
+    if (grid > cap && cap >= 8) grid = cap;
   }
   if (grid <= 0) return hipSuccess;
-  if (grid * (64 * WM * WN) > 0x7fffffff) return hipErrorInvalidValue;
-  return launch_kernel(mm_kernel<LAYOUT, FA, FB, OT, BM, BN, WM, WN, S>, dim3(unsigned(grid)),
-                       dim3(64 * WM * WN), 0, s, p);
+  if (grid * (64 * Z::NW) > 0x7fffffff) return hipErrorInvalidValue;
+  return launch_kernel(kernel, dim3(unsigned(grid)), dim3(64 * Z::NW), 0, s, p);
 }
 
 }  // namespace mm
