@@ -569,11 +569,14 @@ int moe_ffn_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t H, 
 int moe_linear_fwd(const void* x, int64_t ldx, const void* w, const int32_t* expert_offsets,
                    int64_t R, int64_t K, int64_t O, int E, int dtype, void* y, int64_t ldy,
                    void* stream, void* const* stage_events);
-/* dx NULL: not wanted (w may be NULL as well); dw NULL: not wanted (x may be). */
+/* dx NULL: not wanted (w may be NULL as well); dw NULL: not wanted (x may be).
+ * The workspace holds fp32 parts of sums that are divided among blocks;
+ * moe_linear_bwd_workspace_bytes returns 0 for invalid sizes. */
+size_t moe_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E);
 int moe_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
                    const int32_t* expert_offsets, int64_t R, int64_t K, int64_t O, int E,
-                   int dtype, void* dx, int64_t lddx, void* dw, void* stream,
-                   void* const* stage_events);
+                   int dtype, void* dx, int64_t lddx, void* dw, void* workspace,
+                   size_t workspace_bytes, void* stream, void* const* stage_events);
 
 /* ---- matrices and rows in 4 bits ------------------------------------------
  * Groups of 32 consecutive channels of a row (the last may be shorter) with one
@@ -614,7 +617,7 @@ int mx4_linear_fwd(const void* x, int64_t ldx, const uint8_t* x_scale, int rows,
  * dy[r].  The matrices are turned into bf16 (exact) in the workspace first.
  * mx4_linear_bwd_workspace_bytes returns 0 for invalid sizes. */
 #define TOPMOE_MX4_BWD_STAGES 2  /* 0 matrices to bf16, 1 dx */
-size_t mx4_linear_bwd_workspace_bytes(int64_t K, int64_t O, int E);
+size_t mx4_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E);
 int mx4_linear_bwd(const void* dy, int64_t lddy, const uint8_t* wq, const uint8_t* w_scale,
                    const int32_t* expert_offsets, int64_t R, int64_t K, int64_t O, int E,
                    int dtype, void* dx, int64_t lddx, void* workspace, size_t workspace_bytes,

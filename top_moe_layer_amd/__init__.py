@@ -57,7 +57,7 @@ def __getattr__(name):
         return v
     if name in ("moe_linear_fwd", "moe_linear_bwd", "MoeLinearGrads", "Mx4", "mx4_pack",
                 "mx4_unpack", "mx4_linear_fwd", "mx4_linear_bwd",
-                "mx4_linear_bwd_workspace_bytes"):
+                "moe_linear_bwd_workspace_bytes", "mx4_linear_bwd_workspace_bytes"):
         from . import linear
         globals()[name] = v = getattr(linear, name)
         return v

@@ -24,7 +24,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["plan.cpp", "api.hip", "router.hip", "permute.hip", "backward.hip", "gemm_bf16.hip",
            "gemm_f32.hip", "block_api.hip", "rows.hip", "norm.hip", "act8.hip", "linear_api.hip",
-           "mm_bf16.hip", "mm_f32.hip", "mm_mx4.hip", "mx4.hip"]
+           "mm_bf16.hip", "mm_f32.hip", "mm_mx4.hip", "mm_sum.hip", "mx4.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function"]
 # Device code: no packed fp32 instructions (they are generated from plain float

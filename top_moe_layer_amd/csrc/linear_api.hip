@@ -42,6 +42,38 @@ MmParams params(const void* A, int64_t lda, const void* B, const int32_t* offset
   return p;
 }
 
+// Two launches of one stage.
+void in_one(const Launch& L, Launch* first, Launch* second) {
+  *first = L;
+  *second = L;
+  first->stop = second->start = nullptr;
+}
+
+// dx of moe_linear_bwd, with the matrices as they are, or of mx4_linear_bwd, with
+// them in bf16 (by_bf16); `part`: for the sums in parts.
+hipError_t rows_grad(MmParams p, int dtype, bool by_bf16, float* part, const Launch& L) {
+  const bool f32 = dtype == TOPMOE_DTYPE_FP32;
+  auto product = [&](const MmParams& q, const Launch& s, bool parts) {
+    if (f32) return by_bf16 ? launch_mm_f32_by_bf16(q, s) : launch_mm_f32(kMmNN, q, s);
+    return parts ? launch_mm_bf16_parts(q, s) : launch_mm_bf16(kMmNN, q, s);
+  };
+  p.kchunk = mm_nn_chunk(p.R, p.N, p.K, p.E);
+  if (p.kchunk == 0) return product(p, L, false);
+  Launch first, second;
+  in_one(L, &first, &second);
+  MmParams q = p;
+  q.C = part;
+  q.ldc = p.N;
+  const hipError_t e = product(q, first, true);
+  if (e != hipSuccess) return e;
+  L.launched = true;
+  return launch_mm_sum_chunks(part, mm_chunks(p.K, p.kchunk), p.R, p.N, dtype, p.C, p.ldc, second);
+}
+size_t rows_grad_bytes(int64_t R, int64_t K, int64_t O, int E) {
+  const int kchunk = mm_nn_chunk(R, K, O, E);
+  return kchunk > 0 ? size_t(mm_chunks(O, kchunk)) * size_t(R) * size_t(K) * sizeof(float) : 0;
+}
+
 int mx4_shape(int64_t R, int64_t C) {
   if (R < 0 || R > kMaxRows || C <= 0 || C % 8 != 0 || C > kMaxRows) return TOPMOE_ERR_BAD_SHAPE;
   return TOPMOE_OK;
@@ -71,31 +103,48 @@ int moe_linear_fwd(const void* x, int64_t ldx, const void* w, const int32_t* exp
   return TOPMOE_OK;
 }
 
+size_t moe_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E) {
+  int32_t any = 0;
+  if (linear_shape(R, K, O, E, &any, 8) != TOPMOE_OK) return 0;
+  const size_t dx = rows_grad_bytes(R, K, O, E);
+  const size_t dw = size_t(mm_tn_parts(mm_tn_most(R, O, K, E), E)) * size_t(O) * size_t(K) * sizeof(float);
+  return align_up((dx > dw ? dx : dw) + 1);
+}
+
 int moe_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
                    const int32_t* expert_offsets, int64_t R, int64_t K, int64_t O, int E,
-                   int dtype, void* dx, int64_t lddx, void* dw, void* stream,
-                   void* const* stage_events) {
+                   int dtype, void* dx, int64_t lddx, void* dw, void* workspace,
+                   size_t workspace_bytes, void* stream, void* const* stage_events) {
   if (!known_dtype(dtype)) return TOPMOE_ERR_UNSUPPORTED_DTYPE;
   const int status = linear_shape(R, K, O, E, expert_offsets, 8);
   if (status != TOPMOE_OK) return status;
   if (!pitch_ok(lddy, O) || (dw && !pitch_ok(ldx, K)) || (dx && !pitch_ok(lddx, K)))
     return TOPMOE_ERR_BAD_SHAPE;
-  if ((!dx && !dw && R > 0) || (dx && !w) || (R > 0 && (!dy || (dw && !x)))) return TOPMOE_ERR_NULL_ARG;
+  if ((!dx && !dw && R > 0) || (dx && !w) || !workspace || (R > 0 && (!dy || (dw && !x))))
+    return TOPMOE_ERR_NULL_ARG;
+  if (workspace_bytes < moe_linear_bwd_workspace_bytes(R, K, O, E))
+    return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) ||
-      !aligned(dw, 16) || !aligned(expert_offsets, 4))
+      !aligned(dw, 16) || !aligned(expert_offsets, 4) || !aligned(workspace, 256))
     return TOPMOE_ERR_BAD_ARG;
   const Stages st{stage_events, static_cast<hipStream_t>(stream)};
   const Launch rows = st.at(0), weights = st.at(1);
   const bool f32 = dtype == TOPMOE_DTYPE_FP32;
-  if (dx && R > 0) {
-    const MmParams p = params(dy, lddy, w, expert_offsets, R, O, K, E, dx, lddx);
-    TOPMOE_TRY(f32 ? launch_mm_f32(kMmNN, p, rows) : launch_mm_bf16(kMmNN, p, rows));
-  }
+  float* part = static_cast<float*>(workspace);
+  if (dx && R > 0)
+    TOPMOE_TRY(rows_grad(params(dy, lddy, w, expert_offsets, R, O, K, E, dx, lddx), dtype, false,
+                         part, rows));
   if (dw) {
     MmParams p = params(dy, lddy, x, expert_offsets, R, 0, K, E, dw, K);
     p.M = int(O);
     p.ldb = ldx;
-    TOPMOE_TRY(f32 ? launch_mm_f32(kMmTN, p, weights) : launch_mm_bf16(kMmTN, p, weights));
+    p.most = mm_tn_most(R, O, K, E);
+    p.part = part;
+    Launch first = weights, second = weights;
+    if (p.most > 0) in_one(weights, &first, &second);
+    TOPMOE_TRY(f32 ? launch_mm_f32(kMmTN, p, first) : launch_mm_bf16(kMmTN, p, first));
+    weights.launched = true;
+    if (p.most > 0) TOPMOE_TRY(launch_mm_sum_rows(p, dtype, second));
   }
   TOPMOE_TRY(st.close(rows));
   TOPMOE_TRY(st.close(weights));
@@ -162,11 +211,10 @@ int mx4_linear_fwd(const void* x, int64_t ldx, const uint8_t* x_scale, int rows,
   return TOPMOE_OK;
 }
 
-size_t mx4_linear_bwd_workspace_bytes(int64_t K, int64_t O, int E) {
-  if (K <= 0 || K % kMx4Group != 0 || K > kMaxSide || O <= 0 || O % 8 != 0 || O > kMaxSide ||
-      E < 1 || E > kMmMaxExperts || int64_t(E) * O > kMaxOut)
-    return 0;
-  return align_up(size_t(E) * size_t(O) * size_t(K) * 2);
+size_t mx4_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E) {
+  int32_t any = 0;
+  if (linear_shape(R, K, O, E, &any, kMx4Group) != TOPMOE_OK) return 0;
+  return align_up(size_t(E) * size_t(O) * size_t(K) * 2) + align_up(rows_grad_bytes(R, K, O, E));
 }
 
 int mx4_linear_bwd(const void* dy, int64_t lddy, const uint8_t* wq, const uint8_t* w_scale,
@@ -179,7 +227,7 @@ int mx4_linear_bwd(const void* dy, int64_t lddy, const uint8_t* wq, const uint8_
   if (!pitch_ok(lddy, O) || !pitch_ok(lddx, K))
     return TOPMOE_ERR_BAD_SHAPE;
   if (!wq || !w_scale || !workspace || (R > 0 && (!dy || !dx))) return TOPMOE_ERR_NULL_ARG;
-  if (workspace_bytes < mx4_linear_bwd_workspace_bytes(K, O, E))
+  if (workspace_bytes < mx4_linear_bwd_workspace_bytes(R, K, O, E))
     return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(dy, 16) || !aligned(wq, 16) || !aligned(dx, 16) || !aligned(expert_offsets, 4) ||
       !aligned(workspace, 256))
@@ -189,9 +237,9 @@ int mx4_linear_bwd(const void* dy, int64_t lddy, const uint8_t* wq, const uint8_
   if (R > 0) {
     TOPMOE_TRY(launch_mx4_unpack(wq, w_scale, int64_t(E) * O, K, TOPMOE_DTYPE_BF16, workspace, K,
                                  unpack));
-    const MmParams p = params(dy, lddy, workspace, expert_offsets, R, O, K, E, dx, lddx);
-    TOPMOE_TRY(dtype == TOPMOE_DTYPE_FP32 ? launch_mm_f32_by_bf16(p, product)
-                                          : launch_mm_bf16(kMmNN, p, product));
+    char* part = static_cast<char*>(workspace) + align_up(size_t(E) * size_t(O) * size_t(K) * 2);
+    TOPMOE_TRY(rows_grad(params(dy, lddy, workspace, expert_offsets, R, O, K, E, dx, lddx), dtype,
+                         true, reinterpret_cast<float*>(part), product));
   }
   TOPMOE_TRY(st.close(unpack));
   TOPMOE_TRY(st.close(product));

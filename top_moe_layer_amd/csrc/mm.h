@@ -39,6 +39,12 @@ struct MmParams {
   int64_t R;
   int64_t lda, ldb, ldc;  // row pitches of A and C, and of B in TN (else B is dense)
   int E, M, N, K;         // M: TN only; K: NT and NN only
+  // Sums in parts, added up by launch_mm_sum: NN over chunks of kchunk of K
+  // (0: whole), C then being the parts [chunks, R, N] in fp32; TN over parts of
+  // an expert's rows, of most rows each (0: whole), those of experts with more
+  // than one going to part [.., M, N], expert by expert.
+  int kchunk, most;
+  float* part;
 };
 
 constexpr int kMmMaxExperts = 256;
@@ -58,6 +64,54 @@ hipError_t launch_mm_f32(MmLayout layout, const MmParams& p, const Launch& s);
 // kMmE4m3 (C bf16), kMmE4m3Bf (C fp32), kMmE2m1 (either).
 hipError_t launch_mm_mx4(int fa, bool out_bf16, const MmParams& p, const Launch& s);
 hipError_t launch_mm_f32_by_bf16(const MmParams& p, const Launch& s);
+// bf16 NN into fp32 parts.
+hipError_t launch_mm_bf16_parts(const MmParams& p, const Launch& s);
+
+// How the backward divides its sums.  NN: tiles of 64 x 128 fewer than half the
+// blocks that fit on the chip are multiplied by chunks of K, of 128 elements or
+// more (0: whole).  TN: an expert's rows, where some experts may have several
+// times the others' and experts are few, in parts of at most five fourths of an
+// average expert's rows (0: whole).
+inline int mm_nn_chunk(int64_t R, int64_t N, int64_t K, int E) {
+  const int64_t experts = E < R ? E : R;
+  if (experts <= 0) return 0;
+  const int64_t tiles = ((R + E - 1) / E + 63) / 64 * experts * ((N + 127) / 128);
+  int64_t chunks = 512 / tiles;
+  if (chunks > 16) chunks = 16;
+  if (chunks > K / 256) chunks = K / 256;
+  if (chunks < 2) return 0;
+  return int(((K + chunks - 1) / chunks + 127) / 128 * 128);
+}
+inline int64_t mm_chunks(int64_t K, int kchunk) { return kchunk > 0 ? (K + kchunk - 1) / kchunk : 1; }
+constexpr int kMmPartExperts = 64;  // lanes of a wavefront, which number the parts
+inline int mm_tn_most(int64_t R, int64_t M, int64_t N, int E) {
+  if (E < 2 || E > 16 || R / E < 256) return 0;
+  // (a gigabyte of parts at most)
+  if ((8 * int64_t(E) / 5 + 1) * M * N * 4 > int64_t(1) << 30) return 0;
+  return int((R / E * 5 / 4 + 31) / 32 * 32);
+}
+// Experts of two parts or more are at most 4 E / 5, and have at most one part more
+// than their rows / most each, of which all experts' are at most 4 E / 5.
+__host__ __device__ inline int64_t mm_tn_parts(int most, int E) {
+  return most > 0 ? 8 * int64_t(E) / 5 + 1 : 0;
+}
+// Units: an expert's parts, or its whole.
+__host__ __device__ inline int64_t mm_tn_units(int most, int E) {
+  return most > 0 ? E + 4 * int64_t(E) / 5 + 1 : E;
+}
+// Whether the experts with the longest sums start first; of short sums (E = 64,
+// 48 rows each, fp32 768 x 256) finding them costs more than it saves: 50 against
+// 32 us.
+__host__ __device__ inline bool mm_tn_sorted(int64_t R, int E) {
+  return E <= kMmPartExperts && R / E >= 256;
+}
+// Experts that go round the 8 XCDs once or twice are theirs as wholes.
+__host__ __device__ inline bool mm_tn_by_xcd(int E) { return E == 8 || E == 16; }
+// NN: out [R, N] = the sum of the chunks, rounded once to the dtype.
+hipError_t launch_mm_sum_chunks(const float* part, int64_t chunks, int64_t R, int64_t N, int dtype,
+                                void* out, int64_t ldo, const Launch& s);
+// TN: the experts of more than one part.
+hipError_t launch_mm_sum_rows(const MmParams& p, int dtype, const Launch& s);
 
 // ---- 4-bit values (mx4.hip): q [R, C / 2], scale [R, ceil(C / 32)], dense
 hipError_t launch_mx4_pack(const void* x, int64_t ldx, int64_t R, int64_t C, int dtype, uint8_t* q,

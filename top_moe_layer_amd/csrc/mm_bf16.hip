@@ -32,4 +32,8 @@ hipError_t launch_mm_bf16(MmLayout layout, const MmParams& p, const Launch& s) {
   return hipErrorInvalidValue;
 }
 
+hipError_t launch_mm_bf16_parts(const MmParams& p, const Launch& s) {
+  return mm::launch_tile<kMmNN, kMmBf16, kMmBf16, float, 64, 128, 2, 2, 2, 4>(p, s);
+}
+
 }  // namespace topmoe

@@ -252,20 +252,42 @@ __device__ __forceinline__ RowTile row_tile(int t, const int (&o)[5], int incl, 
   return r;
 }
 
-// The expert with the rank-th most rows (ties by number), so that the longest
-// sums start first; beyond 64 experts, where tiles are many and no expert's rows
-// are a large part of all, just the rank-th.
-__device__ __forceinline__ int by_rows(const int32_t* offsets, int E, int64_t R, int rank,
-                                       int lane) {
-  if (offsets == nullptr || E > 64) return rank;
+// The parts that an expert's `rows` are summed in, of `most` at most (0: one).
+__device__ __forceinline__ int parts_of(int rows, int most) {
+  return most > 0 && rows > most ? (rows + most - 1) / most : 1;
+}
+// (Up to 64 experts, one a lane.)  The expert and part that unit u is, longest
+// parts first, so that the longest sums start first, and the number of the part among those that are kept apart;
+// false past the last.
+struct RowPart {
+  int e, part, parts, slot;
+};
+__device__ __forceinline__ bool row_part(const int32_t* offsets, int E, int64_t R, int most, int u,
+                                         int lane, RowPart& out) {
   const int rows = lane < E ? offset_at(offsets, lane + 1, E, R) - offset_at(offsets, lane, E, R)
                             : -1;
-  int mine = 0;
-  for (int e = 0; e < E; ++e) {
-    const int other = __builtin_amdgcn_readlane(rows, e);
-    mine += other > rows || (other == rows && e < lane) ? 1 : 0;
+  const int parts = lane < E ? parts_of(rows, most) : 0;
+  const int kept = parts > 1 ? parts : 0;
+  const int slot = wave_inclusive_scan(kept, lane) - kept;
+  int before;  // units of experts that come first
+  if (!mm_tn_sorted(R, E)) {
+    before = wave_inclusive_scan(parts, lane) - parts;
+  } else {
+    const int len = parts > 0 ? (rows + parts - 1) / parts : -1;
+    before = 0;
+    for (int e = 0; e < E; ++e) {
+      const int other = __builtin_amdgcn_readlane(len, e), n = __builtin_amdgcn_readlane(parts, e);
+      before += other > len || (other == len && e < lane) ? n : 0;
+    }
   }
-  return __ffsll((long long)__ballot(lane < E && mine == rank)) - 1;
+  const uint64_t m = __ballot(lane < E && u >= before && u < before + parts);
+  if (m == 0) return false;
+  const int at = __ffsll((long long)m) - 1;
+  out.e = at;
+  out.part = u - __builtin_amdgcn_readlane(before, at);
+  out.parts = __builtin_amdgcn_readlane(parts, at);
+  out.slot = __builtin_amdgcn_readlane(slot, at) + out.part;
+  return out.parts == 1 || out.slot < mm_tn_parts(most, E);  // (offsets that do decrease)
 }
 
 // Elements of a K slice of Q sub-steps (an e2m1 matrix beside bf16 has four:
@@ -337,41 +359,74 @@ void mm_kernel(MmParams p) {
   const int64_t pitch_b = TN_ ? p.ldb * ESB
                               : TB ? int64_t(p.N) * ESB : int64_t(p.K) * mm_bits(FB) / 8;
 
-  // ---- the block's tiles.  Blocks go to the 8 XCDs round robin: XCD x takes
-  // the x-th eighth of the tiles (TN: of each expert's), in groups of GM row
-  // tiles, column by column, so that blocks running together share rows and
-  // matrix panels in its L2.  NT, NN: the grid's blocks of an XCD take its
-  // tiles in turn; TN, where an expert's rows are the length of its tiles: a
-  // block a tile.
+  // ---- the block's tiles.  Blocks go to the 8 XCDs round robin.  NT, NN: XCD x
+  // takes the x-th eighth of the tiles, in groups of GM row tiles, column by
+  // column, so that blocks running together share rows and matrix panels in its
+  // L2, and the grid's blocks of an XCD take its tiles in turn.  TN, where an
+  // expert's rows are the length of its tiles: a block a tile; each XCD takes
+  // whole experts (or parts of them), so that it reads their rows alone (16384
+  // tokens, top-2 of 8, 768 x 2432: 634 MB past the L2s where every XCD took an
+  // eighth of each expert's tiles, of 209 there are), or, where experts do not
+  // go round, such an eighth.
   constexpr int GM = 8;
   struct Tile {
     const char *a, *b;          // first bytes of the tile's rows and columns
     const uint8_t *sa, *sb;     // and of their scales
     int e, row0, n0, rows, cols, K, KT;  // KT: slices, whole rounds of the ring
+    int part;  // NN: the chunk of K; TN: the sum's number among the parts, or -1
   };
   const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+  constexpr bool CHUNKS = LAYOUT == kMmNN && sizeof(OT) == 4;
+  const int chunks = CHUNKS && p.kchunk > 0 ? (p.K + p.kchunk - 1) / p.kchunk : 1;
   int o[5], incl = 0, last = 0, mts, share, total, mine;
+  const int blocks = gridDim.x >> 3;
+  const bool by_xcd = TN_ && mm_tn_by_xcd(p.E);
   if constexpr (TN_) {
     mts = (p.M + BM - 1) / BM;
     total = mts * nt;
-    share = (total + 7) >> 3;
-    mine = local / share < p.E && xcd * share + local % share < total ? 1 : 0;
+    share = by_xcd ? total : (total + 7) >> 3;
+    const int units = int(mm_tn_units(p.most, p.E)), end = share * (by_xcd ? (units + 7) / 8 : units);
+    mine = local < end ? (end - local + blocks - 1) / blocks : 0;
   } else {
     if (p.offsets != nullptr) mts = row_tiles<BM>(p.offsets, p.E, p.R, lane, o, incl, last);
     else mts = int((p.R + BM - 1) / BM);
-    total = mts * nt;  // at most the tiles the grid was planned for
+    total = mts * nt * chunks;  // at most the tiles the grid was planned for
     share = (total + 7) >> 3;
     const int end = total - xcd * share < share ? total - xcd * share : share;
-    const int blocks = gridDim.x >> 3;
     mine = local < end ? (end - local + blocks - 1) / blocks : 0;
   }
   mine = __builtin_amdgcn_readfirstlane(mine);
+  // opaque: of a loop known to run once the compiler keeps 80 registers more
+  asm volatile("" : "+s"(mine));
   if (mine <= 0) return;
   auto tile = [&](int i) {
     Tile t;
     int at;
-    if constexpr (TN_) at = xcd * share + local % share;
-    else at = xcd * share + local + i * int(gridDim.x >> 3);
+    t.part = 0;
+    RowPart rp{};
+    bool any = true;  // TN: there is such a unit and tile
+    if constexpr (TN_) {
+      const int n = local + i * blocks, round = n / share;
+      // by XCD: back and forth over them
+      const int unit = !by_xcd ? round : 8 * round + (round & 1 ? 7 - xcd : xcd);
+      at = n - round * share + (by_xcd ? 0 : xcd * share);
+      any = at < total;
+      if (p.offsets == nullptr || p.E > kMmPartExperts) {  // one after the other, each whole
+        rp = RowPart{unit, 0, 1, 0};
+        any = any && unit < p.E;
+      } else {
+        any = row_part(p.offsets, p.E, p.R, p.most, unit, lane, rp) && any;
+      }
+      at = any ? at : 0;
+      t.part = rp.parts > 1 ? rp.slot : -1;
+    } else {
+      at = xcd * share + local + i * blocks;
+      if constexpr (CHUNKS) {
+        t.part = at / (mts * nt);
+        at -= t.part * (mts * nt);
+      }
+    }
+    t.part = __builtin_amdgcn_readfirstlane(t.part);
     const int first = at / (GM * nt) * GM, in = at - first * nt;
     const int gsz = mts - first < GM ? mts - first : GM;
     const int mt = first + in % gsz;
@@ -379,16 +434,18 @@ void mm_kernel(MmParams p) {
     t.cols = p.N - t.n0 < BN ? p.N - t.n0 : BN;
     int krow0 = 0;
     if constexpr (TN_) {
-      t.e = __builtin_amdgcn_readfirstlane(by_rows(p.offsets, p.E, p.R, local / share, lane));
+      t.e = __builtin_amdgcn_readfirstlane(rp.e);
       t.row0 = mt * BM;
-      t.rows = p.M - t.row0 < BM ? p.M - t.row0 : BM;
+      t.rows = !any ? 0 : p.M - t.row0 < BM ? p.M - t.row0 : BM;
       int o0 = 0, o1 = int(p.R);
       if (p.offsets != nullptr) {
         o0 = offset_at(p.offsets, t.e, p.E, p.R);
         o1 = offset_at(p.offsets, t.e + 1, p.E, p.R);
       }
-      krow0 = __builtin_amdgcn_readfirstlane(o0);
-      t.K = __builtin_amdgcn_readfirstlane(o1 > o0 ? o1 - o0 : 0);
+      const int n = any && o1 > o0 ? o1 - o0 : 0, len = any ? (n + rp.parts - 1) / rp.parts : 0;
+      const int left = n - rp.part * len;
+      krow0 = __builtin_amdgcn_readfirstlane(o0 + rp.part * len);
+      t.K = __builtin_amdgcn_readfirstlane(left < len ? (left > 0 ? left : 0) : len);
     } else if (p.offsets != nullptr) {
       const RowTile r = row_tile<BM>(mt, o, incl, last, p.E, p.R, lane);
       t.e = __builtin_amdgcn_readfirstlane(r.e);
@@ -403,14 +460,20 @@ void mm_kernel(MmParams p) {
     }
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
     t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    if constexpr (CHUNKS) {
+      if (p.kchunk > 0) {
+        krow0 = t.part * p.kchunk;
+        t.K = t.K - krow0 < p.kchunk ? (t.K > krow0 ? t.K - krow0 : 0) : p.kchunk;
+      }
+    }
     const int slices = (t.K + KS - 1) / KS;
     t.KT = slices > S ? (slices + S - 1) / S * S : S;
     t.a = static_cast<const char*>(p.A);
     t.b = static_cast<const char*>(p.B);
     if constexpr (TA) t.a += krow0 * pitch_a + int64_t(t.row0) * ESA;
-    else t.a += t.row0 * pitch_a;
+    else t.a += t.row0 * pitch_a + int64_t(krow0) * mm_bits(FA) / 8;
     if constexpr (TN_) t.b += krow0 * pitch_b + int64_t(t.n0) * ESB;
-    else if constexpr (TB) t.b += int64_t(t.e) * p.K * pitch_b + int64_t(t.n0) * ESB;
+    else if constexpr (TB) t.b += (int64_t(t.e) * p.K + krow0) * pitch_b + int64_t(t.n0) * ESB;
     else t.b += (int64_t(t.e) * p.N + t.n0) * pitch_b;
     t.sa = SA ? p.As + int64_t(t.row0) * (p.K / 32) : nullptr;
     t.sb = SB ? p.Bs + (int64_t(t.e) * p.N + t.n0) * (p.K / 32) : nullptr;
@@ -714,21 +777,28 @@ void mm_kernel(MmParams p) {
   // fr, column 8 (v / 4) + 4 fg + v % 4.  bf16: two swaps of half-wavefronts and
   // of rows of 16 lanes bring the 32 columns of a row to four lanes, 16 bytes in
   // each.
-  auto put = [&](const Tile& t, auto whole_tile) {
+  // `wide`: fp32 into the parts whatever the dtype (TN).
+  auto put = [&](const Tile& t, auto whole_tile, void* C, int64_t first, bool wide) {
     constexpr bool whole = decltype(whole_tile)::value;
     const int64_t ldc = TN_ ? p.N : p.ldc;
-    const int64_t first = TN_ ? int64_t(t.e) * p.M + t.row0 : int64_t(t.row0);
-    OT* out = static_cast<OT*>(p.C) + first * ldc + t.n0;
-    // opaque, so that no address is kept for the whole block
-    int r0 = wm + (sizeof(OT) == 2 ? lane & 15 : fr);
-    int c0 = wn + (sizeof(OT) == 2 ? 8 * (((lane >> 4) & 1) * 2 + fg) : 4 * fg);
-    asm volatile("" : "+v"(r0), "+v"(c0));
+    const int64_t start = first * ldc + t.n0;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         const f32x16& d = acc[i][j];
-        if constexpr (sizeof(OT) == 2) {
+        if (sizeof(OT) == 4 || wide) {
+          int r = wm + 32 * i + fr, c = wn + 32 * j + 4 * fg;
+          asm volatile("" : "+v"(r), "+v"(c));  // no address is kept for the whole block
+          float* o = static_cast<float*>(C) + start + (uint32_t(r) * uint32_t(ldc) + uint32_t(c));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (whole || (r < t.rows && c + 8 * q < t.cols))
+              *reinterpret_cast<f32x4*>(o + 8 * q) =
+                  f32x4{d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+        } else {
+          int r = wm + 32 * i + (lane & 15), c = wn + 32 * j + 8 * (((lane >> 4) & 1) * 2 + fg);
+          asm volatile("" : "+v"(r), "+v"(c));
           uint32_t w[8];  // columns 8 (k / 2) + 4 fg + 2 (k % 2) ..
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -741,21 +811,12 @@ void mm_kernel(MmParams p) {
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) swap16(w[k], w[4 + k]);
+          bf16_t* o = static_cast<bf16_t*>(C) + start + (uint32_t(r) * uint32_t(ldc) + uint32_t(c));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // rows 0-15, 16-31 of the piece
-            const int r = r0 + 32 * i + 16 * h, c = c0 + 32 * j;
-            if (whole || (r < t.rows && c < t.cols))
-              *reinterpret_cast<u32x4*>(out + (uint32_t(r) * uint32_t(ldc) + uint32_t(c))) =
+          for (int h = 0; h < 2; ++h)  // rows 0-15, 16-31 of the piece
+            if (whole || (r + 16 * h < t.rows && c < t.cols))
+              *reinterpret_cast<u32x4*>(o + 16 * h * ldc) =
                   u32x4{w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = r0 + 32 * i, c = c0 + 32 * j + 8 * q;
-            if (whole || (r < t.rows && c < t.cols))
-              *reinterpret_cast<f32x4*>(out + (uint32_t(r) * uint32_t(ldc) + uint32_t(c))) =
-                  f32x4{d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
-          }
         }
       }
     }
@@ -802,12 +863,16 @@ void mm_kernel(MmParams p) {
       }
     }
     if constexpr (MX) settle();
-    if (cur.rows == BM && cur.cols == BN) {
-      put(cur, std::true_type{});
-      stored = true;
+    const bool whole = cur.rows == BM && cur.cols == BN;
+    if constexpr (TN_) {
+      const bool part = cur.part >= 0;
+      put(cur, std::false_type{}, part ? static_cast<void*>(p.part) : p.C,
+          int64_t(part ? cur.part : cur.e) * p.M + cur.row0, part);
     } else {
-      put(cur, std::false_type{});
-      stored = false;
+      const int64_t first = (CHUNKS ? cur.part * p.R : 0) + cur.row0;
+      if (whole) put(cur, std::true_type{}, p.C, first, false);
+      else put(cur, std::false_type{}, p.C, first, false);
+      stored = whole;
     }
     cur = nxt;
   }
@@ -839,11 +904,14 @@ hipError_t launch_tile(const MmParams& p, const Launch& s) {
   auto kernel = mm_kernel<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>;
   int64_t grid;
   if (LAYOUT == kMmTN) {
-    grid = 8 * int64_t(p.E) * (((p.M + BM - 1) / BM * nt + 7) / 8);
+    const int64_t units = mm_tn_units(p.most, p.E);
+    const int64_t tiles = (p.M + BM - 1) / BM * nt;
+    grid = 8 * (mm_tn_by_xcd(p.E) ? (units + 7) / 8 * tiles : units * ((tiles + 7) / 8));
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
   } else {
     // row tiles at most: every expert's last one, and that of the rows of none, may be partial
     const int64_t full = p.R / BM, parts = p.offsets == nullptr ? 1 : int64_t(p.E) + 1;
-    const int64_t tiles = (full + (parts < p.R ? parts : p.R)) * nt;
+    const int64_t tiles = (full + (parts < p.R ? parts : p.R)) * nt * mm_chunks(p.K, p.kchunk);
     if (tiles > 0x7fffffff) return hipErrorInvalidValue;
     static int cached[64] = {};
     const int64_t cap = resident(kernel, 64 * Z::NW, cached) / 8 * 8;

@@ -5,6 +5,7 @@ caller's stream (the current one by default).  Nothing here computes any part of
 an operator."""
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional, Union
 
 import torch
@@ -74,12 +75,17 @@ def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor,
     return y
 
 
+@functools.lru_cache(maxsize=256)
+def moe_linear_bwd_workspace_bytes(R: int, K: int, O: int, E: int = 1) -> int:
+    return int(B.lib().moe_linear_bwd_workspace_bytes(R, K, O, E))
+
+
 @_on_kernel_stream
 def moe_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torch.Tensor],
                    expert_offsets: Optional[torch.Tensor] = None, *,
                    need_dx: bool = True, need_dw: bool = True,
                    dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
-                   stream=None, stage_events: Optional[B.StageEvents] = None) -> MoeLinearGrads:
+                   workspace: Optional[torch.Tensor] = None, stream=None, stage_events: Optional[B.StageEvents] = None) -> MoeLinearGrads:
     """Gradients of moe_linear_fwd for dy [R, O]: dx[r] = w[e]^T dy[r] (zeros in
     rows of no expert) and dw[e], the sum over e's rows of dy[r] x[r]^T (zeros
     for an expert without rows).  ``need_dx`` / ``need_dw``: what is not needed is
@@ -108,8 +114,11 @@ def moe_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torc
         dx = None
     if dx is None and dw is None:
         return MoeLinearGrads(None, None)
+    wp, wn, ws = _scratch(moe_linear_bwd_workspace_bytes(R, K, O, E), "moe_linear_bwd", dev,
+                          workspace)
     _call("moe_linear_bwd", dev, stage_events, dy.data_ptr(), lddy, _ptr(x) if need_dw else 0, ldx,
-          w.data_ptr(), _ptr(expert_offsets), R, K, O, E, code, _ptr(dx), lddx, _ptr(dw))
+          w.data_ptr(), _ptr(expert_offsets), R, K, O, E, code, _ptr(dx), lddx, _ptr(dw),
+          wp, wn)
     return MoeLinearGrads(dx, dw)
 
 
@@ -225,8 +234,9 @@ def _mx4_fwd(x, rows, w, expert_offsets, dtype, y, stage_events):
     return y
 
 
-def mx4_linear_bwd_workspace_bytes(K: int, O: int, E: int = 1) -> int:
-    return int(B.lib().mx4_linear_bwd_workspace_bytes(K, O, E))
+@functools.lru_cache(maxsize=256)
+def mx4_linear_bwd_workspace_bytes(R: int, K: int, O: int, E: int = 1) -> int:
+    return int(B.lib().mx4_linear_bwd_workspace_bytes(R, K, O, E))
 
 
 @_on_kernel_stream
@@ -244,7 +254,8 @@ def mx4_linear_bwd(dy: torch.Tensor, w: Mx4, expert_offsets: Optional[torch.Tens
     if wo != O:
         raise ValueError(f"dy has {O} channels, w {wo} rows")
     lddy = _pitched(dy, "dy", (R, O), dt, dev)
-    wp, wn, ws = _scratch(mx4_linear_bwd_workspace_bytes(K, O, E), "mx4_linear_bwd", dev, workspace)
+    wp, wn, ws = _scratch(mx4_linear_bwd_workspace_bytes(R, K, O, E), "mx4_linear_bwd", dev,
+                          workspace)
     dx, lddx = _output(dx, "dx", R, K, dt, dev)
     _call("mx4_linear_bwd", dev, stage_events, dy.data_ptr(), lddy, w.q.data_ptr(),
           w.scale.data_ptr(), _ptr(expert_offsets), R, K, O, E, code, dx.data_ptr(), lddx, wp, wn)
