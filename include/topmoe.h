@@ -585,7 +585,7 @@ int moe_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, con
  * byte, the first in the low half; scale the byte e + 127, e being the smallest
  * integer (at least -127) for which the group's largest magnitude is at most
  * 6 * 2^e (448 * 2^e in the 8-bit format above).  A value is thus kept within
- * max(x / 6, 2^e / 4) of itself.  A group with an element that is not finite has the
+ * max(|x| / 5, 2^e / 4) of itself.  A group with an element that is not finite has the
  * scale byte 255 and reads back as NaN.  Read back, 4 * 2^126 and more are
  * infinite.
  *   x [R, C] with a row pitch in elements (a multiple of 8); q [R, C / 2] and
