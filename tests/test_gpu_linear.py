@@ -62,6 +62,8 @@ LARGE = [  # 128 x 256 and 256 x 256 tiles, NT by O, NN by K; sums long enough f
     ([900, 40, 100], 60, 264, 520), ([2400, 0, 260, 300, 280, 310, 250, 1000], 100, 136, 72),
     ([300] * 15 + [1700], 0, 24, 40), ([20], 3, 64, 6464), ([5, 30, 0], 1, 1032, 1160),
     ([1500, 1700], 40, 264, 6152), ([1500, 1700], 0, 6152, 264),  # several tiles a block
+    ([1433, 621], 5, 2568, 2440), ([349, 251], 5, 2568, 2440),  # tiles of 256 x 256 and 128 x 256 for dw
+    ([5000], 9, 136, 264), ([4100, 0, 700], 20, 72, 40),  # parts that fill the CUs
 ]
 
 
@@ -111,7 +113,7 @@ def test_linear_one_matrix(env, dt):
     """Without offsets, [O, K] and [1, O, K]: all rows, nothing behind them."""
     dev, tm = env
     d = DT[dt]
-    for n, K, O in ((1, 64, 72), (50, 136, 40), (300, 72, 264)):
+    for n, K, O in ((1, 64, 72), (50, 136, 40), (300, 72, 264), (2600, 72, 40)):
         x, w, dy = rnd(1, n, K, dt=d), rnd(2, O, K, dt=d), rnd(3, n, O, dt=d)
         D = [t.to(dev) for t in (x, w, dy)]
         y = tm.moe_linear_fwd(D[0], D[1])
@@ -279,6 +281,9 @@ MX = [  # K in whole groups, tails of one to three groups behind slices of 4 and
     ([16, 15, 1], 3, 160, 1000), ([40] * 3, 5, 224, 72), ([130, 0, 65, 257, 5], 70, 352, 136),
     ([64, 128], 0, 128, 256), ([2] * 200, 7, 32, 16), ([700], 0, 64, 12808), ([300] * 4, 9, 416, 2568),
     ([30], 0, 1056, 512), ([700], 1, 96, 17608), ([1500, 1700], 0, 288, 6152),
+    # scales in whole words, and of each shape of tiles
+    ([130, 0, 65, 257, 5], 70, 384, 136), ([1500, 1700], 0, 256, 6152), ([600, 705], 9, 128, 6008),
+    ([1400, 1300], 30, 1152, 3592), ([300] * 4, 9, 1024, 4104),
 ]
 # 8-bit rows with y in bf16: of eight products each may lose what lies 2^-13 and less of the largest
 WINDOW = 8 * 2.0 ** -13
@@ -325,12 +330,13 @@ def test_mx4_linear(env, sizes, extra, K, O, kind):
         BR.check("dx", dx, ref, R.tol(ref, R.grouped(dy.double().abs(), wt.abs(), sizes), O, out))
 
 
+@pytest.mark.parametrize("K", [160, 256])
 @pytest.mark.parametrize("n", [1, 40, 300])
-def test_mx4_linear_scales(env, n):
+def test_mx4_linear_scales(env, n, K):
     """The scales' whole range: matrices of 2^-127 and up, a scale of NaN in one column and in one
     row, rows whose scales meet them."""
     dev, tm = env
-    K, O = 160, 72
+    O = 72
     g = torch.Generator().manual_seed(n)
     q = torch.randint(0, 256, (O, K // 2), generator=g, dtype=torch.int64).to(torch.uint8)
     s = (torch.arange(O * (K // 32)) * 7 % 250).reshape(O, K // 32).to(torch.uint8)
@@ -351,6 +357,31 @@ def test_mx4_linear_scales(env, n):
         assert bool(fine.any()) and torch.equal(y.cpu().isnan(), ref.isnan())
         BR.check("y", torch.where(fine, y.cpu().double(), 0.0), torch.where(fine, ref, 0.0),
                  torch.where(fine, R.tol(ref, mag, K, d), torch.tensor(0.0, dtype=torch.float64)))
+
+
+@pytest.mark.parametrize("n", [3, 70, 700])
+def test_mx4_linear_scales_at_any_address(env, n):
+    """Scales that begin at odd addresses, of rows and of matrices, change no bit."""
+    dev, tm = env
+    K, O = 256, 6152
+    p, W = tm.mx4_pack(rnd(1, n, K).to(dev)), tm.mx4_pack(rnd(2, O, K).to(dev))
+    a8 = tm.act8_pack(rnd(1, n, K).to(dev))
+
+    def moved(t, by):
+        big = torch.full((t.numel() + 64,), 255, dtype=torch.uint8, device=dev)
+        big[by:by + t.numel()] = t.reshape(-1)
+        return big[by:by + t.numel()].view(t.shape)
+
+    for x in (p, a8, rnd(1, n, K).to(dev), rnd(1, n, K).to(dev).bfloat16()):
+        for d in (torch.bfloat16, torch.float32):
+            if isinstance(x, torch.Tensor) and x.dtype != d:
+                continue
+            want = tm.mx4_linear_fwd(x, W, dtype=d)
+            for by in (1, 2, 4):
+                got = tm.mx4_linear_fwd(x, tm.Mx4(W.q, moved(W.scale, by)), dtype=d)
+                assert same(got, want)
+                if not isinstance(x, torch.Tensor):
+                    assert same(tm.mx4_linear_fwd(x._replace(scale=moved(x.scale, by)), W, dtype=d), want)
 
 
 @pytest.mark.parametrize("n", [2, 100])

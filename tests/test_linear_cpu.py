@@ -82,9 +82,11 @@ def test_workspaces():
     assert f(0, 64, 48, 4) > 0 and g(0, 64, 48, 4) >= 4 * 64 * 48 * 2
     # few tiles over a long sum: chunks of it, sixteen at most, of 128 elements or a multiple (512)
     assert f(20, 64, 6464, 1) == 13 * 20 * 64 * 4 + 256
-    # an average of 4096 rows each: 13 parts of dw at most
-    assert f(32768, 768, 2432, 8) == 13 * 768 * 2432 * 4 + 256
-    assert f(32768, 768, 2432, 1) == 256  # one expert: its rows are the average
+    # an average of 4096 rows each, 5120 a part: 6 experts have more, and 12 parts, at most
+    assert f(32768, 768, 2432, 8) == 12 * 768 * 2432 * 4 + 256
+    # one expert's 114 tiles of 128 x 128: four parts, and a fifth where they do not divide
+    assert f(32768, 768, 2432, 1) == 5 * 768 * 2432 * 4 + 256
+    assert f(16384, 768, 2432, 17) == 256
     assert f(1 << 20, 8192, 8192, 16) == 256  # parts of more than a gigabyte are not made
 
 

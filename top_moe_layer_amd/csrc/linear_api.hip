@@ -107,7 +107,7 @@ size_t moe_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E) {
   int32_t any = 0;
   if (linear_shape(R, K, O, E, &any, 8) != TOPMOE_OK) return 0;
   const size_t dx = rows_grad_bytes(R, K, O, E);
-  const size_t dw = size_t(mm_tn_parts(mm_tn_most(R, O, K, E), E)) * size_t(O) * size_t(K) * sizeof(float);
+  const size_t dw = size_t(mm_tn_parts(R, mm_tn_most(R, O, K, E), E)) * size_t(O) * size_t(K) * sizeof(float);
   return align_up((dx > dw ? dx : dw) + 1);
 }
 

@@ -58,6 +58,11 @@ inline int64_t mm_tiles(const MmParams& p, int64_t bm, int64_t bn) {
   return (mm_rows_each(p) + bm - 1) / bm * experts * ((p.N + bn - 1) / bn);
 }
 
+// TN: of one expert.
+inline int64_t mm_tn_tiles(const MmParams& p, int64_t bm, int64_t bn) {
+  return (p.M + bm - 1) / bm * ((p.N + bn - 1) / bn);
+}
+
 hipError_t launch_mm_bf16(MmLayout layout, const MmParams& p, const Launch& s);
 hipError_t launch_mm_f32(MmLayout layout, const MmParams& p, const Launch& s);
 // NT with a matrix in 4 bits (B, Bs); fa: kMmBf16 (C bf16), kMmF32Split (C fp32),
@@ -69,9 +74,15 @@ hipError_t launch_mm_bf16_parts(const MmParams& p, const Launch& s);
 
 // How the backward divides its sums.  NN: tiles of 64 x 128 fewer than half the
 // blocks that fit on the chip are multiplied by chunks of K, of 128 elements or
-// more (0: whole).  TN: an expert's rows, where some experts may have several
-// times the others' and experts are few, in parts of at most five fourths of an
-// average expert's rows (0: whole).
+// more (0: whole).  TN: an expert's rows, experts being few, are added up
+// in parts for one of two reasons (0: whole).  Tiles of 128 x 128 that leave CUs
+// without work: n parts, which save (1 - 1 / n) of an expert's rows at 10 ns
+// each, and cost 8 bytes an element to write and read, 1.6 ps; three or more, as
+// two save less than the launch that adds them up (E = 1, 768 x 2432, us with
+// parts and without: 4096 rows 34 and 42, of 1024 25 and 15 in four parts;
+// fp32 256 x 768, 4096 rows 27 and 73).  Experts with several times the others'
+// rows: parts of five fourths of the average (E = 8, 4096 rows on average, 9000
+// at most, 166 and 201; E = 16, 2048 182 and 185, E = 16, 1024 197 and 166).
 inline int mm_nn_chunk(int64_t R, int64_t N, int64_t K, int E) {
   const int64_t experts = E < R ? E : R;
   if (experts <= 0) return 0;
@@ -85,19 +96,29 @@ inline int mm_nn_chunk(int64_t R, int64_t N, int64_t K, int E) {
 inline int64_t mm_chunks(int64_t K, int kchunk) { return kchunk > 0 ? (K + kchunk - 1) / kchunk : 1; }
 constexpr int kMmPartExperts = 64;  // lanes of a wavefront, which number the parts
 inline int mm_tn_most(int64_t R, int64_t M, int64_t N, int E) {
-  if (E < 2 || E > 16 || R / E < 256) return 0;
+  const int64_t mean = R / E;
+  if (E > 16 || mean < 256) return 0;
+  const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128) * E;
+  int64_t parts = 1;
+  while (parts < 512 / tiles && (parts + 1) * (parts + 1) * E * M * N <= mean * 6400) ++parts;
+  int64_t most = (mean + parts - 1) / parts;
+  if (parts < 3) {
+    if (E < 2 || mean <= 2048) return 0;
+    most = mean * 5 / 4;
+  }
   // (a gigabyte of parts at most)
-  if ((8 * int64_t(E) / 5 + 1) * M * N * 4 > int64_t(1) << 30) return 0;
-  return int((R / E * 5 / 4 + 31) / 32 * 32);
+  if (2 * (R / most) * M * N * 4 > int64_t(1) << 30) return 0;
+  return int((most + 31) / 32 * 32);
 }
-// Experts of two parts or more are at most 4 E / 5, and have at most one part more
-// than their rows / most each, of which all experts' are at most 4 E / 5.
-__host__ __device__ inline int64_t mm_tn_parts(int most, int E) {
-  return most > 0 ? 8 * int64_t(E) / 5 + 1 : 0;
+// The parts kept: those of experts with more rows than `most`, of which there are
+// R / most at most; each has one part more than its rows / most at most.
+__host__ __device__ inline int64_t mm_tn_parts(int64_t R, int most, int E) {
+  const int64_t n = most > 0 ? R / most : 0;
+  return n + (n < E ? n : E);
 }
 // Units: an expert's parts, or its whole.
-__host__ __device__ inline int64_t mm_tn_units(int most, int E) {
-  return most > 0 ? E + 4 * int64_t(E) / 5 + 1 : E;
+__host__ __device__ inline int64_t mm_tn_units(int64_t R, int most, int E) {
+  return E + (most > 0 ? R / most : 0);
 }
 // Whether the experts with the longest sums start first; of short sums (E = 64,
 // 48 rows each, fp32 768 x 256) finding them costs more than it saves: 50 against

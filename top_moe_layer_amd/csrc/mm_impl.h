@@ -44,17 +44,39 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// (Out of the kernel templates, where a target builtin would suppress the host stub.)
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), short(0), int(bytes), 0x00020000);
+// The descriptor of `bytes` bytes from p on; both uniform.
+__device__ __forceinline__ u32x4 buffer(const char* p, uint32_t bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return u32x4{uint32_t(v), uint32_t(v >> 32) & 0xffffu, bytes, 0x00020000u};
 }
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
-                                           int(off), 0, 0, 0);
+// 16 bytes a lane into LDS, lane i's at lds + 16 i; out of a lane's bounds: zeros.
+// In assembly: of loads into LDS that it knows the compiler waits for all before
+// a transposing read, and before a read of LDS that they do not write.  So the
+// waits are this code's own: wait_loads and slot_barrier before a slot is read.
+// (The clobber of m0 is meant: the compiler sets it right before each own use.
+// One wait state between the write of m0 and its use, five between a vector
+// instruction that wrote the descriptor, a readfirstlane say, and its use.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16(u32x4 r, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(off), "s"(r) : "memory", "m0");
 }
-__device__ __forceinline__ u32x2 read_tr(const char* lds) {
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                       (__attribute__((address_space(3))) s16x4*)lds));
+// The same of 4 bytes a lane, lane i's at lds + 4 i.
+__device__ __forceinline__ void dma4(u32x4 r, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(off), "s"(r) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(3))) T* lds_at(uint32_t at) {
+  return reinterpret_cast<__attribute__((address_space(3))) T*>(at);
+}
+__device__ __forceinline__ u32x2 read_tr(uint32_t at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_at<s16x4>(at)));
 }
 // a's lanes 32-63 change places with b's lanes 0-31; a's odd rows of 16 lanes
 // with b's even ones.
@@ -172,28 +194,11 @@ __device__ __forceinline__ float scale_f32(uint32_t byte) {
                    : byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
 }
 
-// n words of scale bytes from kb on of a row of KB, zeros (2^-127) behind its end.
-template <int n>
-__device__ __forceinline__ void scale_words(const uint8_t* row, int kb, int KB, uint32_t (&w)[n]) {
-  typedef uint32_t __attribute__((aligned(1))) any;
-  if (kb + 4 * n <= KB) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) w[i] = *reinterpret_cast<const any*>(row + kb + 4 * i);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < n; ++i) {
-    w[i] = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (kb + 4 * i + j < KB) w[i] |= uint32_t(row[kb + 4 * i + j]) << (8 * j);
-  }
-}
-
 // The offsets' expert e, held inside [0, R] so that no row outside is touched
-// whatever the array holds; expert 0 starts at row 0.
+// whatever the array holds; expert 0 starts at row 0.  No offsets: one expert.
 __device__ __forceinline__ int offset_at(const int32_t* offsets, int e, int E, int64_t R) {
   if (e <= 0) return 0;
+  if (offsets == nullptr) return int(R);
   const int o = offsets[e < E ? e : E];
   return o < 0 ? 0 : o > R ? int(R) : o;
 }
@@ -287,7 +292,7 @@ __device__ __forceinline__ bool row_part(const int32_t* offsets, int E, int64_t 
   out.part = u - __builtin_amdgcn_readlane(before, at);
   out.parts = __builtin_amdgcn_readlane(parts, at);
   out.slot = __builtin_amdgcn_readlane(slot, at) + out.part;
-  return out.parts == 1 || out.slot < mm_tn_parts(most, E);  // (offsets that do decrease)
+  return out.parts == 1 || out.slot < mm_tn_parts(R, most, E);  // (offsets that do decrease)
 }
 
 // Elements of a K slice of Q sub-steps (an e2m1 matrix beside bf16 has four:
@@ -304,11 +309,16 @@ struct Shape {
   static constexpr int RBB = TB ? BN * mm_bits(FB) / 8 : KS * mm_bits(FB) / 8;
   static constexpr int ABYTES = BM * KS * mm_bits(FA) / 8, BBYTES = BN * KS * mm_bits(FB) / 8;
   static constexpr int STAGE = ABYTES + BBYTES;
+  // and the scales' tail, four bytes a row or column
+  static constexpr int SROWS = (mm_scaled(FA) ? BM : 0) + (mm_scaled(FB) ? BN : 0);
+  static constexpr int SLOT = STAGE + SROWS * 4;
   static constexpr int NW = WM * WN;
   static constexpr int LA = (ABYTES / 1024 + NW - 1) / NW, LB = (BBYTES / 1024 + NW - 1) / NW;
+  static constexpr int LS = (SROWS / 64 + NW - 1) / NW;
   // two blocks a CU where their rings fit, else one
-  static constexpr int WAVES = (2 * S * STAGE <= 160 * 1024 ? 2 : 1) * (NW > 4 ? NW / 4 : 1);  // a SIMD
-  static constexpr int LMIN = ABYTES / 1024 / NW + BBYTES / 1024 / NW;  // fewest loads of a wavefront
+  static constexpr int WAVES = (2 * S * SLOT <= 160 * 1024 ? 2 : 1) * (NW > 4 ? NW / 4 : 1);  // a SIMD
+  static constexpr int LMIN =  // fewest loads of a wavefront
+      ABYTES / 1024 / NW + BBYTES / 1024 / NW + SROWS / 64 / NW;
 };
 
 // Chunk position of row `row` in rows of RB bytes along K.
@@ -323,7 +333,9 @@ __device__ __forceinline__ int swz_t(int row) {
   return BITS == 16 ? (row & 3) * 4 : ((row >> 2) & 1) * 8;
 }
 
-template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int Q, int S>
+// W: the scales of a row lie at multiples of four bytes.
+template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int Q, int S,
+          bool W>
 __global__ __launch_bounds__(64 * WM * WN, (Shape<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>::WAVES))
 void mm_kernel(MmParams p) {
   using Z = Shape<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>;
@@ -338,17 +350,15 @@ void mm_kernel(MmParams p) {
   constexpr int LA = Z::LA, LB = Z::LB;
   constexpr int ESA = mm_bits(FA) / 8, ESB = mm_bits(FB) / 8;  // 0 for e2m1
   static_assert(WTM % 32 == 0 && WTN % 32 == 0 && (Q == 2 || Q == 4) && (!WQ || Q == 4), "tile shape");
-  static_assert(!(SA || SB) || S * KS / 32 <= 16, "scales of a round");
-  static_assert((S == 3 || S == 4) && S * STAGE <= 160 * 1024 && (S - 1) * (LA + LB) < 64, "ring");
+  static_assert(!(SA || SB) || KS == 128 || KS == 64, "scales of a slice");
+  static_assert(!(SA || SB) || (BM % 64 == 0 && BN % 64 == 0), "a load's scales are one operand's");
+  static_assert((S == 3 || S == 4) && S * Z::SLOT <= 160 * 1024 && (S - 1) * (LA + LB + Z::LS) < 64,
+                "ring");
   static_assert(!TA || FA == kMmBf16 || FA == kMmF32, "transposed rows");
   static_assert(!TB || FB == kMmBf16 || FB == kMmF32, "transposed matrix");
   static_assert(!TA || RBA % 256 == 0, "transposing reads take whole 256-byte windows");
   static_assert(!TB || RBB % 256 == 0, "transposing reads take whole 256-byte windows");
-  // One object per slot, so that reads of one are known not to touch another.
-  __shared__ __attribute__((aligned(1024))) char ring0[STAGE];
-  __shared__ __attribute__((aligned(1024))) char ring1[STAGE];
-  __shared__ __attribute__((aligned(1024))) char ring2[STAGE];
-  __shared__ __attribute__((aligned(1024))) char ring3[S > 3 ? STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char slots[S * Z::SLOT];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -385,7 +395,7 @@ void mm_kernel(MmParams p) {
     mts = (p.M + BM - 1) / BM;
     total = mts * nt;
     share = by_xcd ? total : (total + 7) >> 3;
-    const int units = int(mm_tn_units(p.most, p.E)), end = share * (by_xcd ? (units + 7) / 8 : units);
+    const int units = int(mm_tn_units(p.R, p.most, p.E)), end = share * (by_xcd ? (units + 7) / 8 : units);
     mine = local < end ? (end - local + blocks - 1) / blocks : 0;
   } else {
     if (p.offsets != nullptr) mts = row_tiles<BM>(p.offsets, p.E, p.R, lane, o, incl, last);
@@ -411,7 +421,7 @@ void mm_kernel(MmParams p) {
       const int unit = !by_xcd ? round : 8 * round + (round & 1 ? 7 - xcd : xcd);
       at = n - round * share + (by_xcd ? 0 : xcd * share);
       any = at < total;
-      if (p.offsets == nullptr || p.E > kMmPartExperts) {  // one after the other, each whole
+      if (p.E > kMmPartExperts) {  // one after the other, each whole
         rp = RowPart{unit, 0, 1, 0};
         any = any && unit < p.E;
       } else {
@@ -437,11 +447,8 @@ void mm_kernel(MmParams p) {
       t.e = __builtin_amdgcn_readfirstlane(rp.e);
       t.row0 = mt * BM;
       t.rows = !any ? 0 : p.M - t.row0 < BM ? p.M - t.row0 : BM;
-      int o0 = 0, o1 = int(p.R);
-      if (p.offsets != nullptr) {
-        o0 = offset_at(p.offsets, t.e, p.E, p.R);
-        o1 = offset_at(p.offsets, t.e + 1, p.E, p.R);
-      }
+      const int o0 = offset_at(p.offsets, t.e, p.E, p.R);
+      const int o1 = offset_at(p.offsets, t.e + 1, p.E, p.R);
       const int n = any && o1 > o0 ? o1 - o0 : 0, len = any ? (n + rp.parts - 1) / rp.parts : 0;
       const int left = n - rp.part * len;
       krow0 = __builtin_amdgcn_readfirstlane(o0 + rp.part * len);
@@ -490,6 +497,7 @@ void mm_kernel(MmParams p) {
                    : NW * 4 % (RBA / 16) == 0, "one chunk a lane");
   static_assert(TB ? (mm_bits(FB) == 16 ? NW * 1024 / RBB % 4 == 0 : NW * 1024 / RBB % 8 == 0)
                    : NW * 4 % (RBB / 16) == 0, "one chunk a lane");
+  const uint32_t ring = lds_address(slots);
   uint32_t off_a[LA], off_b[LB];
 #pragma unroll
   for (int i = 0; i < LA; ++i)
@@ -502,7 +510,7 @@ void mm_kernel(MmParams p) {
   // Across K the slice's last row ends the buffer and lanes past the last
   // column load from beyond it; along K it ends with the last row, and lanes
   // past K load from beyond.
-  auto issue = [&](const Tile& t, int kt, char* slot, int part) {
+  auto issue = [&](const Tile& t, int kt, uint32_t slot, int part) {
     int w = wid;  // opaque, so that the slots' addresses are added up here, not kept
     asm volatile("" : "+s"(w));
     const int left = t.K - kt * KS > 0 ? t.K - kt * KS : 0;  // elements
@@ -529,56 +537,55 @@ void mm_kernel(MmParams p) {
       }
     }
   };
-  auto issue_all = [&](const Tile& t, int kt, char* slot) {
+  // ---- scales: four bytes a row or column into the tail of the slice's slot,
+  // the slice's (KS = 128) or those of its pair of slices (64); zeros (2^-127)
+  // for rows past the tile's and, like all of the slice, past its K.  Scales
+  // that do not lie at multiples of four bytes (!W) take ordinary loads and
+  // stores, which wait for everything in flight.
+  constexpr int SROWS = Z::SROWS, PER = KS / 32;
+  auto issue_scales = [&](const Tile& t, int kt, uint32_t slot) {
+    const int KB = p.K / 32, left = t.K / 32 - kt * PER, kb = PER == 4 ? 4 * kt : 2 * kt & ~3;
+#pragma unroll
+    for (int i = 0; i < Z::LS; ++i) {
+      const int at = wid + NW * i;  // 64 rows or columns
+      if (SROWS / 64 % NW != 0 && at >= SROWS / 64) break;
+      const bool rows = SA && at < BM / 64;
+      const int x0 = rows ? at * 64 : at * 64 - (SA ? BM : 0), n = rows ? t.rows : t.cols;
+      const uint8_t* base = (rows ? t.sa : t.sb) + kb;
+      const uint32_t to = slot + STAGE + at * 256;
+      if constexpr (W) {
+        const uint32_t bytes = left > 0 ? uint32_t(n) * uint32_t(KB) - uint32_t(kb) : 0u;
+        dma4(buffer(reinterpret_cast<const char*>(base), bytes), to,
+             uint32_t(x0 + lane) * uint32_t(KB));
+      } else {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (x0 + lane < n && kb + j < t.K / 32)
+            w |= uint32_t(base[uint32_t(x0 + lane) * uint32_t(KB) + j]) << (8 * j);
+        *lds_at<uint32_t>(to + lane * 4) = w;
+      }
+    }
+  };
+  auto issue_all = [&](const Tile& t, int kt, uint32_t slot) {
 #pragma unroll
     for (int part = 0; part < Q; ++part) issue(t, kt, slot, part);
-  };
-
-  // ---- scales: those of a round of S slices go through registers into LDS (a
-  // row or column a thread), a round ahead, and a lane reads the bytes of its
-  // rows and columns slice by slice.
-  constexpr int NTHR = 64 * NW, SROWS = (SA ? BM : 0) + (SB ? BN : 0);
-  constexpr int SW = (S * KS / 32 + 3) / 4, SP = SW > 2 ? 16 : 8;  // words of a row; its bytes in LDS
-  constexpr int SR = (SROWS + NTHR - 1) / NTHR;                    // rows of a thread
-  __shared__ __attribute__((aligned(16))) char s_scale[SROWS > 0 ? 2 * SROWS * SP : 16];
-  uint32_t sword[SR > 0 ? SR : 1][SW];
-  int sturn = 0;  // the half of s_scale that the current round reads
-  auto fetch_scales = [&](const Tile& t, int kt) {
-    const int KB = t.K / 32;
-#pragma unroll
-    for (int i = 0; i < SR; ++i) {
-      const int x = tid + NTHR * i, c = SA ? x - BM : x;
-      const uint8_t* row = nullptr;
-      if (SA && x < BM) row = t.sa + uint32_t(x < t.rows ? x : t.rows - 1) * uint32_t(KB);
-      else if (SB) row = t.sb + uint32_t(c < t.cols ? c : t.cols - 1) * uint32_t(KB);
-      if (x < SROWS) scale_words<SW>(row, kt * (KS / 32), KB, sword[i]);
-    }
-  };
-  auto keep_scales = [&](int half) {
-#pragma unroll
-    for (int i = 0; i < SR; ++i) {
-      const int x = tid + NTHR * i;
-#pragma unroll
-      for (int w = 0; w < SW; ++w)
-        if (x < SROWS)
-          *reinterpret_cast<uint32_t*>(s_scale + half * SROWS * SP + x * SP + 4 * w) = sword[i][w];
-    }
+    if constexpr (Z::SROWS > 0) issue_scales(t, kt, slot);
   };
   uint32_t sc_a[SA ? TM : 1], sc_b[SB ? TN : 1];  // of the current slice
   uint32_t nx_a[SA ? TM : 1], nx_b[SB ? TN : 1];  // of the next one
-  auto read_scales = [&](int half, int slice) {
-    typedef typename std::conditional<SBYTES == 4, uint32_t, typename std::conditional<
-                                      SBYTES == 2, uint16_t, uint8_t>::type>::type word;
-    const char* at = s_scale + half * SROWS * SP + fr * SP + fg * SBYTES + slice * (KS / 32);
+  auto read_scales = [&](uint32_t slot, int kt) {  // of slice kt
+    typedef typename std::conditional<SBYTES == 2, uint16_t, uint8_t>::type word;
+    const uint32_t at = slot + STAGE + fr * 4 + fg * SBYTES + (PER == 2 ? 2 * (kt & 1) : 0);
     if constexpr (SA) {
 #pragma unroll
       for (int i = 0; i < TM; ++i)
-        nx_a[i] = *reinterpret_cast<const word*>(at + wm * SP + 32 * i * SP);
+        nx_a[i] = *lds_at<const word>(at + wm * 4 + 128 * i);
     }
     if constexpr (SB) {
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        nx_b[j] = *reinterpret_cast<const word*>(at + (wn + (SA ? BM : 0)) * SP + 32 * j * SP);
+        nx_b[j] = *lds_at<const word>(at + (wn + (SA ? BM : 0)) * 4 + 128 * j);
     }
   };
   auto take_scales = [&]() {
@@ -599,14 +606,14 @@ void mm_kernel(MmParams p) {
   //   bytes 16 fg .. of the two groups of 32 that lanes 0-31 and 32-63 scale.
   u32x4 fa[2][TM][PA], fb[2][TN];
   u32x4 raw_b[WQ ? TN : 1];
-  auto load_a = [&](const char* slot, int q, int buf) {
+  auto load_a = [&](uint32_t slot, int q, int buf) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       if constexpr (!TA) {
         const int z = swz<RBA>(fr);
-        const char* row = slot + (wm + fr) * RBA;
+        const uint32_t row = slot + (wm + fr) * RBA;
         auto chunk = [&](int c) {
-          return *reinterpret_cast<const u32x4*>(row + ((c ^ z) << 4) + 32 * i * RBA);
+          return *lds_at<const u32x4>(row + ((c ^ z) << 4) + 32 * i * RBA);
         };
         if constexpr (FA == kMmBf16) {
           fa[buf][i][0] = chunk(WQ ? 4 * fg + q : 2 * q + fg);
@@ -617,8 +624,8 @@ void mm_kernel(MmParams p) {
           fa[buf][i][0] = chunk(c);
           fa[buf][i][1] = chunk(c + 1);
         } else if constexpr (FA == kMmE4m3Bf) {
-          const u32x2 v = *reinterpret_cast<const u32x2*>(row + (((2 * fg + (q >> 1)) ^ z) << 4) +
-                                                          8 * (q & 1) + 32 * i * RBA);
+          const u32x2 v = *lds_at<const u32x2>(row + (((2 * fg + (q >> 1)) ^ z) << 4) + 8 * (q & 1) +
+                                               32 * i * RBA);
           fa[buf][i][0] = u32x4{v.x, v.y, 0u, 0u};
         } else if constexpr (FA == kMmE4m3) {
           fa[buf][i][0] = chunk(2 * q + fg);
@@ -628,28 +635,27 @@ void mm_kernel(MmParams p) {
         }
       } else if constexpr (FA == kMmBf16) {
         const int g = lane >> 4, l = lane & 15, u = ((wm / 32 + i) ^ (l >> 2)) * 64;
-        const char* at = slot + (16 * q + 8 * fg + (l >> 2)) * RBA + u + (g & 1) * 32 + (l & 3) * 8;
+        const uint32_t at = slot + (16 * q + 8 * fg + (l >> 2)) * RBA + u + (g & 1) * 32 + (l & 3) * 8;
         const u32x2 a = read_tr(at), b = read_tr(at + 4 * RBA);
         fa[buf][i][0] = u32x4{a.x, a.y, b.x, b.y};
       } else {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const int k = 8 * q + 4 * fg + s, c = (wm + 32 * i + fr) * 4;
-          fa[buf][i][0][s] = *reinterpret_cast<const uint32_t*>(
-              slot + k * RBA + (c ^ (swz_t<32>(k) << 4)));
+          fa[buf][i][0][s] = *lds_at<const uint32_t>(slot + k * RBA + (c ^ (swz_t<32>(k) << 4)));
         }
       }
     }
   };
-  auto load_b = [&](const char* slot0, int q, int buf) {
-    const char* slot = slot0 + Z::ABYTES;
+  auto load_b = [&](uint32_t slot0, int q, int buf) {
+    const uint32_t slot = slot0 + Z::ABYTES;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       if constexpr (!TB) {
         const int z = swz<RBB>(fr);
-        const char* row = slot + (wn + fr) * RBB;
+        const uint32_t row = slot + (wn + fr) * RBB;
         auto chunk = [&](int c) {
-          return *reinterpret_cast<const u32x4*>(row + ((c ^ z) << 4) + 32 * j * RBB);
+          return *lds_at<const u32x4>(row + ((c ^ z) << 4) + 32 * j * RBB);
         };
         if constexpr (WQ) {
           if (q == 0) raw_b[j] = chunk(fg);
@@ -660,15 +666,14 @@ void mm_kernel(MmParams p) {
         }
       } else if constexpr (FB == kMmBf16) {
         const int g = lane >> 4, l = lane & 15, u = ((wn / 32 + j) ^ (l >> 2)) * 64;
-        const char* at = slot + (16 * q + 8 * fg + (l >> 2)) * RBB + u + (g & 1) * 32 + (l & 3) * 8;
+        const uint32_t at = slot + (16 * q + 8 * fg + (l >> 2)) * RBB + u + (g & 1) * 32 + (l & 3) * 8;
         const u32x2 a = read_tr(at), b = read_tr(at + 4 * RBB);
         fb[buf][j] = u32x4{a.x, a.y, b.x, b.y};
       } else {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const int k = 8 * q + 4 * fg + s, c = (wn + 32 * j + fr) * 4;
-          fb[buf][j][s] = *reinterpret_cast<const uint32_t*>(
-              slot + k * RBB + (c ^ (swz_t<32>(k) << 4)));
+          fb[buf][j][s] = *lds_at<const uint32_t>(slot + k * RBB + (c ^ (swz_t<32>(k) << 4)));
         }
       }
     }
@@ -718,14 +723,18 @@ void mm_kernel(MmParams p) {
   };
   // One slice, read from `cur`, while slice `kt` of tile t goes into `free`, the
   // slot read before; the fragments of the next slice's first sub-step come
-  // from `nxt` under the last one's matrix instructions.  `slice`: its number in
-  // the round; the round's last puts the next round's scales away.  `stored`:
-  // the stores of a tile before may still be under way behind the loads that
-  // are waited for.
+  // from `nxt` under the last one's matrix instructions; `next`: its number.
+  // `stored`: the stores of a tile before may still be under way behind the
+  // loads that are waited for.
   constexpr int NST = sizeof(OT) == 2 ? TM * TN * 2 : TM * TN * 4;  // stores of a whole tile
   constexpr int BEHIND = (S - 2) * Z::LMIN, BEHIND_ST = BEHIND + NST < 63 ? BEHIND + NST : 63;
-  auto step = [&](const char* cur, const char* nxt, char* free, const Tile& t, int kt, int slice,
-                  bool stored) {
+  auto step = [&](int cur_slot, const Tile& t, int kt, int next, bool stored) {
+    uint32_t cur = ring + cur_slot * Z::SLOT, nxt = ring + (cur_slot + 1) % S * Z::SLOT;
+    const uint32_t free = ring + (cur_slot + S - 1) % S * Z::SLOT;
+    // opaque, so that addresses are added up here and not kept for every slot,
+    // which spilled 26 registers of 4-bit 256 x 256 tiles; 1 to 3 percent slower
+    // where nothing spills
+    if constexpr (MX) asm volatile("" : "+s"(cur), "+s"(nxt));
     auto sub = [&](auto qc) {
       constexpr int q = decltype(qc)::value;
       __builtin_amdgcn_sched_barrier(0);
@@ -737,16 +746,11 @@ void mm_kernel(MmParams p) {
         mma(qc, q & 1);
       } else {
         issue(t, kt, free, q);
-        if constexpr (SROWS > 0) {
-          if (slice + 1 == S) {
-            sturn ^= 1;
-            keep_scales(sturn);
-          }
-        }
+        if constexpr (SROWS > 0) issue_scales(t, kt, free);
         if (stored) wait_loads<BEHIND_ST>();
         else wait_loads<BEHIND>();
         slot_barrier();
-        if constexpr (SROWS > 0) read_scales(sturn, slice + 1 == S ? 0 : slice + 1);
+        if constexpr (SROWS > 0) read_scales(nxt, next);
         load_a(nxt, 0, 0);
         load_b(nxt, 0, 0);
         mma(qc, q & 1);
@@ -774,9 +778,8 @@ void mm_kernel(MmParams p) {
   };
 
   // ---- a tile's results.  Lane (fr, fg), register v of a 32 x 32 piece: row
-  // fr, column 8 (v / 4) + 4 fg + v % 4.  bf16: two swaps of half-wavefronts and
-  // of rows of 16 lanes bring the 32 columns of a row to four lanes, 16 bytes in
-  // each.
+  // fr, column 8 (v / 4) + 4 fg + v % 4.  Swaps of half-wavefronts (bf16) and of
+  // rows of 16 lanes bring 64 bytes of a row to four lanes, 16 in each.
   // `wide`: fp32 into the parts whatever the dtype (TN).
   auto put = [&](const Tile& t, auto whole_tile, void* C, int64_t first, bool wide) {
     constexpr bool whole = decltype(whole_tile)::value;
@@ -788,14 +791,24 @@ void mm_kernel(MmParams p) {
       for (int j = 0; j < TN; ++j) {
         const f32x16& d = acc[i][j];
         if (sizeof(OT) == 4 || wide) {
-          int r = wm + 32 * i + fr, c = wn + 32 * j + 4 * fg;
+          int r = wm + 32 * i + (lane & 15), c = wn + 32 * j + 8 * ((lane >> 4) & 1) + 4 * fg;
           asm volatile("" : "+v"(r), "+v"(c));  // no address is kept for the whole block
           float* o = static_cast<float*>(C) + start + (uint32_t(r) * uint32_t(ldc) + uint32_t(c));
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (whole || (r < t.rows && c + 8 * q < t.cols))
-              *reinterpret_cast<f32x4*>(o + 8 * q) =
-                  f32x4{d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+          for (int q = 0; q < 4; q += 2) {
+            uint32_t w[2][4];  // columns 8 q + 4 fg .. and 8 (q + 1) + 4 fg .. of row fr
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              w[0][k] = __float_as_uint(d[4 * q + k]);
+              w[1][k] = __float_as_uint(d[4 * q + 4 + k]);
+              swap16(w[0][k], w[1][k]);  // rows 0-15 of both, then rows 16-31
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (whole || (r + 16 * h < t.rows && c + 8 * q < t.cols))
+                *reinterpret_cast<u32x4*>(o + 16 * h * ldc + 8 * q) =
+                    u32x4{w[h][0], w[h][1], w[h][2], w[h][3]};
+          }
         } else {
           int r = wm + 32 * i + (lane & 15), c = wn + 32 * j + 8 * (((lane >> 4) & 1) * 2 + fg);
           asm volatile("" : "+v"(r), "+v"(c));
@@ -824,19 +837,14 @@ void mm_kernel(MmParams p) {
 
   // ---- the ring runs on from tile to tile: under a tile's last slices the
   // first ones of the next are loaded, and they arrive under its stores.
-  char* const ring[4] = {ring0, ring1, ring2, S > 3 ? ring3 : ring0};
   Tile cur = tile(0);
 #pragma unroll
-  for (int s = 0; s + 1 < S; ++s) issue_all(cur, s, ring[s]);
-  if constexpr (SROWS > 0) {
-    fetch_scales(cur, 0);
-    keep_scales(0);
-  }
+  for (int s = 0; s + 1 < S; ++s) issue_all(cur, s, ring + s * Z::SLOT);
   wait_loads<BEHIND>();
   slot_barrier();
-  if constexpr (SROWS > 0) read_scales(0, 0);
-  load_a(ring0, 0, 0);
-  load_b(ring0, 0, 0);
+  if constexpr (SROWS > 0) read_scales(ring, 0);
+  load_a(ring, 0, 0);
+  load_b(ring, 0, 0);
   if constexpr (SROWS > 0) take_scales();
   convert_b(0, 0);
   bool stored = false;
@@ -848,18 +856,17 @@ void mm_kernel(MmParams p) {
     for (int kt = 0; kt < cur.KT; kt += S) {
       const bool over = kt + S >= cur.KT;
       const bool st = stored && kt == 0;
-      if constexpr (SROWS > 0) fetch_scales(over ? nxt : cur, over ? 0 : kt + S);
-      step(ring0, ring1, ring[S - 1], cur, kt + S - 1, 0, st);
+      step(0, cur, kt + S - 1, kt + 1, st);
       Tile src = cur;
       if (over) src = nxt;
       const int at = over ? 0 : kt + S;
       if constexpr (S == 3) {
-        step(ring1, ring2, ring0, src, at, 1, false);
-        step(ring2, ring0, ring1, src, at + 1, 2, false);
+        step(1, src, at, kt + 2, false);
+        step(2, src, at + 1, at, false);
       } else {
-        step(ring1, ring2, ring0, src, at, 1, st);
-        step(ring2, ring3, ring1, src, at + 1, 2, false);
-        step(ring3, ring0, ring2, src, at + 2, 3, false);
+        step(1, src, at, kt + 2, st);
+        step(2, src, at + 1, kt + 3, false);
+        step(3, src, at + 2, at, false);
       }
     }
     if constexpr (MX) settle();
@@ -897,14 +904,15 @@ int resident(K kernel, int threads, int (&cached)[64]) {
   return cached[dev];
 }
 
-template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int Q, int S>
+template <int LAYOUT, int FA, int FB, typename OT, int BM, int BN, int WM, int WN, int Q, int S,
+          bool W = true>
 hipError_t launch_tile(const MmParams& p, const Launch& s) {
   using Z = Shape<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>;
   const int64_t nt = (p.N + BN - 1) / BN;
-  auto kernel = mm_kernel<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S>;
+  auto kernel = mm_kernel<LAYOUT, FA, FB, OT, BM, BN, WM, WN, Q, S, W>;
   int64_t grid;
   if (LAYOUT == kMmTN) {
-    const int64_t units = mm_tn_units(p.most, p.E);
+    const int64_t units = mm_tn_units(p.R, p.most, p.E);
     const int64_t tiles = (p.M + BM - 1) / BM * nt;
     grid = 8 * (mm_tn_by_xcd(p.E) ? (units + 7) / 8 * tiles : units * ((tiles + 7) / 8));
     if (grid > 0x7fffffff) return hipErrorInvalidValue;

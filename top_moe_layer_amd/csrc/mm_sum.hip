@@ -39,7 +39,7 @@ __global__ __launch_bounds__(256) void sum_rows_kernel(const float* __restrict__
   const int parts = mm::parts_of(rows, most), kept = parts > 1 ? parts : 0;
   const int before = wave_inclusive_scan(kept, lane) - kept;
   const int slot = __builtin_amdgcn_readlane(before, e);
-  const int room = int(mm_tn_parts(most, E)) - slot;  // all of them, unless offsets do decrease
+  const int room = int(mm_tn_parts(R, most, E)) - slot;  // all of them, unless offsets do decrease
   int n = __builtin_amdgcn_readlane(kept, e);
   n = n < room ? n : room;
   if (n <= 0) return;
