@@ -78,17 +78,17 @@ __device__ __forceinline__ __attribute__((address_space(3))) T* lds_at(uint32_t 
 __device__ __forceinline__ u32x2 read_tr(uint32_t at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_at<s16x4>(at)));
 }
-// a's lanes 32-63 change places with b's lanes 0-31; a's odd rows of 16 lanes
-// with b's even ones.
-__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
+// a's odd rows of 16 lanes change places with b's even ones; in each row of 16
+// lanes a's upper 8 lanes with b's lower 8.
 __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
   const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
   a = r[0];
   b = r[1];
+}
+__device__ __forceinline__ void swap8(uint32_t& a, uint32_t& b) {
+  const uint32_t x = a;  // row_ror:8 into the upper, into the lower banks
+  a = __builtin_amdgcn_update_dpp(x, b, 0x128, 0xf, 0xc, false);
+  b = __builtin_amdgcn_update_dpp(b, x, 0x128, 0xf, 0x3, false);
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -363,6 +363,9 @@ void mm_kernel(MmParams p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fr = lane & 31, fg = lane >> 5;
+  // The matrix's column that a lane loads, of 32: bits 2 and 3 of fr in turn, so
+  // that a lane's results are runs of eight columns.
+  const int fc = (fr & 0x13) | (fr & 4) << 1 | (fr & 8) >> 1;
   const int wm = (wid / WN) * WTM, wn = (wid % WN) * WTN;
   const int nt = (p.N + BN - 1) / BN;
   const int64_t pitch_a = TA ? p.lda * ESA : p.lda * mm_bits(FA) / 8;
@@ -576,16 +579,16 @@ void mm_kernel(MmParams p) {
   uint32_t nx_a[SA ? TM : 1], nx_b[SB ? TN : 1];  // of the next one
   auto read_scales = [&](uint32_t slot, int kt) {  // of slice kt
     typedef typename std::conditional<SBYTES == 2, uint16_t, uint8_t>::type word;
-    const uint32_t at = slot + STAGE + fr * 4 + fg * SBYTES + (PER == 2 ? 2 * (kt & 1) : 0);
+    const uint32_t at = slot + STAGE + fg * SBYTES + (PER == 2 ? 2 * (kt & 1) : 0);
     if constexpr (SA) {
 #pragma unroll
       for (int i = 0; i < TM; ++i)
-        nx_a[i] = *lds_at<const word>(at + wm * 4 + 128 * i);
+        nx_a[i] = *lds_at<const word>(at + (wm + fr) * 4 + 128 * i);
     }
     if constexpr (SB) {
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        nx_b[j] = *lds_at<const word>(at + (wn + (SA ? BM : 0)) * 4 + 128 * j);
+        nx_b[j] = *lds_at<const word>(at + (wn + fc + (SA ? BM : 0)) * 4 + 128 * j);
     }
   };
   auto take_scales = [&]() {
@@ -652,8 +655,8 @@ void mm_kernel(MmParams p) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       if constexpr (!TB) {
-        const int z = swz<RBB>(fr);
-        const uint32_t row = slot + (wn + fr) * RBB;
+        const int z = swz<RBB>(fc);
+        const uint32_t row = slot + (wn + fc) * RBB;
         auto chunk = [&](int c) {
           return *lds_at<const u32x4>(row + ((c ^ z) << 4) + 32 * j * RBB);
         };
@@ -666,13 +669,14 @@ void mm_kernel(MmParams p) {
         }
       } else if constexpr (FB == kMmBf16) {
         const int g = lane >> 4, l = lane & 15, u = ((wn / 32 + j) ^ (l >> 2)) * 64;
-        const uint32_t at = slot + (16 * q + 8 * fg + (l >> 2)) * RBB + u + (g & 1) * 32 + (l & 3) * 8;
+        const uint32_t at = slot + (16 * q + 8 * fg + (l >> 2)) * RBB + u + (g & 1) * 32 +
+                            (l & 1) * 16 + (l & 2) * 4;
         const u32x2 a = read_tr(at), b = read_tr(at + 4 * RBB);
         fb[buf][j] = u32x4{a.x, a.y, b.x, b.y};
       } else {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const int k = 8 * q + 4 * fg + s, c = (wn + 32 * j + fr) * 4;
+          const int k = 8 * q + 4 * fg + s, c = (wn + 32 * j + fc) * 4;
           fb[buf][j][s] = *lds_at<const uint32_t>(slot + k * RBB + (c ^ (swz_t<32>(k) << 4)));
         }
       }
@@ -687,7 +691,7 @@ void mm_kernel(MmParams p) {
   };
 
   // The matrix's columns are the instructions' rows, so that a lane ends with
-  // runs of four columns of one row.
+  // runs of columns of one row.
   f32x16 acc[TM][TN];
   auto clear = [&]() {
 #pragma unroll
@@ -777,59 +781,80 @@ void mm_kernel(MmParams p) {
     }
   };
 
-  // ---- a tile's results.  Lane (fr, fg), register v of a 32 x 32 piece: row
-  // fr, column 8 (v / 4) + 4 fg + v % 4.  Swaps of half-wavefronts (bf16) and of
-  // rows of 16 lanes bring 64 bytes of a row to four lanes, 16 in each.
+  // ---- a tile's results.  Lane (fr, fg), register 8 s + v of a 32 x 32 piece:
+  // row fr, column 16 s + 8 fg + v.  Swaps of rows of 16 and of 8 lanes bring
+  // 128 bytes of a row (64 of an odd bf16 piece) to the lanes of one store, 16
+  // in each: whole lines, which are written once, and past the L2's, where the
+  // rows and matrices of the tiles to come stay (bf16, 32768 rows, 768 -> 4864,
+  // and 4-bit rows, 16384 of 2048 -> 6464: 267 and 148 us; through the L2's 294
+  // and 174; halves of lines past them 301 and 161, through them 300 and 178).
   // `wide`: fp32 into the parts whatever the dtype (TN).
   auto put = [&](const Tile& t, auto whole_tile, void* C, int64_t first, bool wide) {
     constexpr bool whole = decltype(whole_tile)::value;
     const int64_t ldc = TN_ ? p.N : p.ldc;
     const int64_t start = first * ldc + t.n0;
+    const int b8 = (lane >> 3) & 1, b16 = (lane >> 4) & 1;
+    // a line of eight chunks of 16 bytes: w[a][b], of row fr, becomes that of row
+    // (lane & 7) + 8 a + 16 b, the lane's bits b8 and b16 the a and b it had
+    auto line = [&](uint32_t (&w)[2][2][4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) swap16(w[a][0][k], w[a][1][k]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) swap8(w[0][b][k], w[1][b][k]);
+      }
+    };
+    auto words = [&](const f32x16& d, int s, uint32_t (&w)[4]) {  // eight bf16
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(d[8 * s + 2 * k]),
+                                                   static_cast<__bf16>(d[8 * s + 2 * k + 1])});
+    };
+    auto store = [&](auto* o, const uint32_t (&w)[4]) {
+      __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(o));
+    };
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const f32x16& d = acc[i][j];
         if (sizeof(OT) == 4 || wide) {
-          int r = wm + 32 * i + (lane & 15), c = wn + 32 * j + 8 * ((lane >> 4) & 1) + 4 * fg;
+          int r = wm + 32 * i + (lane & 7), c = wn + 32 * j + 16 * b16 + 8 * fg + 4 * b8;
           asm volatile("" : "+v"(r), "+v"(c));  // no address is kept for the whole block
           float* o = static_cast<float*>(C) + start + (uint32_t(r) * uint32_t(ldc) + uint32_t(c));
+          uint32_t w[2][2][4];
 #pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            uint32_t w[2][4];  // columns 8 q + 4 fg .. and 8 (q + 1) + 4 fg .. of row fr
+          for (int v = 0; v < 16; ++v)
+            w[(v >> 2) & 1][v >> 3][v & 3] = __float_as_uint(acc[i][j][v]);
+          line(w);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              w[0][k] = __float_as_uint(d[4 * q + k]);
-              w[1][k] = __float_as_uint(d[4 * q + 4 + k]);
-              swap16(w[0][k], w[1][k]);  // rows 0-15 of both, then rows 16-31
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (whole || (r + 16 * h < t.rows && c + 8 * q < t.cols))
-                *reinterpret_cast<u32x4*>(o + 16 * h * ldc + 8 * q) =
-                    u32x4{w[h][0], w[h][1], w[h][2], w[h][3]};
-          }
-        } else {
-          int r = wm + 32 * i + (lane & 15), c = wn + 32 * j + 8 * (((lane >> 4) & 1) * 2 + fg);
+          for (int h = 0; h < 4; ++h)
+            if (whole || (r + 8 * h < t.rows && c < t.cols)) store(o + 8 * h * ldc, w[h & 1][h >> 1]);
+        } else if (j % 2 == 0 && j + 1 < TN) {
+          int r = wm + 32 * i + (lane & 7), c = wn + 32 * j + 32 * b8 + 16 * b16 + 8 * fg;
           asm volatile("" : "+v"(r), "+v"(c));
-          uint32_t w[8];  // columns 8 (k / 2) + 4 fg + 2 (k % 2) ..
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            w[k] = __builtin_bit_cast(
-                uint32_t, bf16x2{static_cast<__bf16>(d[2 * k]), static_cast<__bf16>(d[2 * k + 1])});
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            swap32(w[k], w[2 + k]);      // lanes 0-31: columns 0-7, 32-63: 8-15
-            swap32(w[4 + k], w[6 + k]);  // 16-23, 24-31
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) swap16(w[k], w[4 + k]);
           bf16_t* o = static_cast<bf16_t*>(C) + start + (uint32_t(r) * uint32_t(ldc) + uint32_t(c));
+          uint32_t w[2][2][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)  // rows 0-15, 16-31 of the piece
-            if (whole || (r + 16 * h < t.rows && c < t.cols))
-              *reinterpret_cast<u32x4*>(o + 16 * h * ldc) =
-                  u32x4{w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) words(acc[i][j + a < TN ? j + a : j], s, w[a][s]);
+          line(w);
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if (whole || (r + 8 * h < t.rows && c < t.cols)) store(o + 8 * h * ldc, w[h & 1][h >> 1]);
+        } else if (j % 2 == 0) {
+          int r = wm + 32 * i + (lane & 15), c = wn + 32 * j + 16 * b16 + 8 * fg;
+          asm volatile("" : "+v"(r), "+v"(c));
+          bf16_t* o = static_cast<bf16_t*>(C) + start + (uint32_t(r) * uint32_t(ldc) + uint32_t(c));
+          uint32_t w[2][4];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) words(acc[i][j], s, w[s]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) swap16(w[0][k], w[1][k]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (whole || (r + 16 * h < t.rows && c < t.cols)) store(o + 16 * h * ldc, w[h]);
         }
       }
     }
