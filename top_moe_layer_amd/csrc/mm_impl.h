@@ -354,6 +354,7 @@ void mm_kernel(MmParams p) {
   static_assert(!(SA || SB) || (BM % 64 == 0 && BN % 64 == 0), "a load's scales are one operand's");
   static_assert((S == 3 || S == 4) && S * Z::SLOT <= 160 * 1024 && (S - 1) * (LA + LB + Z::LS) < 64,
                 "ring");
+  static_assert(W || Z::SROWS / 64 < NW, "loads of scales are counted as loads into LDS");
   static_assert(!TA || FA == kMmBf16 || FA == kMmF32, "transposed rows");
   static_assert(!TB || FB == kMmBf16 || FB == kMmF32, "transposed matrix");
   static_assert(!TA || RBA % 256 == 0, "transposing reads take whole 256-byte windows");
@@ -508,14 +509,16 @@ void mm_kernel(MmParams p) {
 #pragma unroll
   for (int i = 0; i < LB; ++i)
     off_b[i] = uint32_t((row_b + i * NW * 1024 / RBB) * pitch_b) + chunk_b * 16;
-  // Slice kt of a tile into a slot, in Q parts, one under each sub-step's matrix
+  // Slice kt of a tile into a slot, in LA + LB loads, spread among the matrix
   // instructions; one past the tile's last is all zeros (an empty buffer).
   // Across K the slice's last row ends the buffer and lanes past the last
   // column load from beyond it; along K it ends with the last row, and lanes
   // past K load from beyond.
-  auto issue = [&](const Tile& t, int kt, uint32_t slot, int part) {
-    int w = wid;  // opaque, so that the slots' addresses are added up here, not kept
-    asm volatile("" : "+s"(w));
+  struct Source {
+    u32x4 ra, rb;
+    bool in_a, in_b;
+  };
+  auto source = [&](const Tile& t, int kt) {
     const int left = t.K - kt * KS > 0 ? t.K - kt * KS : 0;  // elements
     const int take = left < KS ? left : KS;
     const uint32_t rec_a =
@@ -524,20 +527,23 @@ void mm_kernel(MmParams p) {
     const uint32_t rec_b =
         TB ? uint32_t((take - 1) * pitch_b + t.cols * ESB)
            : uint32_t((t.cols - 1) * pitch_b) + uint32_t(int64_t(left) * mm_bits(FB) / 8);
-    const auto ra = buffer(t.a + (TA ? kt * KS * pitch_a : int64_t(kt) * RBA), left ? rec_a : 0u);
-    const auto rb = buffer(t.b + (TB ? kt * KS * pitch_b : int64_t(kt) * RBB), left ? rec_b : 0u);
-    const bool in_a = TA ? chunk_a * 16 < t.rows * ESA : chunk_a * 128 < take * mm_bits(FA);
-    const bool in_b = TB ? chunk_b * 16 < t.cols * ESB : chunk_b * 128 < take * mm_bits(FB);
-#pragma unroll
-    for (int l = part * (LA + LB) / Q; l < (part + 1) * (LA + LB) / Q; ++l) {
-      const int i = l < LA ? l : l - LA, blk = w + NW * i;
-      if (l < LA) {
-        if (Z::ABYTES / 1024 % NW == 0 || blk < Z::ABYTES / 1024)
-          dma16(ra, slot + blk * 1024, in_a ? off_a[i] : kBeyond);
-      } else {
-        if (Z::BBYTES / 1024 % NW == 0 || blk < Z::BBYTES / 1024)
-          dma16(rb, slot + Z::ABYTES + blk * 1024, in_b ? off_b[i] : kBeyond);
-      }
+    Source f;
+    f.ra = buffer(t.a + (TA ? kt * KS * pitch_a : int64_t(kt) * RBA), left ? rec_a : 0u);
+    f.rb = buffer(t.b + (TB ? kt * KS * pitch_b : int64_t(kt) * RBB), left ? rec_b : 0u);
+    f.in_a = TA ? chunk_a * 16 < t.rows * ESA : chunk_a * 128 < take * mm_bits(FA);
+    f.in_b = TB ? chunk_b * 16 < t.cols * ESB : chunk_b * 128 < take * mm_bits(FB);
+    return f;
+  };
+  auto issue = [&](const Source& f, uint32_t slot, int l) {
+    int w = wid;  // opaque, so that the slots' addresses are added up here, not kept
+    asm volatile("" : "+s"(w));
+    const int i = l < LA ? l : l - LA, blk = w + NW * i;
+    if (l < LA) {
+      if (Z::ABYTES / 1024 % NW == 0 || blk < Z::ABYTES / 1024)
+        dma16(f.ra, slot + blk * 1024, f.in_a ? off_a[i] : kBeyond);
+    } else {
+      if (Z::BBYTES / 1024 % NW == 0 || blk < Z::BBYTES / 1024)
+        dma16(f.rb, slot + Z::ABYTES + blk * 1024, f.in_b ? off_b[i] : kBeyond);
     }
   };
   // ---- scales: four bytes a row or column into the tail of the slice's slot,
@@ -571,8 +577,9 @@ void mm_kernel(MmParams p) {
     }
   };
   auto issue_all = [&](const Tile& t, int kt, uint32_t slot) {
+    const Source f = source(t, kt);
 #pragma unroll
-    for (int part = 0; part < Q; ++part) issue(t, kt, slot, part);
+    for (int l = 0; l < LA + LB; ++l) issue(f, slot, l);
     if constexpr (Z::SROWS > 0) issue_scales(t, kt, slot);
   };
   uint32_t sc_a[SA ? TM : 1], sc_b[SB ? TN : 1];  // of the current slice
@@ -609,85 +616,81 @@ void mm_kernel(MmParams p) {
   //   bytes 16 fg .. of the two groups of 32 that lanes 0-31 and 32-63 scale.
   u32x4 fa[2][TM][PA], fb[2][TN];
   u32x4 raw_b[WQ ? TN : 1];
-  auto load_a = [&](uint32_t slot, int q, int buf) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      if constexpr (!TA) {
-        const int z = swz<RBA>(fr);
-        const uint32_t row = slot + (wm + fr) * RBA;
-        auto chunk = [&](int c) {
-          return *lds_at<const u32x4>(row + ((c ^ z) << 4) + 32 * i * RBA);
-        };
-        if constexpr (FA == kMmBf16) {
-          fa[buf][i][0] = chunk(WQ ? 4 * fg + q : 2 * q + fg);
-        } else if constexpr (FA == kMmF32) {
-          fa[buf][i][0] = chunk(2 * q + fg);
-        } else if constexpr (FA == kMmF32Split) {
-          const int c = WQ ? 8 * fg + 2 * q : 4 * q + 2 * fg;
-          fa[buf][i][0] = chunk(c);
-          fa[buf][i][1] = chunk(c + 1);
-        } else if constexpr (FA == kMmE4m3Bf) {
-          const u32x2 v = *lds_at<const u32x2>(row + (((2 * fg + (q >> 1)) ^ z) << 4) + 8 * (q & 1) +
-                                               32 * i * RBA);
-          fa[buf][i][0] = u32x4{v.x, v.y, 0u, 0u};
-        } else if constexpr (FA == kMmE4m3) {
-          fa[buf][i][0] = chunk(2 * q + fg);
-          fa[buf][i][1] = chunk(2 * (Q + q) + fg);
-        } else {
-          fa[buf][i][0] = chunk(Q * fg + q);
-        }
-      } else if constexpr (FA == kMmBf16) {
-        const int g = lane >> 4, l = lane & 15, u = ((wm / 32 + i) ^ (l >> 2)) * 64;
-        const uint32_t at = slot + (16 * q + 8 * fg + (l >> 2)) * RBA + u + (g & 1) * 32 + (l & 3) * 8;
-        const u32x2 a = read_tr(at), b = read_tr(at + 4 * RBA);
-        fa[buf][i][0] = u32x4{a.x, a.y, b.x, b.y};
+  auto load_a = [&](uint32_t slot, int q, int buf, int i) {
+    if constexpr (!TA) {
+      const int z = swz<RBA>(fr);
+      const uint32_t row = slot + (wm + fr) * RBA;
+      auto chunk = [&](int c) {
+        return *lds_at<const u32x4>(row + ((c ^ z) << 4) + 32 * i * RBA);
+      };
+      if constexpr (FA == kMmBf16) {
+        fa[buf][i][0] = chunk(WQ ? 4 * fg + q : 2 * q + fg);
+      } else if constexpr (FA == kMmF32) {
+        fa[buf][i][0] = chunk(2 * q + fg);
+      } else if constexpr (FA == kMmF32Split) {
+        const int c = WQ ? 8 * fg + 2 * q : 4 * q + 2 * fg;
+        fa[buf][i][0] = chunk(c);
+        fa[buf][i][1] = chunk(c + 1);
+      } else if constexpr (FA == kMmE4m3Bf) {
+        const u32x2 v = *lds_at<const u32x2>(row + (((2 * fg + (q >> 1)) ^ z) << 4) + 8 * (q & 1) +
+                                             32 * i * RBA);
+        fa[buf][i][0] = u32x4{v.x, v.y, 0u, 0u};
+      } else if constexpr (FA == kMmE4m3) {
+        fa[buf][i][0] = chunk(2 * q + fg);
+        fa[buf][i][1] = chunk(2 * (Q + q) + fg);
       } else {
+        fa[buf][i][0] = chunk(Q * fg + q);
+      }
+    } else if constexpr (FA == kMmBf16) {
+      const int g = lane >> 4, l = lane & 15, u = ((wm / 32 + i) ^ (l >> 2)) * 64;
+      const uint32_t at = slot + (16 * q + 8 * fg + (l >> 2)) * RBA + u + (g & 1) * 32 + (l & 3) * 8;
+      const u32x2 a = read_tr(at), b = read_tr(at + 4 * RBA);
+      fa[buf][i][0] = u32x4{a.x, a.y, b.x, b.y};
+    } else {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int k = 8 * q + 4 * fg + s, c = (wm + 32 * i + fr) * 4;
-          fa[buf][i][0][s] = *lds_at<const uint32_t>(slot + k * RBA + (c ^ (swz_t<32>(k) << 4)));
-        }
+      for (int s = 0; s < 4; ++s) {
+        const int k = 8 * q + 4 * fg + s, c = (wm + 32 * i + fr) * 4;
+        fa[buf][i][0][s] = *lds_at<const uint32_t>(slot + k * RBA + (c ^ (swz_t<32>(k) << 4)));
       }
     }
   };
-  auto load_b = [&](uint32_t slot0, int q, int buf) {
+  auto load_b = [&](uint32_t slot0, int q, int buf, int j) {
     const uint32_t slot = slot0 + Z::ABYTES;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      if constexpr (!TB) {
-        const int z = swz<RBB>(fc);
-        const uint32_t row = slot + (wn + fc) * RBB;
-        auto chunk = [&](int c) {
-          return *lds_at<const u32x4>(row + ((c ^ z) << 4) + 32 * j * RBB);
-        };
-        if constexpr (WQ) {
-          if (q == 0) raw_b[j] = chunk(fg);
-        } else if constexpr (MX) {
-          fb[buf][j] = chunk(Q * fg + q);
-        } else {
-          fb[buf][j] = chunk(2 * q + fg);
-        }
-      } else if constexpr (FB == kMmBf16) {
-        const int g = lane >> 4, l = lane & 15, u = ((wn / 32 + j) ^ (l >> 2)) * 64;
-        const uint32_t at = slot + (16 * q + 8 * fg + (l >> 2)) * RBB + u + (g & 1) * 32 +
-                            (l & 1) * 16 + (l & 2) * 4;
-        const u32x2 a = read_tr(at), b = read_tr(at + 4 * RBB);
-        fb[buf][j] = u32x4{a.x, a.y, b.x, b.y};
+    if constexpr (!TB) {
+      const int z = swz<RBB>(fc);
+      const uint32_t row = slot + (wn + fc) * RBB;
+      auto chunk = [&](int c) {
+        return *lds_at<const u32x4>(row + ((c ^ z) << 4) + 32 * j * RBB);
+      };
+      if constexpr (WQ) {
+        if (q == 0) raw_b[j] = chunk(fg);
+      } else if constexpr (MX) {
+        fb[buf][j] = chunk(Q * fg + q);
       } else {
+        fb[buf][j] = chunk(2 * q + fg);
+      }
+    } else if constexpr (FB == kMmBf16) {
+      const int g = lane >> 4, l = lane & 15, u = ((wn / 32 + j) ^ (l >> 2)) * 64;
+      const uint32_t at = slot + (16 * q + 8 * fg + (l >> 2)) * RBB + u + (g & 1) * 32 +
+                          (l & 1) * 16 + (l & 2) * 4;
+      const u32x2 a = read_tr(at), b = read_tr(at + 4 * RBB);
+      fb[buf][j] = u32x4{a.x, a.y, b.x, b.y};
+    } else {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int k = 8 * q + 4 * fg + s, c = (wn + 32 * j + fc) * 4;
-          fb[buf][j][s] = *lds_at<const uint32_t>(slot + k * RBB + (c ^ (swz_t<32>(k) << 4)));
-        }
+      for (int s = 0; s < 4; ++s) {
+        const int k = 8 * q + 4 * fg + s, c = (wn + 32 * j + fc) * 4;
+        fb[buf][j][s] = *lds_at<const uint32_t>(slot + k * RBB + (c ^ (swz_t<32>(k) << 4)));
       }
     }
   };
-  auto convert_b = [&](int q, int buf) {  // e2m1 to bf16
-    if constexpr (WQ) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        fb[buf][j] = bf16_of_e2m1x8(raw_b[j][q], __uint_as_float(sc_b[j]));
-    }
+  auto convert_b = [&](int q, int buf, int j) {  // e2m1 to bf16
+    if constexpr (WQ) fb[buf][j] = bf16_of_e2m1x8(raw_b[j][q], __uint_as_float(sc_b[j]));
+  };
+  // The loads of a sub-step's fragments in the order of their first use.
+  auto load = [&](uint32_t slot, int q, int buf, int l) {
+    if (l == 0) load_a(slot, q, buf, 0);
+    else if (l <= TN) load_b(slot, q, buf, l - 1);
+    else load_a(slot, q, buf, l - TN);
   };
 
   // The matrix's columns are the instructions' rows, so that a lane ends with
@@ -701,65 +704,77 @@ void mm_kernel(MmParams p) {
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
   };
-  auto mma = [&](auto qc, int buf) {
+  u32x4 part[NS];  // of the row fragment in use
+  auto mma = [&](auto qc, int buf, int i, int j) {
     constexpr int q = decltype(qc)::value;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      u32x4 part[NS];
+    if (j == 0) {
       if constexpr (FA == kMmF32Split) split3(fa[buf][i][0], fa[buf][i][PA - 1], part);
       else if constexpr (FA == kMmE4m3Bf)
         part[0] = bf16_of_e4m3x8(fa[buf][i][0][0], fa[buf][i][0][1], __uint_as_float(sc_a[i]));
       else part[0] = fa[buf][i][0];
+    }
+    if constexpr (MX) {
+      mfma_mx<FA == kMmE4m3 ? 0 : 4, q>(fb[buf][j], fa[buf][i][0], fa[buf][i][PA - 1], acc[i][j],
+                                        sc_b[j], sc_a[i]);
+    } else if constexpr (F32) {
+      acc[i][j] = mfma_f32(fb[buf][j], part[0], acc[i][j]);
+    } else {
+      // the smallest part first
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        if constexpr (MX) {
-          mfma_mx<FA == kMmE4m3 ? 0 : 4, q>(fb[buf][j], fa[buf][i][0], fa[buf][i][PA - 1],
-                                            acc[i][j], sc_b[j], sc_a[i]);
-        } else if constexpr (F32) {
-          acc[i][j] = mfma_f32(fb[buf][j], part[0], acc[i][j]);
-        } else {
-          // the smallest part first
-#pragma unroll
-          for (int s = NS - 1; s >= 0; --s) acc[i][j] = mfma_bf16(fb[buf][j], part[s], acc[i][j]);
-        }
-      }
+      for (int s = NS - 1; s >= 0; --s) acc[i][j] = mfma_bf16(fb[buf][j], part[s], acc[i][j]);
     }
   };
-  // One slice, read from `cur`, while slice `kt` of tile t goes into `free`, the
-  // slot read before; the fragments of the next slice's first sub-step come
-  // from `nxt` under the last one's matrix instructions; `next`: its number.
+  // One slice, read from slot C, while slice `kt` of tile t goes into the slot
+  // read before; the fragments of the next slice's first sub-step come from the
+  // next slot under the last one's matrix instructions; `next`: its number.
+  // The loads are spread over all sub-steps, so that wavefronts do not queue for
+  // the address unit; those of the last come behind the wait and the barrier.
   // `stored`: the stores of a tile before may still be under way behind the
   // loads that are waited for.
   constexpr int NST = sizeof(OT) == 2 ? TM * TN * 2 : TM * TN * 4;  // stores of a whole tile
-  constexpr int BEHIND = (S - 2) * Z::LMIN, BEHIND_ST = BEHIND + NST < 63 ? BEHIND + NST : 63;
-  auto step = [&](int cur_slot, const Tile& t, int kt, int next, bool stored) {
-    uint32_t cur = ring + cur_slot * Z::SLOT, nxt = ring + (cur_slot + 1) % S * Z::SLOT;
-    const uint32_t free = ring + (cur_slot + S - 1) % S * Z::SLOT;
+  constexpr int LAST_LOADS = LA + LB - (Q - 1) * (LA + LB) / Q;
+  constexpr int WAIT = (S - 2) * Z::LMIN > LAST_LOADS ? (S - 2) * Z::LMIN - LAST_LOADS : 0;
+  constexpr int WAIT_ST = WAIT + NST < 63 ? WAIT + NST : 63;
+  auto step = [&](auto slot_number, const Tile& t, int kt, int next, bool stored) {
+    constexpr int C = decltype(slot_number)::value;
+    uint32_t cur = ring + C * Z::SLOT, nxt = ring + (C + 1) % S * Z::SLOT;
+    const uint32_t free = ring + (C + S - 1) % S * Z::SLOT;
     // opaque, so that addresses are added up here and not kept for every slot,
     // which spilled 26 registers of 4-bit 256 x 256 tiles; 1 to 3 percent slower
     // where nothing spills
     if constexpr (MX) asm volatile("" : "+s"(cur), "+s"(nxt));
+    const Source f = source(t, kt);
     auto sub = [&](auto qc) {
-      constexpr int q = decltype(qc)::value;
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (q + 1 < Q) {
-        load_a(cur, q + 1, (q + 1) & 1);
-        load_b(cur, q + 1, (q + 1) & 1);
-        issue(t, kt, free, q);
-        convert_b(q + 1, (q + 1) & 1);
-        mma(qc, q & 1);
-      } else {
-        issue(t, kt, free, q);
+      constexpr int q = decltype(qc)::value, NM = TM * TN, NL = TM + TN;
+      constexpr bool LAST = q + 1 == Q;
+      constexpr int D0 = q * (LA + LB) / Q, ND = (q + 1) * (LA + LB) / Q - D0;
+      if constexpr (LAST) {
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (SROWS > 0) issue_scales(t, kt, free);
-        if (stored) wait_loads<BEHIND_ST>();
-        else wait_loads<BEHIND>();
+        if (stored) wait_loads<WAIT_ST>();
+        else wait_loads<WAIT>();
         slot_barrier();
         if constexpr (SROWS > 0) read_scales(nxt, next);
-        load_a(nxt, 0, 0);
-        load_b(nxt, 0, 0);
-        mma(qc, q & 1);
+      }
+      // behind each matrix instruction a part of the other work
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        __builtin_amdgcn_sched_barrier(0);
+        mma(qc, q & 1, m / TN, m % TN);
+#pragma unroll
+        for (int l = m * NL / NM; l < (m + 1) * NL / NM; ++l)
+          load(LAST ? nxt : cur, LAST ? 0 : q + 1, (q + 1) & 1, l);
+#pragma unroll
+        for (int l = m * ND / NM; l < (m + 1) * ND / NM; ++l) issue(f, free, D0 + l);
+        if constexpr (!LAST) {
+#pragma unroll
+          for (int j = m * TN / NM; j < (m + 1) * TN / NM; ++j) convert_b(q + 1, (q + 1) & 1, j);
+        }
+      }
+      if constexpr (LAST) {
         if constexpr (SROWS > 0) take_scales();
-        convert_b(0, 0);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) convert_b(0, 0, j);
       }
     };
     sub(std::integral_constant<int, 0>{});
@@ -865,13 +880,14 @@ void mm_kernel(MmParams p) {
   Tile cur = tile(0);
 #pragma unroll
   for (int s = 0; s + 1 < S; ++s) issue_all(cur, s, ring + s * Z::SLOT);
-  wait_loads<BEHIND>();
+  wait_loads<(S - 2) * Z::LMIN>();
   slot_barrier();
   if constexpr (SROWS > 0) read_scales(ring, 0);
-  load_a(ring, 0, 0);
-  load_b(ring, 0, 0);
+#pragma unroll
+  for (int l = 0; l < TM + TN; ++l) load(ring, 0, 0, l);
   if constexpr (SROWS > 0) take_scales();
-  convert_b(0, 0);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) convert_b(0, 0, j);
   bool stored = false;
   for (int i = 0; i < mine; ++i) {
     Tile nxt = cur;
@@ -881,17 +897,21 @@ void mm_kernel(MmParams p) {
     for (int kt = 0; kt < cur.KT; kt += S) {
       const bool over = kt + S >= cur.KT;
       const bool st = stored && kt == 0;
-      step(0, cur, kt + S - 1, kt + 1, st);
       Tile src = cur;
       if (over) src = nxt;
       const int at = over ? 0 : kt + S;
+      constexpr std::integral_constant<int, 0> c0{};
+      constexpr std::integral_constant<int, 1> c1{};
+      constexpr std::integral_constant<int, 2> c2{};
+      step(c0, cur, kt + S - 1, kt + 1, st);
       if constexpr (S == 3) {
-        step(1, src, at, kt + 2, false);
-        step(2, src, at + 1, at, false);
+        step(c1, src, at, kt + 2, false);
+        step(c2, src, at + 1, at, false);
       } else {
-        step(1, src, at, kt + 2, st);
-        step(2, src, at + 1, kt + 3, false);
-        step(3, src, at + 2, at, false);
+        constexpr std::integral_constant<int, 3> c3{};
+        step(c1, src, at, kt + 2, st);
+        step(c2, src, at + 1, kt + 3, false);
+        step(c3, src, at + 2, at, false);
       }
     }
     if constexpr (MX) settle();
