@@ -5,6 +5,8 @@
 //     33.6, 32.1, 28.2; 512: 69.3, 51.3, 56; 2048: 219, 159, 157;  E = 16, 2048 -> 1408  64:
 //     26.2, 42.4, 42.2; 256: 56, 49.4, 58.2; 512: 101, 76.2, 64.3; 2048: 324, 251, 233;  E = 1,
 //     2048 -> 6464  256: 15.5, 35.6, 43.1; 1024: 42, 40.3, 45.4; 2048: 77.1, 68.9, 54.5
+//   64 x 128 and 64 x 64: E = 8, 64 rows 15.6 and 17.2; E = 16, 32 rows 23 and 20.8,
+//     128 rows 32.5 and 39.2; E = 1, 128 rows 16.6 and 10.6
 //   dx of the same, 64 x 128, 128 x 256, 256 x 256 (E = 8, E = 16):  256: 32.3, 73.8,
 //     99.7, 58.9, 53.7, 45.3; 1024: 128, 97.5, 124, 176, 127, 125; 2048: 219, 148, 135, 314, 218, 220
 //   dW, 128 x 128, 128 x 256, 256 x 256, rows an expert all alike: E = 8, 768 x 2432
@@ -27,11 +29,13 @@ hipError_t launch_mm_bf16(MmLayout layout, const MmParams& p, const Launch& s) {
         return launch_few<kMmBf16, kMmBf16, bf16_t, 1, 2, 8>(p, s);
       if (large) return launch_tile<kMmNT, kMmBf16, kMmBf16, bf16_t, 256, 256, 2, 4, 2, 4>(p, s);
       if (mid) return launch_tile<kMmNT, kMmBf16, kMmBf16, bf16_t, 128, 256, 2, 2, 2, 3>(p, s);
+      if (mm_tiles(p, 64, 128) >= 256)
+        return launch_tile<kMmNT, kMmBf16, kMmBf16, bf16_t, 64, 128, 2, 2, 4, 3>(p, s);
       return launch_tile<kMmNT, kMmBf16, kMmBf16, bf16_t, 64, 64, 2, 2, 4, 4>(p, s);
     case kMmNN:
       if (large) return launch_tile<kMmNN, kMmBf16, kMmBf16, bf16_t, 256, 256, 2, 4, 2, 4>(p, s);
       if (mid) return launch_tile<kMmNN, kMmBf16, kMmBf16, bf16_t, 128, 256, 2, 2, 2, 3>(p, s);
-      return launch_tile<kMmNN, kMmBf16, kMmBf16, bf16_t, 64, 128, 2, 2, 2, 4>(p, s);
+      return launch_tile<kMmNN, kMmBf16, kMmBf16, bf16_t, 64, 128, 2, 2, 4, 3>(p, s);
     case kMmTN: {
       const int64_t sums = p.most > 0 && p.R / p.most > p.E ? p.R / p.most : p.E;
       if (mm_tn_tiles(p, 256, 256) * sums >= 200 && p.R / p.E >= 1024)
@@ -45,7 +49,7 @@ hipError_t launch_mm_bf16(MmLayout layout, const MmParams& p, const Launch& s) {
 }
 
 hipError_t launch_mm_bf16_parts(const MmParams& p, const Launch& s) {
-  return mm::launch_tile<kMmNN, kMmBf16, kMmBf16, float, 64, 128, 2, 2, 2, 4>(p, s);
+  return mm::launch_tile<kMmNN, kMmBf16, kMmBf16, float, 64, 128, 2, 2, 4, 3>(p, s);
 }
 
 }  // namespace topmoe

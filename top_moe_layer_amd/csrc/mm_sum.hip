@@ -27,7 +27,7 @@ __global__ __launch_bounds__(256) void sum_chunks_kernel(const float* __restrict
   }
 }
 
-// A block takes 1024 elements of an expert that has several parts.
+// An expert that has several parts, 1024 elements a block and round.
 template <typename T>
 __global__ __launch_bounds__(256) void sum_rows_kernel(const float* __restrict__ part,
                                                        const int32_t* __restrict__ offsets, int E,
@@ -43,17 +43,18 @@ __global__ __launch_bounds__(256) void sum_rows_kernel(const float* __restrict__
   int n = __builtin_amdgcn_readlane(kept, e);
   n = n < room ? n : room;
   if (n <= 0) return;
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= MN) return;
-  const float* p = part + slot * MN + i;
-  f32x4 s = load_vec<true, f32x4>(p);
-  for (int c = 1; c < n; ++c) {
-    const f32x4 v = load_vec<true, f32x4>(p + c * MN);
+  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < MN;
+       i += int64_t(gridDim.x) * 1024) {
+    const float* p = part + slot * MN + i;
+    f32x4 s = load_vec<true, f32x4>(p);
+    for (int c = 1; c < n; ++c) {
+      const f32x4 v = load_vec<true, f32x4>(p + c * MN);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) s[w] += v[w];
+      for (int w = 0; w < 4; ++w) s[w] += v[w];
+    }
+    const float v[4] = {s[0], s[1], s[2], s[3]};
+    store4<T>(out + e * MN + i, v);
   }
-  const float v[4] = {s[0], s[1], s[2], s[3]};
-  store4<T>(out + e * MN + i, v);
 }
 
 }  // namespace
@@ -71,7 +72,9 @@ hipError_t launch_mm_sum_chunks(const float* part, int64_t chunks, int64_t R, in
 
 hipError_t launch_mm_sum_rows(const MmParams& p, int dtype, const Launch& s) {
   const int64_t MN = int64_t(p.M) * p.N;
-  const dim3 grid(unsigned((MN + 1023) / 1024), unsigned(p.E));
+  // few enough blocks that those of experts of one part, which end at once, cost little
+  const int64_t all = (MN + 1023) / 1024, most = 2048 / p.E;  // E <= 16
+  const dim3 grid(unsigned(all < most ? all : most), unsigned(p.E));
   if (dtype == TOPMOE_DTYPE_FP32)
     return launch_kernel(sum_rows_kernel<float>, grid, dim3(256), 0, s, p.part, p.offsets, p.E,
                          p.R, p.most, MN, static_cast<float*>(p.C));
