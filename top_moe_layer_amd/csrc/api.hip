@@ -57,6 +57,8 @@ const char* topmoe_strerror(int status) {
     case TOPMOE_ERR_BAD_SHAPE:
       return "shape outside the supported limits (FFN: H, I multiples of 64, E <= 64; block "
              "operators: H, C multiples of 8, E <= 256, gate rows dividing N, row pitches >= C; "
+             "products by expert: K, O multiples of 8, K of 32 with 4-bit matrices, <= 2^20, "
+             "E <= 256, E * O <= 2^25, row pitches multiples of 8 and <= 2^21; "
              "1 <= k <= E; N >= 0; sizes within 32-bit row ids)";
     case TOPMOE_ERR_UNSUPPORTED_DTYPE: return "dtype must be TOPMOE_DTYPE_FP32 or TOPMOE_DTYPE_BF16";
     case TOPMOE_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than the *_workspace_bytes() size";
@@ -67,7 +69,7 @@ const char* topmoe_strerror(int status) {
     case TOPMOE_ERR_BAD_ARG:
       return "invalid argument (aux_coef, z_coef or capacity_factor negative or not finite, "
              "a negative capacity, aux_grad, z_grad or residual_scale not finite, eps not positive and finite, an "
-             "unknown gate mode, unknown flag bits, a misaligned pointer, or a launch-shape "
+             "unknown gate mode, unknown kind of rows, unknown flag bits, a misaligned pointer, or a launch-shape "
              "override that is not instantiated)";
   }
   return "unknown status";

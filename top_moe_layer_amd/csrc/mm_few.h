@@ -8,7 +8,9 @@
 // column (or of its row) at a time: 32 k of e2m1, 8 of bf16, 4 of fp32; which k
 // a lane group holds does not matter to the sum as long as row and column
 // agree.  Nothing is staged: rows are few and come from the caches.  Bound by
-// the matrix's bytes.
+// the matrix's bytes (bf16, 64 rows of 16 experts, 2048 -> 1408, in 64 x 64 tiles
+// 14 us, 6.5 TB/s) or, where they are few, by one load's way (4-bit, one row, 2048
+// -> 6464: 5.3 us for 7 MB; 64 rows of 16 experts, 2048 -> 1408: 11 for 24 MB).
 #pragma once
 
 #include "mm_impl.h"

@@ -12,7 +12,8 @@
 //
 // A thread converts 16 bytes of a row (8 bf16 or 4 fp32 channels) in registers
 // with v_cvt_scalef32_pk_fp4_f32; the four or eight threads of a group find its
-// largest magnitude with two or three lane exchanges.  Bound by memory.
+// largest magnitude with two or three lane exchanges.  Bound by memory: 16 x 2432
+// x 2048 bf16 packed in 36 us and unpacked in 29 (202 MB each, 5.5 and 6.9 TB/s).
 #include "act8_impl.h"
 #include "mm.h"
 
