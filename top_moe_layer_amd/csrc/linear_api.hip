@@ -107,7 +107,12 @@ size_t moe_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E) {
   int32_t any = 0;
   if (linear_shape(R, K, O, E, &any, 8) != TOPMOE_OK) return 0;
   const size_t dx = rows_grad_bytes(R, K, O, E);
-  const size_t dw = size_t(mm_tn_parts(R, mm_tn_most(R, O, K, E), E)) * size_t(O) * size_t(K) * sizeof(float);
+  int64_t parts = 0;  // of either dtype
+  for (const bool f32 : {false, true}) {
+    const int64_t n = mm_tn_parts(R, mm_tn_most(R, O, K, E, f32), E);
+    parts = n > parts ? n : parts;
+  }
+  const size_t dw = size_t(parts) * size_t(O) * size_t(K) * sizeof(float);
   return align_up((dx > dw ? dx : dw) + 1);
 }
 
@@ -138,7 +143,7 @@ int moe_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, con
     MmParams p = params(dy, lddy, x, expert_offsets, R, 0, K, E, dw, K);
     p.M = int(O);
     p.ldb = ldx;
-    p.most = mm_tn_most(R, O, K, E);
+    p.most = mm_tn_most(R, O, K, E, f32);
     p.part = part;
     Launch first = weights, second = weights;
     if (p.most > 0) in_one(weights, &first, &second);

@@ -75,14 +75,18 @@ hipError_t launch_mm_bf16_parts(const MmParams& p, const Launch& s);
 // How the backward divides its sums.  NN: tiles of 64 x 128 fewer than half the
 // blocks that fit on the chip are multiplied by chunks of K, of 128 elements or
 // more (0: whole).  TN: an expert's rows, experts being few, are added up
-// in parts for one of two reasons (0: whole).  Tiles of 128 x 128 that leave CUs
-// without work: n parts, which save (1 - 1 / n) of an expert's rows at 10 ns
-// each, and cost 8 bytes an element to write and read, 1.6 ps; three or more, as
-// two save less than the launch that adds them up (E = 1, 768 x 2432, us with
-// parts and without: 4096 rows 34 and 42, of 1024 25 and 15 in four parts;
-// fp32 256 x 768, 4096 rows 27 and 73).  Experts with several times the others'
-// rows: parts of five fourths of the average (E = 8, 4096 rows on average, 9000
-// at most, 166 and 201; E = 16, 2048 182 and 185, E = 16, 1024 197 and 166).
+// in parts for one of two reasons (0: whole).  Tiles (128 x 128; 64 x 64 in fp32)
+// that leave CUs without work: n parts, which save (1 - 1 / n) of an expert's
+// rows at 10 ns each (20), and cost 8 bytes an element to write and read, 1.6 ps;
+// three or more, as two save less than the launch that adds them up (E = 1, 768 x
+// 2432, us with parts and without: 4096 rows 34 and 42, of 1024 25 and 15 in four
+// parts; fp32 256 x 768, 4096 rows 27 and 73).  Experts with several times the
+// others' rows: parts of five fourths of the average (us with and without, 768 x
+// 2432, the largest expert in brackets, and where all have as many: E = 8, 4096
+// rows on average (9000) 151 and 201, 129 and 117; 2048 (4500) 94 and 104, 72 and
+// 60; E = 16, 2048 (7000) 184 and 186, 146 and 124; fp32, E = 8, 1024 (2250) 296
+// and 479, 286 and 279; 512 (1100) 183 and 251, 151 and 136; 256 (540) 126 and 133,
+// 117 and 81).
 inline int mm_nn_chunk(int64_t R, int64_t N, int64_t K, int E) {
   const int64_t experts = E < R ? E : R;
   if (experts <= 0) return 0;
@@ -95,15 +99,15 @@ inline int mm_nn_chunk(int64_t R, int64_t N, int64_t K, int E) {
 }
 inline int64_t mm_chunks(int64_t K, int kchunk) { return kchunk > 0 ? (K + kchunk - 1) / kchunk : 1; }
 constexpr int kMmPartExperts = 64;  // lanes of a wavefront, which number the parts
-inline int mm_tn_most(int64_t R, int64_t M, int64_t N, int E) {
-  const int64_t mean = R / E;
+inline int mm_tn_most(int64_t R, int64_t M, int64_t N, int E, bool f32) {
+  const int64_t mean = R / E, side = f32 ? 64 : 128, gain = f32 ? 12800 : 6400;
   if (E > 16 || mean < 256) return 0;
-  const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128) * E;
+  const int64_t tiles = (M + side - 1) / side * ((N + side - 1) / side) * E;
   int64_t parts = 1;
-  while (parts < 512 / tiles && (parts + 1) * (parts + 1) * E * M * N <= mean * 6400) ++parts;
+  while (parts < 512 / tiles && (parts + 1) * (parts + 1) * E * M * N <= mean * gain) ++parts;
   int64_t most = (mean + parts - 1) / parts;
   if (parts < 3) {
-    if (E < 2 || mean <= 2048) return 0;
+    if (E < 2 || (f32 ? mean < 500 : mean <= 2048)) return 0;
     most = mean * 5 / 4;
   }
   // (a gigabyte of parts at most)
