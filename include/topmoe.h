@@ -561,9 +561,9 @@ int moe_ffn_restore8(const void* kept, size_t kept_bytes, int64_t N, int64_t H, 
  *   expert_offsets [E + 1], from 0 on and not decreasing, on the device (other
  *   values give other rows, but no access outside the tensors); NULL with
  *   E == 1: one matrix for all rows.
- * K and O are positive multiples of 8 up to 2^20, R < 2^31, E <= 256, E * O <=
- * 2^25; tensor pointers 16-byte aligned.  Outputs must not alias inputs or each other.  With
- * R == 0 tensors of that size may be NULL. */
+ * K and O are positive multiples of 8 up to 2^20, R <= 2^31 - 2^16, E <= 256, E *
+ * O <= 2^25; tensor pointers 16-byte aligned.  Outputs must not alias inputs or
+ * each other.  With R == 0 tensors of that size may be NULL. */
 #define TOPMOE_LINEAR_MAX_EXPERTS 256
 #define TOPMOE_LINEAR_BWD_STAGES 2  /* 0 dx, 1 dw (forward: one stage) */
 int moe_linear_fwd(const void* x, int64_t ldx, const void* w, const int32_t* expert_offsets,

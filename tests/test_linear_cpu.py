@@ -41,8 +41,8 @@ def test_linear_refusals(name):
     assert call(name, base) == last
     assert call(name, base, dtype=2) == B.ERR_UNSUPPORTED_DTYPE
     assert call(name, base, dtype=-1) == B.ERR_UNSUPPORTED_DTYPE
-    for over in (dict(R=-1), dict(R=1 << 31), dict(K=0), dict(K=-64), dict(K=60),
-                 dict(K=(1 << 20) + 64), dict(O=0), dict(O=44), dict(O=(1 << 20) + 8), dict(E=0),
+    for over in (dict(R=-1), dict(R=1 << 31), dict(R=(1 << 31) - (1 << 16) + 1), dict(K=0),
+                 dict(K=-64), dict(K=60), dict(K=(1 << 20) + 64), dict(O=0), dict(O=44), dict(O=(1 << 20) + 8), dict(E=0),
                  dict(E=257), dict(off=None), dict(E=256, O=(1 << 17) + 8)):
         assert call(name, base, **over) == B.ERR_BAD_SHAPE, over
     if name.startswith("mx4"):  # whole groups of 32

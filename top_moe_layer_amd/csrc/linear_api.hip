@@ -16,6 +16,8 @@ static_assert(kMx4Group == TOPMOE_MX4_GROUP && kMx4Group == kAct8Group, "scale g
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+// The products', so that a row past a tile's or a slice's last still counts in 32 bits.
+constexpr int64_t kMaxLinearRows = (int64_t(1) << 31) - (int64_t(1) << 16);
 constexpr int64_t kMaxSide = int64_t(1) << 20, kMaxPitch = int64_t(1) << 21;
 // Rows of all experts' matrices: what a launch's threads number in 32 bits.
 constexpr int64_t kMaxOut = int64_t(1) << 25;
@@ -27,7 +29,7 @@ bool pitch_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0 && ld <= kM
 
 // K in, O out; step: what K is a multiple of.
 int linear_shape(int64_t R, int64_t K, int64_t O, int E, const int32_t* offsets, int step) {
-  if (R < 0 || R > kMaxRows || K <= 0 || K % step != 0 || K > kMaxSide) return TOPMOE_ERR_BAD_SHAPE;
+  if (R < 0 || R > kMaxLinearRows || K <= 0 || K % step != 0 || K > kMaxSide) return TOPMOE_ERR_BAD_SHAPE;
   if (O <= 0 || O % 8 != 0 || O > kMaxSide) return TOPMOE_ERR_BAD_SHAPE;
   if (E < 1 || E > kMmMaxExperts || (!offsets && E != 1)) return TOPMOE_ERR_BAD_SHAPE;
   if (int64_t(E) * O > kMaxOut) return TOPMOE_ERR_BAD_SHAPE;

@@ -259,11 +259,11 @@ __device__ __forceinline__ RowTile row_tile(int t, const int (&o)[5], int incl, 
 
 // The parts that an expert's `rows` are summed in, of `most` at most (0: one).
 __device__ __forceinline__ int parts_of(int rows, int most) {
-  return most > 0 && rows > most ? (rows + most - 1) / most : 1;
+  return most > 0 && rows > most ? 1 + (rows - 1) / most : 1;
 }
 // (Up to 64 experts, one a lane.)  The expert and part that unit u is, longest
-// parts first, so that the longest sums start first, and the number of the part among those that are kept apart;
-// false past the last.
+// parts first, so that the longest sums start first, and the number of the part
+// among those that are kept apart; false past the last.
 struct RowPart {
   int e, part, parts, slot;
 };

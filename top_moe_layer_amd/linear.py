@@ -85,7 +85,8 @@ def moe_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torc
                    expert_offsets: Optional[torch.Tensor] = None, *,
                    need_dx: bool = True, need_dw: bool = True,
                    dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
-                   workspace: Optional[torch.Tensor] = None, stream=None, stage_events: Optional[B.StageEvents] = None) -> MoeLinearGrads:
+                   workspace: Optional[torch.Tensor] = None, stream=None,
+                   stage_events: Optional[B.StageEvents] = None) -> MoeLinearGrads:
     """Gradients of moe_linear_fwd for dy [R, O]: dx[r] = w[e]^T dy[r] (zeros in
     rows of no expert) and dw[e], the sum over e's rows of dy[r] x[r]^T (zeros
     for an expert without rows).  ``need_dx`` / ``need_dw``: what is not needed is
