@@ -719,3 +719,22 @@ def test_stage_events(env):
     one = tm.StageEvents(1)
     tm.mx4_linear_fwd(x, p, off, stage_events=one)
     assert one.elapsed_ms()[0] > 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("sizes,K,O", [
+    ([700] + [100] * 7, 264, 392), ([0] * 7 + [1400], 264, 392), ([650] + [43] * 15, 264, 392),
+    ([1] * 15 + [1300], 136, 264), ([600] + [26] * 23, 264, 392), ([500] + [10] * 63, 136, 264),
+    ([3200] + [457] * 7, 264, 392), ([5000] + [1000] * 15, 136, 264)])
+def test_dw_of_skewed_experts(env, sizes, K, O, dt):
+    """One expert with most of the rows beside 7, 15 and more others, whole sums and parts."""
+    dev, tm = env
+    d, n = DT[dt], sum(sizes)
+    announce(f"dw of {len(sizes)} experts, {max(sizes)} of {n} rows in one, {K} x {O} {dt}")
+    x, dy, w = rnd(1, n, K, dt=d), rnd(2, n, O, dt=d), torch.empty(len(sizes), O, K, dtype=d, device=dev)
+    off = offsets(sizes).to(dev)
+    dw = tm.moe_linear_bwd(dy.to(dev), x.to(dev), w, off, need_dx=False).dw
+    torch.cuda.synchronize()
+    ref = R.grouped_dw(dy, x, sizes)
+    BR.check("dw", dw, ref, R.tol(ref, R.grouped_dw(dy.abs(), x.abs(), sizes), max(sizes), d))
+    assert same(dw, tm.moe_linear_bwd(dy.to(dev), x.to(dev), w, off, need_dx=False).dw)

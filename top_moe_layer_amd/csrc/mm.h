@@ -81,12 +81,16 @@ hipError_t launch_mm_bf16_parts(const MmParams& p, const Launch& s);
 // three or more, as two save less than the launch that adds them up (E = 1, 768 x
 // 2432, us with parts and without: 4096 rows 34 and 42, of 1024 25 and 15 in four
 // parts; fp32 256 x 768, 4096 rows 27 and 73).  Experts with several times the
-// others' rows: parts of five fourths of the average (us with and without, 768 x
-// 2432, the largest expert in brackets, and where all have as many: E = 8, 4096
-// rows on average (9000) 151 and 201, 129 and 117; 2048 (4500) 94 and 104, 72 and
-// 60; E = 16, 2048 (7000) 184 and 186, 146 and 124; fp32, E = 8, 1024 (2250) 296
-// and 479, 286 and 279; 512 (1100) 183 and 251, 151 and 136; 256 (540) 126 and 133,
-// 117 and 81).
+// others' rows: parts of five fourths of the average (us with and without, the
+// largest expert in brackets, last where all have as many: 768 x 2432, E = 8, 4096
+// rows on average (9000) 182 and 200, (16384) 150 and 322, 126 and 116; 2048 (4500)
+// 104 and 105, 73 and 63; E = 16, 4096 (14000) 289 and 319, 259 and 245; 2048 (7000)
+// 166 and 162, 142 and 125).  In fp32 this is for small matrices, of which an expert
+// has fewer tiles than there are CUs, and costs up to an eighth in large ones (E =
+// 8, 256 x 768, 1024 (2252) 43 and 65, (4096) 49 and 111, 46 and 42; 512 (1126) 28 and
+// 36, 30 and 27; 768 x 768, 1024 (2252) 100 and 92, (4096) 103 and 125, 94 and 90; 768 x
+// 2432, 1024 (2250) 261 and 241, 253 and 250; 512 (1100) 149 and 130, 143 and 132;
+// 256 (540) 101 and 78, 93 and 79).
 inline int mm_nn_chunk(int64_t R, int64_t N, int64_t K, int E) {
   const int64_t experts = E < R ? E : R;
   if (experts <= 0) return 0;
@@ -130,8 +134,6 @@ __host__ __device__ inline int64_t mm_tn_units(int64_t R, int most, int E) {
 __host__ __device__ inline bool mm_tn_sorted(int64_t R, int E) {
   return E <= kMmPartExperts && R / E >= 256;
 }
-// Experts that go round the 8 XCDs once or twice are theirs as wholes.
-__host__ __device__ inline bool mm_tn_by_xcd(int E) { return E == 8 || E == 16; }
 // NN: out [R, N] = the sum of the chunks, rounded once to the dtype.
 hipError_t launch_mm_sum_chunks(const float* part, int64_t chunks, int64_t R, int64_t N, int dtype,
                                 void* out, int64_t ldo, const Launch& s);

@@ -10,8 +10,8 @@
 //   dx of the same, 64 x 128, 128 x 256, 256 x 256 (E = 8, E = 16):  256: 32.3, 73.8,
 //     99.7, 58.9, 53.7, 45.3; 1024: 128, 97.5, 124, 176, 127, 125; 2048: 219, 148, 135, 314, 218, 220
 //   dW, 128 x 128, 128 x 256, 256 x 256, rows an expert all alike: E = 8, 768 x 2432
-//     64: 16.7, 13, 14.2; 512: 31.9, 26.1, 28.3; 4096: 149, 127, 112;  E = 16, 2048 x 1408,
-//     1024: 127, 116, 117;  E = 64, 768 x 2432, 512: 258, 215, 224;  E = 4, 1024: 23.5, 25.8,
+//     64: 15.6, 11.2, 12.7; 512: 27.9, 24.3, 23.7; 4096: 141, 124, 125;  E = 16, 2048 x 1408,
+//     1024: 122, 106, 107;  E = 64, 768 x 2432, 512: 258, 215, 224;  E = 4, 1024: 23.5, 25.8,
 //     35.2;  E = 1, 1024: 14.6, 21, 28.7
 // The kernel for few rows, whose wavefronts divide K, where even 64 x 64 tiles
 // leave CUs without work (E = 1, 2 rows: 7.5 against 9.2; E = 16, 8 rows, 352

@@ -377,11 +377,16 @@ void mm_kernel(MmParams p) {
   // takes the x-th eighth of the tiles, in groups of GM row tiles, column by
   // column, so that blocks running together share rows and matrix panels in its
   // L2, and the grid's blocks of an XCD take its tiles in turn.  TN, where an
-  // expert's rows are the length of its tiles: a block a tile; each XCD takes
-  // whole experts (or parts of them), so that it reads their rows alone (16384
-  // tokens, top-2 of 8, 768 x 2432: 634 MB past the L2s where every XCD took an
-  // eighth of each expert's tiles, of 209 there are), or, where experts do not
-  // go round, such an eighth.
+  // expert's rows are the length of its tiles: a block a tile; each XCD takes an
+  // eighth of every expert's tiles (or of each of its parts'), so that the work is
+  // even however the rows are spread.  Whole experts for an XCD read a third of the
+  // bytes past the L2s (16384 tokens, top-2 of 8, 768 x 2432: 209 MB, of eighths
+  // 634), which gained little and cost up to threefold (us, eighths and wholes):
+  // E = 8, 768 x 2432, 32768 rows, alike 127 and 121, half of them one expert's 150
+  // and 148; 1024 x 4096, 24576 rows in parts, a softmax of scale 0.7 227 and 268;
+  // 4096 x 8192, 16384 rows whole, alike 980 and 990, half one expert's 1040 and 2840;
+  // fp32 768 x 2432, 16384 rows, a third one expert's 497 and 730;  E = 16, 2048 x 1408,
+  // 16384 rows, half one expert's 173 and 326.
   constexpr int GM = 8;
   struct Tile {
     const char *a, *b;          // first bytes of the tile's rows and columns
@@ -394,12 +399,11 @@ void mm_kernel(MmParams p) {
   const int chunks = CHUNKS && p.kchunk > 0 ? (p.K + p.kchunk - 1) / p.kchunk : 1;
   int o[5], incl = 0, last = 0, mts, share, total, mine;
   const int blocks = gridDim.x >> 3;
-  const bool by_xcd = TN_ && mm_tn_by_xcd(p.E);
   if constexpr (TN_) {
     mts = (p.M + BM - 1) / BM;
     total = mts * nt;
-    share = by_xcd ? total : (total + 7) >> 3;
-    const int units = int(mm_tn_units(p.R, p.most, p.E)), end = share * (by_xcd ? (units + 7) / 8 : units);
+    share = (total + 7) >> 3;
+    const int end = share * int(mm_tn_units(p.R, p.most, p.E));
     mine = local < end ? (end - local + blocks - 1) / blocks : 0;
   } else {
     if (p.offsets != nullptr) mts = row_tiles<BM>(p.offsets, p.E, p.R, lane, o, incl, last);
@@ -420,10 +424,8 @@ void mm_kernel(MmParams p) {
     RowPart rp{};
     bool any = true;  // TN: there is such a unit and tile
     if constexpr (TN_) {
-      const int n = local + i * blocks, round = n / share;
-      // by XCD: back and forth over them
-      const int unit = !by_xcd ? round : 8 * round + (round & 1 ? 7 - xcd : xcd);
-      at = n - round * share + (by_xcd ? 0 : xcd * share);
+      const int n = local + i * blocks, unit = n / share;
+      at = n - unit * share + xcd * share;
       any = at < total;
       if (p.E > kMmPartExperts) {  // one after the other, each whole
         rp = RowPart{unit, 0, 1, 0};
@@ -959,7 +961,7 @@ hipError_t launch_tile(const MmParams& p, const Launch& s) {
   if (LAYOUT == kMmTN) {
     const int64_t units = mm_tn_units(p.R, p.most, p.E);
     const int64_t tiles = (p.M + BM - 1) / BM * nt;
-    grid = 8 * (mm_tn_by_xcd(p.E) ? (units + 7) / 8 * tiles : units * ((tiles + 7) / 8));
+    grid = 8 * units * ((tiles + 7) / 8);
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
   } else {
     // row tiles at most: every expert's last one, and that of the rows of none, may be partial
