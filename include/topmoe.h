@@ -570,8 +570,12 @@ int moe_linear_fwd(const void* x, int64_t ldx, const void* w, const int32_t* exp
                    int64_t R, int64_t K, int64_t O, int E, int dtype, void* y, int64_t ldy,
                    void* stream, void* const* stage_events);
 /* dx NULL: not wanted (w may be NULL as well); dw NULL: not wanted (x may be).
- * The workspace holds fp32 parts of sums that are divided among blocks;
- * moe_linear_bwd_workspace_bytes returns 0 for invalid sizes. */
+ * The workspace holds fp32 parts of sums that are divided among blocks, up to a
+ * gigabyte of them and often none; how many goes by the dtype.
+ * moe_linear_bwd_dtype_workspace_bytes is what a call in that dtype needs,
+ * moe_linear_bwd_workspace_bytes enough for either; both return 0 for invalid
+ * sizes. */
+size_t moe_linear_bwd_dtype_workspace_bytes(int64_t R, int64_t K, int64_t O, int E, int dtype);
 size_t moe_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E);
 int moe_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
                    const int32_t* expert_offsets, int64_t R, int64_t K, int64_t O, int E,

@@ -738,3 +738,28 @@ def test_dw_of_skewed_experts(env, sizes, K, O, dt):
     ref = R.grouped_dw(dy, x, sizes)
     BR.check("dw", dw, ref, R.tol(ref, R.grouped_dw(dy.abs(), x.abs(), sizes), max(sizes), d))
     assert same(dw, tm.moe_linear_bwd(dy.to(dev), x.to(dev), w, off, need_dx=False).dw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_bwd_takes_its_dtypes_workspace(env, dt):
+    """As many bytes as the dtype needs are enough, and the front end takes no more."""
+    dev, tm = env
+    d = DT[dt]
+    for sizes, K, O in (([512] * 8, 264, 392), ([2400, 0, 260, 300, 280, 310, 250, 1000], 136, 72), ([20], 64, 6464)):
+        n, E = sum(sizes), len(sizes)
+        x, dy = rnd(1, n, K, dt=d).to(dev), rnd(2, n, O, dt=d).to(dev)
+        w, off = rnd(3, E, O, K, dt=d).to(dev), offsets(sizes).to(dev)
+        need = tm.moe_linear_bwd_workspace_bytes(n, K, O, E, d)
+        ws = torch.full((need + 4096,), 7, dtype=torch.uint8, device=dev)
+        g = tm.moe_linear_bwd(dy, x, w, off, workspace=ws[:need])
+        torch.cuda.synchronize()
+        assert bool((ws[need:] == 7).all())
+        del ws
+        # bytes asked for (allocated ones count the allocator's blocks, up to 1 MiB larger)
+        before = torch.cuda.memory_stats()["requested_bytes.all.current"]
+        torch.cuda.reset_peak_memory_stats()
+        h = tm.moe_linear_bwd(dy, x, w, off)
+        torch.cuda.synchronize()
+        asked = torch.cuda.memory_stats()["requested_bytes.all.peak"] - before
+        assert asked == (x.numel() + w.numel()) * x.element_size() + need
+        assert same(g.dx, h.dx) and same(g.dw, h.dw)

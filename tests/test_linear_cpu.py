@@ -167,3 +167,23 @@ def test_grouped_reference():
     x, w = torch.arange(8.0).reshape(4, 2), torch.tensor([[[1.0, 0.0]], [[0.0, 2.0]]])
     assert R.grouped(x, w, [1, 2]).flatten().tolist() == [0.0, 6.0, 10.0, 0.0]
     assert R.grouped_dw(x[:, :1], x, [1, 2]).tolist() == [[[0.0, 0.0]], [[4 + 16.0, 6 + 20.0]]]
+
+
+def test_workspace_of_a_dtype():
+    f, bf16, fp32 = tm.moe_linear_bwd_workspace_bytes, torch.bfloat16, torch.float32
+    # 1024 rows each: parts in fp32 alone, of 1280 rows: 6 experts have more, and 12 parts, at most
+    assert f(8192, 2048, 4096, 8, bf16) == 256
+    assert f(8192, 2048, 4096, 8, fp32) == 12 * 2048 * 4096 * 4 + 256 == f(8192, 2048, 4096, 8)
+    for R, K, O, E in ((0, 64, 48, 4), (20, 64, 6464, 1), (32768, 768, 2432, 8), (16384, 768, 2432, 17),
+                       (2400, 72, 136, 8), (1 << 20, 8192, 8192, 16)):
+        assert f(R, K, O, E) == max(f(R, K, O, E, bf16), f(R, K, O, E, fp32)) >= 256
+    assert f(8, 60, 48, 4, bf16) == f(8, 64, 48, 257, fp32) == 0
+    assert B.lib().moe_linear_bwd_dtype_workspace_bytes(8, 64, 48, 4, 2) == 0
+    with pytest.raises(TypeError):
+        f(8, 64, 48, 4, torch.float16)
+    # a call asks for what its dtype needs (and refuses the misaligned workspace behind that check)
+    over = dict(R=8192, K=2048, O=4096, E=8, lddy=4096, ldx=2048, lddx=2048, ws=FAKE + 8)
+    for dtype, code in ((bf16, B.DTYPE_BF16), (fp32, B.DTYPE_FP32)):
+        need = f(8192, 2048, 4096, 8, dtype)
+        assert call("moe_linear_bwd", BWD, dtype=code, ws_bytes=need, **over) == B.ERR_BAD_ARG
+        assert call("moe_linear_bwd", BWD, dtype=code, ws_bytes=need - 1, **over) == B.ERR_WORKSPACE_TOO_SMALL

@@ -115,6 +115,7 @@ SIGNATURES = {
     "moe_linear_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp,
                               _vp]),
     "moe_linear_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "moe_linear_bwd_dtype_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
     "moe_linear_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp,
                               _i64, _vp, _vp, _sz, _vp, _vp]),
     "mx4_pack": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),

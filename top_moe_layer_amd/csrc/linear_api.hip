@@ -105,17 +105,20 @@ int moe_linear_fwd(const void* x, int64_t ldx, const void* w, const int32_t* exp
   return TOPMOE_OK;
 }
 
-size_t moe_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E) {
+size_t moe_linear_bwd_dtype_workspace_bytes(int64_t R, int64_t K, int64_t O, int E, int dtype) {
   int32_t any = 0;
-  if (linear_shape(R, K, O, E, &any, 8) != TOPMOE_OK) return 0;
+  if (!known_dtype(dtype) || linear_shape(R, K, O, E, &any, 8) != TOPMOE_OK) return 0;
   const size_t dx = rows_grad_bytes(R, K, O, E);
-  int64_t parts = 0;  // of either dtype
-  for (const bool f32 : {false, true}) {
-    const int64_t n = mm_tn_parts(R, mm_tn_most(R, O, K, E, f32), E);
-    parts = n > parts ? n : parts;
-  }
+  const int64_t parts =
+      mm_tn_parts(R, mm_tn_most(R, O, K, E, dtype == TOPMOE_DTYPE_FP32), E);
   const size_t dw = size_t(parts) * size_t(O) * size_t(K) * sizeof(float);
   return align_up((dx > dw ? dx : dw) + 1);
+}
+
+size_t moe_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E) {
+  const size_t f32 = moe_linear_bwd_dtype_workspace_bytes(R, K, O, E, TOPMOE_DTYPE_FP32);
+  const size_t bf16 = moe_linear_bwd_dtype_workspace_bytes(R, K, O, E, TOPMOE_DTYPE_BF16);
+  return f32 > bf16 ? f32 : bf16;
 }
 
 int moe_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
@@ -129,7 +132,7 @@ int moe_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, con
     return TOPMOE_ERR_BAD_SHAPE;
   if ((!dx && !dw && R > 0) || (dx && !w) || !workspace || (R > 0 && (!dy || (dw && !x))))
     return TOPMOE_ERR_NULL_ARG;
-  if (workspace_bytes < moe_linear_bwd_workspace_bytes(R, K, O, E))
+  if (workspace_bytes < moe_linear_bwd_dtype_workspace_bytes(R, K, O, E, dtype))
     return TOPMOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) ||
       !aligned(dw, 16) || !aligned(expert_offsets, 4) || !aligned(workspace, 256))

@@ -76,8 +76,12 @@ def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor,
 
 
 @functools.lru_cache(maxsize=256)
-def moe_linear_bwd_workspace_bytes(R: int, K: int, O: int, E: int = 1) -> int:
-    return int(B.lib().moe_linear_bwd_workspace_bytes(R, K, O, E))
+def moe_linear_bwd_workspace_bytes(R: int, K: int, O: int, E: int = 1,
+                                   dtype: Optional[torch.dtype] = None) -> int:
+    """What moe_linear_bwd needs for gradients in ``dtype``; without it, enough for any."""
+    if dtype is None:
+        return int(B.lib().moe_linear_bwd_workspace_bytes(R, K, O, E))
+    return int(B.lib().moe_linear_bwd_dtype_workspace_bytes(R, K, O, E, _code(dtype)))
 
 
 @_on_kernel_stream
@@ -115,7 +119,7 @@ def moe_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torc
         dx = None
     if dx is None and dw is None:
         return MoeLinearGrads(None, None)
-    wp, wn, ws = _scratch(moe_linear_bwd_workspace_bytes(R, K, O, E), "moe_linear_bwd", dev,
+    wp, wn, ws = _scratch(moe_linear_bwd_workspace_bytes(R, K, O, E, dt), "moe_linear_bwd", dev,
                           workspace)
     _call("moe_linear_bwd", dev, stage_events, dy.data_ptr(), lddy, _ptr(x) if need_dw else 0, ldx,
           w.data_ptr(), _ptr(expert_offsets), R, K, O, E, code, _ptr(dx), lddx, _ptr(dw),
