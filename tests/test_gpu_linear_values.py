@@ -97,3 +97,121 @@ def test_outlier_channels_in_eight_bits(env, n, K, O, cancel):
     at = torch.meshgrid(rows, cols, indexing="ij")
     BR.check("bf16", y.cpu()[at], ref, R.tol(ref, mag, K, BF16) + lost * (1 + 2.0 ** -8))
     BR.check("fp32", y32.cpu()[at], ref, R.tol(ref, mag, K, FP32))
+
+
+def codes(shape, allowed, seed):
+    """q [.., K / 2] of e2m1 codes out of ``allowed``, either sign."""
+    g = torch.Generator().manual_seed(seed)
+    c = torch.tensor(allowed)[torch.randint(0, len(allowed), shape, generator=g)]
+    c = c + 8 * torch.randint(0, 2, shape, generator=g)
+    return (c[..., 0::2] + 16 * c[..., 1::2]).to(torch.uint8)
+
+
+@pytest.mark.parametrize("K", [160, 256])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_matrices_at_the_ends_of_the_scales(env, n, K):
+    """Scale bytes 0, 1, 253 and 254: what is below 2^128 counts as it is, for all rows; 2^128 and more
+    are infinite where the matrix goes through bf16 (in their own column, or channel of dx), and
+    count as they are beside packed rows otherwise."""
+    dev, tm = env
+    O = 40
+    q = codes((O, K), range(8), n)
+    s = torch.full((O, K // 32), 127, dtype=torch.uint8)
+    for o, byte, allowed in ((3, 253, range(6)), (4, 253, range(8)), (5, 254, range(4)), (6, 254, range(8)),
+                             (7, 0, range(8)), (8, 1, range(8)), (9, 252, range(8))):
+        q[o], s[o] = codes((K,), allowed, o), byte
+    wv = R.from_mx4(q, s)
+    W = tm.Mx4(q.to(dev), s.to(dev))
+    past = (wv.abs() >= 2.0 ** 128).any(1)
+    assert past.nonzero().flatten().tolist() == [4, 6]
+    g = torch.Generator().manual_seed(n + K)
+    x = torch.randn(n, K, generator=g)
+    x = torch.where(x.abs() < 2.0 ** -8, torch.ones(()), x) * 2.0 ** -100  # whole in three bf16 parts
+    xb = x.bfloat16()
+    a8, m4 = tm.act8_pack(x.to(dev)), tm.mx4_pack(x.to(dev))
+    a8v, m4v = BR.act8(x)[2], R.from_mx4(*R.mx4(x))
+    sa, sb = torch.exp2(a8.scale.cpu().double() - 127), torch.exp2(s.double() - 127)
+    lost = kept8(a8v / sa.repeat_interleave(32, -1), sa, wv / sb.repeat_interleave(32, -1), sb)
+    for arg, v, d, through in ((x.to(dev), x, FP32, True), (xb.to(dev), xb, BF16, True), (a8, a8v, FP32, True),
+                               (a8, a8v, BF16, False), (m4, m4v, FP32, False), (m4, m4v, BF16, False)):
+        y = tm.mx4_linear_fwd(arg, W, dtype=d).cpu()
+        ref, mag = v.double() @ wv.T, v.double().abs() @ wv.abs().T
+        tol = R.tol(ref, mag, K, d) + (lost * (1 + 2.0 ** -8) if arg is a8 and d is BF16 else 0)
+        o = ~past if through else torch.ones(O, dtype=torch.bool)
+        BR.check(f"{type(arg).__name__} {d}", y[:, o], ref[:, o], tol[:, o])
+        if through:
+            assert not torch.isfinite(y[:, past]).any()
+    # the matrices' transposes: a channel that holds 2^128 or more has no finite gradient
+    few = wv.clone()
+    few[[4, 6]] = 0.0
+    q2, s2 = q.clone(), s
+    q2[[4, 6]] = 0
+    q2[4, 8], q2[6, 15] = 16 * 7, 15  # 6 in the high half of a byte, -6 in the low one
+    few[4, 17], few[6, 30] = 6 * 2.0 ** 126, -6 * 2.0 ** 127
+    assert torch.equal(R.from_mx4(q2, s2), few)
+    inf = torch.zeros(K, dtype=torch.bool)
+    inf[[17, 30]] = True
+    for d in (FP32, BF16):
+        dy = torch.randn(n, O, generator=g)
+        dy = (torch.where(dy.abs() < 2.0 ** -8, torch.ones(()), dy) * 2.0 ** -100).to(d)
+        dx = tm.mx4_linear_bwd(dy.to(dev), tm.Mx4(q2.to(dev), s2.to(dev))).cpu()
+        assert not torch.isfinite(dx[:, inf]).any()
+        ref, mag = dy.double() @ few, dy.double().abs() @ few.abs()
+        BR.check("dx", dx[:, ~inf], ref[:, ~inf], R.tol(ref, mag, O, d)[:, ~inf])
+
+
+@pytest.mark.parametrize("n", [2, 40, 300])
+def test_small_fp32_rows_keep_24_bits_to_their_end(env, n):
+    """fp32 rows beside a large matrix: whole from 2^-110 on, below that to multiples of 2^-133."""
+    dev, tm = env
+    K, O = 96, 40
+    q, s = R.mx4(torch.randn(O, K, generator=torch.Generator().manual_seed(1)))
+    s = (s.int() + 100).to(torch.uint8)
+    wv = R.from_mx4(q, s)
+    W = tm.Mx4(q.to(dev), s.to(dev))
+    g = torch.Generator().manual_seed(n)
+    for e, whole in ((0, True), (-109, True), (-110, True), (-111, False), (-118, False), (-126, False),
+                     (-132, False), (-140, False), (-149, False)):
+        bits = torch.randint(2 ** 23, 2 ** 24, (n, K), generator=g).double()  # 1 to 2 in 24 bits
+        x = (bits * 2.0 ** (e - 23) * (1 - 2 * torch.randint(0, 2, (n, K), generator=g))).float()
+        for name, m, y in (("y", wv.T, tm.mx4_linear_fwd(x.to(dev), W)),
+                           ("dx", wv[:, :64], tm.mx4_linear_bwd(x[:, :O].to(dev), W)[:, :64])):
+            v = x.double() if name == "y" else x[:, :O].double()
+            ref, mag = v @ m, v.abs() @ m.abs()
+            cut = 0 if whole else 2.0 ** -133 * m.abs().sum(0)
+            BR.check(f"{name} {e}", y, ref, R.tol(ref, mag, v.shape[1], FP32) + cut)
+
+
+@pytest.mark.parametrize("K", [160, 256])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_scales_of_eight_bit_rows(env, n, K):
+    """The scales' whole range for 8-bit rows against the matrix's, NaN in one of each: in bf16 as they
+    are; in fp32 through bf16, which holds those of bytes 3 to 246 whole and others to 2^-133."""
+    dev, tm = env
+    O = 72
+    g = torch.Generator().manual_seed(n)
+    q = codes((O, K), range(8), n + 1)
+    s = (torch.arange(O * (K // 32)) * 7 % 250).reshape(O, K // 32).to(torch.uint8)
+    s[11, 3] = 255
+    wv, sb = R.from_mx4(q, s), torch.exp2(s.double() - 127)
+    wu = R.from_mx4(q, torch.full_like(s, 127))
+    W = tm.Mx4(q.to(dev), s.to(dev))
+    code = torch.randint(0, 127, (n, K), generator=g) + 128 * torch.randint(0, 2, (n, K), generator=g)
+    a = code.to(torch.uint8).view(torch.float8_e4m3fn)
+    byte = (torch.arange(n * (K // 32)) * 11 % 247).reshape(n, K // 32).to(torch.uint8)
+    if n > 1:
+        byte[n // 2, K // 32 - 1] = 255
+    sa = torch.exp2(byte.double() - 127)
+    av = a.double() * torch.where(byte == 255, torch.tensor(float("nan"), dtype=torch.float64),
+                                  sa).repeat_interleave(32, -1)
+    ref, mag = av @ wv.T, av.abs() @ wv.abs().T
+    fine = mag < 2.0 ** 127  # (false for NaN)
+    assert bool(fine.any())
+    lost = kept8(a.double(), sa, wu, sb) * (1 + 2.0 ** -8)
+    low = 2.0 ** -134 * (torch.ones_like(av) * (byte < 3).double().repeat_interleave(32, -1)) @ wv.abs().T
+    zero = torch.zeros((), dtype=torch.float64)
+    for d, more in ((BF16, lost), (FP32, low)):
+        y = tm.mx4_linear_fwd(tm.Act8(a.to(dev), byte.to(dev)), W, dtype=d).cpu().double()
+        assert bool(y[ref.isnan()].isnan().all())
+        BR.check(f"y {d}", torch.where(fine, y, zero), torch.where(fine, ref, zero),
+                 torch.where(fine, R.tol(ref, mag, K, d) + more, zero))

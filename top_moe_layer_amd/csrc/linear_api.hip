@@ -219,7 +219,8 @@ int mx4_linear_fwd(const void* x, int64_t ldx, const uint8_t* x_scale, int rows,
   // (mm_mx4.hip): with one channel in 64 ten times the others, y [32768, 4864] of
   // 768 products each differs from that of whole sums by 1.7e-4 in the norm, a
   // tenth of its rounding; where outliers cancel it can be more than the rounding.
-  // For y in fp32 the 8-bit rows go through bf16, which loses nothing.
+  // For y in fp32 the 8-bit rows go through bf16, which loses nothing between
+  // scale bytes 3 and 246.
   const int fa = plain ? (bf16 ? kMmBf16 : kMmF32Split)
                        : rows == TOPMOE_ROWS_MX4 ? kMmE2m1 : bf16 ? kMmE4m3 : kMmE4m3Bf;
   if (R > 0) TOPMOE_TRY(launch_mm_mx4(fa, bf16, p, L));

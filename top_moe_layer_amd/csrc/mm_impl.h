@@ -24,10 +24,11 @@
 //   bf16           32x32x16 (a lane holds 8 k)
 //   fp32           32x32x2, four for a lane's 4 k
 //   fp32 rows beside bf16 or e2m1 matrices: x = hi + mid + lo, three bf16 parts
-//                  by truncation, exact; three bf16 instructions instead of
-//                  eight fp32 ones at a sixteenth of the rate
+//                  by truncation, exact from 2^-110 on; three bf16 instructions
+//                  instead of eight fp32 ones at a sixteenth of the rate
 //   e2m1 matrix beside bf16 rows: 16 bytes of a lane are its 32 k of a slice,
-//                  turned into bf16 with their scale (exact) as they are used
+//                  turned into bf16 with their scale (exact below 2^128) as they
+//                  are used
 //   e2m1 x e2m1, e4m3 x e2m1: 32x32x64 with the scales as operands
 #pragma once
 
@@ -149,8 +150,9 @@ __device__ __forceinline__ void mfma_mx(u32x4 a, u32x4 b0, u32x4 b1, f32x16& c, 
           : "+v"(c) : "v"(a), "v"(y), "v"(sa), "v"(sb));
   }
 }
-// Two e2m1 / e4m3 values times a scale as two bf16 (exact; a product outside
-// bf16's range becomes infinite, or rounds on its subnormals).
+// Two e2m1 / e4m3 values times a scale as two bf16: exact, but infinite from 2^128
+// on (e2m1 4 and 6 with the scale byte 253, 2 to 6 with 254; e4m3 from 247 on), and
+// e4m3 with bytes below 3 rounded to multiples of 2^-133, bf16's smallest subnormal.
 template <int SEL>
 __device__ __forceinline__ uint32_t bf16_of_e2m1(uint32_t w, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, SEL));
@@ -169,7 +171,9 @@ __device__ __forceinline__ u32x4 bf16_of_e4m3x8(uint32_t w0, uint32_t w1, float 
 }
 // Eight fp32 values (of two 16-byte pieces) as three bf16 parts whose sum they
 // are: the upper 8 bits of the mantissa, of the rest and of its rest, 24 in all.
-// An infinity is its own first part, with no rest; NaN leaves NaN in the rest.
+// Below 2^-110 the last part ends with bf16's subnormals: bits under 2^-133 are
+// dropped.  An infinity is its own first part, with no rest; NaN leaves NaN in the
+// rest.  (Parts that are 0 meet an infinite element of the matrix as NaN.)
 __device__ __forceinline__ void split3(u32x4 a, u32x4 b, u32x4 (&p)[3]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

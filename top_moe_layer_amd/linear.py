@@ -201,7 +201,8 @@ def mx4_linear_fwd(x: Union[torch.Tensor, Act8, Mx4], w: Mx4,
     own, which is all a plain x can have, and by default bfloat16 for packed
     rows.  K is a multiple of 32.  Of each eight consecutive products of 8-bit rows
     a bfloat16 y misses up to 2^-12 of the largest, which shows where large ones
-    cancel; dtype=torch.float32 has whole sums."""
+    cancel; dtype=torch.float32 has whole sums.  To plain rows,
+    and to 8-bit rows with a float32 y, matrix elements of 2^128 and more are infinite."""
     packed = isinstance(x, (Act8, Mx4))
     return _mx4_fwd(x.q if packed else x, x, w, expert_offsets, dtype, y, stage_events,
                     stream=stream)
