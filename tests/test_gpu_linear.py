@@ -763,3 +763,32 @@ def test_bwd_takes_its_dtypes_workspace(env, dt):
         asked = torch.cuda.memory_stats()["requested_bytes.all.peak"] - before
         assert asked == (x.numel() + w.numel()) * x.element_size() + need
         assert same(g.dx, h.dx) and same(g.dw, h.dw)
+
+
+def test_four_bits_on_two_streams_at_once(env):
+    """4-bit products and gradients on two streams (whose gradients keep unpacked matrices and parts in
+    workspaces from launch to launch), one of them a raw handle: the bits of one after the other."""
+    dev, tm = env
+    S = [torch.cuda.Stream() for _ in range(2)]
+    cases = []
+    for i, (sizes, K, O) in enumerate((([900, 40, 100], 288, 544), ([300, 0, 141], 544, 288))):
+        n, off = sum(sizes), offsets(sizes).to(dev)
+        p = tm.mx4_pack(rnd(10 * i, 3, O, K).to(dev))
+        for d in DT.values():
+            cases.append((i, rnd(10 * i + 1, n, K, dt=d).to(dev), rnd(10 * i + 2, n, O, dt=d).to(dev), p, off))
+
+    def step(x, dy, p, off, **on):
+        a8, m4 = tm.act8_pack(x, **on), tm.mx4_pack(x, **on)
+        return [tm.mx4_linear_fwd(x, p, off, **on), tm.mx4_linear_fwd(a8, p, off, dtype=x.dtype, **on),
+                tm.mx4_linear_fwd(m4, p, off, dtype=x.dtype, **on), tm.mx4_linear_bwd(dy, p, off, **on),
+                tm.mx4_unpack(p, dtype=x.dtype, **on)]
+
+    want = [step(*c[1:]) for c in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for i, *c in cases:
+            got.append(step(*c, stream=S[i] if i else S[i].cuda_stream))
+    torch.cuda.synchronize()
+    for j, outs in enumerate(got):
+        assert all(same(a, b) for a, b in zip(outs, want[j % len(cases)])), j
