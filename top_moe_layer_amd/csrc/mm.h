@@ -1,5 +1,5 @@
 // Products of rows grouped by expert with each expert's matrix (mm_impl.h,
-// mm_few.hip): what a launch needs, in elements unless said.
+// mm_few.h): what a launch needs, in elements unless said.
 #pragma once
 
 #include "kernels.h"
@@ -39,7 +39,7 @@ struct MmParams {
   int64_t R;
   int64_t lda, ldb, ldc;  // row pitches of A and C, and of B in TN (else B is dense)
   int E, M, N, K;         // M: TN only; K: NT and NN only
-  // Sums in parts, added up by launch_mm_sum: NN over chunks of kchunk of K
+  // Sums in parts, added up by launch_mm_sum_chunks and _rows: NN over chunks of kchunk of K
   // (0: whole), C then being the parts [chunks, R, N] in fp32; TN over parts of
   // an expert's rows, of most rows each (0: whole), those of experts with more
   // than one going to part [.., M, N], expert by expert.
@@ -73,8 +73,8 @@ hipError_t launch_mm_f32_by_bf16(const MmParams& p, const Launch& s);
 hipError_t launch_mm_bf16_parts(const MmParams& p, const Launch& s);
 
 // How the backward divides its sums.  NN: tiles of 64 x 128 fewer than half the
-// blocks that fit on the chip are multiplied by chunks of K, of 128 elements or
-// more (0: whole).  TN: an expert's rows, experts being few, are added up
+// blocks that fit on the chip are multiplied by chunks of K, of 256 elements or
+// more in multiples of 128, and what is left (0: whole).  TN: an expert's rows, experts being few, are added up
 // in parts for one of two reasons (0: whole).  Tiles (128 x 128; 64 x 64 in fp32)
 // that leave CUs without work: n parts, which save (1 - 1 / n) of an expert's
 // rows at 10 ns each (20), and cost 8 bytes an element to write and read, 1.6 ps;

@@ -11,6 +11,14 @@
 // the matrix's bytes (bf16, 64 rows of 16 experts, 2048 -> 1408, in 64 x 64 tiles
 // 14 us, 6.5 TB/s) or, where they are few, by one load's way (4-bit, one row, 2048
 // -> 6464: 5.3 us for 7 MB; 64 rows of 16 experts, 2048 -> 1408: 11 for 24 MB).
+// The launchers take it by the average rows of an expert, which is all the host
+// knows; an expert of many more has no more blocks for them, and each reads its
+// columns again for every 16 RT rows (us here and in tiles: 64 experts, 2048 ->
+// 1408, 8 rows each, bf16 by 4 bits 38 and 86; 64 experts, 768 -> 256, one of 600
+// rows and 4 each in the others, bf16 97 and 9, fp32 124 and 30, bf16 by 4 bits 49
+// and 11; 256 experts, 768 -> 768, one of 2000 and 1 each, fp32 499 and 184, bf16 by
+// 4 bits 171 and 74; 16 experts, 2048 -> 1408, one of 200 and 3 each, 4-bit rows 34
+// and 12).
 #pragma once
 
 #include "mm_impl.h"

@@ -38,8 +38,10 @@ bool few(const MmParams& p, const Launch& s, hipError_t* e) {
 
 // The scales of every row lie at multiples of four bytes: their rows are and
 // they begin there.  Else all products that are not few rows' take 64 x 128 tiles
-// with ordinary loads of the scales (K = 2080 for 2048: 466
-// for 184 us of 4-bit rows, 863 for 398 of bf16).
+// with ordinary loads of the scales, which wait for all loads in flight (16384
+// rows, us: K = 2080 for 2048, to 6464: 422 for 147 of 4-bit rows, 441 for 211 of
+// 8-bit, 739 for 380 of bf16; K = 6464 for 6400, to 2048: 673 for 141, 691 for 168,
+// 1039 for 322).
 bool words(const MmParams& p) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.As) | reinterpret_cast<uintptr_t>(p.Bs);
   return p.K % 128 == 0 && at % 4 == 0;
