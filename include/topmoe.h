@@ -608,16 +608,17 @@ int mx4_unpack(const uint8_t* q, const uint8_t* scale, int64_t R, int64_t C, int
  * The product is that of the values the bytes stand for; y has the dtype.  Sums
  * are fp32; with 8-bit rows and y in bf16, however, the matrix instructions add
  * the products of eight consecutive channels at a time and cut each of them
- * toward zero where it loses less than 2^-12 of the largest of the eight.  That
- * is relative to the products: where large ones cancel, y loses more than its
- * rounding to bf16 does (y in fp32 loses nothing).  A scale byte of 255 is NaN.
+ * toward zero, by less than 2^-12 of the largest of the eight.  That goes by the
+ * products: where large ones cancel, y can lose more than by its rounding to
+ * bf16 (y in fp32 loses nothing).  A scale byte of 255 is NaN.
  * Plain rows, 8-bit rows with y in fp32 and the gradient below take the matrix
  * through bf16: there its values of 2^128 and more (4 and 6 with the scale byte
  * 253, 2 to 6 with 254) are infinite, as they are read back, and a sum that has
  * one, whatever it is multiplied with, is infinite or NaN.  fp32 rows count to
  * 2^-133 (whole, with 24 bits, from 2^-110 on), so do 8-bit rows with y in fp32
- * (whole with scale bytes 3 to 246; theirs of 2^128 and more are infinite).  K is a multiple of 32, so that every group is whole; x and wq 16-byte
- * aligned; the rest as for moe_linear_fwd. */
+ * (whole with scale bytes 3 to 246; theirs of 2^128 and more are infinite).
+ * K is a multiple of 32, so that every group is whole; x and wq 16-byte aligned;
+ * the rest as for moe_linear_fwd. */
 #define TOPMOE_ROWS_PLAIN 0
 #define TOPMOE_ROWS_ACT8 1
 #define TOPMOE_ROWS_MX4 2
@@ -627,8 +628,7 @@ int mx4_linear_fwd(const void* x, int64_t ldx, const uint8_t* x_scale, int rows,
                    void* stream, void* const* stage_events);
 /* dx of it for frozen matrices (adapters trained around them): dx[r] = w_e^T
  * dy[r].  The matrices are turned into bf16 (exact below 2^128) in the workspace
- * first.
- * mx4_linear_bwd_workspace_bytes returns 0 for invalid sizes. */
+ * first.  mx4_linear_bwd_workspace_bytes returns 0 for invalid sizes. */
 #define TOPMOE_MX4_BWD_STAGES 2  /* 0 matrices to bf16, 1 dx */
 size_t mx4_linear_bwd_workspace_bytes(int64_t R, int64_t K, int64_t O, int E);
 int mx4_linear_bwd(const void* dy, int64_t lddy, const uint8_t* wq, const uint8_t* w_scale,

@@ -61,8 +61,8 @@ def moe_linear_fwd(x: torch.Tensor, w: torch.Tensor,
     """A linear layer per expert: y[r] = w[e] x[r] for the rows r in
     [expert_offsets[e], expert_offsets[e + 1]).  x [R, K] as moe_dispatch_fwd
     lays rows out (a row pitch is fine), w [E, O, K], expert_offsets [E + 1]
-    int32; without them w [O, K] or [1, O, K] takes all rows.  y [R, O]; rows of
-    no expert, behind expert_offsets[E], are zeros."""
+    int32; without them w [O, K] or [1, O, K] takes all rows.  y [R, O], which must
+    not overlap x or w; rows of no expert, behind expert_offsets[E], are zeros."""
     R, K = _matrix(x, "x")
     dev, dt = x.device, x.dtype
     code = _code(dt)
